@@ -520,6 +520,136 @@ tern_status tern_check(void* stream);
 #define TERN_SELFTEST_MAX_POLLS (1u << 20)
 tern_status tern_selftest_wait(uint32_t polls, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache and drafted-token trees
+ *
+ * What stands between the qkv and the output linear of a decode step that
+ * verifies drafted tokens: where the new tokens go (tern_kv_plan), their
+ * keys and values put there (tern_kv_write), attention of each request's
+ * tree of drafted tokens over its cached tokens and its tree
+ * (tern_tree_attention), and, once the accepted path is known, that path
+ * made contiguous (tern_kv_commit).
+ *
+ * Notation: B requests; request b has ctx_len[b] cached tokens and
+ * n_b = row_start[b + 1] - row_start[b] new ones, rows row_start[b] .. of
+ * the step's T rows; new token i of request b stands at position
+ * ctx_len[b] + i.  Position p of request b is in page table[b][p / P], at
+ * row p % P of it (P = page_size); its slot is page * P + p % P, a 64-bit
+ * number.  H key heads, Hq = H * group query heads (query head h reads key
+ * head h / group), D the head size.
+ *
+ * Lengths, tables, slots, masks and paths are read on the GPU: no call
+ * copies them to the host, so every call can be captured in a graph and
+ * replayed with other lengths.  What they hold is checked in the kernels:
+ * an entry out of range is skipped as stated at each call, never followed.
+ * ---------------------------------------------------------------------- */
+
+#define TERN_KV_BF16 0
+#define TERN_KV_F16 1
+
+/* A cache of keys and values: element [page][row][head][d] of either is at
+ * page * page_stride + row * token_stride + head * head_stride + d (strides
+ * in elements, multiples of 8), so pages may hold rows of heads or heads of
+ * rows.  page_size is a power of two, 8 to 256; dim is 64, 128 or 256;
+ * pages < 2^31. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t pages, page_size, heads, dim;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t dtype; /* TERN_KV_BF16 or TERN_KV_F16: 2 bytes an element */
+} tern_kv_cache;
+
+/* tern_kv_plan -- block tables and slot maps of one step, on the GPU.
+ *
+ *   ctx_len, new_len  int32 [B]: cached and new tokens (a negative length
+ *                     counts as 0 and sets flag 8)
+ *   table             int32 [B][table_width], rows table_stride apart, in
+ *                     and out: entries below ceil(ctx_len / P) are kept, the
+ *                     new tokens' further pages are written behind them
+ *   free_pages        int32 [n_free]: pages not in use; pages are taken from
+ *                     index *free_head on (NULL: 0), in request order
+ *   free_head         int32 [1] or NULL
+ * outputs:
+ *   row_start  int32 [B + 1]   first row of each request
+ *   slots      int64 [capacity] slot of every row; -1 past the last row and
+ *                               where a token has no page
+ *   positions  int32 [capacity] position of every row (0 past the last)
+ *   request    int32 [capacity] request of every row (-1 past the last)
+ *   info       int32 [4]       rows in all, pages taken, the next free_head,
+ *                              flags: 1 free pages ran out (the table gets
+ *                              -1), 2 a request longer than its table row,
+ *                              4 more rows than capacity, 8 a negative length
+ * No output may overlap an input other than the table.
+ * Requirements: page_size a power of two, 1 <= page_size <= 65536;
+ * 0 <= B <= 16384; capacity, n_free < 2^31; table_width * page_size < 2^31. */
+tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
+                         int64_t page_size, int32_t* table, int64_t table_stride,
+                         int64_t table_width, const int32_t* free_pages, int64_t n_free,
+                         const int32_t* free_head, int32_t* row_start, int64_t capacity,
+                         int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
+                         void* stream);
+
+/* tern_kv_write -- rows of keys and values into the cache's slots.
+ *   k, v   [T][H][D] of the cache's type; rows token_stride and heads
+ *          head_stride elements apart (multiples of 8), as slices of the qkv
+ *          linear's output are
+ *   slots  int64 [T]; a slot outside [0, pages * P) leaves the cache as it is
+ * Two rows of one call must not have the same slot. */
+tern_status tern_kv_write(const tern_kv_cache* cache, const void* k, const void* v,
+                          int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                          int64_t v_head_stride, const int64_t* slots, int64_t T, void* stream);
+
+/* tern_kv_commit -- the accepted path of every request made contiguous.
+ *   caches     host array of `layers` caches of the same shape and strides
+ *   path       int32 [B][path_width]: indices of the accepted tokens among
+ *              the request's new ones, strictly increasing (a token stands
+ *              behind its ancestors); path_len int32 [B]
+ *   ctx_out    int32 [B]: ctx_len + the tokens kept; not ctx_len itself
+ * For j < path_len[b]: row ctx_len[b] + path[b][j] of the keys and values
+ * goes to row ctx_len[b] + j, in every layer.  A path is cut at its first
+ * entry that does not increase, is negative, or has no page.
+ * Requirements: 0 <= path_width <= 256, 0 <= B <= 65535, layers <= 65535. */
+tern_status tern_kv_commit(const tern_kv_cache* caches, int64_t layers, const int32_t* table,
+                           int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                           const int32_t* path, int64_t path_width, const int32_t* path_len,
+                           int32_t* ctx_out, int64_t B, void* stream);
+
+/* tern_tree_attention -- attention of new tokens over the paged cache.
+ *
+ *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,
+ *   lse = ln sum_j exp(s_j)
+ * over the cached positions j < ctx_len[b] and, of the new tokens i of the
+ * same request (already written at position ctx_len[b] + i), those whose bit
+ * is set in the row's mask.
+ *
+ *   q          [T][Hq][D] of the cache's type, rows q_token_stride and heads
+ *              q_head_stride elements apart (multiples of 8)
+ *   row_start  int32 [B + 1], as tern_kv_plan gives it
+ *   mask       uint64 [T][mask_words]: bit i % 64 of word i / 64 of a row
+ *              says that the row sees new token i of its request; NULL: a
+ *              chain (token i sees new tokens 0 .. i)
+ *   max_new    the most new tokens any request may have, known on the host; it
+ *              chooses the kernel's tile
+ *   out        [T][Hq][D], dense;  lse  float [T][Hq] or NULL
+ *   ws         tern_tree_attention_workspace_bytes(), any contents
+ * A row that sees nothing (or only scores of -infinity) has out = 0 and
+ * lse = -infinity.  What a row does not see has no influence on it: masked
+ * keys and values may hold infinities or NaN, and the cache past a request's
+ * last token is not looked at.  Positions whose page is out of range count
+ * as zero keys and values; rows past row_start[B] are not written.
+ * Requirements: Hq a multiple of H; 0 <= B <= 65536;
+ * T * Hq * D < 2^34; max_new <= 256, and mask_words <= 4; 1 <= H <= 65535;
+ * table_width * P < 2^31. */
+size_t tern_tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D);
+tern_status tern_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                const tern_kv_cache* cache, const int32_t* table,
+                                int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                                const int32_t* row_start, const uint64_t* mask,
+                                int64_t mask_words, int64_t B, int64_t T, int64_t Hq,
+                                int64_t max_new, float scale, void* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

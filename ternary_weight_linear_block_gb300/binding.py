@@ -35,6 +35,8 @@ TERN_FWHT_DECODE = 1
 TERN_FWHT_I8 = 2
 TERN_FWHT_F16 = 3
 TERN_FWHT_I8H = 4
+TERN_KV_BF16 = 0
+TERN_KV_F16 = 1
 TERN_OP_GEMV = 1
 TERN_OP_GEMM = 2
 TERN_OP_GEMM_PACKED = 3
@@ -47,6 +49,8 @@ STATUS_NAMES = {0: "TERN_OK", 1: "TERN_ERR_INVALID_ARG", 2: "TERN_ERR_SHAPE", 3:
 _i64 = ctypes.c_int64
 _p = ctypes.c_void_p
 _sz = ctypes.c_size_t
+_i32 = ctypes.c_int32
+_f32 = ctypes.c_float
 _SIGS = {
     "tern_status_str": (ctypes.c_char_p, [ctypes.c_int]),
     "tern_version": (ctypes.c_int, []),
@@ -76,7 +80,21 @@ _SIGS = {
     "tern_gemv_decode_noalloc": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p]),
     "tern_linear_decode": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p, _sz, _p]),
     "tern_gemv_decode_f32": (ctypes.c_int, [_p, _p, _i64, _i64, _i64, _p, _p, _sz, _p]),
+    "tern_kv_plan": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _i64, _p,
+                                    _p, _p, _p, _p]),
+    "tern_kv_write": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _i64, _p]),
+    "tern_kv_commit": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p]),
+    "tern_tree_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "tern_tree_attention": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i64,
+                                           _i64, _i64, _i64, _i64, _f32, _p, _p, _p, _sz, _p]),
 }
+
+
+class KVCacheDesc(ctypes.Structure):
+    """tern_kv_cache of include/tern.h."""
+    _fields_ = [("k", _p), ("v", _p), ("pages", _i64), ("page_size", _i64), ("heads", _i64),
+                ("dim", _i64), ("page_stride", _i64), ("token_stride", _i64),
+                ("head_stride", _i64), ("dtype", _i32)]
 
 _lib = None
 
@@ -261,6 +279,46 @@ def tern_gemv_decode_noalloc(packed, xh, xs, m, n, k, y, stream=None):
     allocation), for callers that cannot allocate device memory."""
     return _call("tern_gemv_decode_noalloc", _ptr(packed), _ptr(xh), _ptr(xs), m, n, k, _ptr(y),
                  _stream(stream))
+
+
+def _desc(cache):
+    """Address of a KVCacheDesc (or of an array of them)."""
+    return cache if cache is None or isinstance(cache, int) else ctypes.addressof(cache)
+
+
+def tern_kv_plan(ctx_len, new_len, b, page_size, table, table_stride, table_width, free_pages,
+                 n_free, free_head, row_start, capacity, slots, positions, request, info,
+                 stream=None):
+    return _call("tern_kv_plan", _ptr(ctx_len), _ptr(new_len), b, page_size, _ptr(table),
+                 table_stride, table_width, _ptr(free_pages), n_free, _ptr(free_head),
+                 _ptr(row_start), capacity, _ptr(slots), _ptr(positions), _ptr(request),
+                 _ptr(info), _stream(stream))
+
+
+def tern_kv_write(cache, k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots,
+                  t, stream=None):
+    return _call("tern_kv_write", _desc(cache), _ptr(k), _ptr(v), k_token_stride, k_head_stride,
+                 v_token_stride, v_head_stride, _ptr(slots), t, _stream(stream))
+
+
+def tern_kv_commit(caches, layers, table, table_stride, table_width, ctx_len, path, path_width,
+                   path_len, ctx_out, b, stream=None):
+    return _call("tern_kv_commit", _desc(caches), layers, _ptr(table), table_stride, table_width,
+                 _ptr(ctx_len), _ptr(path), path_width, _ptr(path_len), _ptr(ctx_out), b,
+                 _stream(stream))
+
+
+def tern_tree_attention_workspace_bytes(max_new: int, hq: int, h: int, d: int) -> int:
+    return lib().tern_tree_attention_workspace_bytes(max_new, hq, h, d)
+
+
+def tern_tree_attention(q, q_token_stride, q_head_stride, cache, table, table_stride, table_width,
+                        ctx_len, row_start, mask, mask_words, b, t, hq, max_new, scale, out, lse,
+                        ws, ws_bytes, stream=None):
+    return _call("tern_tree_attention", _ptr(q), q_token_stride, q_head_stride, _desc(cache),
+                 _ptr(table), table_stride, table_width, _ptr(ctx_len), _ptr(row_start),
+                 _ptr(mask), mask_words, b, t, hq, max_new, scale, _ptr(out), _ptr(lse), _ptr(ws),
+                 ws_bytes, _stream(stream))
 
 
 # ---------------------------------------------------------------- conveniences

@@ -1,0 +1,421 @@
+// The paged key/value cache around the attention of drafted tokens: block
+// tables and slot maps from the requests' lengths (kv_plan), the new rows
+// into their slots (kv_write), and the accepted path of every tree made
+// contiguous (kv_commit).  All three move integers or 16-bit rows and do no
+// arithmetic on them.
+#include <algorithm>
+
+#include "kv_internal.cuh"
+#include "tern_internal.cuh"
+
+namespace tern {
+namespace {
+
+// ------------------------------------------------------------------ plan
+//
+// Two sums over the requests carry everything: the rows before request b
+// (its row start) and the further pages taken before it.  Every CTA adds
+// them up for itself (B is at most 16384 lengths, read from L2) and keeps
+// both sums in shared memory, so one launch is enough and no CTA waits for
+// another; a row or a page then finds its request by bisection.  Bound: the
+// launch and two dependent round trips to L2 up to about 100,000 rows, then
+// the 16 bytes written for each row.
+
+constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_ROWS = 4;   // consecutive rows of one thread: 16-byte stores
+
+struct PlanArgs {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  int32_t* table;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* row_start;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* request;
+  int32_t* info;
+  int64_t table_stride;
+  int B, shift, width, n_free, capacity;
+};
+
+struct Need {
+  int64_t rows;   // new tokens
+  int64_t pages;  // further pages
+  int held;       // pages of the cached tokens
+  int flags;
+};
+
+__device__ __forceinline__ Need need_of(const PlanArgs& a, int b) {
+  const int c0 = a.ctx_len[b], n0 = a.new_len[b];
+  Need r;
+  r.flags = (c0 < 0 || n0 < 0) ? 8 : 0;
+  const int64_t c = max(c0, 0), n = max(n0, 0), page = int64_t(1) << a.shift;
+  const int64_t held = (c + page - 1) >> a.shift, all = (c + n + page - 1) >> a.shift;
+  if (all > a.width) r.flags |= 2;
+  r.rows = n;
+  r.held = static_cast<int>(held < a.width ? held : a.width);
+  r.pages = (all < a.width ? all : a.width) - r.held;
+  return r;
+}
+
+// Largest b with start[b] <= x (start[0] = 0, not decreasing, B entries).
+__device__ __forceinline__ int request_of(const int* start, int B, int x) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+  extern __shared__ int s_sums[];
+  int* s_row = s_sums;              // [B + 1] rows before request b
+  int* s_page = s_sums + a.B + 1;   // [B + 1] further pages before it
+  __shared__ int64_t s_warp[2][PLAN_THREADS / 32];
+  __shared__ int64_t s_carry[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  int64_t rows0 = 0, pages0 = 0;
+  int flags = 0;
+  for (int base = 0; base < a.B; base += PLAN_THREADS) {
+    const int b = base + tid;
+    Need w{0, 0, 0, 0};
+    if (b < a.B) w = need_of(a, b);
+    flags |= w.flags;
+    int64_t rows = w.rows, pages = w.pages;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t r = __shfl_up_sync(~0u, rows, d), p = __shfl_up_sync(~0u, pages, d);
+      if (lane >= d) {
+        rows += r;
+        pages += p;
+      }
+    }
+    if (lane == 31) {
+      s_warp[0][warp] = rows;
+      s_warp[1][warp] = pages;
+    }
+    __syncthreads();
+    int64_t before_r = rows0, before_p = pages0;
+    for (int w2 = 0; w2 < warp; ++w2) {
+      before_r += s_warp[0][w2];
+      before_p += s_warp[1][w2];
+    }
+    rows += before_r;
+    pages += before_p;
+    if (b < a.B) {   // sums past 2^31 stay at its end: they are past every row asked for
+      s_row[b + 1] = static_cast<int>(min(rows, int64_t(INT32_MAX)));
+      s_page[b + 1] = static_cast<int>(min(pages, int64_t(INT32_MAX)));
+    }
+    if (tid == PLAN_THREADS - 1) {
+      s_carry[0] = rows;
+      s_carry[1] = pages;
+    }
+    __syncthreads();
+    rows0 = s_carry[0];
+    pages0 = s_carry[1];
+  }
+  if (tid == 0) s_row[0] = s_page[0] = 0;
+  const int any_flags = __syncthreads_or(flags & 2) ? 2 : 0;
+  const int neg_flags = __syncthreads_or(flags & 8) ? 8 : 0;
+  const int head = a.free_head != nullptr ? min(max(*a.free_head, 0), a.n_free) : 0;
+  const int64_t avail = a.n_free - head;
+  const int total = s_row[a.B];
+  const int pages_all = s_page[a.B];
+
+  if (blockIdx.x == 0) {
+    for (int b = tid; b <= a.B; b += PLAN_THREADS) a.row_start[b] = s_row[b];
+    if (tid == 0) {
+      const int taken = static_cast<int>(min(pages0, avail));
+      a.info[0] = total;
+      a.info[1] = taken;
+      a.info[2] = head + taken;
+      a.info[3] = any_flags | neg_flags | (pages0 > avail ? 1 : 0) | (rows0 > a.capacity ? 4 : 0);
+    }
+  }
+
+  const int64_t threads = int64_t(gridDim.x) * PLAN_THREADS;
+  const int64_t me = int64_t(blockIdx.x) * PLAN_THREADS + tid;
+  // the further pages into the table
+  for (int64_t p = me; p < pages_all; p += threads) {
+    const int b = request_of(s_page, a.B, static_cast<int>(p));
+    const Need w = need_of(a, b);
+    const int64_t at = w.held + (p - s_page[b]);
+    if (at < a.width) a.table[b * a.table_stride + at] = p < avail ? a.free_pages[head + p] : -1;
+  }
+  // the rows
+  for (int64_t q = me; q * PLAN_ROWS < a.capacity; q += threads) {
+    const int r0 = static_cast<int>(q * PLAN_ROWS);
+    int64_t slot[PLAN_ROWS];
+    int pos[PLAN_ROWS], req[PLAN_ROWS];
+    int b = r0 < total ? request_of(s_row, a.B, r0) : a.B;
+    int known = -1, c = 0, held = 0;
+#pragma unroll
+    for (int i = 0; i < PLAN_ROWS; ++i) {
+      const int r = r0 + i;
+      slot[i] = -1;
+      pos[i] = 0;
+      req[i] = -1;
+      if (r < total && r < a.capacity) {
+        while (b + 1 < a.B && s_row[b + 1] <= r) ++b;
+        if (b != known) {
+          known = b;
+          c = max(a.ctx_len[b], 0);
+          held = need_of(a, b).held;
+        }
+        const int64_t p = int64_t(c) + (r - s_row[b]);
+        const int64_t at = p >> a.shift;
+        int page = -1;
+        if (at < held) {
+          page = a.table[b * a.table_stride + at];
+        } else if (at < a.width) {
+          const int64_t taken = s_page[b] + (at - held);
+          if (taken < avail) page = a.free_pages[head + taken];
+        }
+        if (page >= 0) slot[i] = (int64_t(page) << a.shift) + (p & ((int64_t(1) << a.shift) - 1));
+        pos[i] = static_cast<int>(min(p, int64_t(INT32_MAX)));
+        req[i] = b;
+      }
+    }
+    if (r0 + PLAN_ROWS <= a.capacity) {
+      *reinterpret_cast<longlong2*>(a.slots + r0) = make_longlong2(slot[0], slot[1]);
+      *reinterpret_cast<longlong2*>(a.slots + r0 + 2) = make_longlong2(slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.request + r0) = make_int4(req[0], req[1], req[2], req[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PLAN_ROWS; ++i) {
+        if (r0 + i < a.capacity) {
+          a.slots[r0 + i] = slot[i];
+          a.positions[r0 + i] = pos[i];
+          a.request[r0 + i] = req[i];
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ write
+//
+// A copy of 16-byte chunks to slots: `tpt` threads (a power of two) share a
+// row, so that a few rows still use many threads and many rows keep a warp's
+// accesses in one row.  Bound: the rows read and written once.
+
+constexpr int COPY_THREADS = 256;
+
+struct WriteArgs {
+  const uint16_t* k;
+  const uint16_t* v;
+  uint16_t* ck;
+  uint16_t* cv;
+  const int64_t* slots;
+  int64_t k_token, k_head, v_token, v_head;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t T, n_slots;
+  int chunks;                             // 16-byte chunks of a row of all heads
+  int dim_shift, page_shift, tpt_shift;   // log2 of chunks a head, of the page size, of tpt
+};
+
+__global__ void __launch_bounds__(COPY_THREADS) write_kernel(const WriteArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tpt = 1 << a.tpt_shift;
+  const int64_t step = (int64_t(gridDim.x) * COPY_THREADS) >> a.tpt_shift;
+  const int part = threadIdx.x & (tpt - 1);
+  for (int64_t t = (int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x) >> a.tpt_shift; t < a.T;
+       t += step) {
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.n_slots) continue;
+    const int64_t to = (slot >> a.page_shift) * a.page_stride +
+                       (slot & ((int64_t(1) << a.page_shift) - 1)) * a.token_stride;
+    const uint16_t* k = a.k + t * a.k_token;
+    const uint16_t* v = a.v + t * a.v_token;
+#pragma unroll 4
+    for (int c = part; c < a.chunks; c += tpt) {
+      const int64_t h = c >> a.dim_shift;
+      const int64_t d = (c & ((1 << a.dim_shift) - 1)) * 8;
+      const uint4 kk = *reinterpret_cast<const uint4*>(k + h * a.k_head + d);
+      const uint4 vv = *reinterpret_cast<const uint4*>(v + h * a.v_head + d);
+      *reinterpret_cast<uint4*>(a.ck + to + h * a.head_stride + d) = kk;
+      *reinterpret_cast<uint4*>(a.cv + to + h * a.head_stride + d) = vv;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ commit
+//
+// A thread owns one 16-byte column of a request's rows and moves it for the
+// whole path.  A path increases, so path[j] >= j: row j is written only
+// after it was read as a source (path[j'] = j needs j' <= j), and a later
+// source path[j'] > path[j] >= j is never a row already written.  So loads
+// may run ahead of stores and no thread waits for another.  Bound: the
+// moved rows read and written once; at decode sizes the launch and three
+// dependent round trips (path, table, rows).
+
+constexpr int MAX_PATH = 256;
+constexpr int COMMIT_LAYERS = 64;   // layers of one launch: their pointers are kernel arguments
+
+struct CommitArgs {
+  uint16_t* ptr[2 * COMMIT_LAYERS];   // keys, values of each layer
+  const int32_t* table;
+  const int32_t* ctx_len;
+  const int32_t* path;
+  const int32_t* path_len;
+  int32_t* ctx_out;
+  int64_t table_stride, path_stride;
+  int64_t page_stride, token_stride, head_stride, pages;
+  int width, path_width, chunks, dim_shift, page_shift;
+};
+
+__global__ void __launch_bounds__(COPY_THREADS) commit_kernel(const __grid_constant__ CommitArgs a) {
+  __shared__ int64_t s_from[MAX_PATH], s_to[MAX_PATH];
+  __shared__ int s_count;
+  const int b = blockIdx.y, tid = threadIdx.x;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int ctx = a.ctx_len[b];
+  const int len = ctx < 0 ? 0 : min(max(a.path_len[b], 0), a.path_width);
+  if (tid == 0) s_count = len;
+  __syncthreads();
+  // row of position p in the cache, or -1
+  const auto place = [&](int64_t p) -> int64_t {
+    const int64_t at = p >> a.page_shift;
+    if (at >= a.width) return -1;
+    const int64_t page = a.table[b * a.table_stride + at];
+    if (page < 0 || page >= a.pages) return -1;
+    return page * a.page_stride + (p & ((int64_t(1) << a.page_shift) - 1)) * a.token_stride;
+  };
+  for (int j = tid; j < len; j += COPY_THREADS) {
+    const int p = a.path[b * a.path_stride + j];
+    const int prev = j > 0 ? a.path[b * a.path_stride + j - 1] : -1;
+    int64_t from = -1, to = -1;
+    if (p >= 0 && p > prev) {
+      from = place(int64_t(ctx) + p);
+      to = p == j ? from : place(int64_t(ctx) + j);
+    }
+    if (from < 0 || to < 0) atomicMin(&s_count, j);
+    s_from[j] = from;
+    s_to[j] = to;
+  }
+  __syncthreads();
+  const int count = s_count;
+  if (a.ctx_out != nullptr && blockIdx.x == 0 && blockIdx.z == 0 && tid == 0)
+    a.ctx_out[b] = ctx + count;
+  const int c = blockIdx.x * COPY_THREADS + tid;
+  if (c >= a.chunks) return;
+  const int64_t col = int64_t(c >> a.dim_shift) * a.head_stride +
+                      (c & ((1 << a.dim_shift) - 1)) * 8;
+  uint16_t* x = a.ptr[blockIdx.z] + col;   // keys and values are two planes of z
+  constexpr int U = 4;
+  for (int j0 = 0; j0 < count; j0 += U) {
+    uint4 r[U];
+    bool move[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      move[i] = j0 + i < count && s_from[j0 + i] != s_to[j0 + i];
+      if (move[i]) r[i] = *reinterpret_cast<const uint4*>(x + s_from[j0 + i]);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (move[i]) *reinterpret_cast<uint4*>(x + s_to[j0 + i]) = r[i];
+  }
+}
+
+int log2_of(int64_t v) {
+  int s = 0;
+  while ((int64_t(1) << s) < v) ++s;
+  return s;
+}
+
+}  // namespace
+
+int kv_sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  return n;
+}
+
+cudaError_t launch_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
+                           int64_t page_size, int32_t* table, int64_t table_stride,
+                           int64_t table_width, const int32_t* free_pages, int64_t n_free,
+                           const int32_t* free_head, int32_t* row_start, int64_t capacity,
+                           int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
+                           cudaStream_t st) {
+  static std::atomic<unsigned long long> attr_done{0};
+  const size_t smem = static_cast<size_t>(2 * (B + 1)) * sizeof(int);
+  const cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                2 * (16384 + 1) * static_cast<int>(sizeof(int)));
+  });
+  if (e != cudaSuccess) return e;
+  PlanArgs a{ctx_len, new_len, table, free_pages, free_head, row_start, slots, positions, request,
+             info, table_stride, static_cast<int>(B), log2_of(page_size),
+             static_cast<int>(table_width), static_cast<int>(n_free), static_cast<int>(capacity)};
+  const int64_t per_block = PLAN_THREADS * PLAN_ROWS;
+  const int64_t blocks = std::min<int64_t>((capacity + per_block - 1) / per_block,
+                                           int64_t(4) * kv_sm_count());
+  return launch(plan_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))),
+                dim3(PLAN_THREADS), smem, st, a);
+}
+
+cudaError_t launch_kv_write(const tern_kv_cache& c, const void* k, const void* v, int64_t k_token,
+                            int64_t k_head, int64_t v_token, int64_t v_head, const int64_t* slots,
+                            int64_t T, cudaStream_t st) {
+  WriteArgs a{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+              static_cast<uint16_t*>(c.k), static_cast<uint16_t*>(c.v), slots, k_token, k_head,
+              v_token, v_head, c.page_stride, c.token_stride, c.head_stride, T,
+              c.pages * c.page_size, static_cast<int>(c.heads * c.dim / 8), log2_of(c.dim / 8),
+              log2_of(c.page_size), 0};
+  // one chunk a thread while that fits the GPU once, at most a warp a row beyond
+  const int64_t room = int64_t(kv_sm_count()) * 2048;
+  int shift = 0;
+  while (shift < 8 && (2 << shift) <= a.chunks && (shift < 5 || (T << (shift + 1)) <= room)) ++shift;
+  a.tpt_shift = shift;
+  const int64_t blocks = std::min<int64_t>(((T << shift) + COPY_THREADS - 1) / COPY_THREADS,
+                                           int64_t(kv_sm_count()) * 8);
+  return launch(write_kernel, dim3(static_cast<unsigned>(blocks)), dim3(COPY_THREADS), 0, st, a);
+}
+
+cudaError_t launch_kv_commit(const tern_kv_cache* caches, int64_t layers, const int32_t* table,
+                             int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                             const int32_t* path, int64_t path_width, const int32_t* path_len,
+                             int32_t* ctx_out, int64_t B, cudaStream_t st) {
+  const tern_kv_cache& c = caches[0];
+  const int chunks = static_cast<int>(c.heads * c.dim / 8);
+  for (int64_t l0 = 0; l0 < layers; l0 += COMMIT_LAYERS) {
+    const int n = static_cast<int>(std::min<int64_t>(layers - l0, COMMIT_LAYERS));
+    CommitArgs a{};
+    for (int l = 0; l < n; ++l) {
+      a.ptr[2 * l] = static_cast<uint16_t*>(caches[l0 + l].k);
+      a.ptr[2 * l + 1] = static_cast<uint16_t*>(caches[l0 + l].v);
+    }
+    a.table = table;
+    a.ctx_len = ctx_len;
+    a.path = path;
+    a.path_len = path_len;
+    a.ctx_out = l0 == 0 ? ctx_out : nullptr;
+    a.table_stride = table_stride;
+    a.path_stride = path_width;
+    a.page_stride = c.page_stride;
+    a.token_stride = c.token_stride;
+    a.head_stride = c.head_stride;
+    a.pages = c.pages;
+    a.width = static_cast<int>(table_width);
+    a.path_width = static_cast<int>(path_width);
+    a.chunks = chunks;
+    a.dim_shift = log2_of(c.dim / 8);
+    a.page_shift = log2_of(c.page_size);
+    const dim3 grid(static_cast<unsigned>((chunks + COPY_THREADS - 1) / COPY_THREADS),
+                    static_cast<unsigned>(B), static_cast<unsigned>(2 * n));
+    const cudaError_t e = launch(commit_kernel, grid, dim3(COPY_THREADS), 0, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace tern

@@ -3,6 +3,7 @@
 // point is stated in include/tern.h.
 #include <cstdio>
 
+#include "kv_internal.cuh"
 #include "tern_internal.cuh"
 
 namespace tern {
@@ -61,6 +62,29 @@ size_t gemm_int8_split_offset(int64_t M, int64_t N, int64_t K) {
 }
 size_t gemm_int8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return gemm_int8_split_offset(M, N, K) + gemm_dense_workspace_bytes(M, N, K);
+}
+
+bool pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
+
+// A stride in elements of a 16-bit tensor that 16-byte accesses and TMA take.
+bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s < (int64_t(1) << 39); }
+
+tern_status cache_ok(const tern_kv_cache* c) {
+  if (c == nullptr) return TERN_ERR_INVALID_ARG;
+  if (c->dtype != TERN_KV_BF16 && c->dtype != TERN_KV_F16) return TERN_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->pages >= (int64_t(1) << 31) || c->heads < 1 || c->heads > 65535)
+    return TERN_ERR_SHAPE;
+  if (!pow2(c->page_size) || c->page_size < 8 || c->page_size > 256) return TERN_ERR_SHAPE;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return TERN_ERR_SHAPE;
+  if (c->k == nullptr || c->v == nullptr) return TERN_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || !stride_ok(c->page_stride) ||
+      !stride_ok(c->token_stride) || !stride_ok(c->head_stride))
+    return TERN_ERR_ALIGN;
+  return TERN_OK;
+}
+
+bool table_ok(int64_t stride, int64_t width, int64_t page_size) {
+  return width >= 0 && stride >= width && width < (int64_t(1) << 31) / page_size;
 }
 
 }  // namespace
@@ -419,10 +443,117 @@ tern_status tern_selftest_wait(uint32_t polls, void* stream) {
 tern_status tern_check(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return TERN_ERR_CUDA;
-  unsigned int err_gemm = 0, err_gemv = 0;
+  unsigned int err_gemm = 0, err_gemv = 0, err_attn = 0;
   if (gemm_read_clear_error(&err_gemm) != cudaSuccess) return TERN_ERR_CUDA;
   if (gemv_read_clear_error(&err_gemv) != cudaSuccess) return TERN_ERR_CUDA;
-  return (err_gemm | err_gemv) ? TERN_ERR_TIMEOUT : TERN_OK;
+  if (attn_read_clear_error(&err_attn) != cudaSuccess) return TERN_ERR_CUDA;
+  return (err_gemm | err_gemv | err_attn) ? TERN_ERR_TIMEOUT : TERN_OK;
+}
+
+tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
+                         int64_t page_size, int32_t* table, int64_t table_stride,
+                         int64_t table_width, const int32_t* free_pages, int64_t n_free,
+                         const int32_t* free_head, int32_t* row_start, int64_t capacity,
+                         int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
+                         void* stream) {
+  if (B < 0 || capacity < 0 || n_free < 0) return TERN_ERR_INVALID_ARG;
+  if (!pow2(page_size) || page_size > 65536 || B > 16384 || capacity >= (int64_t(1) << 31) ||
+      n_free >= (int64_t(1) << 31) || !table_ok(table_stride, table_width, page_size))
+    return TERN_ERR_SHAPE;
+  if (row_start == nullptr || info == nullptr ||
+      (B > 0 && (ctx_len == nullptr || new_len == nullptr)) ||
+      (B > 0 && table_width > 0 && table == nullptr) || (n_free > 0 && free_pages == nullptr) ||
+      (capacity > 0 && (slots == nullptr || positions == nullptr || request == nullptr)))
+    return TERN_ERR_INVALID_ARG;
+  if (!aligned16(slots) || !aligned16(positions) || !aligned16(request)) return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_kv_plan(ctx_len, new_len, B, page_size, table, table_stride, table_width,
+                                  free_pages, n_free, free_head, row_start, capacity, slots,
+                                  positions, request, info, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_kv_write(const tern_kv_cache* cache, const void* k, const void* v,
+                          int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                          int64_t v_head_stride, const int64_t* slots, int64_t T, void* stream) {
+  if (T < 0) return TERN_ERR_INVALID_ARG;
+  const tern_status ok = cache_ok(cache);
+  if (ok != TERN_OK) return ok;
+  if (T >= (int64_t(1) << 31)) return TERN_ERR_SHAPE;
+  if (T == 0) return TERN_OK;
+  if (k == nullptr || v == nullptr || slots == nullptr) return TERN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !stride_ok(k_token_stride) || !stride_ok(k_head_stride) ||
+      !stride_ok(v_token_stride) || !stride_ok(v_head_stride))
+    return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_kv_write(*cache, k, v, k_token_stride, k_head_stride, v_token_stride,
+                                   v_head_stride, slots, T, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_kv_commit(const tern_kv_cache* caches, int64_t layers, const int32_t* table,
+                           int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                           const int32_t* path, int64_t path_width, const int32_t* path_len,
+                           int32_t* ctx_out, int64_t B, void* stream) {
+  if (B < 0 || layers < 1 || path_width < 0 || caches == nullptr) return TERN_ERR_INVALID_ARG;
+  for (int64_t l = 0; l < layers; ++l) {
+    const tern_status ok = cache_ok(caches + l);
+    if (ok != TERN_OK) return ok;
+    const tern_kv_cache &c = caches[l], &c0 = caches[0];
+    if (c.pages != c0.pages || c.page_size != c0.page_size || c.heads != c0.heads ||
+        c.dim != c0.dim || c.page_stride != c0.page_stride ||
+        c.token_stride != c0.token_stride || c.head_stride != c0.head_stride)
+      return TERN_ERR_SHAPE;
+  }
+  if (B > 65535 || layers > 65535 || path_width > 256 ||
+      !table_ok(table_stride, table_width, caches->page_size))
+    return TERN_ERR_SHAPE;
+  if (B == 0) return TERN_OK;
+  if (ctx_len == nullptr || path_len == nullptr || ctx_out == nullptr || ctx_out == ctx_len ||
+      (path_width > 0 && path == nullptr) || (table_width > 0 && table == nullptr))
+    return TERN_ERR_INVALID_ARG;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_kv_commit(caches, layers, table, table_stride, table_width, ctx_len, path,
+                                    path_width, path_len, ctx_out, B,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+size_t tern_tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
+  if (max_new < 1 || max_new > 256 || H < 1 || Hq < H || Hq % H != 0 ||
+      (D != 64 && D != 128 && D != 256))
+    return 0;
+  return tree_attention_workspace_bytes(max_new, Hq, H, D);
+}
+
+tern_status tern_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                const tern_kv_cache* cache, const int32_t* table,
+                                int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                                const int32_t* row_start, const uint64_t* mask,
+                                int64_t mask_words, int64_t B, int64_t T, int64_t Hq,
+                                int64_t max_new, float scale, void* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (B < 0 || T < 0 || mask_words < 0 || max_new < 0 || !(scale == scale) ||
+      scale - scale != 0.0f)
+    return TERN_ERR_INVALID_ARG;
+  const tern_status ok = cache_ok(cache);
+  if (ok != TERN_OK) return ok;
+  if (Hq < 1 || Hq % cache->heads != 0 || B > 65536 || max_new > 256 || mask_words > 4 ||
+      !table_ok(table_stride, table_width, cache->page_size) ||
+      T >= (int64_t(1) << 34) / (Hq * cache->dim))
+    return TERN_ERR_SHAPE;
+  if (B == 0 || T == 0 || max_new == 0) return TERN_OK;
+  if (q == nullptr || ctx_len == nullptr || row_start == nullptr || out == nullptr ||
+      (table_width > 0 && table == nullptr) || (mask != nullptr && mask_words == 0))
+    return TERN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !stride_ok(q_token_stride) || !stride_ok(q_head_stride))
+    return TERN_ERR_ALIGN;
+  if (ws == nullptr ||
+      ws_bytes < tree_attention_workspace_bytes(max_new, Hq, cache->heads, cache->dim))
+    return TERN_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  const TreeAttnCall call{q, q_token_stride, q_head_stride, *cache, table, table_stride,
+                          table_width, ctx_len, row_start, mask, mask_words, B, T, Hq, max_new,
+                          scale, out, lse, ws};
+  return from_cuda(launch_tree_attention(call, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
