@@ -137,8 +137,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:       # the handle itself: building a Stream object costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
@@ -282,8 +282,8 @@ def tern_gemv_decode_noalloc(packed, xh, xs, m, n, k, y, stream=None):
 
 
 def _desc(cache):
-    """Address of a KVCacheDesc (or of an array of them)."""
-    return cache if cache is None or isinstance(cache, int) else ctypes.addressof(cache)
+    """A KVCacheDesc's address; bytes of one or more in a row are passed as they are."""
+    return ctypes.addressof(cache) if isinstance(cache, ctypes.Structure) else cache
 
 
 def tern_kv_plan(ctx_len, new_len, b, page_size, table, table_stride, table_width, free_pages,

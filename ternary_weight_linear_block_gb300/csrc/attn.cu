@@ -7,11 +7,14 @@
 // rescaled where m grows.  The probabilities are rounded to the cache's type
 // for the second product, as its values are; l sums them unrounded.
 //
-// attn_rows_kernel: 16 rows an item, tiles of 64 keys.  A producer warp
+// attn_rows_kernel: up to 32 rows an item, tiles of 64 keys.  A producer warp
 // copies each page's part of a tile with TMA into a ring; four warps take 16
-// keys of a tile each and keep their own (m, l, out) of all 16 rows, so that
-// no warp waits for another inside an item; they join at its end.  The
-// products are mma.sync m16n8k16.
+// keys of a tile each and keep their own (m, l, out) of all the item's rows,
+// so that no warp waits for another inside an item; they join at its end.
+// The products are mma.sync m16n8k16 with the keys (and the values' columns)
+// on the 16 side and 8 rows on the other: one to eight rows cost one
+// instruction of a tile, not two of which half is padding, and each
+// ldmatrix of keys or values serves all the rows.
 #include <algorithm>
 
 #include "attn_dev.cuh"
@@ -66,20 +69,36 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Transposes an 8x8 matrix of 16-bit values held one row in 4 lanes.
+__device__ __forceinline__ uint32_t movm(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // ------------------------------------------------------------------ rows kernel
 
-constexpr int RT = 16;             // rows of an item
 constexpr int TK = 64;             // keys of a tile
 constexpr int NW = 4;              // consumer warps
 constexpr int THREADS = (NW + 1) * 32;
 
-template <int D>
+// NT: eights of rows in an item.  The accumulators (D / 4 * NT registers a
+// thread) and the query fragments (D / 8 * NT) decide how many CTAs an SM
+// holds, and so the ring's size.  Joining the warps takes two buffers of the
+// item's rows; `COLS` columns of them at a time where two CTAs share an SM.
+template <int D, int NT>
 struct Rows {
+  static constexpr int RT = 8 * NT;
   static constexpr int STAGE = 2 * TK * D * 2;            // keys and values of a tile
-  static constexpr int STAGES = D == 64 ? 6 : 3;
-  static constexpr int CTAS = D == 256 ? 1 : 2;           // per SM
-  static constexpr int MERGE = RT * D * 4;
-  static constexpr size_t SMEM = size_t(STAGES) * STAGE + MERGE + 1024 + 1024;
+  static constexpr int CTAS = D * NT <= 256 && D < 256 ? 2 : 1;   // per SM
+  static constexpr int COLS = CTAS == 2 && D * NT == 256 ? D / 2 : D;
+  static constexpr int LD = COLS + 4;                     // no two lanes of a store share a bank
+  static constexpr int MERGE = 2 * RT * LD * 4;
+  static constexpr int ROOM = (CTAS == 2 ? 115200 : 232448) - MERGE - 1024 - 1280;
+  static constexpr int FIT = ROOM / STAGE;
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
+  static constexpr size_t SMEM = size_t(STAGES) * STAGE + MERGE + 1024;
+  static_assert(STAGES >= 2, "ring");
 };
 
 // One tile's copies, spread over the producer warp: box i of `boxes` covers
@@ -103,11 +122,12 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* tk, const CUtensorM
   }
 }
 
-template <bool BF16, int D>
-__global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
+template <bool BF16, int D, int NT>
+__global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
     attn_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
-  using C = Rows<D>;
+  using C = Rows<D, NT>;
+  constexpr int RT = C::RT;
   constexpr int HALVES = D / 64;
   constexpr int HB = TK * 128;
   constexpr int KS = D / 16;
@@ -116,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
                                              ~static_cast<uintptr_t>(1023));
   float* merge = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
   __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
-  __shared__ int64_t scratch[THREADS / 32 + 3];
+  __shared__ PieceScratch<THREADS> scratch;
   __shared__ float2 s_ml[NW][RT];
   __shared__ unsigned int s_bad[8];     // new tokens with a non-finite value, by index
   __shared__ int s_any_bad;
@@ -204,44 +224,61 @@ __global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
   // ---------------- consumers: warp w has keys 16 w .. 16 w + 15 of each tile
   int st = 0;
   uint32_t phase = 0;
-  const int row_a = lane >> 2;           // this lane's rows: row_a, row_a + 8
   const uint32_t ring_u = ptx::smem_u32(ring);
-  // ldmatrix rows: keys by key (matrices: keys 0-7 d 0-7, keys 0-7 d 8-15, keys 8-15 ...)
-  const int k_row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
-  const int k_chunk = (lane >> 3) & 1;
-  // values transposed (matrices: keys 0-7 d 0-7, keys 8-15 d 0-7, keys 0-7 d 8-15 ...)
-  const int v_row = warp * 16 + (lane & 15);
-  const int v_chunk = lane >> 4;
+  const int row_b = lane >> 2;           // query row (of 8) whose fragment this lane holds
+  const int row_c = (lane & 3) * 2;      // score rows of this lane: row_c, row_c + 1
+  // ldmatrix: keys (matrices: keys 0-7 d 0-7, keys 8-15 d 0-7, keys 0-7 d 8-15, ...)
+  const int k_row = warp * 16 + (lane & 15);
+  const int k_chunk = lane >> 4;
+  // values transposed (matrices: keys 0-7 d 0-7, keys 0-7 d 8-15, keys 8-15 d 0-7, ...)
+  const int v_row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+  const int v_chunk = (lane >> 3) & 1;
   bool ok = true;
   while (walk.next(s)) {
     const int rows_all = s.r.n * a.group;
     const int r0 = s.rt * RT;
     const int rows = min(RT, rows_all - r0);
     // query fragments, rows past the tile's last are zero
-    uint32_t qf[KS][4];
-    const uint64_t* mw[2] = {nullptr, nullptr};
-    int tok[2];
+    uint32_t qf[KS][NT][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = r0 + row_a + 8 * e;
+    for (int n = 0; n < NT; ++n) {
+      const int r = r0 + n * 8 + row_b;
       const bool in = r < rows_all;
-      tok[e] = in ? r / a.group : 0;
-      const int64_t t = s.r.row0 + tok[e];
-      if (a.mask != nullptr) mw[e] = a.mask + t * a.mask_words;
-      const uint16_t* q = a.q + t * a.q_token +
+      const uint16_t* q = a.q + (s.r.row0 + int64_t(in ? r / a.group : 0)) * a.q_token +
                           int64_t(s.h * a.group + (in ? r % a.group : 0)) * a.q_head + (lane & 3) * 2;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        qf[k][e] = in ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
-        qf[k][e + 2] = in ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
+        qf[k][n][0] = in ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
+        qf[k][n][1] = in ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
       }
     }
-    float o[D / 8][4];
+    float o[KS][NT][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
 
     for (int t = s.t0; t < s.t1; ++t) {
+      const int k0 = t * TK + warp * 16;       // this warp's first key
+      const bool edge = k0 + 16 > s.r.ctx;     // new tokens, or past the last
+      uint32_t vis[NT][2];
+      if (edge) {                              // read while the tile is on its way
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = r0 + n * 8 + row_c + e;
+            const int tok = r < rows_all ? r / a.group : 0;
+            vis[n][e] = sees_bits<16>(a, a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words
+                                                    : nullptr, tok, k0, s.r);
+          }
+      }
       // a warp whose wait gave up reads no more tiles, but still meets the
       // others at the barriers below
       if (ok) {
@@ -251,13 +288,12 @@ __global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
       if (!ok) break;
       const uint32_t kbase = ring_u + st * C::STAGE;
       const uint32_t vbase = kbase + HALVES * HB;
-      const int k0 = t * TK + warp * 16;       // this warp's first key
-      const bool edge = k0 + 16 > s.r.ctx;     // new tokens, or past the last
       if (edge) {
         // values past the last token count as zero, and so does a non-finite
         // value of a new token here: it is added at the item's end, to the
         // rows that see that token
         uint8_t* vw = ring + st * C::STAGE + HALVES * HB;
+#pragma unroll 4
         for (int i = lane; i < 16 * (D / 8); i += 32) {
           const int kr = warp * 16 + i / (D / 8), c = i % (D / 8);
           uint4* at = reinterpret_cast<uint4*>(vw + (c >> 3) * HB + kr * 128 +
@@ -287,71 +323,65 @@ __global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
         ptx::fence_proxy_async_smem();   // before the ring's next copy into this place
         __syncwarp();
       }
-      float c[2][4];
+      float c[NT][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+      for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        uint32_t b[4];
+        uint32_t x[4];
         const int chunk = (k & 3) * 2 + k_chunk;
-        ldsm_x4(kbase + (k >> 2) * HB + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), b);
-        mma16816<BF16>(c[0], qf[k], b[0], b[1]);
-        mma16816<BF16>(c[1], qf[k], b[2], b[3]);
+        ldsm_x4(kbase + (k >> 2) * HB + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), x);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<BF16>(c[n], x, qf[k][n][0], qf[k][n][1]);
       }
+      // c[n]: keys lane / 4 and + 8, rows row_c and + 1
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[i][e] *= a.scale_log2;
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = k0 + i * 8 + (lane & 3) * 2 + (e & 1);
-            const bool seen = j < s.r.ctx || (j < s.r.len &&
-                              sees(a, mw[e >> 1], tok[e >> 1], j - s.r.ctx, s.r.n));
-            if (!seen) c[i][e] = -INFINITY;
-          }
-      }
-      float ms[2], al[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(c[0][2 * e], c[0][2 * e + 1]), fmaxf(c[1][2 * e], c[1][2 * e + 1]));
-        x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-        const float mn = fmaxf(m[e], x);
-        ms[e] = mn == -INFINITY ? 0.f : mn;
-        al[e] = ex2(m[e] - ms[e]);
-        m[e] = mn;
-      }
-      uint32_t p[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[i][e] = ex2(c[i][e] - ms[e >> 1]);
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        l[e] = l[e] * al[e] + ((c[0][2 * e] + c[0][2 * e + 1]) + (c[1][2 * e] + c[1][2 * e + 1]));
-      p[0] = pack2<BF16>(c[0][0], c[0][1]);
-      p[1] = pack2<BF16>(c[0][2], c[0][3]);
-      p[2] = pack2<BF16>(c[1][0], c[1][1]);
-      p[3] = pack2<BF16>(c[1][2], c[1][3]);
-      if (__any_sync(~0u, al[0] != 1.f || al[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= al[0];
-          o[i][1] *= al[0];
-          o[i][2] *= al[1];
-          o[i][3] *= al[1];
+        for (int e = 0; e < 4; ++e) {
+          c[n][e] *= a.scale_log2;
+          if (edge && !((vis[n][e & 1] >> (row_b + (e >> 1) * 8)) & 1)) c[n][e] = -INFINITY;
         }
+      float al[NT][2];
+      bool moved = false;
+      uint32_t p[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float ms[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(c[n][e], c[n][e + 2]);
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+          const float mn = fmaxf(m[n][e], x);
+          ms[e] = mn == -INFINITY ? 0.f : mn;
+          al[n][e] = ex2(m[n][e] - ms[e]);
+          moved |= mn != m[n][e];
+          m[n][e] = mn;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[n][e] = ex2(c[n][e] - ms[e & 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[n][e] = l[n][e] * al[n][e] + (c[n][e] + c[n][e + 2]);
+        p[n][0] = movm(pack2<BF16>(c[n][0], c[n][1]));
+        p[n][1] = movm(pack2<BF16>(c[n][2], c[n][3]));
+      }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][n][e] *= al[n][e & 1];
       }
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
-        uint32_t b[4];
+        uint32_t x[4];
         const int chunk = (i & 3) * 2 + v_chunk;
-        ldsm_x4_t(vbase + (i >> 2) * HB + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), b);
-        mma16816<BF16>(o[2 * i], p, b[0], b[1]);
-        mma16816<BF16>(o[2 * i + 1], p, b[2], b[3]);
+        ldsm_x4_t(vbase + (i >> 2) * HB + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), x);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma16816<BF16>(o[i][n], x, p[n][0], p[n][1]);
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&empty[st]);
@@ -361,79 +391,93 @@ __global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
       }
     }
 
-    // ---- join the four warps: factors from every warp's (m, l), then the
-    // outputs added in the order of the warps
+    // ---- join the four warps: factors from every warp's (m, l); warps 0, 1
+    // store, warps 2, 3 add to what they stored, and the two sums are added
+    // as they are read
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[e] += __shfl_xor_sync(~0u, l[e], 1);
-      l[e] += __shfl_xor_sync(~0u, l[e], 2);
-      if ((lane & 3) == 0) s_ml[warp][row_a + 8 * e] = make_float2(m[e], l[e]);
-    }
-    ptx::named_sync(1, NW * 32);
-    float f[2];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) mm = fmaxf(mm, s_ml[w][row_a + 8 * e].x);
-      f[e] = mm == -INFINITY ? 0.f : ex2(m[e] - mm);
-    }
-    for (int w = 0; w < NW; ++w) {
-      if (w == warp) {
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float2* at = reinterpret_cast<float2*>(merge + (row_a + 8 * e) * D + i * 8 + (lane & 3) * 2);
-            float2 x = make_float2(o[i][2 * e] * f[e], o[i][2 * e + 1] * f[e]);
-            if (w > 0) {
-              x.x += at->x;
-              x.y += at->y;
-            }
-            *at = x;
-          }
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(~0u, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(~0u, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(~0u, l[n][e], 16);
+        if (lane < 4) s_ml[warp][n * 8 + row_c + e] = make_float2(m[n][e], l[n][e]);
       }
-      ptx::named_sync(1, NW * 32);
-    }
-    // ---- write: thread -> 4 consecutive values of a row
+    ptx::named_sync(1, NW * 32);
+    float f[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, s_ml[w][n * 8 + row_c + e].x);
+        f[n][e] = mm == -INFINITY ? 0.f : ex2(m[n][e] - mm);
+      }
     const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
     const int64_t slot = 2 * int64_t(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
     const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
-    for (int i = tid; i < rows * (D / 4); i += NW * 32) {
-      const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-      float4 x = *reinterpret_cast<const float4*>(merge + r * D + d);
-      const int token = (r0 + r) / a.group, head = s.h * a.group + (r0 + r) % a.group;
-      if (any_bad) {
-        const uint64_t* mr = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(token)) * a.mask_words : nullptr;
-        for (int j = 0; j < min(s.r.n, 256); ++j) {
-          if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mr, token, j, s.r.n)) continue;
-          const int64_t pos = int64_t(s.r.ctx) + j;
-          const int pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
-          if (pg < 0 || pg >= a.pages) continue;
-          const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
-                              (pos & ((1 << a.page_shift) - 1)) * a.token_stride +
-                              int64_t(s.h) * a.head_stride + d;
-          float* xf = reinterpret_cast<float*>(&x);
-          for (int e = 0; e < 4; ++e)
-            if (nonfinite2<BF16>(v[e]) & 1) xf[e] += widen<BF16>(v[e]);
+    float* mine = merge + (warp & 1) * (RT * C::LD);
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += C::COLS) {
+      if (c0 > 0) ptx::named_sync(1, NW * 32);
+#pragma unroll
+      for (int round = 0; round < 2; ++round) {
+        if ((warp >> 1) == round) {
+#pragma unroll
+          for (int i = 0; i < C::COLS / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float* at = mine + (n * 8 + row_c + (e & 1)) * C::LD + i * 16 + row_b + (e >> 1) * 8;
+                float x = o[c0 / 16 + i][n][e] * f[n][e & 1];
+                if (round > 0) x += *at;
+                *at = x;
+              }
         }
+        ptx::named_sync(1, NW * 32);
       }
-      float mm = -INFINITY, ll = 0.f;
+      // ---- write: thread -> 4 consecutive values of a row
+      for (int i = tid; i < rows * (C::COLS / 4); i += NW * 32) {
+        const int r = i / (C::COLS / 4), dc = (i % (C::COLS / 4)) * 4, d = c0 + dc;
+        float4 x = *reinterpret_cast<const float4*>(merge + r * C::LD + dc);
+        const float4 y = *reinterpret_cast<const float4*>(merge + (RT + r) * C::LD + dc);
+        x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        const int token = (r0 + r) / a.group, head = s.h * a.group + (r0 + r) % a.group;
+        if (any_bad) {
+          const uint64_t* mr = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(token)) * a.mask_words
+                                                 : nullptr;
+          for (int j = 0; j < min(s.r.n, 256); ++j) {
+            if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mr, token, j, s.r.n)) continue;
+            const int64_t pos = int64_t(s.r.ctx) + j;
+            const int pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
+            if (pg < 0 || pg >= a.pages) continue;
+            const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
+                                (pos & ((1 << a.page_shift) - 1)) * a.token_stride +
+                                int64_t(s.h) * a.head_stride + d;
+            float* xf = reinterpret_cast<float*>(&x);
+            for (int e = 0; e < 4; ++e)
+              if (nonfinite2<BF16>(v[e]) & 1) xf[e] += widen<BF16>(v[e]);
+          }
+        }
+        float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) mm = fmaxf(mm, s_ml[w][r].x);
+        for (int w = 0; w < NW; ++w) mm = fmaxf(mm, s_ml[w][r].x);
 #pragma unroll
-      for (int w = 0; w < NW; ++w)
-        ll += s_ml[w][r].y * (mm == -INFINITY ? 0.f : ex2(s_ml[w][r].x - mm));
-      if (whole) {
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        const int64_t at = (int64_t(s.r.row0) + token) * a.Hq + head;
-        *reinterpret_cast<uint2*>(a.out + at * D + d) =
-            make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
-        if (d == 0 && a.lse != nullptr)
-          a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d) = x;
-        if (d == 0) a.part_ml[slot * RT + r] = make_float2(mm, ll);
+        for (int w = 0; w < NW; ++w)
+          ll += s_ml[w][r].y * (mm == -INFINITY ? 0.f : ex2(s_ml[w][r].x - mm));
+        if (whole) {
+          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          const int64_t at = (int64_t(s.r.row0) + token) * a.Hq + head;
+          *reinterpret_cast<uint2*>(a.out + at * D + d) =
+              make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
+          if (d == 0 && a.lse != nullptr)
+            a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d) = x;
+          if (d == 0) a.part_ml[slot * RT + r] = make_float2(mm, ll);
+        }
       }
     }
     if (!whole && s.t0 == 0 && tid == 0) {
@@ -451,6 +495,523 @@ __global__ void __launch_bounds__(THREADS, Rows<D>::CTAS)
       ptx::named_sync(1, NW * 32);
     }
   }
+}
+
+// ------------------------------------------------------------------ tile kernel
+//
+// Up to 128 or 256 rows an item on tcgen05: S = Q K^T with 128 rows on the M
+// side, the accumulator in tensor memory; a thread reads one row of S, writes
+// the row's probabilities over it as 16-bit values, and out += P V takes P
+// from tensor memory and V from the ring as its pages hold it (columns of V
+// along the MMA's N side: the MN-major operand).  Keys and values arrive in a
+// ring of 32 KB slots in the order K0 K1 V0 K2 V1 K3 ...
+//
+// Two streams, each with its S, its out accumulator and a warpgroup, so that
+// one stream's softmax runs beside the other's MMAs:
+//   KEYS  rows <= 128:  the streams take the even and the odd key tiles
+//   ROWS  rows <= 256:  each has 128 rows; a key tile serves both
+//   COLS  head size 256: each has 128 columns of V (an accumulator of 256
+//         columns for each would not fit); both compute S
+// The maximum that a row's exponents refer to only moves when it grows by
+// more than 2^8: until then nothing is rescaled (probabilities up to 256 are
+// as exact in the 16-bit types, and sums are in 32 bits), so the pass over
+// the accumulator is rare.  Rows past the item's last cost their MMAs alone:
+// whole warps of them skip the softmax.
+
+constexpr int TILE_THREADS = 384;   // producer, MMA, TMEM, spare; two warpgroups
+enum Mode { KEYS, ROWS, COLS };
+
+template <int D, int MODE>
+struct Tile {
+  static constexpr int TKT = D == 256 ? 64 : 128;        // keys of a tile
+  static constexpr int RT = MODE == ROWS ? 256 : 128;
+  static constexpr int SLOT = TKT * D * 2;
+  static constexpr int QB = 128 * D * 2;                 // one Q tile
+  static constexpr int QBYTES = MODE == ROWS ? 2 * QB : QB;
+  static constexpr int FIT = (232448 - 1024 - 6144 - QBYTES) / SLOT;
+  static constexpr int SLOTS = FIT < 8 ? FIT : 8;
+  static constexpr size_t SMEM = size_t(SLOTS) * SLOT + QBYTES + 1024;
+  static constexpr int DV = MODE == COLS ? 128 : D;      // columns of an accumulator
+  static constexpr uint32_t S_COL = 0, O_COL = 256;      // stream x: + 128 x
+  static_assert(SLOTS >= 4, "ring");
+};
+
+// Descriptor of V [keys][64 columns] as the MN-major B operand: 8 keys of 128
+// bytes make an atom of the 128-byte swizzle, atoms 1024 bytes apart along
+// the keys (stride byte offset), the next 64 columns `lbo` bytes on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+template <bool BF16>
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn) {
+  return (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+template <bool BF16, int D, int MODE>
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  using C = Tile<D, MODE>;
+  constexpr int TKT = C::TKT, RT = C::RT, SLOTS = C::SLOTS, DV = C::DV;
+  constexpr int HALVES = D / 64;
+  constexpr int HB = TKT * 128;          // 64 columns of a key or value tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sq = ring + SLOTS * C::SLOT;
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, o_full, done, s_full[2], p_full[2];
+  __shared__ PieceScratch<TILE_THREADS> scratch;
+  __shared__ float2 s_ml[2][128];
+  __shared__ unsigned int s_bad[8];
+  __shared__ int s_any_bad;
+  __shared__ int s_abort;
+  __shared__ uint32_t s_tmem;
+  volatile int* abort_flag = &s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < SLOTS; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    ptx::mbar_init(&q_full, 8);
+    ptx::mbar_init(&o_full, 1);
+    ptx::mbar_init(&done, 1);
+    for (int x = 0; x < 2; ++x) {
+      ptx::mbar_init(&s_full[x], 1);
+      ptx::mbar_init(&p_full[x], 4);
+    }
+    s_abort = 0;
+    s_any_bad = 0;
+    for (int i = 0; i < 8; ++i) s_bad[i] = 0;
+    ptx::mbar_fence_init();
+    ptx::prefetch_tmap(&tm_k);
+    ptx::prefetch_tmap(&tm_v);
+  }
+  if (warp == 2) {
+    ptx::tmem_alloc(&s_tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  pdl_wait();
+  pdl_launch_dependents();
+  const Piece piece = find_piece<TKT, RT, TILE_THREADS>(a, scratch);   // synchronises the CTA
+  ptx::tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  if (tid == 0) a.join[blockIdx.x].follow = 0;
+  Walk<TKT, RT> walk(a, piece);
+  Seg s;
+
+  if (warp == 0) {
+    // ---------------- producer
+    int st = 0;
+    uint32_t phase = 0;
+    long issued = 0;
+    bool ok = true;
+    const int box_shift = min(a.page_shift, TKT == 128 ? 7 : 6);
+    const int per_tile = TKT >> box_shift;
+    const auto load = [&](const CUtensorMap* map, int t, int page) {
+      const int k0 = t * TKT;
+      const int keys = min(TKT, s.r.len - k0);
+      const int boxes = keys > 0 ? (keys + (1 << box_shift) - 1) >> box_shift : 0;
+      ok = ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT);
+      if (!ok) {
+        if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
+        return;
+      }
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(boxes << box_shift) * D * 2u);
+      __syncwarp();
+      const int box = lane / HALVES, half = lane % HALVES;
+      const int pg = __shfl_sync(~0u, page, box & 31);
+      if (box < boxes)
+        tma_load_4d(ring + st * C::SLOT + half * HB + (box << box_shift) * 128, map, &full[st],
+                    half * 64, k0 & ((1 << a.page_shift) - 1), s.h, pg);
+      ++issued;
+      if (++st == SLOTS) {
+        st = 0;
+        phase ^= 1u;
+      }
+    };
+    while (ok && walk.next(s)) {
+      const int32_t* row = a.table + int64_t(s.b) * a.table_stride;
+      const auto page_at = [&](int t) {
+        const int64_t pos = int64_t(t) * TKT + (int64_t(lane) << box_shift);
+        int pg = -1;
+        if (lane < per_tile && pos < s.r.len) pg = row[pos >> a.page_shift];
+        return pg < 0 || pg >= a.pages ? a.pages : pg;
+      };
+      int cur = page_at(s.t0), next = s.t0 + 1 < s.t1 ? page_at(s.t0 + 1) : 0;
+      load(&tm_k, s.t0, cur);
+      for (int t = s.t0; t < s.t1 && ok; ++t) {
+        const int after = t + 2 < s.t1 ? page_at(t + 2) : 0;
+        if (t + 1 < s.t1) load(&tm_k, t + 1, next);
+        if (ok) load(&tm_v, t, cur);
+        cur = next;
+        next = after;
+      }
+    }
+    if (!ok) {
+      const long back = issued < SLOTS ? issued : SLOTS;
+      for (long i = 0; i < back; ++i) {
+        if (--st < 0) {
+          st = SLOTS - 1;
+          phase ^= 1u;
+        }
+        if (!ptx::mbar_wait_bounded(&full[st], phase, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer (one thread)
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t seq0 = 0, q_phase = 0, p_phase[2] = {0, 0};
+      const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!ok) return;
+        ok = ptx::mbar_wait(bar, parity, abort_flag, WAIT_LIMIT);
+        if (!ok && !*abort_flag) fail(abort_flag, ERR_CONSUMER);
+        ptx::tc_fence_after();
+      };
+      const uint32_t ring_u = ptx::smem_u32(ring), sq_u = ptx::smem_u32(sq);
+      while (ok && walk.next(s)) {
+        const int cnt = s.t1 - s.t0;
+        // place of K(i) and V(i) in the ring's order
+        const auto k_seq = [&](int i) { return seq0 + (i == 0 ? 0u : 2u * i - 1u); };
+        const auto v_seq = [&](int i) { return seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u); };
+        const auto mma_s = [&](int i, int x, bool last) {
+          const uint32_t n = k_seq(i), sl = n % SLOTS;
+          wait(&full[sl], (n / SLOTS) & 1u);
+          if (!ok) return;
+          const uint32_t qb = sq_u + (MODE == ROWS ? x * C::QB : 0);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t da = ptx::sw128_kmajor_desc(qb + (k >> 2) * (128 * 128)) + 2u * (k & 3);
+            const uint64_t db = ptx::sw128_kmajor_desc(ring_u + sl * C::SLOT + (k >> 2) * HB) + 2u * (k & 3);
+            ptx::mma_f16_ss(tmem + C::S_COL + 128 * x, da, db, idesc<BF16>(TKT, false), k > 0);
+          }
+          if (last) ptx::mma_commit(&empty[sl]);
+          ptx::mma_commit(&s_full[x]);
+        };
+        const auto mma_o = [&](int i, int x, bool first, bool last) {
+          wait(&p_full[x], p_phase[x]);
+          p_phase[x] ^= 1u;
+          const uint32_t n = v_seq(i), sl = n % SLOTS;
+          wait(&full[sl], (n / SLOTS) & 1u);
+          if (!ok) return;
+          const uint32_t vb = ring_u + sl * C::SLOT + (MODE == COLS ? x * 2 * HB : 0);
+#pragma unroll
+          for (int k = 0; k < TKT / 16; ++k)
+            ptx::mma_f16_ts(tmem + C::O_COL + 128 * x, tmem + C::S_COL + 128 * x + k * 8,
+                            sw128_mn_desc(vb + k * 2048, HB), idesc<BF16>(DV, true),
+                            (!first || k > 0) ? 1u : 0u);
+          if (last) ptx::mma_commit(&empty[sl]);
+        };
+        wait(&q_full, q_phase);
+        q_phase ^= 1u;
+        if constexpr (MODE == KEYS) {
+          mma_s(0, 0, true);
+          if (cnt > 1) mma_s(1, 1, true);
+          for (int i = 0; i < cnt && ok; ++i) {
+            mma_o(i, i & 1, i < 2, true);
+            if (i + 2 < cnt) mma_s(i + 2, i & 1, true);
+          }
+        } else {
+          mma_s(0, 0, false);
+          mma_s(0, 1, true);
+          for (int i = 0; i < cnt && ok; ++i)
+            for (int x = 0; x < 2; ++x) {
+              mma_o(i, x, i == 0, x == 1);
+              if (i + 1 < cnt) mma_s(i + 1, x, x == 1);
+            }
+        }
+        if (ok) ptx::mma_commit(&o_full);
+        seq0 += 2u * cnt;
+      }
+      ptx::mma_commit(&done);
+      if (!ptx::mbar_wait_bounded(&done, 0, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------- softmax and output: warpgroup x has stream x, a thread
+    // one row of it
+    const int x = (warp - 4) >> 2;
+    const int lrow = (warp & 3) * 32 + lane;           // row of the stream's tile, its lane
+    const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + C::S_COL + 128 * x + lane_addr;
+    const uint32_t o_addr = tmem + C::O_COL + 128 * x + lane_addr;
+    const int wid = tid - 128;                         // 0 .. 255
+    bool ok = true;
+    uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!ok) return;
+      ok = ptx::mbar_wait_warp(bar, parity, abort_flag, WAIT_LIMIT);
+      if (!ok && lane == 0 && !*abort_flag) fail(abort_flag, ERR_CONSUMER);
+      ptx::tc_fence_after();
+    };
+    while (walk.next(s)) {
+      const int rows_all = s.r.n * a.group;
+      const int r0 = s.rt * RT;
+      const int rows = min(RT, rows_all - r0);
+      const int cnt = s.t1 - s.t0;
+      // the item's query rows, swizzled as TMA would; rows past the last are zero
+      constexpr int QROWS = MODE == ROWS ? 256 : 128;
+#pragma unroll 4
+      for (int i = wid; i < QROWS * (D / 8); i += 256) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int g = r0 + r;
+          v = *reinterpret_cast<const uint4*>(
+              a.q + (s.r.row0 + int64_t(g / a.group)) * a.q_token +
+              int64_t(s.h * a.group + g % a.group) * a.q_head + c * 8);
+        }
+        *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QB + (c >> 3) * (128 * 128) + (r & 127) * 128 +
+                                  (((c & 7) ^ (r & 7)) << 4)) = v;
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&q_full);
+
+      const int my = (MODE == ROWS ? 128 * x : 0) + lrow;      // row of the item
+      const bool active = (MODE == ROWS ? 128 * x : 0) + (warp & 3) * 32 < rows;
+      const int tok = my < rows ? (r0 + my) / a.group : 0;
+      const uint64_t* mw = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words : nullptr;
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int i = MODE == KEYS ? x : 0; i < cnt; i += MODE == KEYS ? 2 : 1) {
+        const int k0 = (s.t0 + i) * TKT;
+        const bool edge = k0 + TKT > s.r.ctx;
+        uint32_t vis[TKT / 32];
+        if (edge && active) {
+#pragma unroll
+          for (int c = 0; c < TKT / 32; ++c) vis[c] = sees_bits<32>(a, mw, tok, k0 + 32 * c, s.r);
+        }
+        wait(&s_full[x], s_phase);
+        s_phase ^= 1u;
+        if (!ok) break;
+        if (active) {
+          uint32_t v[TKT / 32][32];
+#pragma unroll
+          for (int c = 0; c < TKT / 32; ++c) ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, v[c]);
+          ptx::tmem_ld_wait();
+          float mt = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < TKT / 32; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float t = __uint_as_float(v[c][e]) * a.scale_log2;
+              if (edge && !((vis[c] >> e) & 1)) t = -INFINITY;
+              v[c][e] = __float_as_uint(t);
+              mt = fmaxf(mt, t);
+            }
+          float f = 1.f;
+          if (mt > m + 8.f || (m == -INFINITY && mt != m)) {
+            f = ex2(m - mt);
+            m = mt;
+          }
+          if (any && __any_sync(~0u, f != 1.f)) {
+#pragma unroll
+            for (int c = 0; c < DV / 32; ++c) {
+              uint32_t o[32];
+              ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  w[e] = __float_as_uint(__uint_as_float(o[16 * h + e]) * f);
+                tmem_st_x16(o_addr + 32 * c + 16 * h, w);
+              }
+            }
+          }
+          any = true;
+          const float ms = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < TKT / 32; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float p0 = ex2(__uint_as_float(v[c][2 * e]) - ms);
+              const float p1 = ex2(__uint_as_float(v[c][2 * e + 1]) - ms);
+              sum[e & 3] += p0 + p1;
+              w[e] = pack2<BF16>(p0, p1);
+            }
+            tmem_st_x16(s_addr + 16 * c, w);
+          }
+          l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          ptx::tmem_st_wait();
+        }
+        if (edge && (MODE == KEYS || x == 0)) {
+          // values past the last token count as zero, and so does a non-finite
+          // value of a new token here (added at the item's end)
+          const uint32_t n = seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u);
+          wait(&full[n % SLOTS], (n / SLOTS) & 1u);
+          if (!ok) break;
+          uint8_t* vt = ring + (n % SLOTS) * C::SLOT;
+          for (int u = lrow; u < TKT * (D / 8); u += 128) {
+            const int kr = u / (D / 8), c = u % (D / 8);
+            const int j = k0 + kr;
+            if (j < s.r.ctx) continue;
+            uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * HB + kr * 128 + (((c & 7) ^ (kr & 7)) << 4));
+            if (j >= s.r.len) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint4 y = *at;
+            uint32_t bad = 0;
+            uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t b = nonfinite2<BF16>(yw[e]);
+              if (b & 1) yw[e] &= 0xFFFF0000u;
+              if (b & 2) yw[e] &= 0x0000FFFFu;
+              bad |= b;
+            }
+            if (bad) {
+              *at = y;
+              const int jj = j - s.r.ctx;
+              if (jj < 256) atomicOr(&s_bad[jj >> 5], 1u << (jj & 31));
+              s_any_bad = 1;
+            }
+          }
+          ptx::fence_proxy_async_smem();   // before the MMA reads it
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&p_full[x]);
+      }
+      // ---- the item's part is complete
+      wait(&o_full, o_phase);
+      o_phase ^= 1u;
+      seq0 += 2u * cnt;
+      if constexpr (MODE == KEYS) s_ml[x][lrow] = make_float2(m, l);
+      ptx::named_sync(1, 256);
+      const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
+      const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
+      const int64_t slot = 2 * int64_t(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
+      if (ok && active) {
+        float f0 = 1.f, f1 = 0.f;
+        if constexpr (MODE == KEYS) {
+          const float2 y = s_ml[x ^ 1][lrow];
+          const float mm = fmaxf(m, y.x);
+          f0 = mm == -INFINITY ? 0.f : ex2(m - mm);
+          f1 = mm == -INFINITY ? 0.f : ex2(y.x - mm);
+          l = l * f0 + y.y * f1;
+          m = mm;
+          if (x == 1) {        // f0 is stream 0's
+            const float z = f0;
+            f0 = f1;
+            f1 = z;
+          }
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t at = (int64_t(s.r.row0) + tok) * a.Hq + s.h * a.group + (r0 + my) % a.group;
+        // KEYS: this warpgroup's half of the columns from both accumulators;
+        // ROWS: all columns of its rows; COLS: its columns
+        constexpr int NC = MODE == KEYS ? D / 2 : DV;
+        const int col0 = MODE == ROWS ? 0 : x * NC;
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) {
+          float o[32];
+          uint32_t u[32];
+          if constexpr (MODE == KEYS) {
+            const uint32_t base = tmem + C::O_COL + lane_addr + col0 + 32 * c;
+            ptx::tmem_ld_32x32b_x32(base, u);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f0;
+            if (cnt > 1) {
+              ptx::tmem_ld_32x32b_x32(base + 128, u);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(u[e]) * f1;
+            }
+          } else {
+            ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, u);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+          }
+          if (my < rows) {
+            const int d = col0 + 32 * c;
+            if (any_bad) {
+              for (int j = 0; j < min(s.r.n, 256); ++j) {
+                if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mw, tok, j, s.r.n)) continue;
+                const int64_t pos = int64_t(s.r.ctx) + j;
+                const int pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
+                if (pg < 0 || pg >= a.pages) continue;
+                const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
+                                    (pos & ((1 << a.page_shift) - 1)) * a.token_stride +
+                                    int64_t(s.h) * a.head_stride + d;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (nonfinite2<BF16>(v[e]) & 1) o[e] += widen<BF16>(v[e]);
+              }
+            }
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint4 w;
+                w.x = pack2<BF16>(o[8 * e] * inv, o[8 * e + 1] * inv);
+                w.y = pack2<BF16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+                w.z = pack2<BF16>(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+                w.w = pack2<BF16>(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+                *reinterpret_cast<uint4*>(a.out + at * D + d + 8 * e) = w;
+              }
+            } else {
+              float* po = a.part_o + (slot * RT + my) * D + d;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<float4*>(po + 4 * e) =
+                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          }
+        }
+        if (my < rows && (MODE == ROWS || x == 0)) {
+          if (!whole)
+            a.part_ml[slot * RT + my] = make_float2(m, l);
+          else if (a.lse != nullptr)
+            a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+      }
+      if (!whole && s.t0 == 0 && wid == 0) {
+        Join* j = a.join + blockIdx.x;
+        j->row0 = s.r.row0;
+        j->r0 = r0;
+        j->rows = rows;
+        j->head = s.h;
+        j->follow = cta_of(piece, s.end - 1) - static_cast<int>(blockIdx.x);
+      }
+      ptx::tc_fence_before();
+      ptx::named_sync(1, 256);   // accumulators, Q, s_ml and s_bad are free again
+      if (any_bad) {
+        if (wid < 8) s_bad[wid] = 0;
+        if (wid == 0) s_any_bad = 0;
+        ptx::named_sync(1, 256);
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == 2) ptx::tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ join
@@ -555,38 +1116,95 @@ Ws ws_layout(int64_t grid, int64_t rt, int64_t D) {
   return w;
 }
 
-int rows_grid(int64_t D) { return kv_sm_count() * (D == 256 ? 1 : 2); }
+// Which kernel serves requests of up to `rows` rows on a key head, as its
+// rows an item and its CTAs an SM.
+struct Choice {
+  int nt;         // rows kernel: eights of rows; 0: tile kernel
+  int mode;       // tile kernel
+  int rt, ctas;
+};
+Choice choose(int64_t rows, int64_t D) {
+  if (rows <= 8) return {1, 0, 8, D == 256 ? 1 : 2};
+  if (rows <= 16) return {2, 0, 16, D == 256 ? 1 : 2};
+  if (D == 256) return {0, COLS, 128, 1};
+  return rows <= 128 ? Choice{0, KEYS, 128, 1} : Choice{0, ROWS, 256, 1};
+}
 
-template <bool BF16, int D>
-cudaError_t launch_rows(const TreeAttnCall& call, Args a, cudaStream_t st) {
-  using C = Rows<D>;
-  static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = once_per_device(attr_done, [] {
-    return cudaFuncSetAttribute(attn_rows_kernel<BF16, D>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(C::SMEM));
-  });
-  if (e != cudaSuccess) return e;
-  const int box = static_cast<int>(std::min<int64_t>(call.cache.page_size, TK));
-  CUtensorMap tk, tv;
+cudaError_t set_up(const TreeAttnCall& call, int keys, int grid, int rt, Args& a, CUtensorMap& tk,
+                   CUtensorMap& tv) {
+  const int box = static_cast<int>(std::min<int64_t>(call.cache.page_size, keys));
   if (!make_map(&tk, call.cache, call.cache.k, box) || !make_map(&tv, call.cache, call.cache.v, box))
     return cudaErrorInvalidValue;
-  const int grid = rows_grid(D);
-  const Ws w = ws_layout(grid, RT, D);
+  const Ws w = ws_layout(grid, rt, call.cache.dim);
   uint8_t* ws = static_cast<uint8_t*>(call.ws);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.join = reinterpret_cast<Join*>(ws + w.join);
-  e = launch(attn_rows_kernel<BF16, D>, dim3(grid), dim3(THREADS), C::SMEM, st, tk, tv, a);
+  return cudaSuccess;
+}
+
+template <bool BF16, int D>
+cudaError_t launch_join(const Args& a, int grid, int rt, cudaStream_t st) {
+  return launch(combine_kernel<BF16, D>, dim3(grid, (rt + JOIN_WARPS - 1) / JOIN_WARPS),
+                dim3(JOIN_WARPS * 32), 0, st, a, rt);
+}
+
+template <bool BF16, int D, int NT>
+cudaError_t launch_rows(const TreeAttnCall& call, Args a, cudaStream_t st) {
+  using C = Rows<D, NT>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(attn_rows_kernel<BF16, D, NT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(C::SMEM));
+  });
   if (e != cudaSuccess) return e;
-  return launch(combine_kernel<BF16, D>, dim3(grid, RT / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, st,
-                a, RT);
+  const int grid = kv_sm_count() * C::CTAS;
+  CUtensorMap tk, tv;
+  e = set_up(call, TK, grid, C::RT, a, tk, tv);
+  if (e != cudaSuccess) return e;
+  e = launch(attn_rows_kernel<BF16, D, NT>, dim3(grid), dim3(THREADS), C::SMEM, st, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  return launch_join<BF16, D>(a, grid, C::RT, st);
+}
+
+template <bool BF16, int D, int MODE>
+cudaError_t launch_tile(const TreeAttnCall& call, Args a, cudaStream_t st) {
+  using C = Tile<D, MODE>;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(attn_tile_kernel<BF16, D, MODE>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(C::SMEM));
+  });
+  if (e != cudaSuccess) return e;
+  const int grid = kv_sm_count();
+  CUtensorMap tk, tv;
+  e = set_up(call, C::TKT, grid, C::RT, a, tk, tv);
+  if (e != cudaSuccess) return e;
+  e = launch(attn_tile_kernel<BF16, D, MODE>, dim3(grid), dim3(TILE_THREADS), C::SMEM, st, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  return launch_join<BF16, D>(a, grid, C::RT, st);
+}
+
+template <bool BF16, int D>
+cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st) {
+  const Choice c = choose(call.max_new * a.group, D);
+  if (c.nt == 1) return launch_rows<BF16, D, 1>(call, a, st);
+  if (c.nt == 2) return launch_rows<BF16, D, 2>(call, a, st);
+  if constexpr (D == 256) {
+    return launch_tile<BF16, D, COLS>(call, a, st);
+  } else {
+    return c.mode == KEYS ? launch_tile<BF16, D, KEYS>(call, a, st)
+                          : launch_tile<BF16, D, ROWS>(call, a, st);
+  }
 }
 
 }  // namespace
 
-size_t tree_attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t D) {
-  return ws_layout(rows_grid(D), RT, D).bytes;
+size_t tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
+  const Choice c = choose(max_new * (Hq / H), D);
+  return ws_layout(int64_t(kv_sm_count()) * c.ctas, c.rt, D).bytes;
 }
 
 cudaError_t launch_tree_attention(const TreeAttnCall& call, cudaStream_t st) {
@@ -617,10 +1235,10 @@ cudaError_t launch_tree_attention(const TreeAttnCall& call, cudaStream_t st) {
   a.group = static_cast<int>(call.Hq / c.heads);
   a.scale_log2 = call.scale * 1.4426950408889634f;
   const bool bf = c.dtype == TERN_KV_BF16;
-  if (c.dim == 64) return bf ? launch_rows<true, 64>(call, a, st) : launch_rows<false, 64>(call, a, st);
+  if (c.dim == 64) return bf ? launch_dim<true, 64>(call, a, st) : launch_dim<false, 64>(call, a, st);
   if (c.dim == 128)
-    return bf ? launch_rows<true, 128>(call, a, st) : launch_rows<false, 128>(call, a, st);
-  return bf ? launch_rows<true, 256>(call, a, st) : launch_rows<false, 256>(call, a, st);
+    return bf ? launch_dim<true, 128>(call, a, st) : launch_dim<false, 128>(call, a, st);
+  return bf ? launch_dim<true, 256>(call, a, st) : launch_dim<false, 256>(call, a, st);
 }
 
 cudaError_t attn_read_clear_error(unsigned int* err) {

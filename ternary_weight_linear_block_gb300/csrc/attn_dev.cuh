@@ -77,22 +77,32 @@ __device__ __forceinline__ Req load_req(const Args& a, int b) {
 struct Piece {
   int64_t lo, hi, total, base;
   int b, ctas;
+  Req r;   // request b
 };
 
-// Every thread of a CTA of NT threads; `s` is shared scratch of NT / 32 + 3
-// 64-bit words.
+// Shared scratch of find_piece for a CTA of NT threads.
+template <int NT>
+struct PieceScratch {
+  int64_t warp[NT / 32];
+  int64_t base;
+  int b;
+  Req r;
+};
+
+// Every thread of a CTA of NT threads (it synchronises them).
 template <int TK, int RT, int NT>
-__device__ __forceinline__ Piece find_piece(const Args& a, int64_t* s) {
+__device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = NT / 32;
-  Piece p;
+  Piece p{};
   int64_t carry = 0;
   int64_t mine = 0, before = 0;   // of this thread's request in the last round of the scan
+  Req r{};
   const auto round = [&](int base) {
     const int b = base + tid;
     mine = 0;
     if (b < a.B) {
-      const Req r = load_req<TK, RT>(a, b);
+      r = load_req<TK, RT>(a, b);
       mine = int64_t(a.H) * r.rts * r.tiles;
     }
     int64_t x = mine;
@@ -102,11 +112,11 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int64_t* s) {
       if (lane >= d) x += y;
     }
     __syncthreads();
-    if (lane == 31) s[warp] = x;
+    if (lane == 31) s.warp[warp] = x;
     __syncthreads();
     int64_t below = carry;
     for (int w = 0; w < W; ++w) {
-      const int64_t y = s[w];
+      const int64_t y = s.warp[w];
       if (w < warp) below += y;
       carry += y;
     }
@@ -121,24 +131,26 @@ __device__ __forceinline__ Piece find_piece(const Args& a, int64_t* s) {
   if (static_cast<int>(blockIdx.x) >= p.ctas) return p;
   p.lo = p.total * blockIdx.x / p.ctas;
   p.hi = p.total * (blockIdx.x + 1) / p.ctas;
-  if (a.B <= NT) {
+  const auto found = [&](int b) {
     if (before <= p.lo && p.lo < before + mine) {
-      s[W] = before;
-      s[W + 1] = tid;
+      s.base = before;
+      s.b = b;
+      s.r = r;
     }
+  };
+  if (a.B <= NT) {
+    found(tid);
   } else {
     carry = 0;
     for (int base = 0; base < a.B && carry <= p.lo; base += NT) {
       round(base);
-      if (before <= p.lo && p.lo < before + mine) {
-        s[W] = before;
-        s[W + 1] = base + tid;
-      }
+      found(base + tid);
     }
   }
   __syncthreads();
-  p.base = s[W];
-  p.b = static_cast<int>(s[W + 1]);
+  p.base = s.base;
+  p.b = s.b;
+  p.r = s.r;
   return p;
 }
 
@@ -164,11 +176,8 @@ struct Walk {
   int64_t size;
 
   __device__ __forceinline__ Walk(const Args& args, const Piece& p)
-      : a(args), w(p.lo), hi(p.hi), base(p.base), b(p.b), size(0) {
-    if (w < hi) {
-      r = load_req<TK, RT>(a, b);
-      size = int64_t(a.H) * r.rts * r.tiles;
-    }
+      : a(args), w(p.lo), hi(p.hi), base(p.base), b(p.b), r(p.r) {
+    size = int64_t(a.H) * r.rts * r.tiles;
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (w >= hi) return false;
@@ -197,6 +206,29 @@ __device__ __forceinline__ bool sees(const Args& a, const uint64_t* mw, int i, i
   if (j >= n) return false;
   if (a.mask == nullptr) return j <= i;
   return (j >> 6) < a.mask_words && ((mw[j >> 6] >> (j & 63)) & 1);
+}
+
+// The same for the N (16 or 32) keys from position k0 on, as bits: cached keys
+// are seen, keys past the request's last are not.
+template <int N>
+__device__ __forceinline__ uint32_t sees_bits(const Args& a, const uint64_t* mw, int i, int k0,
+                                              const Req& r) {
+  const int j0 = k0 - r.ctx;              // k0 as a new token, below 0: cached
+  const int lo = max(j0, 0), skip = min(lo - j0, N);
+  uint64_t x = 0;
+  if (skip < N) {
+    if (a.mask == nullptr) {
+      const int up = i - lo + 1;          // new tokens lo .. i
+      x = up <= 0 ? 0 : up >= N ? 0xFFFFFFFFu : (1u << up) - 1;
+    } else {
+      const int w = lo >> 6, sh = lo & 63;
+      if (w < a.mask_words) x = mw[w] >> sh;
+      if (sh > 64 - N && w + 1 < a.mask_words) x |= mw[w + 1] << (64 - sh);
+    }
+  }
+  const uint64_t bits = (x << skip) | ((uint64_t(1) << skip) - 1);
+  const int valid = min(max(r.len - k0, 0), N);
+  return static_cast<uint32_t>(bits & ((uint64_t(1) << valid) - 1));
 }
 
 __device__ __forceinline__ float ex2(float x) {

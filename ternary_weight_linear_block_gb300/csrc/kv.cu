@@ -333,10 +333,15 @@ int log2_of(int64_t v) {
 
 }  // namespace
 
+// SMs of the current device (asked once per device; 152, GB300's, without one).
 int kv_sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+  known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

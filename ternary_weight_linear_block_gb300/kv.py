@@ -15,7 +15,6 @@ read, so a step can be captured in a CUDA graph and replayed as they change.
 
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Sequence
 
 import torch
@@ -54,8 +53,6 @@ def _heads(t: torch.Tensor, heads: int, dim: int, dtype, name: str):
 
 def _on(stream):
     """Allocate on the stream that the call runs on."""
-    if stream is None:
-        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
@@ -79,6 +76,7 @@ class KVCache:
                       for i in range(3))
         self.desc = B.KVCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.page_size,
                                   self.heads, self.dim, ps, ts, hs, _TYPES[k.dtype])
+        self.desc_bytes = bytes(self.desc)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, dim: int, dtype=torch.bfloat16,
@@ -127,8 +125,11 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
         _check(free_head.is_cuda and free_head.dtype == torch.int32 and free_head.numel() == 1,
                "free_head: expected one int32 on the GPU")
     if plan is None:
-        with _on(stream):
+        if stream is None:
             plan = KVPlan.empty(b, capacity, ctx_len.device)
+        else:
+            with _on(stream):
+                plan = KVPlan.empty(b, capacity, ctx_len.device)
     else:
         _ints(plan.row_start, "plan.row_start")
         _ints(plan.slots, "plan.slots", torch.int64)
@@ -178,18 +179,25 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
         _ints(mask, "mask", torch.int64, 2)
         words = mask.shape[1]
         _check(mask.shape[0] >= t and words > 0, "mask: expected [rows, words]")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((t, hq, cache.dim), dtype=cache.dtype, device=q.device)
-        if return_lse and lse is None:
-            lse = torch.empty((t, hq), dtype=torch.float32, device=q.device)
-        nb = B.tern_tree_attention_workspace_bytes(max_new, hq, cache.heads, cache.dim)
-        buf = (ws or B.Workspace(q.device)).scratch(nb, stream)
-    _check(out.is_cuda and out.dtype == cache.dtype and out.shape == (t, hq, cache.dim) and
-           out.is_contiguous(), "out: expected a contiguous [rows, query heads, dim]")
+    if out is not None:
+        _check(out.is_cuda and out.dtype == cache.dtype and out.shape == (t, hq, cache.dim) and
+               out.is_contiguous(), "out: expected a contiguous [rows, query heads, dim]")
     if lse is not None:
         _check(lse.is_cuda and lse.dtype == torch.float32 and lse.shape == (t, hq) and
                lse.is_contiguous(), "lse: expected a contiguous fp32 [rows, query heads]")
+    nb = B.tern_tree_attention_workspace_bytes(max_new, hq, cache.heads, cache.dim)
+
+    def buffers():
+        return (torch.empty((t, hq, cache.dim), dtype=cache.dtype, device=q.device)
+                if out is None else out,
+                torch.empty((t, hq), dtype=torch.float32, device=q.device)
+                if return_lse and lse is None else lse,
+                (ws or B.Workspace(q.device)).scratch(nb, stream))
+    if stream is None:
+        out, lse, buf = buffers()
+    else:
+        with _on(stream):
+            out, lse, buf = buffers()
     B.tern_tree_attention(q, qt, qh, cache.desc, table, stride, table.shape[1], ctx_len, row_start,
                           mask, words, b, t, hq, max_new,
                           cache.dim ** -0.5 if scale is None else scale, out, lse, buf, buf.numel(),
@@ -214,13 +222,15 @@ def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len:
     _check(path.shape[0] == b and path_len.shape[0] == b, "path, path_len: expected a row each request")
     stride = _table(table, b)
     if ctx_out is None:
-        with _on(stream):
+        if stream is None:
             ctx_out = torch.empty_like(ctx_len)
+        else:
+            with _on(stream):
+                ctx_out = torch.empty_like(ctx_len)
     else:
         _ints(ctx_out, "ctx_out")
         _check(ctx_out.shape[0] == b, "ctx_out: expected as many requests as ctx_len")
-    descs = (B.KVCacheDesc * len(caches))(*(c.desc for c in caches))
-    B.tern_kv_commit(descs, len(caches), table, stride, table.shape[1], ctx_len, path,
+    B.tern_kv_commit(b"".join([c.desc_bytes for c in caches]), len(caches), table, stride, table.shape[1], ctx_len, path,
                      path.shape[1], path_len, ctx_out, b, stream)
     return ctx_out
 
