@@ -562,6 +562,27 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       : "memory");
 }
 
+// Wait for this thread's loads from tensor memory; what was loaded into v
+// cannot be used before it.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                   "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                   "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]), "+r"(v[17]),
+                   "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+// Scores that a row does not see.
+__device__ __forceinline__ void mask_out(uint32_t (&v)[32], uint32_t vis) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!((vis >> e) & 1)) v[e] = 0xFF800000u;
+}
+
 template <bool BF16, int D, int MODE>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -755,6 +776,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t s_addr = tmem + C::S_COL + 128 * x + lane_addr;
     const uint32_t o_addr = tmem + C::O_COL + 128 * x + lane_addr;
     const int wid = tid - 128;                         // 0 .. 255
+    // the maximum is taken of the products themselves, so the scale must not
+    // be negative (the queries' signs are turned instead) nor zero
+    const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    const uint32_t turn = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -779,6 +804,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           v = *reinterpret_cast<const uint4*>(
               a.q + (s.r.row0 + int64_t(g / a.group)) * a.q_token +
               int64_t(s.h * a.group + g % a.group) * a.q_head + c * 8);
+          v = make_uint4(v.x ^ turn, v.y ^ turn, v.z ^ turn, v.w ^ turn);
         }
         *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QB + (c >> 3) * (128 * 128) + (r & 127) * 128 +
                                   (((c & 7) ^ (r & 7)) << 4)) = v;
@@ -805,20 +831,23 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         s_phase ^= 1u;
         if (!ok) break;
         if (active) {
-          uint32_t v[TKT / 32][32];
+          // a row of S is read twice, 32 columns at a time with the next 32
+          // on their way: held whole it would not fit the registers
+          uint32_t v[2][32];
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c) ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, v[c]);
-          ptx::tmem_ld_wait();
-          float mt = -INFINITY;
+          for (int c = 0; c < TKT / 32; ++c) {
+            tmem_ld_wait_for(v[c & 1]);
+            if (c + 1 < TKT / 32) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+            if (edge) mask_out(v[c & 1], vis[c]);
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              float t = __uint_as_float(v[c][e]) * a.scale_log2;
-              if (edge && !((vis[c] >> e) & 1)) t = -INFINITY;
-              v[c][e] = __float_as_uint(t);
-              mt = fmaxf(mt, t);
-            }
+            for (int e = 0; e < 32; e += 2)
+              mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(v[c & 1][e]),
+                                                               __uint_as_float(v[c & 1][e + 1])));
+          }
+          ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           float f = 1.f;
           if (mt > m + 8.f || (m == -INFINITY && mt != m)) {
             f = ex2(m - mt);
@@ -829,7 +858,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             for (int c = 0; c < DV / 32; ++c) {
               uint32_t o[32];
               ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
-              ptx::tmem_ld_wait();
+              tmem_ld_wait_for(o);
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 uint32_t w[16];
@@ -845,11 +874,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int c = 0; c < TKT / 32; ++c) {
+            // P's columns 16 c .. overwrite columns of S that were read before
+            tmem_ld_wait_for(v[c & 1]);
+            if (c + 1 < TKT / 32) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
+            if (edge) mask_out(v[c & 1], vis[c]);
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(__uint_as_float(v[c][2 * e]) - ms);
-              const float p1 = ex2(__uint_as_float(v[c][2 * e + 1]) - ms);
+              const float p0 = ex2(fmaf(__uint_as_float(v[c & 1][2 * e]), scale, -ms));
+              const float p1 = ex2(fmaf(__uint_as_float(v[c & 1][2 * e + 1]), scale, -ms));
               sum[e & 3] += p0 + p1;
               w[e] = pack2<BF16>(p0, p1);
             }
@@ -934,18 +967,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           if constexpr (MODE == KEYS) {
             const uint32_t base = tmem + C::O_COL + lane_addr + col0 + 32 * c;
             ptx::tmem_ld_32x32b_x32(base, u);
-            ptx::tmem_ld_wait();
+            tmem_ld_wait_for(u);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f0;
             if (cnt > 1) {
               ptx::tmem_ld_32x32b_x32(base + 128, u);
-              ptx::tmem_ld_wait();
+              tmem_ld_wait_for(u);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(u[e]) * f1;
             }
           } else {
             ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, u);
-            ptx::tmem_ld_wait();
+            tmem_ld_wait_for(u);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
           }
