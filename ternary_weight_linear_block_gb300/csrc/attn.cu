@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
   if (tid == 0) a.join[blockIdx.x].follow = 0;
   if (piece.lo >= piece.hi) return;
   Walk<TK, RT> walk(a, piece);
-  Seg s;
+  Seg s{};
 
   if (warp == NW) {
     // ---------------- producer
@@ -576,6 +576,34 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
                : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)),
+        "l"(reinterpret_cast<uint64_t&>(z)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
+  return d;
+}
+
 // Scores that a row does not see.
 __device__ __forceinline__ void mask_out(uint32_t (&v)[32], uint32_t vis) {
 #pragma unroll
@@ -596,6 +624,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sq = ring + SLOTS * C::SLOT;
   __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, o_full, done, s_full[2], p_full[2];
+  __shared__ uint64_t turn[2][4];
   __shared__ PieceScratch<TILE_THREADS> scratch;
   __shared__ float2 s_ml[2][128];
   __shared__ unsigned int s_bad[8];
@@ -616,6 +645,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     for (int x = 0; x < 2; ++x) {
       ptx::mbar_init(&s_full[x], 1);
       ptx::mbar_init(&p_full[x], 4);
+      for (int q = 0; q < 4; ++q) ptx::mbar_init(&turn[x][q], 1);
     }
     s_abort = 0;
     s_any_bad = 0;
@@ -636,7 +666,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const uint32_t tmem = s_tmem;
   if (tid == 0) a.join[blockIdx.x].follow = 0;
   Walk<TKT, RT> walk(a, piece);
-  Seg s;
+  Seg s{};
 
   if (warp == 0) {
     // ---------------- producer
@@ -698,75 +728,93 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer (one thread)
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t seq0 = 0, q_phase = 0, p_phase[2] = {0, 0};
-      const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    // ---------------- MMA issuer: the whole warp waits and counts, one elected
+    // lane issues.  Counters are made uniform over the warp (shuffles, votes),
+    // so that descriptors are built in uniform registers: issued from a
+    // lane-dependent branch an MMA took 65 to 90 cycles, more than the 32 to
+    // 64 that it runs.
+    bool ok = true;
+    uint32_t seq0 = 0, q_phase = 0, p_phase = 0;
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!ok) return;
+      ok = ptx::mbar_wait_warp(bar, parity, abort_flag, WAIT_LIMIT);
+      if (!ok && lane == 0 && !*abort_flag) fail(abort_flag, ERR_CONSUMER);
+      ptx::tc_fence_after();
+    };
+    // addresses stay below 2^18, so offsets add to a descriptor's address field
+    const uint64_t q_desc = ptx::sw128_kmajor_desc(ptx::smem_u32(sq));
+    const uint64_t k_desc = ptx::sw128_kmajor_desc(ptx::smem_u32(ring));
+    const uint64_t v_desc = sw128_mn_desc(ptx::smem_u32(ring), HB);
+    const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    while (ok && __any_sync(~0u, walk.next(s))) {
+      const int cnt = __shfl_sync(~0u, s.t1 - s.t0, 0);
+      // place of K(i) and V(i) in the ring's order
+      const auto k_seq = [&](int i) { return seq0 + (i == 0 ? 0u : 2u * i - 1u); };
+      const auto v_seq = [&](int i) { return seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u); };
+      const auto mma_s = [&](int i, int x, bool last) {
+        const uint32_t n = k_seq(i), sl = n % SLOTS;
+        wait(&full[sl], (n / SLOTS) & 1u);
         if (!ok) return;
-        ok = ptx::mbar_wait(bar, parity, abort_flag, WAIT_LIMIT);
-        if (!ok && !*abort_flag) fail(abort_flag, ERR_CONSUMER);
-        ptx::tc_fence_after();
-      };
-      const uint32_t ring_u = ptx::smem_u32(ring), sq_u = ptx::smem_u32(sq);
-      while (ok && walk.next(s)) {
-        const int cnt = s.t1 - s.t0;
-        // place of K(i) and V(i) in the ring's order
-        const auto k_seq = [&](int i) { return seq0 + (i == 0 ? 0u : 2u * i - 1u); };
-        const auto v_seq = [&](int i) { return seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u); };
-        const auto mma_s = [&](int i, int x, bool last) {
-          const uint32_t n = k_seq(i), sl = n % SLOTS;
-          wait(&full[sl], (n / SLOTS) & 1u);
-          if (!ok) return;
-          const uint32_t qb = sq_u + (MODE == ROWS ? x * C::QB : 0);
+        // 16 values further: 32 bytes (2 in the descriptor) in a swizzled
+        // row, or the next 64 columns
+        const uint64_t da = q_desc + (MODE == ROWS ? x * (C::QB >> 4) : 0);
+        const uint64_t db = k_desc + sl * (C::SLOT >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t da = ptx::sw128_kmajor_desc(qb + (k >> 2) * (128 * 128)) + 2u * (k & 3);
-            const uint64_t db = ptx::sw128_kmajor_desc(ring_u + sl * C::SLOT + (k >> 2) * HB) + 2u * (k & 3);
-            ptx::mma_f16_ss(tmem + C::S_COL + 128 * x, da, db, idesc<BF16>(TKT, false), k > 0);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            ptx::mma_f16_ss(tm + C::S_COL + 128 * x, da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)),
+                            db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
           if (last) ptx::mma_commit(&empty[sl]);
           ptx::mma_commit(&s_full[x]);
-        };
-        const auto mma_o = [&](int i, int x, bool first, bool last) {
-          wait(&p_full[x], p_phase[x]);
-          p_phase[x] ^= 1u;
-          const uint32_t n = v_seq(i), sl = n % SLOTS;
-          wait(&full[sl], (n / SLOTS) & 1u);
-          if (!ok) return;
-          const uint32_t vb = ring_u + sl * C::SLOT + (MODE == COLS ? x * 2 * HB : 0);
+        }
+        __syncwarp();
+      };
+      const auto mma_o = [&](int i, int x, bool first, bool last) {
+        wait(&p_full[x], (p_phase >> x) & 1u);
+        p_phase ^= 1u << x;
+        const uint32_t n = v_seq(i), sl = n % SLOTS;
+        wait(&full[sl], (n / SLOTS) & 1u);
+        if (!ok) return;
+        const uint64_t dv = v_desc + (sl * (C::SLOT >> 4) + (MODE == COLS ? x * (2 * HB >> 4) : 0));
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TKT / 16; ++k)
-            ptx::mma_f16_ts(tmem + C::O_COL + 128 * x, tmem + C::S_COL + 128 * x + k * 8,
-                            sw128_mn_desc(vb + k * 2048, HB), idesc<BF16>(DV, true),
+            ptx::mma_f16_ts(tm + C::O_COL + 128 * x, tm + C::S_COL + 128 * x + k * 8,
+                            dv + k * (2048 >> 4), idesc<BF16>(DV, true),
                             (!first || k > 0) ? 1u : 0u);
           if (last) ptx::mma_commit(&empty[sl]);
-        };
-        wait(&q_full, q_phase);
-        q_phase ^= 1u;
-        if constexpr (MODE == KEYS) {
-          mma_s(0, 0, true);
-          if (cnt > 1) mma_s(1, 1, true);
-          for (int i = 0; i < cnt && ok; ++i) {
-            mma_o(i, i & 1, i < 2, true);
-            if (i + 2 < cnt) mma_s(i + 2, i & 1, true);
-          }
-        } else {
-          mma_s(0, 0, false);
-          mma_s(0, 1, true);
-          for (int i = 0; i < cnt && ok; ++i)
-            for (int x = 0; x < 2; ++x) {
-              mma_o(i, x, i == 0, x == 1);
-              if (i + 1 < cnt) mma_s(i + 1, x, x == 1);
-            }
         }
-        if (ok) ptx::mma_commit(&o_full);
-        seq0 += 2u * cnt;
+        __syncwarp();
+      };
+      wait(&q_full, q_phase);
+      q_phase ^= 1u;
+      if constexpr (MODE == KEYS) {
+        mma_s(0, 0, true);
+        if (cnt > 1) mma_s(1, 1, true);
+        for (int i = 0; i < cnt && ok; i += 2) {
+          mma_o(i, 0, i == 0, true);
+          if (i + 2 < cnt) mma_s(i + 2, 0, true);
+          if (i + 1 < cnt) mma_o(i + 1, 1, i == 0, true);
+          if (i + 3 < cnt) mma_s(i + 3, 1, true);
+        }
+      } else {
+        mma_s(0, 0, false);
+        mma_s(0, 1, true);
+        for (int i = 0; i < cnt && ok; ++i) {
+          mma_o(i, 0, i == 0, false);
+          if (i + 1 < cnt) mma_s(i + 1, 0, false);
+          mma_o(i, 1, i == 0, true);
+          if (i + 1 < cnt) mma_s(i + 1, 1, true);
+        }
       }
-      ptx::mma_commit(&done);
-      if (!ptx::mbar_wait_bounded(&done, 0, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
+      if (ok && elect_one()) ptx::mma_commit(&o_full);
+      __syncwarp();
+      seq0 += 2u * cnt;
     }
+    // every MMA issued has completed once `done` fires
+    if (elect_one()) ptx::mma_commit(&done);
     __syncwarp();
+    if (!ptx::mbar_wait_bounded(&done, 0, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
   } else if (warp >= 4) {
     // ---------------- softmax and output: warpgroup x has stream x, a thread
     // one row of it
@@ -779,9 +827,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     // the maximum is taken of the products themselves, so the scale must not
     // be negative (the queries' signs are turned instead) nor zero
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
-    const uint32_t turn = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
+    uint32_t turns = 0;      // arrivals on this warp's turn barrier before this item
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!ok) return;
       ok = ptx::mbar_wait_warp(bar, parity, abort_flag, WAIT_LIMIT);
@@ -804,7 +853,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           v = *reinterpret_cast<const uint4*>(
               a.q + (s.r.row0 + int64_t(g / a.group)) * a.q_token +
               int64_t(s.h * a.group + g % a.group) * a.q_head + c * 8);
-          v = make_uint4(v.x ^ turn, v.y ^ turn, v.z ^ turn, v.w ^ turn);
+          v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
         }
         *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QB + (c >> 3) * (128 * 128) + (r & 127) * 128 +
                                   (((c & 7) ^ (r & 7)) << 4)) = v;
@@ -815,6 +864,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 
       const int my = (MODE == ROWS ? 128 * x : 0) + lrow;      // row of the item
       const bool active = (MODE == ROWS ? 128 * x : 0) + (warp & 3) * 32 < rows;
+      const bool paired = (MODE == ROWS ? 128 : 0) + (warp & 3) * 32 < rows;   // both streams' are
       const int tok = my < rows ? (r0 + my) / a.group : 0;
       const uint64_t* mw = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words : nullptr;
       float m = -INFINITY, l = 0.f;
@@ -829,6 +879,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         wait(&s_full[x], s_phase);
         s_phase ^= 1u;
+        // the two warps of an SM quarter, one of each stream, take turns: one's
+        // exponentials then run beside the other's MMAs, not beside the
+        // other's exponentials
+        const uint32_t at_turn = MODE == KEYS ? i >> 1 : i;      // tile of the stream
+        if (paired && (x == 1 || at_turn > 0))
+          wait(&turn[x][warp & 3], (turns + at_turn - (x ^ 1)) & 1u);
         if (!ok) break;
         if (active) {
           // a row of S is read twice, 32 columns at a time with the next 32
@@ -871,7 +927,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           }
           any = true;
           const float ms = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 sc2 = make_float2(scale, scale), ms2 = make_float2(-ms, -ms);
+          float2 sum[4] = {};
 #pragma unroll
           for (int c = 0; c < TKT / 32; ++c) {
             // P's columns 16 c .. overwrite columns of S that were read before
@@ -881,14 +938,17 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(__uint_as_float(v[c & 1][2 * e]), scale, -ms));
-              const float p1 = ex2(fmaf(__uint_as_float(v[c & 1][2 * e + 1]), scale, -ms));
-              sum[e & 3] += p0 + p1;
-              w[e] = pack2<BF16>(p0, p1);
+              const float2 t = fma2(make_float2(__uint_as_float(v[c & 1][2 * e]),
+                                                __uint_as_float(v[c & 1][2 * e + 1])), sc2, ms2);
+              const float2 p = make_float2(ex2(t.x), ex2(t.y));
+              sum[e & 3] = add2(sum[e & 3], p);
+              w[e] = pack2<BF16>(p.x, p.y);
             }
             tmem_st_x16(s_addr + 16 * c, w);
           }
-          l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          l = l * f + (all.x + all.y);
+          if (paired && lane == 0) ptx::mbar_arrive(&turn[x ^ 1][warp & 3]);
           ptx::tmem_st_wait();
         }
         if (edge && (MODE == KEYS || x == 0)) {
@@ -934,6 +994,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       wait(&o_full, o_phase);
       o_phase ^= 1u;
       seq0 += 2u * cnt;
+      // the other stream's warp arrived once for each of its tiles
+      if (paired) turns += MODE == KEYS ? (cnt + x) >> 1 : cnt;
       if constexpr (MODE == KEYS) s_ml[x][lrow] = make_float2(m, l);
       ptx::named_sync(1, 256);
       const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
