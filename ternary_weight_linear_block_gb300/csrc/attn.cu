@@ -624,7 +624,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sq = ring + SLOTS * C::SLOT;
   __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, o_full, done, s_full[2], p_full[2];
-  __shared__ uint64_t turn[2][4];
   __shared__ PieceScratch<TILE_THREADS> scratch;
   __shared__ float2 s_ml[2][128];
   __shared__ unsigned int s_bad[8];
@@ -645,7 +644,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     for (int x = 0; x < 2; ++x) {
       ptx::mbar_init(&s_full[x], 1);
       ptx::mbar_init(&p_full[x], 4);
-      for (int q = 0; q < 4; ++q) ptx::mbar_init(&turn[x][q], 1);
     }
     s_abort = 0;
     s_any_bad = 0;
@@ -751,60 +749,65 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       // place of K(i) and V(i) in the ring's order
       const auto k_seq = [&](int i) { return seq0 + (i == 0 ? 0u : 2u * i - 1u); };
       const auto v_seq = [&](int i) { return seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u); };
-      const auto mma_s = [&](int i, int x, bool last) {
-        const uint32_t n = k_seq(i), sl = n % SLOTS;
-        wait(&full[sl], (n / SLOTS) & 1u);
-        if (!ok) return;
-        // 16 values further: 32 bytes (2 in the descriptor) in a swizzled
-        // row, or the next 64 columns
+      // S of stream x from the keys in slot sl (one lane): 16 values further
+      // is 32 bytes (2 in the descriptor) in a swizzled row, or the next 64
+      // columns
+      const auto issue_s = [&](uint32_t sl, int x, bool last) {
         const uint64_t da = q_desc + (MODE == ROWS ? x * (C::QB >> 4) : 0);
         const uint64_t db = k_desc + sl * (C::SLOT >> 4);
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            ptx::mma_f16_ss(tm + C::S_COL + 128 * x, da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)),
-                            db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
-          if (last) ptx::mma_commit(&empty[sl]);
-          ptx::mma_commit(&s_full[x]);
-        }
-        __syncwarp();
+        for (int k = 0; k < D / 16; ++k)
+          ptx::mma_f16_ss(tm + C::S_COL + 128 * x, da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)),
+                          db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
+        if (last) ptx::mma_commit(&empty[sl]);
+        ptx::mma_commit(&s_full[x]);
       };
-      const auto mma_o = [&](int i, int x, bool first, bool last) {
+      // one stream's step: out += P V of tile i, then S of its next tile j
+      // (none: j >= cnt).  The ring's barriers are waited for before the
+      // stream's P, which is the last to be ready.
+      const auto step = [&](int i, int j, int x, bool first, bool ring, bool last) {
+        const uint32_t nv = v_seq(i), nk = k_seq(j);
+        const uint32_t sv = nv % SLOTS, sk = nk % SLOTS;
+        if (ring) {
+          wait(&full[sv], (nv / SLOTS) & 1u);
+          if (j < cnt) wait(&full[sk], (nk / SLOTS) & 1u);
+        }
         wait(&p_full[x], (p_phase >> x) & 1u);
         p_phase ^= 1u << x;
-        const uint32_t n = v_seq(i), sl = n % SLOTS;
-        wait(&full[sl], (n / SLOTS) & 1u);
         if (!ok) return;
-        const uint64_t dv = v_desc + (sl * (C::SLOT >> 4) + (MODE == COLS ? x * (2 * HB >> 4) : 0));
+        const uint64_t dv = v_desc + (sv * (C::SLOT >> 4) + (MODE == COLS ? x * (2 * HB >> 4) : 0));
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TKT / 16; ++k)
             ptx::mma_f16_ts(tm + C::O_COL + 128 * x, tm + C::S_COL + 128 * x + k * 8,
                             dv + k * (2048 >> 4), idesc<BF16>(DV, true),
                             (!first || k > 0) ? 1u : 0u);
-          if (last) ptx::mma_commit(&empty[sl]);
+          if (last) ptx::mma_commit(&empty[sv]);
+          if (j < cnt) issue_s(sk, x, last);
         }
+        __syncwarp();
+      };
+      const auto begin = [&](int i, int x, bool ring, bool last) {
+        const uint32_t nk = k_seq(i), sk = nk % SLOTS;
+        if (ring) wait(&full[sk], (nk / SLOTS) & 1u);
+        if (ok && elect_one()) issue_s(sk, x, last);
         __syncwarp();
       };
       wait(&q_full, q_phase);
       q_phase ^= 1u;
       if constexpr (MODE == KEYS) {
-        mma_s(0, 0, true);
-        if (cnt > 1) mma_s(1, 1, true);
+        begin(0, 0, true, true);
+        if (cnt > 1) begin(1, 1, true, true);
         for (int i = 0; i < cnt && ok; i += 2) {
-          mma_o(i, 0, i == 0, true);
-          if (i + 2 < cnt) mma_s(i + 2, 0, true);
-          if (i + 1 < cnt) mma_o(i + 1, 1, i == 0, true);
-          if (i + 3 < cnt) mma_s(i + 3, 1, true);
+          step(i, i + 2, 0, i == 0, true, true);
+          if (i + 1 < cnt) step(i + 1, i + 3, 1, i == 0, true, true);
         }
       } else {
-        mma_s(0, 0, false);
-        mma_s(0, 1, true);
+        begin(0, 0, true, false);
+        begin(0, 1, false, true);
         for (int i = 0; i < cnt && ok; ++i) {
-          mma_o(i, 0, i == 0, false);
-          if (i + 1 < cnt) mma_s(i + 1, 0, false);
-          mma_o(i, 1, i == 0, true);
-          if (i + 1 < cnt) mma_s(i + 1, 1, true);
+          step(i, i + 1, 0, i == 0, true, false);
+          step(i, i + 1, 1, i == 0, false, true);
         }
       }
       if (ok && elect_one()) ptx::mma_commit(&o_full);
@@ -830,7 +833,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
-    uint32_t turns = 0;      // arrivals on this warp's turn barrier before this item
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!ok) return;
       ok = ptx::mbar_wait_warp(bar, parity, abort_flag, WAIT_LIMIT);
@@ -864,7 +866,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 
       const int my = (MODE == ROWS ? 128 * x : 0) + lrow;      // row of the item
       const bool active = (MODE == ROWS ? 128 * x : 0) + (warp & 3) * 32 < rows;
-      const bool paired = (MODE == ROWS ? 128 : 0) + (warp & 3) * 32 < rows;   // both streams' are
       const int tok = my < rows ? (r0 + my) / a.group : 0;
       const uint64_t* mw = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words : nullptr;
       float m = -INFINITY, l = 0.f;
@@ -879,30 +880,29 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         wait(&s_full[x], s_phase);
         s_phase ^= 1u;
-        // the two warps of an SM quarter, one of each stream, take turns: one's
-        // exponentials then run beside the other's MMAs, not beside the
-        // other's exponentials
-        const uint32_t at_turn = MODE == KEYS ? i >> 1 : i;      // tile of the stream
-        if (paired && (x == 1 || at_turn > 0))
-          wait(&turn[x][warp & 3], (turns + at_turn - (x ^ 1)) & 1u);
         if (!ok) break;
         if (active) {
-          // a row of S is read twice, 32 columns at a time with the next 32
-          // on their way: held whole it would not fit the registers
+          // a row of S is read twice, 64 columns at a time: held whole it would
+          // not fit the registers
           uint32_t v[2][32];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c) {
-            tmem_ld_wait_for(v[c & 1]);
-            if (c + 1 < TKT / 32) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
-            if (edge) mask_out(v[c & 1], vis[c]);
+          for (int c = 0; c < TKT / 32; c += 2) {
+            ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, v[0]);
+            ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 32, v[1]);
+            tmem_ld_wait_for(v[0]);
+            tmem_ld_wait_for(v[1]);
+            if (edge) {
+              mask_out(v[0], vis[c]);
+              mask_out(v[1], vis[c + 1]);
+            }
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(v[c & 1][e]),
-                                                               __uint_as_float(v[c & 1][e + 1])));
+            for (int e = 0; e < 64; e += 2)
+              mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(v[e >> 5][e & 31]),
+                                                               __uint_as_float(v[e >> 5][(e & 31) + 1])));
           }
           ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
+          ptx::tmem_ld_32x32b_x32(s_addr + 32, v[1]);
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           float f = 1.f;
           if (mt > m + 8.f || (m == -INFINITY && mt != m)) {
@@ -930,25 +930,32 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           const float2 sc2 = make_float2(scale, scale), ms2 = make_float2(-ms, -ms);
           float2 sum[4] = {};
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c) {
+          for (int c = 0; c < TKT / 32; c += 2) {
             // P's columns 16 c .. overwrite columns of S that were read before
-            tmem_ld_wait_for(v[c & 1]);
-            if (c + 1 < TKT / 32) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
-            if (edge) mask_out(v[c & 1], vis[c]);
-            uint32_t w[16];
+            tmem_ld_wait_for(v[0]);
+            tmem_ld_wait_for(v[1]);
+            if (edge) {
+              mask_out(v[0], vis[c]);
+              mask_out(v[1], vis[c + 1]);
+            }
+            uint32_t w[2][16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float2 t = fma2(make_float2(__uint_as_float(v[c & 1][2 * e]),
-                                                __uint_as_float(v[c & 1][2 * e + 1])), sc2, ms2);
+            for (int e = 0; e < 32; ++e) {
+              const float2 t = fma2(make_float2(__uint_as_float(v[e >> 4][2 * (e & 15)]),
+                                                __uint_as_float(v[e >> 4][2 * (e & 15) + 1])), sc2, ms2);
               const float2 p = make_float2(ex2(t.x), ex2(t.y));
               sum[e & 3] = add2(sum[e & 3], p);
-              w[e] = pack2<BF16>(p.x, p.y);
+              w[e >> 4][e & 15] = pack2<BF16>(p.x, p.y);
             }
-            tmem_st_x16(s_addr + 16 * c, w);
+            if (c + 2 < TKT / 32) {
+              ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 64, v[0]);
+              ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 96, v[1]);
+            }
+            tmem_st_x16(s_addr + 16 * c, w[0]);
+            tmem_st_x16(s_addr + 16 * c + 16, w[1]);
           }
           const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           l = l * f + (all.x + all.y);
-          if (paired && lane == 0) ptx::mbar_arrive(&turn[x ^ 1][warp & 3]);
           ptx::tmem_st_wait();
         }
         if (edge && (MODE == KEYS || x == 0)) {
@@ -994,8 +1001,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       wait(&o_full, o_phase);
       o_phase ^= 1u;
       seq0 += 2u * cnt;
-      // the other stream's warp arrived once for each of its tiles
-      if (paired) turns += MODE == KEYS ? (cnt + x) >> 1 : cnt;
       if constexpr (MODE == KEYS) s_ml[x][lrow] = make_float2(m, l);
       ptx::named_sync(1, 256);
       const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
