@@ -7,7 +7,7 @@
 // rescaled where m grows.  The probabilities are rounded to the cache's type
 // for the second product, as its values are; l sums them unrounded.
 //
-// attn_rows_kernel: up to 32 rows an item, tiles of 64 keys.  A producer warp
+// attn_rows_kernel: up to 16 rows an item, tiles of 64 keys.  A producer warp
 // copies each page's part of a tile with TMA into a ring; four warps take 16
 // keys of a tile each and keep their own (m, l, out) of all the item's rows,
 // so that no warp waits for another inside an item; they join at its end.
@@ -79,55 +79,67 @@ __device__ __forceinline__ uint32_t movm(uint32_t x) {
 // ------------------------------------------------------------------ rows kernel
 
 constexpr int TK = 64;             // keys of a tile
-constexpr int NW = 4;              // consumer warps
-constexpr int THREADS = (NW + 1) * 32;
+constexpr int NW = 4;              // warps that share a tile's keys, 16 each
 
 // NT: eights of rows in an item.  The accumulators (D / 4 * NT registers a
 // thread) and the query fragments (D / 8 * NT) decide how many CTAs an SM
 // holds, and so the ring's size.  Joining the warps takes two buffers of the
-// item's rows; `COLS` columns of them at a time where two CTAs share an SM.
+// item's rows, `COLS` columns of them at a time where two CTAs share an SM.
 template <int D, int NT>
 struct Rows {
   static constexpr int RT = 8 * NT;
+  static constexpr int THREADS = (NW + 2) * 32;           // and a producer each of K and V
   static constexpr int STAGE = 2 * TK * D * 2;            // keys and values of a tile
-  static constexpr int CTAS = D * NT <= 256 && D < 256 ? 2 : 1;   // per SM
+  static constexpr int CTAS = D < 256 ? 2 : 1;            // per SM
   static constexpr int COLS = CTAS == 2 && D * NT == 256 ? D / 2 : D;
   static constexpr int LD = COLS + 4;                     // no two lanes of a store share a bank
   static constexpr int MERGE = 2 * RT * LD * 4;
-  static constexpr int ROOM = (CTAS == 2 ? 115200 : 232448) - MERGE - 1024 - 1280;
+  static constexpr int ROOM = (CTAS == 2 ? 115200 : 232448) - MERGE - 1024 - 3072;
   static constexpr int FIT = ROOM / STAGE;
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
   static constexpr size_t SMEM = size_t(STAGES) * STAGE + MERGE + 1024;
   static_assert(STAGES >= 2, "ring");
 };
 
-// One tile's copies, spread over the producer warp: box i of `boxes` covers
-// box_rows keys of one page; D / 64 halves of 128 bytes a key (the swizzled
-// row), keys then values.
+// The pages of a tile of TKEYS keys: lane i has the page of its i-th box (a
+// page's part of the tile, 1 << box_shift keys); a page out of range is turned
+// into one past the last, of which TMA copies zeros.
+template <int TKEYS>
+__device__ __forceinline__ int page_at(const Args& a, const Seg& s, int t, int box_shift, int lane) {
+  const int64_t pos = int64_t(t) * TKEYS + (int64_t(lane) << box_shift);
+  int pg = -1;
+  if (lane < (TKEYS >> box_shift) && pos < s.r.len)
+    pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
+  return pg < 0 || pg >= a.pages ? a.pages : pg;
+}
+
+// Keys or values of tile t into `dst` (64-column halves of TKEYS rows of 128
+// swizzled bytes), one box and half a lane; the warp first announces the
+// bytes on `bar`.
 template <int D, int TKEYS>
-__device__ __forceinline__ void load_tile(const CUtensorMap* tk, const CUtensorMap* tv,
-                                          uint8_t* stage, uint64_t* bar, int page, int boxes,
-                                          int box_shift, int row, int h, int lane) {
+__device__ __forceinline__ void load_tile(const Args& a, const CUtensorMap* map, uint8_t* dst,
+                                          uint64_t* bar, const Seg& s, int t, int page,
+                                          int box_shift, int lane) {
   constexpr int HALVES = D / 64;
-  constexpr int HB = TKEYS * 128;
-  for (int i0 = 0; i0 < boxes * HALVES; i0 += 32) {
-    const int i = i0 + lane;
-    const int box = i / HALVES, half = i % HALVES;
-    const int pg = __shfl_sync(~0u, page, box & 31);
-    if (i < boxes * HALVES) {
-      uint8_t* dst = stage + half * HB + (box << box_shift) * 128;
-      tma_load_4d(dst, tk, bar, half * 64, row, h, pg);
-      tma_load_4d(dst + HALVES * HB, tv, bar, half * 64, row, h, pg);
-    }
-  }
+  const int k0 = t * TKEYS;
+  const int keys = min(TKEYS, s.r.len - k0);
+  const int boxes = keys > 0 ? (keys + (1 << box_shift) - 1) >> box_shift : 0;
+  if (lane == 0)
+    ptx::mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes << box_shift) * D * 2u);
+  __syncwarp();
+  const int box = lane / HALVES, half = lane % HALVES;   // at most 32: 8 keys a box or more
+  const int pg = __shfl_sync(~0u, page, box);
+  if (box < boxes)
+    tma_load_4d(dst + half * (TKEYS * 128) + (box << box_shift) * 128, map, bar, half * 64,
+                k0 & ((1 << a.page_shift) - 1), s.h, pg);
 }
 
 template <bool BF16, int D, int NT>
-__global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
+__global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
     attn_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
   using C = Rows<D, NT>;
-  constexpr int RT = C::RT;
+  constexpr int RT = C::RT, THREADS = C::THREADS;
   constexpr int HALVES = D / 64;
   constexpr int HB = TK * 128;
   constexpr int KS = D / 16;
@@ -146,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
 
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&full[s], 2);
       ptx::mbar_init(&empty[s], NW);
     }
     s_abort = 0;
@@ -164,42 +176,28 @@ __global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
   Walk<TK, RT> walk(a, piece);
   Seg s{};
 
-  if (warp == NW) {
-    // ---------------- producer
+  if (warp >= NW) {
+    // ---------------- producers: one warp copies the keys, one the values
+    // (issued by one warp, pages of 16 rows held a long context to two thirds
+    // of its rate)
+    const bool vals = warp > NW;
+    const CUtensorMap* map = vals ? &tm_v : &tm_k;
     int st = 0;
     uint32_t phase = 0;
     long issued = 0;
     bool ok = true;
-    const int page_rows = 1 << a.page_shift;
     const int box_shift = min(a.page_shift, 6);      // rows of a box: a page, or the tile
-    const int per_tile = TK >> box_shift;
     while (ok && walk.next(s)) {
-      const int32_t* row = a.table + int64_t(s.b) * a.table_stride;
-      // lane i: page of box i of a tile, read one tile ahead
-      const auto page_at = [&](int t) {
-        const int64_t p = (int64_t(t) * TK + (int64_t(lane) << box_shift)) >> a.page_shift;
-        int pg = -1;
-        if (lane < per_tile && (int64_t(t) * TK + (int64_t(lane) << box_shift)) < s.r.len)
-          pg = row[p];
-        return pg < 0 || pg >= a.pages ? a.pages : pg;   // out of range: zeros are copied
-      };
-      int page = page_at(s.t0);
+      int page = page_at<TK>(a, s, s.t0, box_shift, lane);
       for (int t = s.t0; t < s.t1; ++t) {
-        const int k0 = t * TK;
-        const int keys = min(TK, s.r.len - k0);
-        const int boxes = keys > 0 ? (keys + (1 << box_shift) - 1) >> box_shift : 0;
-        const int ahead = t + 1 < s.t1 ? page_at(t + 1) : 0;
+        const int ahead = t + 1 < s.t1 ? page_at<TK>(a, s, t + 1, box_shift, lane) : 0;
         ok = ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT);
         if (!ok) {
           if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
           break;
         }
-        if (lane == 0)
-          ptx::mbar_arrive_expect_tx(&full[st],
-                                     static_cast<uint32_t>(boxes << box_shift) * D * 4u);
-        __syncwarp();
-        load_tile<D, TK>(&tm_k, &tm_v, ring + st * C::STAGE, &full[st], page, boxes, box_shift,
-                         k0 & (page_rows - 1), s.h, lane);
+        load_tile<D, TK>(a, map, ring + st * C::STAGE + (vals ? HALVES * HB : 0), &full[st], s, t,
+                         page, box_shift, lane);
         page = ahead;
         ++issued;
         if (++st == C::STAGES) {
@@ -265,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
     }
 
     for (int t = s.t0; t < s.t1; ++t) {
-      const int k0 = t * TK + warp * 16;       // this warp's first key
+      const int k0 = t * TK + warp * 16;         // this warp's first key
       const bool edge = k0 + 16 > s.r.ctx;     // new tokens, or past the last
       uint32_t vis[NT][2];
       if (edge) {                              // read while the tile is on its way
@@ -391,8 +389,8 @@ __global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
       }
     }
 
-    // ---- join the four warps: factors from every warp's (m, l); warps 0, 1
-    // store, warps 2, 3 add to what they stored, and the two sums are added
+    // ---- join the four warps: factors from every warp's (m, l); two of them
+    // store, the other two add to what they stored, and the two sums are added
     // as they are read
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -518,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, (Rows<D, NT>::CTAS))
 // the accumulator is rare.  Rows past the item's last cost their MMAs alone:
 // whole warps of them skip the softmax.
 
-constexpr int TILE_THREADS = 384;   // producer, MMA, TMEM, spare; two warpgroups
+constexpr int TILE_THREADS = 384;   // K producer, MMA, TMEM, V producer; two warpgroups
 enum Mode { KEYS, ROWS, COLS };
 
 template <int D, int MODE>
@@ -535,6 +533,12 @@ struct Tile {
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // stream x: + 128 x
   static_assert(SLOTS >= 4, "ring");
 };
+
+// Places of the keys and values of an item's i-th tile of cnt in the ring's order.
+__device__ __forceinline__ uint32_t k_place(int i) { return i == 0 ? 0u : 2u * i - 1u; }
+__device__ __forceinline__ uint32_t v_place(int i, int cnt) {
+  return i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u;
+}
 
 // Descriptor of V [keys][64 columns] as the MN-major B operand: 8 keys of 128
 // bytes make an atom of the 128-byte swizzle, atoms 1024 bytes apart along
@@ -666,65 +670,37 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   Walk<TKT, RT> walk(a, piece);
   Seg s{};
 
-  if (warp == 0) {
-    // ---------------- producer
-    int st = 0;
-    uint32_t phase = 0;
-    long issued = 0;
+  if (warp == 0 || warp == 3) {
+    // ---------------- producers: warp 0 copies the keys, warp 3 the values
+    const bool vals = warp == 3;
+    const CUtensorMap* map = vals ? &tm_v : &tm_k;
+    uint32_t seq0 = 0;
+    uint32_t mine = 0, parity = 0;      // slots this warp filled last, and their phases
     bool ok = true;
     const int box_shift = min(a.page_shift, TKT == 128 ? 7 : 6);
-    const int per_tile = TKT >> box_shift;
-    const auto load = [&](const CUtensorMap* map, int t, int page) {
-      const int k0 = t * TKT;
-      const int keys = min(TKT, s.r.len - k0);
-      const int boxes = keys > 0 ? (keys + (1 << box_shift) - 1) >> box_shift : 0;
-      ok = ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT);
-      if (!ok) {
-        if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
-        return;
-      }
-      if (lane == 0)
-        ptx::mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(boxes << box_shift) * D * 2u);
-      __syncwarp();
-      const int box = lane / HALVES, half = lane % HALVES;
-      const int pg = __shfl_sync(~0u, page, box & 31);
-      if (box < boxes)
-        tma_load_4d(ring + st * C::SLOT + half * HB + (box << box_shift) * 128, map, &full[st],
-                    half * 64, k0 & ((1 << a.page_shift) - 1), s.h, pg);
-      ++issued;
-      if (++st == SLOTS) {
-        st = 0;
-        phase ^= 1u;
-      }
-    };
     while (ok && walk.next(s)) {
-      const int32_t* row = a.table + int64_t(s.b) * a.table_stride;
-      const auto page_at = [&](int t) {
-        const int64_t pos = int64_t(t) * TKT + (int64_t(lane) << box_shift);
-        int pg = -1;
-        if (lane < per_tile && pos < s.r.len) pg = row[pos >> a.page_shift];
-        return pg < 0 || pg >= a.pages ? a.pages : pg;
-      };
-      int cur = page_at(s.t0), next = s.t0 + 1 < s.t1 ? page_at(s.t0 + 1) : 0;
-      load(&tm_k, s.t0, cur);
-      for (int t = s.t0; t < s.t1 && ok; ++t) {
-        const int after = t + 2 < s.t1 ? page_at(t + 2) : 0;
-        if (t + 1 < s.t1) load(&tm_k, t + 1, next);
-        if (ok) load(&tm_v, t, cur);
-        cur = next;
-        next = after;
-      }
-    }
-    if (!ok) {
-      const long back = issued < SLOTS ? issued : SLOTS;
-      for (long i = 0; i < back; ++i) {
-        if (--st < 0) {
-          st = SLOTS - 1;
-          phase ^= 1u;
+      const int cnt = s.t1 - s.t0;
+      int page = page_at<TKT>(a, s, s.t0, box_shift, lane);
+      for (int i = 0; i < cnt; ++i) {
+        const int ahead = i + 1 < cnt ? page_at<TKT>(a, s, s.t0 + i + 1, box_shift, lane) : 0;
+        const uint32_t n = seq0 + (vals ? v_place(i, cnt) : k_place(i));
+        const uint32_t sl = n % SLOTS, par = (n / SLOTS) & 1u;
+        ok = ptx::mbar_wait_warp(&empty[sl], par ^ 1u, abort_flag, WAIT_LIMIT);
+        if (!ok) {
+          if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
+          break;
         }
-        if (!ptx::mbar_wait_bounded(&full[st], phase, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
+        load_tile<D, TKT>(a, map, ring + sl * C::SLOT, &full[sl], s, s.t0 + i, page, box_shift, lane);
+        mine |= 1u << sl;
+        parity = (parity & ~(1u << sl)) | (par << sl);
+        page = ahead;
       }
+      seq0 += 2u * cnt;
     }
+    if (!ok)   // let the copies in flight land before the CTA exits
+      for (int sl = 0; sl < SLOTS; ++sl)
+        if (((mine >> sl) & 1u) && !ptx::mbar_wait_bounded(&full[sl], (parity >> sl) & 1u, WAIT_LIMIT))
+          atomicOr(&g_attn_error, ERR_DRAIN);
   } else if (warp == 1) {
     // ---------------- MMA issuer: the whole warp waits and counts, one elected
     // lane issues.  Counters are made uniform over the warp (shuffles, votes),
@@ -746,9 +722,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t tm = __shfl_sync(~0u, tmem, 0);
     while (ok && __any_sync(~0u, walk.next(s))) {
       const int cnt = __shfl_sync(~0u, s.t1 - s.t0, 0);
-      // place of K(i) and V(i) in the ring's order
-      const auto k_seq = [&](int i) { return seq0 + (i == 0 ? 0u : 2u * i - 1u); };
-      const auto v_seq = [&](int i) { return seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u); };
       // S of stream x from the keys in slot sl (one lane): 16 values further
       // is 32 bytes (2 in the descriptor) in a swizzled row, or the next 64
       // columns
@@ -766,7 +739,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       // (none: j >= cnt).  The ring's barriers are waited for before the
       // stream's P, which is the last to be ready.
       const auto step = [&](int i, int j, int x, bool first, bool ring, bool last) {
-        const uint32_t nv = v_seq(i), nk = k_seq(j);
+        const uint32_t nv = seq0 + v_place(i, cnt), nk = seq0 + k_place(j);
         const uint32_t sv = nv % SLOTS, sk = nk % SLOTS;
         if (ring) {
           wait(&full[sv], (nv / SLOTS) & 1u);
@@ -788,7 +761,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         __syncwarp();
       };
       const auto begin = [&](int i, int x, bool ring, bool last) {
-        const uint32_t nk = k_seq(i), sk = nk % SLOTS;
+        const uint32_t nk = seq0 + k_place(i), sk = nk % SLOTS;
         if (ring) wait(&full[sk], (nk / SLOTS) & 1u);
         if (ok && elect_one()) issue_s(sk, x, last);
         __syncwarp();
@@ -961,7 +934,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (edge && (MODE == KEYS || x == 0)) {
           // values past the last token count as zero, and so does a non-finite
           // value of a new token here (added at the item's end)
-          const uint32_t n = seq0 + (i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u);
+          const uint32_t n = seq0 + v_place(i, cnt);
           wait(&full[n % SLOTS], (n / SLOTS) & 1u);
           if (!ok) break;
           uint8_t* vt = ring + (n % SLOTS) * C::SLOT;
@@ -1224,8 +1197,9 @@ struct Choice {
   int rt, ctas;
 };
 Choice choose(int64_t rows, int64_t D) {
-  if (rows <= 8) return {1, 0, 8, D == 256 ? 1 : 2};
-  if (rows <= 16) return {2, 0, 16, D == 256 ? 1 : 2};
+  const int ctas = D == 256 ? 1 : 2;
+  if (rows <= 8) return {1, 0, 8, ctas};
+  if (rows <= 16) return {2, 0, 16, ctas};
   if (D == 256) return {0, COLS, 128, 1};
   return rows <= 128 ? Choice{0, KEYS, 128, 1} : Choice{0, ROWS, 256, 1};
 }
@@ -1263,7 +1237,7 @@ cudaError_t launch_rows(const TreeAttnCall& call, Args a, cudaStream_t st) {
   CUtensorMap tk, tv;
   e = set_up(call, TK, grid, C::RT, a, tk, tv);
   if (e != cudaSuccess) return e;
-  e = launch(attn_rows_kernel<BF16, D, NT>, dim3(grid), dim3(THREADS), C::SMEM, st, tk, tv, a);
+  e = launch(attn_rows_kernel<BF16, D, NT>, dim3(grid), dim3(C::THREADS), C::SMEM, st, tk, tv, a);
   if (e != cudaSuccess) return e;
   return launch_join<BF16, D>(a, grid, C::RT, st);
 }
