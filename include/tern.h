@@ -632,7 +632,11 @@ tern_status tern_kv_commit(const tern_kv_cache* caches, int64_t layers, const in
  *   max_new    the most new tokens any request may have, known on the host; it
  *              chooses the kernel's tile
  *   out        [T][Hq][D], dense;  lse  float [T][Hq] or NULL
- *   ws         tern_tree_attention_workspace_bytes(), any contents
+ *   ws         tern_tree_attention_workspace_bytes() bytes, of which the first
+ *              TERN_TREE_ATTENTION_ZERO_BYTES are zero before the first call
+ *              (tern_workspace_init); a call leaves them zero.  Calls that may
+ *              run at the same time need a workspace each; after a timeout
+ *              (tern_check) the bytes must be zeroed again
  * A row that sees nothing (or only scores of -infinity) has out = 0 and
  * lse = -infinity.  What a row does not see has no influence on it: masked
  * keys and values may hold infinities or NaN, and the cache past a request's
@@ -641,6 +645,7 @@ tern_status tern_kv_commit(const tern_kv_cache* caches, int64_t layers, const in
  * Requirements: Hq a multiple of H; 0 <= B <= 65536;
  * T * Hq * D < 2^34; max_new <= 256, and mask_words <= 4; 1 <= H <= 65535;
  * table_width * P < 2^31. */
+#define TERN_TREE_ATTENTION_ZERO_BYTES 8192
 size_t tern_tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D);
 tern_status tern_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                 const tern_kv_cache* cache, const int32_t* table,

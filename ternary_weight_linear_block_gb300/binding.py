@@ -37,6 +37,7 @@ TERN_FWHT_F16 = 3
 TERN_FWHT_I8H = 4
 TERN_KV_BF16 = 0
 TERN_KV_F16 = 1
+TERN_TREE_ATTENTION_ZERO_BYTES = 8192
 TERN_OP_GEMV = 1
 TERN_OP_GEMM = 2
 TERN_OP_GEMM_PACKED = 3
@@ -138,7 +139,7 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:       # the handle itself: building a Stream object costs more than a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
@@ -247,8 +248,9 @@ def tern_quant_rotated(xr, m, k, mode, out, out_scale, stream=None):
 def tern_check(stream=None):
     """Synchronise and report bounded-wait timeouts.  After a timeout the
     decode GEMV may have left published partial sums (nonzero words) in its
-    workspace, so every live ``Workspace`` is marked dirty (its next ``get``
-    zero-fills it again)."""
+    workspace, and the tree attention counts of arrived pieces, so every live
+    ``Workspace`` is marked dirty (its next ``get`` or ``head`` zero-fills it
+    again)."""
     st = lib().tern_check(_stream(stream))
     if st == TERN_ERR_TIMEOUT:
         for w in list(_WORKSPACES):
@@ -432,6 +434,16 @@ class Workspace:
         if self.clean < nbytes:
             tern_workspace_init(self.buf, self.buf.numel(), stream)
             self.clean = self.buf.numel()
+        return self.buf
+
+    def head(self, nbytes: int, zero: int, stream=None) -> torch.Tensor:
+        """The buffer of at least ``nbytes`` bytes whose first ``zero`` bytes are
+        zero and stay so, for tern_tree_attention (which leaves partial sums
+        behind them)."""
+        self._ensure(nbytes)
+        if self.clean < zero:
+            tern_workspace_init(self.buf, zero, stream)
+        self.clean = zero
         return self.buf
 
     def scratch(self, nbytes: int, stream=None) -> torch.Tensor:

@@ -88,6 +88,7 @@ constexpr int NW = 4;              // warps that share a tile's keys, 16 each
 template <int D, int NT>
 struct Rows {
   static constexpr int RT = 8 * NT;
+  static constexpr int PAD = D == 64 ? 4 : 3;             // an item's cost beside its tiles
   static constexpr int THREADS = (NW + 2) * 32;           // and a producer each of K and V
   static constexpr int STAGE = 2 * TK * D * 2;            // keys and values of a tile
   static constexpr int CTAS = D < 256 ? 2 : 1;            // per SM
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   __shared__ PieceScratch<THREADS> scratch;
   __shared__ float2 s_ml[NW][RT];
   __shared__ unsigned int s_bad[8];     // new tokens with a non-finite value, by index
-  __shared__ int s_any_bad;
+  __shared__ int s_any_bad, s_last;
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -170,10 +171,9 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   }
   pdl_wait();
   pdl_launch_dependents();
-  const Piece piece = find_piece<TK, RT, THREADS>(a, scratch);   // synchronises the CTA
-  if (tid == 0) a.join[blockIdx.x].follow = 0;
+  const Piece piece = find_piece<TK, RT, C::PAD, THREADS>(a, scratch);   // synchronises the CTA
   if (piece.lo >= piece.hi) return;
-  Walk<TK, RT> walk(a, piece);
+  Walk<TK, RT, C::PAD> walk(a, piece);
   Seg s{};
 
   if (warp >= NW) {
@@ -262,20 +262,28 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       l[n][0] = l[n][1] = 0.f;
     }
 
+    int tok[NT][2];            // of this lane's score rows: the new token, its mask's first word
+    uint64_t word0[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + n * 8 + row_c + e;
+        tok[n][e] = r < rows_all ? r / a.group : 0;
+        word0[n][e] = first_word(a, a.mask + (s.r.row0 + int64_t(tok[n][e])) * a.mask_words);
+      }
+
     for (int t = s.t0; t < s.t1; ++t) {
       const int k0 = t * TK + warp * 16;         // this warp's first key
       const bool edge = k0 + 16 > s.r.ctx;     // new tokens, or past the last
       uint32_t vis[NT][2];
-      if (edge) {                              // read while the tile is on its way
+      if (edge) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = r0 + n * 8 + row_c + e;
-            const int tok = r < rows_all ? r / a.group : 0;
-            vis[n][e] = sees_bits<16>(a, a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words
-                                                    : nullptr, tok, k0, s.r);
-          }
+          for (int e = 0; e < 2; ++e)
+            vis[n][e] = sees_bits<16>(a, a.mask + (s.r.row0 + int64_t(tok[n][e])) * a.mask_words,
+                                      word0[n][e], tok[n][e], k0, s.r);
       }
       // a warp whose wait gave up reads no more tiles, but still meets the
       // others at the barriers below
@@ -286,41 +294,6 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       if (!ok) break;
       const uint32_t kbase = ring_u + st * C::STAGE;
       const uint32_t vbase = kbase + HALVES * HB;
-      if (edge) {
-        // values past the last token count as zero, and so does a non-finite
-        // value of a new token here: it is added at the item's end, to the
-        // rows that see that token
-        uint8_t* vw = ring + st * C::STAGE + HALVES * HB;
-#pragma unroll 4
-        for (int i = lane; i < 16 * (D / 8); i += 32) {
-          const int kr = warp * 16 + i / (D / 8), c = i % (D / 8);
-          uint4* at = reinterpret_cast<uint4*>(vw + (c >> 3) * HB + kr * 128 +
-                                               (((c & 7) ^ (kr & 7)) << 4));
-          const int j = t * TK + kr;
-          if (j >= s.r.len) {
-            *at = make_uint4(0, 0, 0, 0);
-          } else if (j >= s.r.ctx) {
-            uint4 x = *at;
-            uint32_t bad = 0;
-            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t b = nonfinite2<BF16>(xw[e]);
-              if (b & 1) xw[e] &= 0xFFFF0000u;
-              if (b & 2) xw[e] &= 0x0000FFFFu;
-              bad |= b;
-            }
-            if (bad) {
-              *at = x;
-              const int jj = j - s.r.ctx;
-              if (jj < 256) atomicOr(&s_bad[jj >> 5], 1u << (jj & 31));
-              s_any_bad = 1;
-            }
-          }
-        }
-        ptx::fence_proxy_async_smem();   // before the ring's next copy into this place
-        __syncwarp();
-      }
       float c[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
@@ -378,6 +351,28 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         uint32_t x[4];
         const int chunk = (i & 3) * 2 + v_chunk;
         ldsm_x4_t(vbase + (i >> 2) * HB + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), x);
+        if (edge) {
+          // values past the last token count as zero, and so does a non-finite
+          // value of a new token here: it is added at the item's end, to the
+          // rows that see that token
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = k0 + (e >> 1) * 8 + (lane & 3) * 2;      // keys j, j + 1
+            if (j >= s.r.len) x[e] = 0;
+            if (j + 1 >= s.r.len) x[e] &= 0x0000FFFFu;
+            const uint32_t b = nonfinite2<BF16>(x[e]);
+            if (b != 0) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int jj = j + h - s.r.ctx;
+                if (!((b >> h) & 1) || jj < 0) continue;           // a cached key's stays
+                x[e] &= h == 0 ? 0xFFFF0000u : 0x0000FFFFu;
+                if (jj < 256) atomicOr(&s_bad[jj >> 5], 1u << (jj & 31));
+                s_any_bad = 1;
+              }
+            }
+          }
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma16816<BF16>(o[i][n], x, p[n][0], p[n][1]);
       }
@@ -437,8 +432,9 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         ptx::named_sync(1, NW * 32);
       }
       // ---- write: thread -> 4 consecutive values of a row
-      for (int i = tid; i < rows * (C::COLS / 4); i += NW * 32) {
-        const int r = i / (C::COLS / 4), dc = (i % (C::COLS / 4)) * 4, d = c0 + dc;
+      for (int i = tid; i < RT * (C::COLS / 4); i += NW * 32) {
+        const int r = i % RT, dc = i / RT * 4, d = c0 + dc;
+        if (r >= rows) continue;
         float4 x = *reinterpret_cast<const float4*>(merge + r * C::LD + dc);
         const float4 y = *reinterpret_cast<const float4*>(merge + (RT + r) * C::LD + dc);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
@@ -473,18 +469,15 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
           if (d == 0 && a.lse != nullptr)
             a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
         } else {
-          *reinterpret_cast<float4*>(a.part_o + (slot * RT + r) * D + d) = x;
+          *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + d / 4) * RT + r) * 4) = x;
           if (d == 0) a.part_ml[slot * RT + r] = make_float2(mm, ll);
         }
       }
     }
-    if (!whole && s.t0 == 0 && tid == 0) {
-      Join* j = a.join + blockIdx.x;
-      j->row0 = s.r.row0;
-      j->r0 = r0;
-      j->rows = rows;
-      j->head = s.h;
-      j->follow = cta_of(piece, s.end - 1) - static_cast<int>(blockIdx.x);
+    if (!whole) {
+      const int first = cta_of(piece, s.first);
+      join_piece<BF16, D, RT, NW * 32>(
+          a, Item{first, cta_of(piece, s.end - 1) - first, s.r.row0, r0, rows, s.h}, tid, &s_last);
     }
     ptx::named_sync(1, NW * 32);   // s_ml, merge and s_bad are free again
     if (any_bad) {
@@ -523,6 +516,7 @@ template <int D, int MODE>
 struct Tile {
   static constexpr int TKT = D == 256 ? 64 : 128;        // keys of a tile
   static constexpr int RT = MODE == ROWS ? 256 : 128;
+  static constexpr int PAD = D == 64 ? 3 : 2;            // an item's cost beside its tiles
   static constexpr int SLOT = TKT * D * 2;
   static constexpr int QB = 128 * D * 2;                 // one Q tile
   static constexpr int QBYTES = MODE == ROWS ? 2 * QB : QB;
@@ -627,7 +621,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sq = ring + SLOTS * C::SLOT;
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, o_full, done, s_full[2], p_full[2];
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, q_empty, o_full, done, s_full[2], p_full[2];
   __shared__ PieceScratch<TILE_THREADS> scratch;
   __shared__ float2 s_ml[2][128];
   __shared__ unsigned int s_bad[8];
@@ -642,7 +636,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
-    ptx::mbar_init(&q_full, 8);
+    ptx::mbar_init(&q_full, 1);
+    ptx::mbar_init(&q_empty, 1);
     ptx::mbar_init(&o_full, 1);
     ptx::mbar_init(&done, 1);
     for (int x = 0; x < 2; ++x) {
@@ -663,11 +658,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   ptx::tc_fence_before();
   pdl_wait();
   pdl_launch_dependents();
-  const Piece piece = find_piece<TKT, RT, TILE_THREADS>(a, scratch);   // synchronises the CTA
+  const Piece piece = find_piece<TKT, RT, C::PAD, TILE_THREADS>(a, scratch);   // synchronises the CTA
   ptx::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  if (tid == 0) a.join[blockIdx.x].follow = 0;
-  Walk<TKT, RT> walk(a, piece);
+  if (tid == 128) a.items[blockIdx.x].follow = 0;   // the thread that may set it below
+  Walk<TKT, RT, C::PAD> walk(a, piece);
   Seg s{};
 
   if (warp == 0 || warp == 3) {
@@ -725,7 +720,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       // S of stream x from the keys in slot sl (one lane): 16 values further
       // is 32 bytes (2 in the descriptor) in a swizzled row, or the next 64
       // columns
-      const auto issue_s = [&](uint32_t sl, int x, bool last) {
+      const auto issue_s = [&](uint32_t sl, int i, int x, bool last) {
         const uint64_t da = q_desc + (MODE == ROWS ? x * (C::QB >> 4) : 0);
         const uint64_t db = k_desc + sl * (C::SLOT >> 4);
 #pragma unroll
@@ -734,6 +729,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                           db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
         if (last) ptx::mma_commit(&empty[sl]);
         ptx::mma_commit(&s_full[x]);
+        if (last && i == cnt - 1) ptx::mma_commit(&q_empty);   // the item's queries were read
       };
       // one stream's step: out += P V of tile i, then S of its next tile j
       // (none: j >= cnt).  The ring's barriers are waited for before the
@@ -756,14 +752,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                             dv + k * (2048 >> 4), idesc<BF16>(DV, true),
                             (!first || k > 0) ? 1u : 0u);
           if (last) ptx::mma_commit(&empty[sv]);
-          if (j < cnt) issue_s(sk, x, last);
+          if (j < cnt) issue_s(sk, j, x, last);
         }
         __syncwarp();
       };
       const auto begin = [&](int i, int x, bool ring, bool last) {
         const uint32_t nk = seq0 + k_place(i), sk = nk % SLOTS;
         if (ring) wait(&full[sk], (nk / SLOTS) & 1u);
-        if (ok && elect_one()) issue_s(sk, x, last);
+        if (ok && elect_one()) issue_s(sk, i, x, last);
         __syncwarp();
       };
       wait(&q_full, q_phase);
@@ -791,6 +787,47 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     if (elect_one()) ptx::mma_commit(&done);
     __syncwarp();
     if (!ptx::mbar_wait_bounded(&done, 0, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
+  } else if (warp == 2) {
+    // ---------------- queries: an item's rows, swizzled as TMA would, as soon
+    // as the item before needs its own no more.  Rows past the item's last
+    // keep what was there: they reach only their own rows of S.
+    bool ok = true;
+    uint32_t parity = 1;
+    while (ok && walk.next(s)) {
+      const int r0 = s.rt * RT;
+      const int rows = min(RT, s.r.n * a.group - r0);
+      ok = ptx::mbar_wait_warp(&q_empty, parity, abort_flag, WAIT_LIMIT);
+      if (!ok) {
+        if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
+        break;
+      }
+      parity ^= 1u;
+      const auto place = [&](int i) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        return sq + (r >> 7) * C::QB + (c >> 3) * (128 * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
+      };
+#pragma unroll 4
+      for (int i = lane; i < rows * (D / 8); i += 32) {
+        const int g = r0 + i / (D / 8);
+        const int token = g / a.group;
+        const uint16_t* q = a.q + (s.r.row0 + int64_t(token)) * a.q_token +
+                            int64_t(s.h * a.group + (g - token * a.group)) * a.q_head + i % (D / 8) * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(place(i))),
+                     "l"(q)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (a.scale_log2 < 0.f)    // the softmax takes the scale's absolute value
+        for (int i = lane; i < rows * (D / 8); i += 32) {
+          uint4* at = reinterpret_cast<uint4*>(place(i));
+          const uint4 v = *at;
+          constexpr uint32_t F = 0x80008000u;
+          *at = make_uint4(v.x ^ F, v.y ^ F, v.z ^ F, v.w ^ F);
+        }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&q_full);
+    }
   } else if (warp >= 4) {
     // ---------------- softmax and output: warpgroup x has stream x, a thread
     // one row of it
@@ -801,9 +838,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t o_addr = tmem + C::O_COL + 128 * x + lane_addr;
     const int wid = tid - 128;                         // 0 .. 255
     // the maximum is taken of the products themselves, so the scale must not
-    // be negative (the queries' signs are turned instead) nor zero
+    // be negative (the queries' signs are turned as they are loaded) nor zero
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -817,30 +853,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       const int r0 = s.rt * RT;
       const int rows = min(RT, rows_all - r0);
       const int cnt = s.t1 - s.t0;
-      // the item's query rows, swizzled as TMA would; rows past the last are zero
-      constexpr int QROWS = MODE == ROWS ? 256 : 128;
-#pragma unroll 4
-      for (int i = wid; i < QROWS * (D / 8); i += 256) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const int g = r0 + r;
-          v = *reinterpret_cast<const uint4*>(
-              a.q + (s.r.row0 + int64_t(g / a.group)) * a.q_token +
-              int64_t(s.h * a.group + g % a.group) * a.q_head + c * 8);
-          v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
-        }
-        *reinterpret_cast<uint4*>(sq + (r >> 7) * C::QB + (c >> 3) * (128 * 128) + (r & 127) * 128 +
-                                  (((c & 7) ^ (r & 7)) << 4)) = v;
-      }
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&q_full);
-
       const int my = (MODE == ROWS ? 128 * x : 0) + lrow;      // row of the item
       const bool active = (MODE == ROWS ? 128 * x : 0) + (warp & 3) * 32 < rows;
       const int tok = my < rows ? (r0 + my) / a.group : 0;
       const uint64_t* mw = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words : nullptr;
+      const uint64_t word0 = first_word(a, mw);
       float m = -INFINITY, l = 0.f;
       bool any = false;
       for (int i = MODE == KEYS ? x : 0; i < cnt; i += MODE == KEYS ? 2 : 1) {
@@ -849,7 +866,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         uint32_t vis[TKT / 32];
         if (edge && active) {
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c) vis[c] = sees_bits<32>(a, mw, tok, k0 + 32 * c, s.r);
+          for (int c = 0; c < TKT / 32; ++c) vis[c] = sees_bits<32>(a, mw, word0, tok, k0 + 32 * c, s.r);
         }
         wait(&s_full[x], s_phase);
         s_phase ^= 1u;
@@ -1049,10 +1066,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 *reinterpret_cast<uint4*>(a.out + at * D + d + 8 * e) = w;
               }
             } else {
-              float* po = a.part_o + (slot * RT + my) * D + d;
+              float* po = a.part_o + ((slot * (D / 4) + d / 4) * RT + my) * 4;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<float4*>(po + 4 * e) =
+                *reinterpret_cast<float4*>(po + 4 * RT * e) =
                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
           }
@@ -1065,15 +1082,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
       }
       if (!whole && s.t0 == 0 && wid == 0) {
-        Join* j = a.join + blockIdx.x;
-        j->row0 = s.r.row0;
-        j->r0 = r0;
-        j->rows = rows;
-        j->head = s.h;
-        j->follow = cta_of(piece, s.end - 1) - static_cast<int>(blockIdx.x);
+        const int first = static_cast<int>(blockIdx.x);
+        a.items[first] = Item{first, cta_of(piece, s.end - 1) - first, s.r.row0, r0, rows, s.h};
       }
       ptx::tc_fence_before();
-      ptx::named_sync(1, 256);   // accumulators, Q, s_ml and s_bad are free again
+      ptx::named_sync(1, 256);   // accumulators, s_ml and s_bad are free again
       if (any_bad) {
         if (wid < 8) s_bad[wid] = 0;
         if (wid == 0) s_any_bad = 0;
@@ -1089,50 +1102,87 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 
 // ------------------------------------------------------------------ join
 //
-// One warp a row: its pieces' (m, l) give the factors, then the pieces'
-// outputs are added in the order of the keys.
-constexpr int JOIN_WARPS = 4;
+// The items that several CTAs of the tile kernel share, a thread for each
+// (row, 4 columns) place, rows first as the pieces are stored.  Hundreds of
+// pieces (one long context on one key head) would be read one after another
+// that way, so from JOIN_GROUPS pieces on a place has that many threads, each
+// with a running sum over every JOIN_GROUPS-th piece, which are added in
+// order.  The blocks share the passes of all items (each adds up for itself
+// where they lie), because a few items with many pieces and many with few
+// would otherwise leave most blocks without work.  Bound by the launch and
+// three round trips to L2, with many rows by L2's rate.
+constexpr int JOIN_THREADS = 256, JOIN_GROUPS = 8;
+// Room for the arrival counters of this many CTAs (two an SM).
+constexpr int MAX_GRID = TERN_TREE_ATTENTION_ZERO_BYTES / (3 * sizeof(int));
 
 template <bool BF16, int D>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) combine_kernel(const Args a, int rt) {
+__global__ void __launch_bounds__(JOIN_THREADS) combine_kernel(const Args a, int rt, int ctas) {
+  __shared__ float4 s_o[JOIN_THREADS];
+  __shared__ float2 s_ml[JOIN_THREADS];
+  __shared__ int s_first[MAX_GRID + 1];     // passes before each CTA's item
+  __shared__ int s_warp[JOIN_THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const auto groups_of = [](int follow) { return follow + 1 < JOIN_GROUPS ? 1 : JOIN_GROUPS; };
   pdl_wait();
   pdl_launch_dependents();
-  const Join j = a.join[blockIdx.x];
-  const int r = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (j.follow == 0 || r >= j.rows) return;
-  const int64_t c = blockIdx.x;
-  // piece i: slot 1 of CTA c, then slot 0 of CTA c + i
-  const auto slot_of = [&](int i) { return 2 * (c + i) + (i == 0 ? 1 : 0); };
-  float mm = -INFINITY;
-  for (int i = lane; i <= j.follow; i += 32) mm = fmaxf(mm, a.part_ml[slot_of(i) * rt + r].x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, d));
-  constexpr int V = D / 32;
-  float x[V] = {};
-  float ll = 0.f;
-#pragma unroll 4
-  for (int i = 0; i <= j.follow; ++i) {
-    const int64_t at = slot_of(i) * rt + r;
-    const float2 ml = a.part_ml[at];
-    const float f = mm == -INFINITY ? 0.f : ex2(ml.x - mm);
-    ll += ml.y * f;
-    const float* o = a.part_o + at * D + lane * V;
-#pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(o + e);
-      x[e] += v.x * f;
-      x[e + 1] += v.y * f;
+  int total = 0;
+  for (int base = 0; base < ctas; base += JOIN_THREADS) {
+    int n = 0;
+    if (base + tid < ctas) {
+      const int follow = a.items[base + tid].follow;
+      const int width = JOIN_THREADS / groups_of(follow);
+      if (follow > 0) n = (a.items[base + tid].rows * (D / 4) + width - 1) / width;
     }
-  }
-  const float inv = ll == 0.f ? 0.f : 1.f / ll;
-  const int token = (j.r0 + r) / a.group, head = j.head * a.group + (j.r0 + r) % a.group;
-  const int64_t at = (int64_t(j.row0) + token) * a.Hq + head;
+    int x = n;
 #pragma unroll
-  for (int e = 0; e < V; e += 2)
-    *reinterpret_cast<uint32_t*>(a.out + at * D + lane * V + e) =
-        pack2<BF16>(x[e] * inv, x[e + 1] * inv);
-  if (lane == 0 && a.lse != nullptr)
-    a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(~0u, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) s_warp[tid >> 5] = x;
+    __syncthreads();
+    int below = total;
+    for (int w = 0; w < JOIN_THREADS / 32; ++w) {
+      if (w < (tid >> 5)) below += s_warp[w];
+      total += s_warp[w];
+    }
+    if (base + tid < ctas) s_first[base + tid] = below + x - n;
+    __syncthreads();
+  }
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    int lo = 0, hi = ctas;                   // the last CTA with s_first <= u has pass u
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_first[mid] <= u) lo = mid; else hi = mid;
+    }
+    const Item it = a.items[lo];
+    const int groups = groups_of(it.follow), width = JOIN_THREADS / groups;
+    const int p = tid % width, g = tid / width;
+    const int place = (u - s_first[lo]) * width + p;
+    const bool in = place < it.rows * (D / 4);
+    const int d4 = place / it.rows, r = place - d4 * it.rows;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+      // piece i: slot 1 of CTA `first`, then slot 0 of CTA first + i
+#pragma unroll 4
+      for (int i = g; i <= it.follow; i += groups) {
+        const int64_t slot = 2 * (int64_t(it.first) + i) + (i == 0 ? 1 : 0);
+        add_piece(m, l, o, a.part_ml[slot * rt + r],
+                  *reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + d4) * rt + r) * 4));
+      }
+    }
+    if (groups > 1) {
+      s_o[tid] = o;
+      s_ml[tid] = make_float2(m, l);
+      __syncthreads();
+      if (g == 0)
+        for (int i = 1; i < JOIN_GROUPS; ++i)
+          add_piece(m, l, o, s_ml[i * width + p], s_o[i * width + p]);
+    }
+    if (g == 0 && in) write_joined<BF16, D>(a, it, r, d4, m, l, o);
+    if (groups > 1) __syncthreads();
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -1177,15 +1227,17 @@ bool make_map(CUtensorMap* map, const tern_kv_cache& c, void* base, int rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The workspace: arrival counters, which are zero between calls, then the
+// pieces.
 struct Ws {
-  size_t o, ml, join, bytes;
+  size_t o, ml, items, bytes;
 };
 Ws ws_layout(int64_t grid, int64_t rt, int64_t D) {
   Ws w;
-  w.o = 0;
+  w.o = TERN_TREE_ATTENTION_ZERO_BYTES;
   w.ml = w.o + static_cast<size_t>(2 * grid * rt * D) * sizeof(float);
-  w.join = w.ml + static_cast<size_t>(2 * grid * rt) * sizeof(float2);
-  w.bytes = w.join + static_cast<size_t>(grid) * sizeof(Join);
+  w.items = w.ml + static_cast<size_t>(4 * grid * rt) * sizeof(float2);
+  w.bytes = w.items + static_cast<size_t>(grid) * sizeof(Item);
   return w;
 }
 
@@ -1213,14 +1265,9 @@ cudaError_t set_up(const TreeAttnCall& call, int keys, int grid, int rt, Args& a
   uint8_t* ws = static_cast<uint8_t*>(call.ws);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.join = reinterpret_cast<Join*>(ws + w.join);
+  a.arrived = reinterpret_cast<int*>(ws);
+  a.items = reinterpret_cast<Item*>(ws + w.items);
   return cudaSuccess;
-}
-
-template <bool BF16, int D>
-cudaError_t launch_join(const Args& a, int grid, int rt, cudaStream_t st) {
-  return launch(combine_kernel<BF16, D>, dim3(grid, (rt + JOIN_WARPS - 1) / JOIN_WARPS),
-                dim3(JOIN_WARPS * 32), 0, st, a, rt);
 }
 
 template <bool BF16, int D, int NT>
@@ -1233,13 +1280,11 @@ cudaError_t launch_rows(const TreeAttnCall& call, Args a, cudaStream_t st) {
                                 static_cast<int>(C::SMEM));
   });
   if (e != cudaSuccess) return e;
-  const int grid = kv_sm_count() * C::CTAS;
+  const int grid = std::min(kv_sm_count() * C::CTAS, MAX_GRID);
   CUtensorMap tk, tv;
   e = set_up(call, TK, grid, C::RT, a, tk, tv);
   if (e != cudaSuccess) return e;
-  e = launch(attn_rows_kernel<BF16, D, NT>, dim3(grid), dim3(C::THREADS), C::SMEM, st, tk, tv, a);
-  if (e != cudaSuccess) return e;
-  return launch_join<BF16, D>(a, grid, C::RT, st);
+  return launch(attn_rows_kernel<BF16, D, NT>, dim3(grid), dim3(C::THREADS), C::SMEM, st, tk, tv, a);
 }
 
 template <bool BF16, int D, int MODE>
@@ -1252,13 +1297,14 @@ cudaError_t launch_tile(const TreeAttnCall& call, Args a, cudaStream_t st) {
                                 static_cast<int>(C::SMEM));
   });
   if (e != cudaSuccess) return e;
-  const int grid = kv_sm_count();
+  const int grid = std::min(kv_sm_count(), MAX_GRID);
   CUtensorMap tk, tv;
   e = set_up(call, C::TKT, grid, C::RT, a, tk, tv);
   if (e != cudaSuccess) return e;
   e = launch(attn_tile_kernel<BF16, D, MODE>, dim3(grid), dim3(TILE_THREADS), C::SMEM, st, tk, tv, a);
   if (e != cudaSuccess) return e;
-  return launch_join<BF16, D>(a, grid, C::RT, st);
+  return launch(combine_kernel<BF16, D>, dim3(4 * kv_sm_count()), dim3(JOIN_THREADS), 0, st, a, C::RT,
+                grid);
 }
 
 template <bool BF16, int D>
@@ -1278,7 +1324,7 @@ cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st)
 
 size_t tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
   const Choice c = choose(max_new * (Hq / H), D);
-  return ws_layout(int64_t(kv_sm_count()) * c.ctas, c.rt, D).bytes;
+  return ws_layout(std::min(kv_sm_count() * c.ctas, MAX_GRID), c.rt, D).bytes;
 }
 
 cudaError_t launch_tree_attention(const TreeAttnCall& call, cudaStream_t st) {

@@ -5,11 +5,14 @@
 // tiles of RT rows (a row is a new token with one of the `group` query heads
 // of a key head) and `tiles` key tiles; an item is one (row tile, key head)
 // of a request, and the items' tiles in order form one line, of which each
-// CTA takes an equal piece.  So a single long context uses every SM and
+// CTA takes an equal piece.  An item counts PAD tiles more than it has, for
+// what it costs beside its tiles (queries, masks, output), so that a CTA with
+// many short items has as long as one with a long one.  So a single long context uses every SM and
 // uneven contexts balance without the host knowing the lengths; a CTA's
 // piece begins and ends inside an item at most once each, and those partial
 // results (running maximum, sum and unnormalised output) go to the
-// workspace, where combine_kernel joins them.
+// workspace, where they are joined: by the last of the item's CTAs to arrive
+// (join_piece, few rows) or by a second kernel (combine_kernel, many).
 #pragma once
 
 #include <cuda.h>
@@ -32,30 +35,26 @@ struct Args {
   const int32_t* ctx_len;
   const int32_t* row_start;
   const uint64_t* mask;
-  float* part_o;            // [2 grid][RT][D] unnormalised outputs
-  float2* part_ml;          // [2 grid][RT] (maximum, sum), base 2
-  struct Join* join;        // [grid]
+  float* part_o;            // [2 grid][D / 4][RT][4] unnormalised outputs
+  float2* part_ml;          // [2 grid pieces, 2 grid sums][RT] (maximum, sum), base 2
+  int* arrived;             // [3 grid] pieces that have arrived, 0 between calls
+  struct Item* items;       // [grid] the item that each CTA's piece begins but does not end
   int64_t q_token, q_head, table_stride;
   int64_t page_stride, token_stride, head_stride;
   int width, pages, page_shift, mask_words, B, T, H, group, Hq;
   float scale_log2;
 };
 
-// What a CTA leaves to be joined: the item that its piece begins but does
-// not end (slot 1 of this CTA, then slot 0 of the next `follow` CTAs).
-struct Join {
-  int follow;   // 0: nothing
-  int row0;     // first row of the request
-  int r0;       // first row of the row tile
-  int rows;     // its rows
-  int head;     // key head
-  int pad[3];
-};
-
 // One request.
 struct Req {
   int ctx, n, row0, len, tiles, rts;
 };
+
+// Tiles that an item counts for.
+template <int PAD>
+__device__ __forceinline__ int64_t line_of(const Args& a, const Req& r) {
+  return r.n > 0 ? int64_t(a.H) * r.rts * (r.tiles + PAD) : 0;
+}
 
 template <int TK, int RT>
 __device__ __forceinline__ Req load_req(const Args& a, int b) {
@@ -68,8 +67,14 @@ __device__ __forceinline__ Req load_req(const Args& a, int b) {
   r.ctx = min(max(a.ctx_len[b], 0), cap);
   r.len = static_cast<int>(min(int64_t(r.ctx) + r.n, int64_t(cap)));
   r.tiles = r.n > 0 ? max((r.len + TK - 1) / TK, 1) : 0;
-  r.rts = static_cast<int>((int64_t(r.n) * a.group + RT - 1) / RT);
+  r.rts = static_cast<int>((uint32_t(r.n) * uint32_t(a.group) + RT - 1) / RT);   // below 2^28 rows
   return r;
+}
+
+// a / b of numbers that are not negative; two of 32 bits are the usual case and
+// cost a fifth of a 64-bit division.
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
 // A CTA's piece [lo, hi) of the line of tiles, and the request where it
@@ -90,7 +95,7 @@ struct PieceScratch {
 };
 
 // Every thread of a CTA of NT threads (it synchronises them).
-template <int TK, int RT, int NT>
+template <int TK, int RT, int PAD, int NT>
 __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = NT / 32;
@@ -103,7 +108,7 @@ __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) 
     mine = 0;
     if (b < a.B) {
       r = load_req<TK, RT>(a, b);
-      mine = int64_t(a.H) * r.rts * r.tiles;
+      mine = line_of<PAD>(a, r);
     }
     int64_t x = mine;
 #pragma unroll
@@ -129,8 +134,8 @@ __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) 
   p.base = 0;
   p.lo = p.hi = 0;
   if (static_cast<int>(blockIdx.x) >= p.ctas) return p;
-  p.lo = p.total * blockIdx.x / p.ctas;
-  p.hi = p.total * (blockIdx.x + 1) / p.ctas;
+  p.lo = quot(p.total * blockIdx.x, p.ctas);
+  p.hi = quot(p.total * (blockIdx.x + 1), p.ctas);
   const auto found = [&](int b) {
     if (before <= p.lo && p.lo < before + mine) {
       s.base = before;
@@ -156,18 +161,18 @@ __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) 
 
 // Last CTA whose piece touches tile x of the line.
 __device__ __forceinline__ int cta_of(const Piece& p, int64_t x) {
-  return static_cast<int>(((x + 1) * p.ctas - 1) / p.total);
+  return static_cast<int>(quot((x + 1) * p.ctas - 1, p.total));
 }
 
 // One item's part in a CTA's piece.
 struct Seg {
   Req r;
   int b, h, rt, t0, t1;   // key tiles [t0, t1)
-  int64_t end;            // first tile of the line past the item
+  int64_t first, end;     // the item's first tile on the line, and the place past its last
 };
 
 // Steps through a piece item by item.  Each role of a CTA walks on its own.
-template <int TK, int RT>
+template <int TK, int RT, int PAD>
 struct Walk {
   const Args& a;
   int64_t w, hi, base;
@@ -176,28 +181,33 @@ struct Walk {
   int64_t size;
 
   __device__ __forceinline__ Walk(const Args& args, const Piece& p)
-      : a(args), w(p.lo), hi(p.hi), base(p.base), b(p.b), r(p.r) {
-    size = int64_t(a.H) * r.rts * r.tiles;
-  }
+      : a(args), w(p.lo), hi(p.hi), base(p.base), b(p.b), r(p.r), size(line_of<PAD>(args, p.r)) {}
   __device__ __forceinline__ bool next(Seg& s) {
-    if (w >= hi) return false;
-    while (w - base >= size) {   // total covers w: a request with tiles follows
-      base += size;
-      ++b;
-      r = load_req<TK, RT>(a, b);
-      size = int64_t(a.H) * r.rts * r.tiles;
+    while (w < hi) {
+      while (w - base >= size) {   // the line covers w: a request with tiles follows
+        base += size;
+        ++b;
+        r = load_req<TK, RT>(a, b);
+        size = line_of<PAD>(a, r);
+      }
+      const int64_t off = w - base;
+      const int span = r.tiles + PAD;            // PAD places, then the tiles
+      const int64_t item = quot(off, span);
+      const int at = static_cast<int>(off - item * span);
+      const int to = static_cast<int>(min(int64_t(span), at + (hi - w)));
+      w += to - at;
+      if (to <= PAD) continue;                   // no tile of it: the next CTA begins it
+      s.r = r;
+      s.b = b;
+      s.t0 = max(at - PAD, 0);
+      s.t1 = to - PAD;
+      s.h = static_cast<int>(quot(item, r.rts));
+      s.rt = static_cast<int>(item - int64_t(s.h) * r.rts);
+      s.first = base + item * span + PAD;
+      s.end = base + (item + 1) * span;
+      return true;
     }
-    const int64_t off = w - base;
-    const int64_t item = off / r.tiles;
-    s.r = r;
-    s.b = b;
-    s.t0 = static_cast<int>(off - item * r.tiles);
-    s.t1 = static_cast<int>(min(int64_t(r.tiles), s.t0 + (hi - w)));
-    s.h = static_cast<int>(item / r.rts);
-    s.rt = static_cast<int>(item - int64_t(s.h) * r.rts);
-    s.end = base + (item + 1) * r.tiles;
-    w += s.t1 - s.t0;
-    return true;
+    return false;
   }
 };
 
@@ -208,11 +218,17 @@ __device__ __forceinline__ bool sees(const Args& a, const uint64_t* mw, int i, i
   return (j >> 6) < a.mask_words && ((mw[j >> 6] >> (j & 63)) & 1);
 }
 
+// The first word of a row's mask, which covers most trees: read with the row's
+// queries, so that the tiles of new tokens do not wait for it.
+__device__ __forceinline__ uint64_t first_word(const Args& a, const uint64_t* mw) {
+  return a.mask != nullptr ? __ldg(mw) : 0;
+}
+
 // The same for the N (16 or 32) keys from position k0 on, as bits: cached keys
 // are seen, keys past the request's last are not.
 template <int N>
-__device__ __forceinline__ uint32_t sees_bits(const Args& a, const uint64_t* mw, int i, int k0,
-                                              const Req& r) {
+__device__ __forceinline__ uint32_t sees_bits(const Args& a, const uint64_t* mw, uint64_t word0,
+                                              int i, int k0, const Req& r) {
   const int j0 = k0 - r.ctx;              // k0 as a new token, below 0: cached
   const int lo = max(j0, 0), skip = min(lo - j0, N);
   uint64_t x = 0;
@@ -222,7 +238,7 @@ __device__ __forceinline__ uint32_t sees_bits(const Args& a, const uint64_t* mw,
       x = up <= 0 ? 0 : up >= N ? 0xFFFFFFFFu : (1u << up) - 1;
     } else {
       const int w = lo >> 6, sh = lo & 63;
-      if (w < a.mask_words) x = mw[w] >> sh;
+      if (w < a.mask_words) x = (w == 0 ? word0 : mw[w]) >> sh;
       if (sh > 64 - N && w + 1 < a.mask_words) x |= mw[w + 1] << (64 - sh);
     }
   }
@@ -260,6 +276,102 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
 }
 
 constexpr float kLn2 = 0.69314718055994530942f;
+
+// ------------------------------------------------------------------ join
+//
+// out = sum 2^(m_i - m) out_i / sum 2^(m_i - m) l_i over the pieces of an item
+// that several CTAs share: slot 1 of CTA `first`, then slot 0 of the next
+// `follow` CTAs.  Each CTA stores its piece and counts itself; whoever counts
+// last adds all pieces, in the order of the keys, so the result does not
+// depend on who that was.  From JOIN_ALL pieces on they are first added in
+// groups of about their square root, by each group's last, then the groups:
+// one long context on one key head makes hundreds.  For up to 16 rows: with
+// more, adding up is work for more than one SM.
+constexpr int JOIN_ALL = 24;
+
+// An item that several CTAs share.
+struct Item {
+  int first, follow;        // CTAs: the one that begins it, and how many follow
+  int row0, r0, rows, head; // first row of the request and of the tile, its rows, key head
+};
+
+// One piece more to a running (m, l, o).
+__device__ __forceinline__ void add_piece(float& m, float& l, float4& o, float2 ml, float4 x) {
+  const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+  const float f = ex2(m - ms), e = ex2(ml.x - ms);
+  m = mn;
+  l = l * f + ml.y * e;
+  o = make_float4(o.x * f + x.x * e, o.y * f + x.y * e, o.z * f + x.z * e, o.w * f + x.w * e);
+}
+
+// Four columns of a joined row to the output.
+template <bool BF16, int D>
+__device__ __forceinline__ void write_joined(const Args& a, const Item& it, int r, int d4, float m,
+                                             float l, float4 o) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int token = (it.r0 + r) / a.group, head = it.head * a.group + (it.r0 + r) % a.group;
+  const int64_t at = (int64_t(it.row0) + token) * a.Hq + head;
+  *reinterpret_cast<uint2*>(a.out + at * D + d4 * 4) =
+      make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+  if (d4 == 0 && a.lse != nullptr)
+    a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// N threads of a CTA, one of which each has `tid` 0 .. N - 1, synchronised by
+// named barrier 1; every one has stored its part of the piece.
+template <bool BF16, int D, int RT, int N>
+__device__ __forceinline__ void join_piece(const Args& a, const Item& it, int tid, int* s_last) {
+  const int count = it.follow + 1, grid = static_cast<int>(gridDim.x);
+  const auto slot_of = [&](int i) { return 2 * (int64_t(it.first) + i) + (i == 0 ? 1 : 0); };
+  // counts one arrival; true for every thread if it was the last of `all`
+  const auto last_of = [&](int* counter, int all) {
+    __threadfence();
+    ptx::named_sync(1, N);
+    if (tid == 0) {
+      *s_last = atomicAdd(counter, 1) == all - 1;
+      if (*s_last) *counter = 0;
+      __threadfence();
+    }
+    ptx::named_sync(1, N);
+    return *reinterpret_cast<volatile int*>(s_last) != 0;
+  };
+  // pieces i0, i0 + step, .. below i1: to the output, or as the group's sum to
+  // piece i0's place.  A group's (m, l) has a place of its own, 2 grid slots
+  // on, since every column's thread reads the piece's.
+  const auto add_up = [&](int i0, int i1, int step, bool out) {
+    const int64_t sums = step > 1 ? 2 * int64_t(grid) : 0;
+    for (int p = tid; p < it.rows * (D / 4); p += N) {
+      const int d4 = p / it.rows, r = p - d4 * it.rows;
+      float m = -INFINITY, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = i0; i < i1; i += step) {
+        const int64_t slot = slot_of(i);
+        const float2 ml = __ldcg(a.part_ml + (sums + slot) * RT + r);
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + d4) * RT + r) * 4));
+        add_piece(m, l, o, ml, x);
+      }
+      if (out) {
+        write_joined<BF16, D>(a, it, r, d4, m, l, o);
+      } else {
+        const int64_t slot = slot_of(i0);
+        *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + d4) * RT + r) * 4) = o;
+        if (d4 == 0) a.part_ml[(2 * int64_t(grid) + slot) * RT + r] = make_float2(m, l);
+      }
+    }
+  };
+  if (count < JOIN_ALL) {
+    if (last_of(a.arrived + it.first, count)) add_up(0, count, 1, true);
+    return;
+  }
+  int size = 5;
+  while (size * size < count) ++size;
+  const int i0 = (static_cast<int>(blockIdx.x) - it.first) / size * size;
+  if (last_of(a.arrived + grid + slot_of(i0), min(size, count - i0))) {
+    add_up(i0, min(i0 + size, count), 1, false);
+    if (last_of(a.arrived + it.first, (count + size - 1) / size)) add_up(0, count, size, true);
+  }
+}
 
 }  // namespace attn
 }  // namespace tern

@@ -15,6 +15,8 @@ read, so a step can be captured in a CUDA graph and replayed as they change.
 
 from __future__ import annotations
 
+import ctypes
+import functools
 from typing import NamedTuple, Sequence
 
 import torch
@@ -30,25 +32,41 @@ def _check(ok: bool, what: str):
 
 
 def _ints(t: torch.Tensor, name: str, dtype=torch.int32, ndim: int = 1):
-    if not (t.is_cuda and t.dtype == dtype and t.ndim == ndim and t.is_contiguous()):
+    if not (t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous {ndim}-D CUDA tensor of {dtype}")
 
 
 def _table(t: torch.Tensor, b: int):
-    """Row stride of a block table (rows may be longer than the part in use)."""
-    if not (t.is_cuda and t.dtype == torch.int32 and t.ndim == 2 and t.shape[0] == b and
-            (t.shape[1] <= 1 or t.stride(1) == 1) and (b <= 1 or t.stride(0) >= t.shape[1])):
-        raise ValueError("table: expected an int32 CUDA tensor [requests, width], rows dense")
-    return t.stride(0) if b > 1 else max(t.shape[1], 1)
+    """Row stride and width of a block table (rows may be longer than the part in use)."""
+    if t.is_cuda and t.dtype is torch.int32 and t.dim() == 2:
+        rows, width = t.shape
+        stride, one = t.stride()
+        if rows == b and (one == 1 or width <= 1) and (stride >= width or b <= 1):
+            return (stride if b > 1 else max(width, 1)), width
+    raise ValueError("table: expected an int32 CUDA tensor [requests, width], rows dense")
 
 
 def _heads(t: torch.Tensor, heads: int, dim: int, dtype, name: str):
     """Row and head strides of [rows, heads, dim], e.g. a slice of the qkv linear's output."""
-    if not (t.is_cuda and t.dtype == dtype and t.ndim == 3 and t.shape[1] == heads and
-            t.shape[2] == dim and t.stride(2) == 1):
-        raise ValueError(f"{name}: expected a CUDA tensor [rows, {heads}, {dim}] of {dtype}, "
-                         "dense along the last axis")
-    return (t.stride(0) if t.shape[0] > 1 else heads * dim), (t.stride(1) if heads > 1 else dim)
+    if t.is_cuda and t.dtype is dtype and t.dim() == 3:
+        rows, h, d = t.shape
+        row, head, one = t.stride()
+        if h == heads and d == dim and one == 1:
+            return (row if rows > 1 else heads * dim), (head if heads > 1 else dim)
+    raise ValueError(f"{name}: expected a CUDA tensor [rows, {heads}, {dim}] of {dtype}, "
+                     "dense along the last axis")
+
+
+def _done(name: str, status: int):
+    """The entry points are called without the wrappers of ``binding``: at decode
+    sizes the wrappers would cost as much host time as the launch."""
+    if status:
+        raise B.TernError(name, status)
+
+
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int) -> int:
+    return B.tern_tree_attention_workspace_bytes(max_new, hq, heads, dim)
 
 
 def _on(stream):
@@ -77,6 +95,7 @@ class KVCache:
         self.desc = B.KVCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.page_size,
                                   self.heads, self.dim, ps, ts, hs, _TYPES[k.dtype])
         self.desc_bytes = bytes(self.desc)
+        self.address = ctypes.addressof(self.desc)
 
     @classmethod
     def empty(cls, pages: int, page_size: int, heads: int, dim: int, dtype=torch.bfloat16,
@@ -120,7 +139,7 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
     _ints(new_len, "new_len")
     _ints(free_pages, "free_pages")
     _check(new_len.shape[0] == b, "new_len: expected as many requests as ctx_len")
-    stride = _table(table, b)
+    stride, width = _table(table, b)
     if free_head is not None:
         _check(free_head.is_cuda and free_head.dtype == torch.int32 and free_head.numel() == 1,
                "free_head: expected one int32 on the GPU")
@@ -137,9 +156,13 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
             _ints(getattr(plan, name), f"plan.{name}")
         _check(plan.row_start.shape[0] == b + 1 and plan.info.shape[0] == 4 and
                all(t.shape[0] >= capacity for t in plan[1:4]), "plan: buffers too small")
-    B.tern_kv_plan(ctx_len, new_len, b, page_size, table, stride, table.shape[1], free_pages,
-                   free_pages.shape[0], free_head, plan.row_start, capacity, plan.slots,
-                   plan.positions, plan.request, plan.info, stream)
+    row_start, slots, positions, request, info = plan
+    _done("tern_kv_plan", B.lib().tern_kv_plan(
+        ctx_len.data_ptr(), new_len.data_ptr(), b, page_size, table.data_ptr(), stride, width,
+        free_pages.data_ptr(), free_pages.shape[0],
+        None if free_head is None else free_head.data_ptr(), row_start.data_ptr(), capacity,
+        slots.data_ptr(), positions.data_ptr(), request.data_ptr(), info.data_ptr(),
+        B._stream(stream)))
     return plan
 
 
@@ -150,7 +173,9 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     _ints(slots, "slots", torch.int64)
     t = k.shape[0]
     _check(v.shape[0] == t and slots.shape[0] >= t, "v, slots: expected as many rows as k")
-    B.tern_kv_write(cache.desc, k, v, kt, kh, vt, vh, slots, t, stream)
+    _done("tern_kv_write", B.lib().tern_kv_write(
+        cache.address, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), t,
+        B._stream(stream)))
 
 
 def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len: torch.Tensor,
@@ -166,42 +191,42 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
     also the logarithm of each row's sum of exponentials (fp32 [T, query heads]).
     A row that sees nothing is 0, its lse -infinity."""
     b = ctx_len.shape[0]
-    hq = q.shape[1] if q.ndim == 3 else 0
-    qt, qh = _heads(q, hq, cache.dim, cache.dtype, "q")
-    t = q.shape[0]
-    _check(hq > 0 and hq % cache.heads == 0, "q: expected a multiple of the cache's heads")
+    t, hq, _ = q.shape
+    heads, dim, dtype = cache.heads, cache.dim, cache.dtype
+    qt, qh = _heads(q, hq, dim, dtype, "q")
+    _check(hq > 0 and hq % heads == 0, "q: expected a multiple of the cache's heads")
     _ints(ctx_len, "ctx_len")
     _ints(row_start, "row_start")
     _check(row_start.shape[0] == b + 1, "row_start: expected one more entry than requests")
-    stride = _table(table, b)
+    stride, width = _table(table, b)
     words = 0
     if mask is not None:
         _ints(mask, "mask", torch.int64, 2)
-        words = mask.shape[1]
-        _check(mask.shape[0] >= t and words > 0, "mask: expected [rows, words]")
+        rows, words = mask.shape
+        _check(rows >= t and words > 0, "mask: expected [rows, words]")
     if out is not None:
-        _check(out.is_cuda and out.dtype == cache.dtype and out.shape == (t, hq, cache.dim) and
+        _check(out.is_cuda and out.dtype is dtype and out.shape == (t, hq, dim) and
                out.is_contiguous(), "out: expected a contiguous [rows, query heads, dim]")
     if lse is not None:
-        _check(lse.is_cuda and lse.dtype == torch.float32 and lse.shape == (t, hq) and
+        _check(lse.is_cuda and lse.dtype is torch.float32 and lse.shape == (t, hq) and
                lse.is_contiguous(), "lse: expected a contiguous fp32 [rows, query heads]")
-    nb = B.tern_tree_attention_workspace_bytes(max_new, hq, cache.heads, cache.dim)
-
-    def buffers():
-        return (torch.empty((t, hq, cache.dim), dtype=cache.dtype, device=q.device)
-                if out is None else out,
-                torch.empty((t, hq), dtype=torch.float32, device=q.device)
-                if return_lse and lse is None else lse,
-                (ws or B.Workspace(q.device)).scratch(nb, stream))
-    if stream is None:
-        out, lse, buf = buffers()
-    else:
-        with _on(stream):
-            out, lse, buf = buffers()
-    B.tern_tree_attention(q, qt, qh, cache.desc, table, stride, table.shape[1], ctx_len, row_start,
-                          mask, words, b, t, hq, max_new,
-                          cache.dim ** -0.5 if scale is None else scale, out, lse, buf, buf.numel(),
-                          stream)
+    if stream is not None and (out is None or ws is None or (return_lse and lse is None)):
+        with _on(stream):          # what is allocated here belongs to that stream
+            return tree_attention(q, cache, table, ctx_len, row_start, max_new, mask, scale, out,
+                                  return_lse, lse, ws)
+    if out is None:
+        out = torch.empty((t, hq, dim), dtype=dtype, device=cache.device)
+    if return_lse and lse is None:
+        lse = torch.empty((t, hq), dtype=torch.float32, device=cache.device)
+    nb = _workspace_bytes(max_new, hq, heads, dim)
+    if ws is None:
+        ws = B.Workspace(cache.device)
+    buf = ws.head(nb, B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
+    _done("tern_tree_attention", B.lib().tern_tree_attention(
+        q.data_ptr(), qt, qh, cache.address, table.data_ptr(), stride, width, ctx_len.data_ptr(),
+        row_start.data_ptr(), None if mask is None else mask.data_ptr(), words, b, t, hq, max_new,
+        dim ** -0.5 if scale is None else scale, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), B._stream(stream)))
     return (out, lse) if return_lse else out
 
 
@@ -220,18 +245,20 @@ def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len:
     _ints(path_len, "path_len")
     _ints(path, "path", torch.int32, 2)
     _check(path.shape[0] == b and path_len.shape[0] == b, "path, path_len: expected a row each request")
-    stride = _table(table, b)
+    stride, width = _table(table, b)
     if ctx_out is None:
         if stream is None:
-            ctx_out = torch.empty_like(ctx_len)
+            ctx_out = torch.empty(b, dtype=torch.int32, device=ctx_len.device)
         else:
             with _on(stream):
-                ctx_out = torch.empty_like(ctx_len)
+                ctx_out = torch.empty(b, dtype=torch.int32, device=ctx_len.device)
     else:
         _ints(ctx_out, "ctx_out")
         _check(ctx_out.shape[0] == b, "ctx_out: expected as many requests as ctx_len")
-    B.tern_kv_commit(b"".join([c.desc_bytes for c in caches]), len(caches), table, stride, table.shape[1], ctx_len, path,
-                     path.shape[1], path_len, ctx_out, b, stream)
+    _done("tern_kv_commit", B.lib().tern_kv_commit(
+        b"".join([c.desc_bytes for c in caches]), len(caches), table.data_ptr(), stride, width,
+        ctx_len.data_ptr(), path.data_ptr(), path.shape[1], path_len.data_ptr(),
+        ctx_out.data_ptr(), b, B._stream(stream)))
     return ctx_out
 
 
