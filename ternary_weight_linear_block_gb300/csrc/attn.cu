@@ -84,7 +84,7 @@ constexpr int NW = 4;              // warps that share a tile's keys, 16 each
 // NT: eights of rows in an item.  The accumulators (D / 4 * NT registers a
 // thread) and the query fragments (D / 8 * NT) decide how many CTAs an SM
 // holds, and so the ring's size.  Joining the warps takes two buffers of the
-// item's rows, `COLS` columns of them at a time where two CTAs share an SM.
+// item's rows, `COLS` columns of them at a time.
 template <int D, int NT>
 struct Rows {
   static constexpr int RT = 8 * NT;
@@ -92,15 +92,40 @@ struct Rows {
   static constexpr int THREADS = (NW + 2) * 32;           // and a producer each of K and V
   static constexpr int STAGE = 2 * TK * D * 2;            // keys and values of a tile
   static constexpr int CTAS = D < 256 ? 2 : 1;            // per SM
-  static constexpr int COLS = CTAS == 2 && D * NT == 256 ? D / 2 : D;
+  static constexpr int COLS = D * NT <= 128 || NT == 1 ? D : D / 2;
   static constexpr int LD = COLS + 4;                     // no two lanes of a store share a bank
   static constexpr int MERGE = 2 * RT * LD * 4;
-  static constexpr int ROOM = (CTAS == 2 ? 115200 : 232448) - MERGE - 1024 - 3072;
+  static constexpr int QLD = D * 2 + 16;                  // bytes of a query row
+  static constexpr int QBYTES = RT * QLD;
+  static constexpr int ROOM = (CTAS == 2 ? 115200 : 232448) - MERGE - QBYTES - 1024 - 1536;
   static constexpr int FIT = ROOM / STAGE;
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
-  static constexpr size_t SMEM = size_t(STAGES) * STAGE + MERGE + 1024;
+  static constexpr size_t SMEM = size_t(STAGES) * STAGE + MERGE + QBYTES + 1024;
   static_assert(STAGES >= 2, "ring");
 };
+
+// What the keys' producer tells the consumers of an item's part.
+struct Part {
+  int b, h, r0, rows, row0, ctx, n, len;
+  int t0, t1;             // key tiles; none: there is no further item
+  int whole, begins;      // all of the item's tiles; its first
+  int first, follow;      // CTAs that share it
+  int pad[2];
+};
+
+// Whether any of the N threads at named barrier `id` says so.
+__device__ __forceinline__ bool named_any(int id, int count, bool mine) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\n"
+      "setp.ne.u32 p, %3, 0;\n"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return r != 0;
+}
 
 // The pages of a tile of TKEYS keys: lane i has the page of its i-th box (a
 // page's part of the tile, 1 << box_shift keys); a page out of range is turned
@@ -148,7 +173,10 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   float* merge = reinterpret_cast<float*>(ring + C::STAGES * C::STAGE);
-  __shared__ uint64_t full[C::STAGES], empty[C::STAGES];
+  uint8_t* sq = ring + C::STAGES * C::STAGE + C::MERGE;
+  __shared__ uint64_t full[C::STAGES], empty[C::STAGES], q_full, q_empty;
+  __shared__ __align__(16) Part s_part;
+  __shared__ uint64_t s_word0[RT];      // of each row's mask
   __shared__ PieceScratch<THREADS> scratch;
   __shared__ float2 s_ml[NW][RT];
   __shared__ unsigned int s_bad[8];     // new tokens with a non-finite value, by index
@@ -162,6 +190,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       ptx::mbar_init(&full[s], 2);
       ptx::mbar_init(&empty[s], NW);
     }
+    ptx::mbar_init(&q_full, 1);
+    ptx::mbar_init(&q_empty, NW);
     s_abort = 0;
     s_any_bad = 0;
     for (int i = 0; i < 8; ++i) s_bad[i] = 0;
@@ -173,29 +203,58 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   pdl_launch_dependents();
   const Piece piece = find_piece<TK, RT, C::PAD, THREADS>(a, scratch);   // synchronises the CTA
   if (piece.lo >= piece.hi) return;
-  Walk<TK, RT, C::PAD> walk(a, piece);
-  Seg s{};
 
   if (warp >= NW) {
     // ---------------- producers: one warp copies the keys, one the values
     // (issued by one warp, pages of 16 rows held a long context to two thirds
-    // of its rate)
+    // of its rate).  The keys' also copies each item's queries and says what
+    // the item is, while the consumers are still at the one before: found out
+    // by themselves, that was a third of a short item's time.
     const bool vals = warp > NW;
     const CUtensorMap* map = vals ? &tm_v : &tm_k;
+    Walk<TK, RT, C::PAD> walk(a, piece);
+    Seg s{};
     int st = 0;
-    uint32_t phase = 0;
-    long issued = 0;
+    uint32_t phase = 0, q_phase = 1;
+    long issued = 0, q_issued = 0;
     bool ok = true;
     const int box_shift = min(a.page_shift, 6);      // rows of a box: a page, or the tile
+    const auto give_up = [&](bool good) {
+      if (!good && lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
+      return good;
+    };
+    // the item's description and queries, or (none) the end
+    const auto post = [&](bool item) {
+      ok = give_up(ptx::mbar_wait_warp(&q_empty, q_phase, abort_flag, WAIT_LIMIT));
+      if (!ok) return;
+      q_phase ^= 1u;
+      ++q_issued;
+      const int r0 = s.rt * RT;
+      const int rows = item ? min(RT, s.r.n * a.group - r0) : 0;
+      const int tok = div_group(a, r0 + lane);
+      if (a.mask != nullptr && lane < rows)
+        s_word0[lane] = a.mask[(s.r.row0 + int64_t(tok)) * a.mask_words];
+      if (lane == 0) {
+        const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
+        const int first = whole ? 0 : cta_of(piece, s.first);
+        s_part = Part{s.b, s.h, r0, rows, s.r.row0, s.r.ctx, s.r.n, s.r.len, s.t0, item ? s.t1 : s.t0,
+                      whole, s.t0 == 0, first, whole ? 0 : cta_of(piece, s.end - 1) - first, {0, 0}};
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(rows) * D * 2);
+      __syncwarp();
+      if (lane < rows)
+        ptx::bulk_load(sq + lane * C::QLD,
+                       a.q + (s.r.row0 + int64_t(tok)) * a.q_token +
+                           int64_t(s.h * a.group + (r0 + lane - tok * a.group)) * a.q_head,
+                       D * 2, &q_full);
+    };
     while (ok && walk.next(s)) {
       int page = page_at<TK>(a, s, s.t0, box_shift, lane);
-      for (int t = s.t0; t < s.t1; ++t) {
+      for (int t = s.t0; t < s.t1 && ok; ++t) {
         const int ahead = t + 1 < s.t1 ? page_at<TK>(a, s, t + 1, box_shift, lane) : 0;
-        ok = ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT);
-        if (!ok) {
-          if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
-          break;
-        }
+        ok = give_up(ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT));
+        if (!ok) break;
         load_tile<D, TK>(a, map, ring + st * C::STAGE + (vals ? HALVES * HB : 0), &full[st], s, t,
                          page, box_shift, lane);
         page = ahead;
@@ -204,8 +263,10 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
           st = 0;
           phase ^= 1u;
         }
+        if (!vals && t == s.t0) post(true);
       }
     }
+    if (ok && !vals) post(false);
     if (!ok) {   // let the copies in flight land before the CTA exits
       const long back = issued < C::STAGES ? issued : C::STAGES;
       for (long i = 0; i < back; ++i) {
@@ -215,6 +276,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         }
         if (!ptx::mbar_wait_bounded(&full[st], phase, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
       }
+      if (q_issued > 0 && !ptx::mbar_wait_bounded(&q_full, q_phase, WAIT_LIMIT))
+        atomicOr(&g_attn_error, ERR_DRAIN);
     }
     return;
   }
@@ -232,24 +295,41 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   const int v_row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
   const int v_chunk = (lane >> 3) & 1;
   bool ok = true;
-  while (walk.next(s)) {
-    const int rows_all = s.r.n * a.group;
-    const int r0 = s.rt * RT;
-    const int rows = min(RT, rows_all - r0);
-    // query fragments, rows past the tile's last are zero
+  uint32_t q_phase = 0;
+  while (true) {
+    ok = ok && ptx::mbar_wait_warp(&q_full, q_phase, abort_flag, WAIT_LIMIT);
+    q_phase ^= 1u;
+    // all four warps go on or none does (and the buffers below are free again)
+    if (named_any(1, NW * 32, !ok)) {
+      if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_CONSUMER);
+      break;
+    }
+    const Part s = s_part;
+    if (s.t1 <= s.t0) break;
+    const int rows = s.rows, r0 = s.r0;
+    // query fragments (rows past the item's last are what the place held
+    // before: they reach only their own scores), and of this lane's score
+    // rows the new token and its mask's first word
     uint32_t qf[KS][NT][2];
+    int tok[NT][2];
+    uint64_t word0[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int r = r0 + n * 8 + row_b;
-      const bool in = r < rows_all;
-      const uint16_t* q = a.q + (s.r.row0 + int64_t(in ? r / a.group : 0)) * a.q_token +
-                          int64_t(s.h * a.group + (in ? r % a.group : 0)) * a.q_head + (lane & 3) * 2;
+      const uint8_t* q = sq + (n * 8 + row_b) * C::QLD + (lane & 3) * 4;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        qf[k][n][0] = in ? *reinterpret_cast<const uint32_t*>(q + k * 16) : 0u;
-        qf[k][n][1] = in ? *reinterpret_cast<const uint32_t*>(q + k * 16 + 8) : 0u;
+        qf[k][n][0] = *reinterpret_cast<const uint32_t*>(q + k * 32);
+        qf[k][n][1] = *reinterpret_cast<const uint32_t*>(q + k * 32 + 16);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = n * 8 + row_c + e;
+        tok[n][e] = r < rows ? div_group(a, r0 + r) : 0;
+        word0[n][e] = r < rows ? s_word0[r] : 0;
       }
     }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&q_empty);
     float o[KS][NT][4];
 #pragma unroll
     for (int i = 0; i < KS; ++i)
@@ -262,28 +342,17 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       l[n][0] = l[n][1] = 0.f;
     }
 
-    int tok[NT][2];            // of this lane's score rows: the new token, its mask's first word
-    uint64_t word0[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = r0 + n * 8 + row_c + e;
-        tok[n][e] = r < rows_all ? r / a.group : 0;
-        word0[n][e] = first_word(a, a.mask + (s.r.row0 + int64_t(tok[n][e])) * a.mask_words);
-      }
-
     for (int t = s.t0; t < s.t1; ++t) {
       const int k0 = t * TK + warp * 16;         // this warp's first key
-      const bool edge = k0 + 16 > s.r.ctx;     // new tokens, or past the last
+      const bool edge = k0 + 16 > s.ctx;     // new tokens, or past the last
       uint32_t vis[NT][2];
       if (edge) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            vis[n][e] = sees_bits<16>(a, a.mask + (s.r.row0 + int64_t(tok[n][e])) * a.mask_words,
-                                      word0[n][e], tok[n][e], k0, s.r);
+            vis[n][e] = sees_bits<16>(a, a.mask + (s.row0 + int64_t(tok[n][e])) * a.mask_words,
+                                      word0[n][e], tok[n][e], k0, s.ctx, s.len);
       }
       // a warp whose wait gave up reads no more tiles, but still meets the
       // others at the barriers below
@@ -358,13 +427,13 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = k0 + (e >> 1) * 8 + (lane & 3) * 2;      // keys j, j + 1
-            if (j >= s.r.len) x[e] = 0;
-            if (j + 1 >= s.r.len) x[e] &= 0x0000FFFFu;
+            if (j >= s.len) x[e] = 0;
+            if (j + 1 >= s.len) x[e] &= 0x0000FFFFu;
             const uint32_t b = nonfinite2<BF16>(x[e]);
             if (b != 0) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const int jj = j + h - s.r.ctx;
+                const int jj = j + h - s.ctx;
                 if (!((b >> h) & 1) || jj < 0) continue;           // a cached key's stays
                 x[e] &= h == 0 ? 0xFFFF0000u : 0x0000FFFFu;
                 if (jj < 256) atomicOr(&s_bad[jj >> 5], 1u << (jj & 31));
@@ -407,8 +476,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         for (int w = 0; w < NW; ++w) mm = fmaxf(mm, s_ml[w][n * 8 + row_c + e].x);
         f[n][e] = mm == -INFINITY ? 0.f : ex2(m[n][e] - mm);
       }
-    const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
+    const bool whole = s.whole != 0;
+    const int64_t slot = 2 * int64_t(blockIdx.x) + s.begins;
     const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
     float* mine = merge + (warp & 1) * (RT * C::LD);
 #pragma unroll
@@ -438,13 +507,13 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         float4 x = *reinterpret_cast<const float4*>(merge + r * C::LD + dc);
         const float4 y = *reinterpret_cast<const float4*>(merge + (RT + r) * C::LD + dc);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
-        const int token = (r0 + r) / a.group, head = s.h * a.group + (r0 + r) % a.group;
+        const int token = div_group(a, r0 + r), head = s.h * a.group + (r0 + r - token * a.group);
         if (any_bad) {
-          const uint64_t* mr = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(token)) * a.mask_words
+          const uint64_t* mr = a.mask != nullptr ? a.mask + (s.row0 + int64_t(token)) * a.mask_words
                                                  : nullptr;
-          for (int j = 0; j < min(s.r.n, 256); ++j) {
-            if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mr, token, j, s.r.n)) continue;
-            const int64_t pos = int64_t(s.r.ctx) + j;
+          for (int j = 0; j < min(s.n, 256); ++j) {
+            if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mr, token, j, s.n)) continue;
+            const int64_t pos = int64_t(s.ctx) + j;
             const int pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
             if (pg < 0 || pg >= a.pages) continue;
             const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
@@ -463,7 +532,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
           ll += s_ml[w][r].y * (mm == -INFINITY ? 0.f : ex2(s_ml[w][r].x - mm));
         if (whole) {
           const float inv = ll == 0.f ? 0.f : 1.f / ll;
-          const int64_t at = (int64_t(s.r.row0) + token) * a.Hq + head;
+          const int64_t at = (int64_t(s.row0) + token) * a.Hq + head;
           *reinterpret_cast<uint2*>(a.out + at * D + d) =
               make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
           if (d == 0 && a.lse != nullptr)
@@ -474,16 +543,12 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         }
       }
     }
-    if (!whole) {
-      const int first = cta_of(piece, s.first);
-      join_piece<BF16, D, RT, NW * 32>(
-          a, Item{first, cta_of(piece, s.end - 1) - first, s.r.row0, r0, rows, s.h}, tid, &s_last);
-    }
-    ptx::named_sync(1, NW * 32);   // s_ml, merge and s_bad are free again
+    if (!whole)
+      join_piece<BF16, D, RT, NW * 32>(a, Item{s.first, s.follow, s.row0, r0, rows, s.h}, tid, &s_last);
     if (any_bad) {
+      ptx::named_sync(1, NW * 32);
       if (tid < 8) s_bad[tid] = 0;
       if (tid == 0) s_any_bad = 0;
-      ptx::named_sync(1, NW * 32);
     }
   }
 }
@@ -809,7 +874,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 #pragma unroll 4
       for (int i = lane; i < rows * (D / 8); i += 32) {
         const int g = r0 + i / (D / 8);
-        const int token = g / a.group;
+        const int token = div_group(a, g);
         const uint16_t* q = a.q + (s.r.row0 + int64_t(token)) * a.q_token +
                             int64_t(s.h * a.group + (g - token * a.group)) * a.q_head + i % (D / 8) * 8;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(place(i))),
@@ -855,7 +920,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       const int cnt = s.t1 - s.t0;
       const int my = (MODE == ROWS ? 128 * x : 0) + lrow;      // row of the item
       const bool active = (MODE == ROWS ? 128 * x : 0) + (warp & 3) * 32 < rows;
-      const int tok = my < rows ? (r0 + my) / a.group : 0;
+      const int tok = my < rows ? div_group(a, r0 + my) : 0;
       const uint64_t* mw = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words : nullptr;
       const uint64_t word0 = first_word(a, mw);
       float m = -INFINITY, l = 0.f;
@@ -866,7 +931,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         uint32_t vis[TKT / 32];
         if (edge && active) {
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c) vis[c] = sees_bits<32>(a, mw, word0, tok, k0 + 32 * c, s.r);
+          for (int c = 0; c < TKT / 32; ++c) vis[c] = sees_bits<32>(a, mw, word0, tok, k0 + 32 * c, s.r.ctx, s.r.len);
         }
         wait(&s_full[x], s_phase);
         s_phase ^= 1u;
@@ -1012,7 +1077,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t at = (int64_t(s.r.row0) + tok) * a.Hq + s.h * a.group + (r0 + my) % a.group;
+        const int64_t at = (int64_t(s.r.row0) + tok) * a.Hq + s.h * a.group + (r0 + my - tok * a.group);
         // KEYS: this warpgroup's half of the columns from both accumulators;
         // ROWS: all columns of its rows; COLS: its columns
         constexpr int NC = MODE == KEYS ? D / 2 : DV;
@@ -1353,6 +1418,7 @@ cudaError_t launch_tree_attention(const TreeAttnCall& call, cudaStream_t st) {
   a.H = static_cast<int>(c.heads);
   a.Hq = static_cast<int>(call.Hq);
   a.group = static_cast<int>(call.Hq / c.heads);
+  a.group_mul = a.group > 1 && a.group < 4096 ? static_cast<uint32_t>((uint64_t(1) << 32) / a.group + 1) : 0;
   a.scale_log2 = call.scale * 1.4426950408889634f;
   const bool bf = c.dtype == TERN_KV_BF16;
   if (c.dim == 64) return bf ? launch_dim<true, 64>(call, a, st) : launch_dim<false, 64>(call, a, st);

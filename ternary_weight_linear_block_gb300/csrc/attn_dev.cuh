@@ -42,6 +42,7 @@ struct Args {
   int64_t q_token, q_head, table_stride;
   int64_t page_stride, token_stride, head_stride;
   int width, pages, page_shift, mask_words, B, T, H, group, Hq;
+  uint32_t group_mul;       // 2^32 / group + 1, or 0 (div_group)
   float scale_log2;
 };
 
@@ -49,6 +50,13 @@ struct Args {
 struct Req {
   int ctx, n, row0, len, tiles, rts;
 };
+
+// Row r of a request on a key head -> its new token.  r is below 256 group, so
+// the product with 2^32 / group + 1 is exact while group < 4096.
+__device__ __forceinline__ int div_group(const Args& a, int r) {
+  if (a.group_mul != 0) return static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.group_mul));
+  return a.group == 1 ? r : r / a.group;
+}
 
 // Tiles that an item counts for.
 template <int PAD>
@@ -228,8 +236,8 @@ __device__ __forceinline__ uint64_t first_word(const Args& a, const uint64_t* mw
 // are seen, keys past the request's last are not.
 template <int N>
 __device__ __forceinline__ uint32_t sees_bits(const Args& a, const uint64_t* mw, uint64_t word0,
-                                              int i, int k0, const Req& r) {
-  const int j0 = k0 - r.ctx;              // k0 as a new token, below 0: cached
+                                              int i, int k0, int ctx, int len) {
+  const int j0 = k0 - ctx;              // k0 as a new token, below 0: cached
   const int lo = max(j0, 0), skip = min(lo - j0, N);
   uint64_t x = 0;
   if (skip < N) {
@@ -243,7 +251,7 @@ __device__ __forceinline__ uint32_t sees_bits(const Args& a, const uint64_t* mw,
     }
   }
   const uint64_t bits = (x << skip) | ((uint64_t(1) << skip) - 1);
-  const int valid = min(max(r.len - k0, 0), N);
+  const int valid = min(max(len - k0, 0), N);
   return static_cast<uint32_t>(bits & ((uint64_t(1) << valid) - 1));
 }
 
@@ -309,7 +317,8 @@ template <bool BF16, int D>
 __device__ __forceinline__ void write_joined(const Args& a, const Item& it, int r, int d4, float m,
                                              float l, float4 o) {
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int token = (it.r0 + r) / a.group, head = it.head * a.group + (it.r0 + r) % a.group;
+  const int token = div_group(a, it.r0 + r);
+  const int head = it.head * a.group + (it.r0 + r - token * a.group);
   const int64_t at = (int64_t(it.row0) + token) * a.Hq + head;
   *reinterpret_cast<uint2*>(a.out + at * D + d4 * 4) =
       make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
