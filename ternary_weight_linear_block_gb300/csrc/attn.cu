@@ -163,7 +163,7 @@ __device__ __forceinline__ void load_tile(const Args& a, const CUtensorMap* map,
 template <bool BF16, int D, int NT>
 __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
     attn_rows_kernel(const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const Args a) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a) {
   using C = Rows<D, NT>;
   constexpr int RT = C::RT, THREADS = C::THREADS;
   constexpr int HALVES = D / 64;
@@ -223,6 +223,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       if (!good && lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
       return good;
     };
+    uint64_t word0 = 0;      // lane r: of the mask of the item's row r
+    const auto rows_of = [&] { return min(RT, s.r.n * a.group - s.rt * RT); };
     // the item's description and queries, or (none) the end
     const auto post = [&](bool item) {
       ok = give_up(ptx::mbar_wait_warp(&q_empty, q_phase, abort_flag, WAIT_LIMIT));
@@ -230,10 +232,15 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       q_phase ^= 1u;
       ++q_issued;
       const int r0 = s.rt * RT;
-      const int rows = item ? min(RT, s.r.n * a.group - r0) : 0;
-      const int tok = div_group(a, r0 + lane);
-      if (a.mask != nullptr && lane < rows)
-        s_word0[lane] = a.mask[(s.r.row0 + int64_t(tok)) * a.mask_words];
+      const int rows = item ? rows_of() : 0;
+      if (lane < rows) {
+        const int tok = div_group(a, r0 + lane);
+        ptx::bulk_load(sq + lane * C::QLD,
+                       a.q + (s.r.row0 + int64_t(tok)) * a.q_token +
+                           int64_t(s.h * a.group + (r0 + lane - tok * a.group)) * a.q_head,
+                       D * 2, &q_full);
+        s_word0[lane] = word0;
+      }
       if (lane == 0) {
         const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
         const int first = whole ? 0 : cta_of(piece, s.first);
@@ -242,15 +249,11 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(rows) * D * 2);
-      __syncwarp();
-      if (lane < rows)
-        ptx::bulk_load(sq + lane * C::QLD,
-                       a.q + (s.r.row0 + int64_t(tok)) * a.q_token +
-                           int64_t(s.h * a.group + (r0 + lane - tok * a.group)) * a.q_head,
-                       D * 2, &q_full);
     };
     while (ok && walk.next(s)) {
       int page = page_at<TK>(a, s, s.t0, box_shift, lane);
+      if (!vals && a.mask != nullptr && lane < rows_of())
+        word0 = a.mask[(s.r.row0 + int64_t(div_group(a, s.rt * RT + lane))) * a.mask_words];
       for (int t = s.t0; t < s.t1 && ok; ++t) {
         const int ahead = t + 1 < s.t1 ? page_at<TK>(a, s, t + 1, box_shift, lane) : 0;
         ok = give_up(ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT));
@@ -296,6 +299,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   const int v_chunk = (lane >> 3) & 1;
   bool ok = true;
   uint32_t q_phase = 0;
+  Item joins[2];
+  int n_joins = 0;
   while (true) {
     ok = ok && ptx::mbar_wait_warp(&q_full, q_phase, abort_flag, WAIT_LIMIT);
     q_phase ^= 1u;
@@ -351,8 +356,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            vis[n][e] = sees_bits<16>(a, a.mask + (s.row0 + int64_t(tok[n][e])) * a.mask_words,
-                                      word0[n][e], tok[n][e], k0, s.ctx, s.len);
+            vis[n][e] = sees16(a, a.mask + (s.row0 + int64_t(tok[n][e])) * a.mask_words,
+                               word0[n][e], tok[n][e], k0, s.ctx, s.len);
       }
       // a warp whose wait gave up reads no more tiles, but still meets the
       // others at the barriers below
@@ -363,6 +368,11 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       if (!ok) break;
       const uint32_t kbase = ring_u + st * C::STAGE;
       const uint32_t vbase = kbase + HALVES * HB;
+      if (edge) {
+        clean_values<BF16, D>(ring + st * C::STAGE + HALVES * HB, HB, t * TK, warp * 16,
+                              warp * 16 + 16, s.ctx, s.len, lane, 32, s_bad, &s_any_bad);
+        __syncwarp();
+      }
       float c[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
@@ -420,28 +430,6 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         uint32_t x[4];
         const int chunk = (i & 3) * 2 + v_chunk;
         ldsm_x4_t(vbase + (i >> 2) * HB + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), x);
-        if (edge) {
-          // values past the last token count as zero, and so does a non-finite
-          // value of a new token here: it is added at the item's end, to the
-          // rows that see that token
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = k0 + (e >> 1) * 8 + (lane & 3) * 2;      // keys j, j + 1
-            if (j >= s.len) x[e] = 0;
-            if (j + 1 >= s.len) x[e] &= 0x0000FFFFu;
-            const uint32_t b = nonfinite2<BF16>(x[e]);
-            if (b != 0) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int jj = j + h - s.ctx;
-                if (!((b >> h) & 1) || jj < 0) continue;           // a cached key's stays
-                x[e] &= h == 0 ? 0xFFFF0000u : 0x0000FFFFu;
-                if (jj < 256) atomicOr(&s_bad[jj >> 5], 1u << (jj & 31));
-                s_any_bad = 1;
-              }
-            }
-          }
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) mma16816<BF16>(o[i][n], x, p[n][0], p[n][1]);
       }
@@ -483,7 +471,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += C::COLS) {
       if (c0 > 0) ptx::named_sync(1, NW * 32);
-#pragma unroll
+#pragma unroll 1
       for (int round = 0; round < 2; ++round) {
         if ((warp >> 1) == round) {
 #pragma unroll
@@ -501,6 +489,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         ptx::named_sync(1, NW * 32);
       }
       // ---- write: thread -> 4 consecutive values of a row
+#pragma unroll 1
       for (int i = tid; i < RT * (C::COLS / 4); i += NW * 32) {
         const int r = i % RT, dc = i / RT * 4, d = c0 + dc;
         if (r >= rows) continue;
@@ -508,22 +497,6 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
         const float4 y = *reinterpret_cast<const float4*>(merge + (RT + r) * C::LD + dc);
         x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         const int token = div_group(a, r0 + r), head = s.h * a.group + (r0 + r - token * a.group);
-        if (any_bad) {
-          const uint64_t* mr = a.mask != nullptr ? a.mask + (s.row0 + int64_t(token)) * a.mask_words
-                                                 : nullptr;
-          for (int j = 0; j < min(s.n, 256); ++j) {
-            if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mr, token, j, s.n)) continue;
-            const int64_t pos = int64_t(s.ctx) + j;
-            const int pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
-            if (pg < 0 || pg >= a.pages) continue;
-            const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
-                                (pos & ((1 << a.page_shift) - 1)) * a.token_stride +
-                                int64_t(s.h) * a.head_stride + d;
-            float* xf = reinterpret_cast<float*>(&x);
-            for (int e = 0; e < 4; ++e)
-              if (nonfinite2<BF16>(v[e]) & 1) xf[e] += widen<BF16>(v[e]);
-          }
-        }
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) mm = fmaxf(mm, s_ml[w][r].x);
@@ -541,16 +514,23 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
           *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + d / 4) * RT + r) * 4) = x;
           if (d == 0) a.part_ml[slot * RT + r] = make_float2(mm, ll);
         }
+        if (any_bad)
+          add_bad<BF16>(a, s_bad, s.b, s.h, s.ctx, s.n, s.row0, token, d, 4,
+                        whole ? a.out + ((int64_t(s.row0) + token) * a.Hq + head) * D + d : nullptr,
+                        a.part_o + ((slot * (D / 4) + d / 4) * RT + r) * 4, 4);
       }
     }
-    if (!whole)
-      join_piece<BF16, D, RT, NW * 32>(a, Item{s.first, s.follow, s.row0, r0, rows, s.h}, tid, &s_last);
+    if (!whole) {
+      const Item it{s.first, s.follow, s.row0, r0, rows, s.h};
+      if (n_joins++ == 0) joins[0] = it; else joins[1] = it;
+    }
     if (any_bad) {
       ptx::named_sync(1, NW * 32);
       if (tid < 8) s_bad[tid] = 0;
       if (tid == 0) s_any_bad = 0;
     }
   }
+  if (n_joins > 0) join_pieces<BF16, D, RT, NW * 32>(a, joins, n_joins, tid, &s_last);
 }
 
 // ------------------------------------------------------------------ tile kernel
@@ -677,7 +657,7 @@ __device__ __forceinline__ void mask_out(uint32_t (&v)[32], uint32_t vis) {
 template <bool BF16, int D, int MODE>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const Args a) {
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a) {
   using C = Tile<D, MODE>;
   constexpr int TKT = C::TKT, RT = C::RT, SLOTS = C::SLOTS, DV = C::DV;
   constexpr int HALVES = D / 64;
@@ -928,10 +908,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       for (int i = MODE == KEYS ? x : 0; i < cnt; i += MODE == KEYS ? 2 : 1) {
         const int k0 = (s.t0 + i) * TKT;
         const bool edge = k0 + TKT > s.r.ctx;
-        uint32_t vis[TKT / 32];
+        uint64_t vis[TKT / 64];
         if (edge && active) {
 #pragma unroll
-          for (int c = 0; c < TKT / 32; ++c) vis[c] = sees_bits<32>(a, mw, word0, tok, k0 + 32 * c, s.r.ctx, s.r.len);
+          for (int c = 0; c < TKT / 64; ++c)
+            vis[c] = sees64(a, mw, word0, tok, k0 + 64 * c, s.r.ctx, s.r.len);
         }
         wait(&s_full[x], s_phase);
         s_phase ^= 1u;
@@ -941,15 +922,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           // not fit the registers
           uint32_t v[2][32];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < TKT / 32; c += 2) {
             ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, v[0]);
             ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 32, v[1]);
             tmem_ld_wait_for(v[0]);
             tmem_ld_wait_for(v[1]);
             if (edge) {
-              mask_out(v[0], vis[c]);
-              mask_out(v[1], vis[c + 1]);
+              const uint64_t bits = TKT == 64 || c == 0 ? vis[0] : vis[TKT / 64 - 1];
+              mask_out(v[0], static_cast<uint32_t>(bits));
+              mask_out(v[1], static_cast<uint32_t>(bits >> 32));
             }
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
@@ -965,7 +947,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             m = mt;
           }
           if (any && __any_sync(~0u, f != 1.f)) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DV / 32; ++c) {
               uint32_t o[32];
               ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
@@ -984,14 +966,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           const float ms = m == -INFINITY ? 0.f : m;
           const float2 sc2 = make_float2(scale, scale), ms2 = make_float2(-ms, -ms);
           float2 sum[4] = {};
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < TKT / 32; c += 2) {
             // P's columns 16 c .. overwrite columns of S that were read before
             tmem_ld_wait_for(v[0]);
             tmem_ld_wait_for(v[1]);
             if (edge) {
-              mask_out(v[0], vis[c]);
-              mask_out(v[1], vis[c + 1]);
+              const uint64_t bits = TKT == 64 || c == 0 ? vis[0] : vis[TKT / 64 - 1];
+              mask_out(v[0], static_cast<uint32_t>(bits));
+              mask_out(v[1], static_cast<uint32_t>(bits >> 32));
             }
             uint32_t w[2][16];
 #pragma unroll
@@ -1019,34 +1002,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           const uint32_t n = seq0 + v_place(i, cnt);
           wait(&full[n % SLOTS], (n / SLOTS) & 1u);
           if (!ok) break;
-          uint8_t* vt = ring + (n % SLOTS) * C::SLOT;
-          for (int u = lrow; u < TKT * (D / 8); u += 128) {
-            const int kr = u / (D / 8), c = u % (D / 8);
-            const int j = k0 + kr;
-            if (j < s.r.ctx) continue;
-            uint4* at = reinterpret_cast<uint4*>(vt + (c >> 3) * HB + kr * 128 + (((c & 7) ^ (kr & 7)) << 4));
-            if (j >= s.r.len) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint4 y = *at;
-            uint32_t bad = 0;
-            uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t b = nonfinite2<BF16>(yw[e]);
-              if (b & 1) yw[e] &= 0xFFFF0000u;
-              if (b & 2) yw[e] &= 0x0000FFFFu;
-              bad |= b;
-            }
-            if (bad) {
-              *at = y;
-              const int jj = j - s.r.ctx;
-              if (jj < 256) atomicOr(&s_bad[jj >> 5], 1u << (jj & 31));
-              s_any_bad = 1;
-            }
-          }
-          ptx::fence_proxy_async_smem();   // before the MMA reads it
+          clean_values<BF16, D>(ring + (n % SLOTS) * C::SLOT, HB, k0, 0, TKT, s.r.ctx, s.r.len, lrow,
+                                128, s_bad, &s_any_bad);
         }
         ptx::tc_fence_before();
         __syncwarp();
@@ -1082,7 +1039,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         // ROWS: all columns of its rows; COLS: its columns
         constexpr int NC = MODE == KEYS ? D / 2 : DV;
         const int col0 = MODE == ROWS ? 0 : x * NC;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < NC / 32; ++c) {
           float o[32];
           uint32_t u[32];
@@ -1106,20 +1063,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           }
           if (my < rows) {
             const int d = col0 + 32 * c;
-            if (any_bad) {
-              for (int j = 0; j < min(s.r.n, 256); ++j) {
-                if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mw, tok, j, s.r.n)) continue;
-                const int64_t pos = int64_t(s.r.ctx) + j;
-                const int pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
-                if (pg < 0 || pg >= a.pages) continue;
-                const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
-                                    (pos & ((1 << a.page_shift) - 1)) * a.token_stride +
-                                    int64_t(s.h) * a.head_stride + d;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (nonfinite2<BF16>(v[e]) & 1) o[e] += widen<BF16>(v[e]);
-              }
-            }
             if (whole) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -1137,6 +1080,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 *reinterpret_cast<float4*>(po + 4 * RT * e) =
                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
+            if (any_bad)
+              add_bad<BF16>(a, s_bad, s.b, s.h, s.r.ctx, s.r.n, s.r.row0, tok, d, 32,
+                            whole ? a.out + at * D + d : nullptr,
+                            a.part_o + ((slot * (D / 4) + d / 4) * RT + my) * 4, 4 * RT);
           }
         }
         if (my < rows && (MODE == ROWS || x == 0)) {

@@ -283,6 +283,86 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
   return ((x & E) == E ? 1u : 0u) | (((x >> 16) & E) == E ? 2u : 0u);
 }
 
+// The rare paths are functions of their own, not inlined: a kernel whose loop
+// does not fit the instruction cache fetches it again from an L2 that its
+// copies keep busy, 1.5 us a miss.
+
+// sees_bits for 64 keys, and for 16.
+__device__ __noinline__ uint64_t sees64(const Args& a, const uint64_t* mw, uint64_t word0, int i,
+                                        int k0, int ctx, int len) {
+  return sees_bits<32>(a, mw, word0, i, k0, ctx, len) |
+         static_cast<uint64_t>(sees_bits<32>(a, mw, word0, i, k0 + 32, ctx, len)) << 32;
+}
+__device__ __noinline__ uint32_t sees16(const Args& a, const uint64_t* mw, uint64_t word0, int i,
+                                        int k0, int ctx, int len) {
+  return sees_bits<16>(a, mw, word0, i, k0, ctx, len);
+}
+
+// Values of a tile (64-column parts `part` bytes apart, rows of 128 swizzled
+// bytes) in rows [r0, r1), of which row 0 is key k0: those past the request's
+// last token become zero, and so do non-finite ones of new tokens, which
+// s_bad (by token) and s_any_bad note; add_bad adds them to the rows that see
+// them.  For `count` threads.
+template <bool BF16, int D>
+__device__ __noinline__ void clean_values(uint8_t* tile, int part, int k0, int r0, int r1, int ctx,
+                                          int len, int thread, int count, unsigned int* s_bad,
+                                          int* s_any_bad) {
+  r0 = max(r0, ctx - k0);
+#pragma unroll 1
+  for (int i = thread; i < (r1 - r0) * (D / 8); i += count) {
+    const int r = r0 + i / (D / 8), c = i % (D / 8);
+    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * part + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+    if (k0 + r >= len) {
+      *at = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *at;
+    uint32_t bad = 0;
+    uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t b = nonfinite2<BF16>(xw[e]);
+      if (b & 1) xw[e] &= 0xFFFF0000u;
+      if (b & 2) xw[e] &= 0x0000FFFFu;
+      bad |= b;
+    }
+    if (bad) {
+      *at = x;
+      const int j = k0 + r - ctx;
+      if (j < 256) atomicOr(&s_bad[j >> 5], 1u << (j & 31));
+      *s_any_bad = 1;
+    }
+  }
+  ptx::fence_proxy_async_smem();   // before an MMA's reading and the ring's next copy
+}
+
+// Adds the non-finite values of the new tokens that a row sees to columns
+// [d0, d0 + n_cols) of what this thread stored for the row: its output
+// (`out`), or its part of a piece (`part`, four columns every `step` floats).
+template <bool BF16>
+__device__ __noinline__ void add_bad(const Args& a, const unsigned int* s_bad, int b, int h, int ctx,
+                                     int n, int row0, int token, int d0, int n_cols, uint16_t* out,
+                                     float* part, int step) {
+  const uint64_t* mw = a.mask != nullptr ? a.mask + (row0 + int64_t(token)) * a.mask_words : nullptr;
+#pragma unroll 1
+  for (int j = 0; j < min(n, 256); ++j) {
+    if (!((s_bad[j >> 5] >> (j & 31)) & 1) || !sees(a, mw, token, j, n)) continue;
+    const int64_t pos = int64_t(ctx) + j;
+    const int pg = a.table[int64_t(b) * a.table_stride + (pos >> a.page_shift)];
+    if (pg < 0 || pg >= a.pages) continue;
+    const uint16_t* v = a.v + int64_t(pg) * a.page_stride +
+                        (pos & ((1 << a.page_shift) - 1)) * a.token_stride + int64_t(h) * a.head_stride + d0;
+#pragma unroll 1
+    for (int d = 0; d < n_cols; ++d) {
+      if (!(nonfinite2<BF16>(v[d]) & 1)) continue;
+      if (out != nullptr)
+        out[d] = static_cast<uint16_t>(pack2<BF16>(widen<BF16>(out[d]) + widen<BF16>(v[d]), 0.f));
+      else
+        part[d / 4 * step + d % 4] += widen<BF16>(v[d]);
+    }
+  }
+}
+
 constexpr float kLn2 = 0.69314718055994530942f;
 
 // ------------------------------------------------------------------ join
@@ -326,36 +406,52 @@ __device__ __forceinline__ void write_joined(const Args& a, const Item& it, int 
     a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// N threads of a CTA, one of which each has `tid` 0 .. N - 1, synchronised by
-// named barrier 1; every one has stored its part of the piece.
+// The one or two items whose parts a CTA stored (the first and the last of its
+// piece), after both: N threads with `tid` 0 .. N - 1, synchronised by named
+// barrier 1.
 template <bool BF16, int D, int RT, int N>
-__device__ __forceinline__ void join_piece(const Args& a, const Item& it, int tid, int* s_last) {
-  const int count = it.follow + 1, grid = static_cast<int>(gridDim.x);
-  const auto slot_of = [&](int i) { return 2 * (int64_t(it.first) + i) + (i == 0 ? 1 : 0); };
-  // counts one arrival; true for every thread if it was the last of `all`
-  const auto last_of = [&](int* counter, int all) {
-    __threadfence();
+__device__ __forceinline__ void join_pieces(const Args& a, const Item (&items)[2], int n, int tid,
+                                            int* s_last) {
+  const int grid = static_cast<int>(gridDim.x);
+  const auto slot_of = [](const Item& it, int i) { return 2 * (int64_t(it.first) + i) + (i == 0 ? 1 : 0); };
+  const auto group_of = [](const Item& it) {     // pieces that are added first
+    int size = it.follow + 1;
+    if (size >= JOIN_ALL) {
+      size = 5;
+      while (size * size < it.follow + 1) ++size;
+    }
+    return size;
+  };
+  // Counts one arrival each; which were the last ones, for every thread.  The
+  // barrier and thread 0's fence publish what all of them stored.
+  const auto count = [&](int* c0, int all0, int* c1, int all1) {
     ptx::named_sync(1, N);
     if (tid == 0) {
-      *s_last = atomicAdd(counter, 1) == all - 1;
-      if (*s_last) *counter = 0;
       __threadfence();
+      const int at0 = atomicAdd(c0, 1);
+      const int at1 = c1 != nullptr ? atomicAdd(c1, 1) : -2;
+      const int last = (at0 == all0 - 1 ? 1 : 0) | (at1 == all1 - 1 ? 2 : 0);
+      if (last & 1) *c0 = 0;
+      if (last & 2) *c1 = 0;
+      __threadfence();
+      *s_last = last;
     }
     ptx::named_sync(1, N);
-    return *reinterpret_cast<volatile int*>(s_last) != 0;
+    return *reinterpret_cast<volatile int*>(s_last);
   };
   // pieces i0, i0 + step, .. below i1: to the output, or as the group's sum to
   // piece i0's place.  A group's (m, l) has a place of its own, 2 grid slots
   // on, since every column's thread reads the piece's.
-  const auto add_up = [&](int i0, int i1, int step, bool out) {
+  const auto add_up = [&](const Item& it, int i0, int i1, int step, bool out) {
     const int64_t sums = step > 1 ? 2 * int64_t(grid) : 0;
+#pragma unroll 1
     for (int p = tid; p < it.rows * (D / 4); p += N) {
       const int d4 = p / it.rows, r = p - d4 * it.rows;
       float m = -INFINITY, l = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 2
       for (int i = i0; i < i1; i += step) {
-        const int64_t slot = slot_of(i);
+        const int64_t slot = slot_of(it, i);
         const float2 ml = __ldcg(a.part_ml + (sums + slot) * RT + r);
         const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + d4) * RT + r) * 4));
         add_piece(m, l, o, ml, x);
@@ -363,22 +459,40 @@ __device__ __forceinline__ void join_piece(const Args& a, const Item& it, int ti
       if (out) {
         write_joined<BF16, D>(a, it, r, d4, m, l, o);
       } else {
-        const int64_t slot = slot_of(i0);
+        const int64_t slot = slot_of(it, i0);
         *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + d4) * RT + r) * 4) = o;
         if (d4 == 0) a.part_ml[(2 * int64_t(grid) + slot) * RT + r] = make_float2(m, l);
       }
     }
   };
-  if (count < JOIN_ALL) {
-    if (last_of(a.arrived + it.first, count)) add_up(0, count, 1, true);
-    return;
-  }
-  int size = 5;
-  while (size * size < count) ++size;
-  const int i0 = (static_cast<int>(blockIdx.x) - it.first) / size * size;
-  if (last_of(a.arrived + grid + slot_of(i0), min(size, count - i0))) {
-    add_up(i0, min(i0 + size, count), 1, false);
-    if (last_of(a.arrived + it.first, (count + size - 1) / size)) add_up(0, count, size, true);
+  // where item k's arrival is counted first, and how many are awaited there
+  const auto first_count = [&](const Item& it, int*& c, int& all) {
+    const int size = group_of(it), pieces = it.follow + 1;
+    const int i0 = (static_cast<int>(blockIdx.x) - it.first) / size * size;
+    c = size == pieces ? a.arrived + it.first : a.arrived + grid + slot_of(it, i0);
+    all = min(size, pieces - i0);
+  };
+  int *c0 = nullptr, *c1 = nullptr, all0 = 0, all1 = 0;
+  first_count(items[0], c0, all0);
+  if (n > 1) first_count(items[1], c1, all1);
+  const int last = count(c0, all0, c1, all1);
+#pragma unroll 1
+  for (int k = 0; k < n; ++k) {
+    if (!((last >> k) & 1)) continue;
+    const Item it = k == 0 ? items[0] : items[1];
+    const int size = group_of(it), pieces = it.follow + 1;
+    const int i0 = (static_cast<int>(blockIdx.x) - it.first) / size * size;
+    int from = i0, to = min(i0 + size, pieces), step = 1;
+    bool out = size == pieces;
+#pragma unroll 1
+    while (true) {
+      add_up(it, from, to, step, out);
+      if (out || !(count(a.arrived + it.first, (pieces + size - 1) / size, nullptr, 0) & 1)) break;
+      from = 0;
+      to = pieces;
+      step = size;
+      out = true;
+    }
   }
 }
 
