@@ -540,14 +540,17 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // the row's probabilities over it as 16-bit values, and out += P V takes P
 // from tensor memory and V from the ring as its pages hold it (columns of V
 // along the MMA's N side: the MN-major operand).  Keys and values arrive in a
-// ring of 32 KB slots in the order K0 K1 V0 K2 V1 K3 ...
+// ring of slots in the order K0 K1 V0 K2 V1 K3 ...
 //
 // Two streams, each with its S, its out accumulator and a warpgroup, so that
 // one stream's softmax runs beside the other's MMAs:
 //   KEYS  rows <= 128:  the streams take the even and the odd key tiles
 //   ROWS  rows <= 256:  each has 128 rows; a key tile serves both
-//   COLS  head size 256: each has 128 columns of V (an accumulator of 256
-//         columns for each would not fit); both compute S
+//   SHARED head size 256, whose accumulator of 256 columns fits tensor memory
+//         once: the warpgroups take the tiles in turn and share it.  A row's
+//         reference maximum goes from one to the other through shared memory,
+//         tile by tile, and whoever has to move it waits for the MMA before
+//         and rescales.  S has three buffers and runs two tiles ahead.
 // The maximum that a row's exponents refer to only moves when it grows by
 // more than 2^8: until then nothing is rescaled (probabilities up to 256 are
 // as exact in the 16-bit types, and sums are in 32 bits), so the pass over
@@ -555,28 +558,36 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // whole warps of them skip the softmax.
 
 constexpr int TILE_THREADS = 384;   // K producer, MMA, TMEM, V producer; two warpgroups
-enum Mode { KEYS, ROWS, COLS };
+enum Mode { KEYS, ROWS, SHARED };
 
 template <int D, int MODE>
 struct Tile {
   static constexpr int TKT = D == 256 ? 64 : 128;        // keys of a tile
   static constexpr int RT = MODE == ROWS ? 256 : 128;
-  static constexpr int PAD = D == 64 ? 3 : 2;            // an item's cost beside its tiles
+  static constexpr int PAD = D == 64 ? 3 : 2;             // an item's cost beside its tiles
   static constexpr int SLOT = TKT * D * 2;
   static constexpr int QB = 128 * D * 2;                 // one Q tile
   static constexpr int QBYTES = MODE == ROWS ? 2 * QB : QB;
   static constexpr int FIT = (232448 - 1024 - 6144 - QBYTES) / SLOT;
   static constexpr int SLOTS = FIT < 8 ? FIT : 8;
   static constexpr size_t SMEM = size_t(SLOTS) * SLOT + QBYTES + 1024;
-  static constexpr int DV = MODE == COLS ? 128 : D;      // columns of an accumulator
-  static constexpr uint32_t S_COL = 0, O_COL = 256;      // stream x: + 128 x
+  static constexpr int AHEAD = MODE == SHARED ? 2 : 1;    // tiles that S runs ahead
+  static constexpr int NS = MODE == SHARED ? 3 : 2;      // buffers of S
+  static constexpr int S_STEP = MODE == SHARED ? TKT : 128;
+  // accumulators: stream x at O_COL + 128 x; SHARED: one
+  static constexpr uint32_t S_COL = 0, O_COL = 256;
   static_assert(SLOTS >= 4, "ring");
 };
 
-// Places of the keys and values of an item's i-th tile of cnt in the ring's order.
-__device__ __forceinline__ uint32_t k_place(int i) { return i == 0 ? 0u : 2u * i - 1u; }
+// Places of the keys and values of an item's i-th tile of cnt in the ring's
+// order, the keys AHEAD tiles before the values.
+template <int AHEAD>
+__device__ __forceinline__ uint32_t k_place(int i) {
+  return i <= AHEAD ? i : 2 * i - AHEAD;
+}
+template <int AHEAD>
 __device__ __forceinline__ uint32_t v_place(int i, int cnt) {
-  return i == cnt - 1 ? 2u * i + 1u : 2u * i + 2u;
+  return 2 * i + 1 + AHEAD - max(0, i - (cnt - 1 - AHEAD));
 }
 
 // Descriptor of V [keys][64 columns] as the MN-major B operand: 8 keys of 128
@@ -659,14 +670,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a) {
   using C = Tile<D, MODE>;
-  constexpr int TKT = C::TKT, RT = C::RT, SLOTS = C::SLOTS, DV = C::DV;
+  constexpr int TKT = C::TKT, RT = C::RT, SLOTS = C::SLOTS, NS = C::NS;
   constexpr int HALVES = D / 64;
   constexpr int HB = TKT * 128;          // 64 columns of a key or value tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sq = ring + SLOTS * C::SLOT;
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, q_empty, o_full, done, s_full[2], p_full[2];
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], q_full, q_empty, o_full, done, s_full[NS], p_full[NS];
+  // SHARED: out of an even or odd tile added (of the two, only one can be in
+  // flight when its phase is awaited); a tile's maximum known
+  __shared__ uint64_t o_step[2], m_ready[4];
+  __shared__ float s_m[MODE == SHARED ? 128 : 1];
   __shared__ PieceScratch<TILE_THREADS> scratch;
   __shared__ float2 s_ml[2][128];
   __shared__ unsigned int s_bad[8];
@@ -685,10 +700,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     ptx::mbar_init(&q_empty, 1);
     ptx::mbar_init(&o_full, 1);
     ptx::mbar_init(&done, 1);
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < NS; ++x) {
       ptx::mbar_init(&s_full[x], 1);
       ptx::mbar_init(&p_full[x], 4);
     }
+    for (int e = 0; e < 2; ++e) ptx::mbar_init(&o_step[e], 1);
+    for (int q = 0; q < 4; ++q) ptx::mbar_init(&m_ready[q], 1);
     s_abort = 0;
     s_any_bad = 0;
     for (int i = 0; i < 8; ++i) s_bad[i] = 0;
@@ -723,7 +740,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       int page = page_at<TKT>(a, s, s.t0, box_shift, lane);
       for (int i = 0; i < cnt; ++i) {
         const int ahead = i + 1 < cnt ? page_at<TKT>(a, s, s.t0 + i + 1, box_shift, lane) : 0;
-        const uint32_t n = seq0 + (vals ? v_place(i, cnt) : k_place(i));
+        const uint32_t n = seq0 + (vals ? v_place<C::AHEAD>(i, cnt) : k_place<C::AHEAD>(i));
         const uint32_t sl = n % SLOTS, par = (n / SLOTS) & 1u;
         ok = ptx::mbar_wait_warp(&empty[sl], par ^ 1u, abort_flag, WAIT_LIMIT);
         if (!ok) {
@@ -749,6 +766,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     // 64 that it runs.
     bool ok = true;
     uint32_t seq0 = 0, q_phase = 0, p_phase = 0;
+    uint32_t tile0 = 0;      // tiles of the items before
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!ok) return;
       ok = ptx::mbar_wait_warp(bar, parity, abort_flag, WAIT_LIMIT);
@@ -770,8 +788,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         const uint64_t db = k_desc + sl * (C::SLOT >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          ptx::mma_f16_ss(tm + C::S_COL + 128 * x, da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)),
-                          db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
+          ptx::mma_f16_ss(tm + C::S_COL + C::S_STEP * x,
+                          da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)), db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
         if (last) ptx::mma_commit(&empty[sl]);
         ptx::mma_commit(&s_full[x]);
         if (last && i == cnt - 1) ptx::mma_commit(&q_empty);   // the item's queries were read
@@ -780,7 +798,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       // (none: j >= cnt).  The ring's barriers are waited for before the
       // stream's P, which is the last to be ready.
       const auto step = [&](int i, int j, int x, bool first, bool ring, bool last) {
-        const uint32_t nv = seq0 + v_place(i, cnt), nk = seq0 + k_place(j);
+        const uint32_t nv = seq0 + v_place<C::AHEAD>(i, cnt), nk = seq0 + k_place<C::AHEAD>(j);
         const uint32_t sv = nv % SLOTS, sk = nk % SLOTS;
         if (ring) {
           wait(&full[sv], (nv / SLOTS) & 1u);
@@ -789,27 +807,36 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         wait(&p_full[x], (p_phase >> x) & 1u);
         p_phase ^= 1u << x;
         if (!ok) return;
-        const uint64_t dv = v_desc + (sv * (C::SLOT >> 4) + (MODE == COLS ? x * (2 * HB >> 4) : 0));
+        const uint64_t dv = v_desc + sv * (C::SLOT >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TKT / 16; ++k)
-            ptx::mma_f16_ts(tm + C::O_COL + 128 * x, tm + C::S_COL + 128 * x + k * 8,
-                            dv + k * (2048 >> 4), idesc<BF16>(DV, true),
-                            (!first || k > 0) ? 1u : 0u);
+            ptx::mma_f16_ts(tm + C::O_COL + (MODE == SHARED ? 0 : 128 * x),
+                            tm + C::S_COL + C::S_STEP * x + k * 8, dv + k * (2048 >> 4),
+                            idesc<BF16>(D, true), (!first || k > 0) ? 1u : 0u);
+          if (MODE == SHARED) ptx::mma_commit(&o_step[(tile0 + i) & 1u]);
           if (last) ptx::mma_commit(&empty[sv]);
           if (j < cnt) issue_s(sk, j, x, last);
         }
         __syncwarp();
       };
       const auto begin = [&](int i, int x, bool ring, bool last) {
-        const uint32_t nk = seq0 + k_place(i), sk = nk % SLOTS;
+        const uint32_t nk = seq0 + k_place<C::AHEAD>(i), sk = nk % SLOTS;
         if (ring) wait(&full[sk], (nk / SLOTS) & 1u);
         if (ok && elect_one()) issue_s(sk, i, x, last);
         __syncwarp();
       };
       wait(&q_full, q_phase);
       q_phase ^= 1u;
-      if constexpr (MODE == KEYS) {
+      if constexpr (MODE == SHARED) {
+        // S of tile i + 2 goes to the buffer whose P the MMA before read
+        for (int i = 0; i < min(cnt, 2); ++i) begin(i, (tile0 + i) % NS, true, true);
+        for (int i = 0; i < cnt && ok; ++i) {
+          if (i + 2 < cnt) begin(i + 2, (tile0 + i + 2) % NS, true, true);
+          step(i, cnt, (tile0 + i) % NS, i == 0, true, true);
+        }
+        tile0 += cnt;
+      } else if constexpr (MODE == KEYS) {
         begin(0, 0, true, true);
         if (cnt > 1) begin(1, 1, true, true);
         for (int i = 0; i < cnt && ok; i += 2) {
@@ -879,14 +906,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const int x = (warp - 4) >> 2;
     const int lrow = (warp & 3) * 32 + lane;           // row of the stream's tile, its lane
     const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + C::S_COL + 128 * x + lane_addr;
-    const uint32_t o_addr = tmem + C::O_COL + 128 * x + lane_addr;
+    uint32_t s_addr = tmem + C::S_COL + 128 * x + lane_addr;
+    const uint32_t o_addr = tmem + C::O_COL + (MODE == SHARED ? 0 : 128 * x) + lane_addr;
     const int wid = tid - 128;                         // 0 .. 255
     // the maximum is taken of the products themselves, so the scale must not
     // be negative (the queries' signs are turned as they are loaded) nor zero
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
+    uint32_t tile0 = 0;                                // tiles of the items before
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!ok) return;
       ok = ptx::mbar_wait_warp(bar, parity, abort_flag, WAIT_LIMIT);
@@ -905,7 +933,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       const uint64_t word0 = first_word(a, mw);
       float m = -INFINITY, l = 0.f;
       bool any = false;
-      for (int i = MODE == KEYS ? x : 0; i < cnt; i += MODE == KEYS ? 2 : 1) {
+      // KEYS: the stream's tiles are those of its parity; SHARED: the same,
+      // counted on over the items
+      for (int i = MODE == ROWS ? 0 : MODE == KEYS ? x : (tile0 + x) & 1; i < cnt;
+           i += MODE == ROWS ? 1 : 2) {
+        const int buf = MODE == SHARED ? (tile0 + i) % NS : x;
+        if constexpr (MODE == SHARED) {
+          s_addr = tmem + C::S_COL + C::S_STEP * buf + lane_addr;
+          s_phase = ((tile0 + i) / NS) & 1u;
+        }
         const int k0 = (s.t0 + i) * TKT;
         const bool edge = k0 + TKT > s.r.ctx;
         uint64_t vis[TKT / 64];
@@ -914,7 +950,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           for (int c = 0; c < TKT / 64; ++c)
             vis[c] = sees64(a, mw, word0, tok, k0 + 64 * c, s.r.ctx, s.r.len);
         }
-        wait(&s_full[x], s_phase);
+        wait(&s_full[buf], s_phase);
         s_phase ^= 1u;
         if (!ok) break;
         if (active) {
@@ -941,14 +977,39 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
           ptx::tmem_ld_32x32b_x32(s_addr + 32, v[1]);
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-          float f = 1.f;
-          if (mt > m + 8.f || (m == -INFINITY && mt != m)) {
-            f = ex2(m - mt);
-            m = mt;
+          float f = 1.f;            // of this thread's sum
+          bool move = false;        // of the accumulator, by `fo`
+          float fo = 1.f;
+          if constexpr (MODE == SHARED) {
+            float mp = -INFINITY;   // the other warpgroup's, of the tile before
+            if (i > 0) {
+              wait(&m_ready[warp & 3], (tile0 + i - 1) & 1u);
+              mp = *reinterpret_cast<volatile float*>(&s_m[lrow]);
+            }
+            float mn = mp;
+            if (mt > mp + 8.f || (mp == -INFINITY && mt != mp)) mn = mt;
+            *reinterpret_cast<volatile float*>(&s_m[lrow]) = mn;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&m_ready[warp & 3]);
+            if (mn != m) f = ex2(m - mn);
+            m = mn;
+            if (mn != mp) fo = ex2(mp - mn);
+            move = i > 0 && __any_sync(~0u, fo != 1.f);
+            if (move) {
+              wait(&o_step[(tile0 + i - 1) & 1u], ((tile0 + i - 1) >> 1) & 1u);
+              move = ok;
+            }
+          } else {
+            if (mt > m + 8.f || (m == -INFINITY && mt != m)) {
+              f = ex2(m - mt);
+              m = mt;
+            }
+            fo = f;
+            move = any && __any_sync(~0u, f != 1.f);
           }
-          if (any && __any_sync(~0u, f != 1.f)) {
+          if (move) {
 #pragma unroll 1
-            for (int c = 0; c < DV / 32; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
               tmem_ld_wait_for(o);
@@ -957,7 +1018,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                  w[e] = __float_as_uint(__uint_as_float(o[16 * h + e]) * f);
+                  w[e] = __float_as_uint(__uint_as_float(o[16 * h + e]) * fo);
                 tmem_st_x16(o_addr + 32 * c + 16 * h, w);
               }
             }
@@ -995,11 +1056,17 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           l = l * f + (all.x + all.y);
           ptx::tmem_st_wait();
+        } else if (MODE == SHARED && lane == 0) {
+          ptx::mbar_arrive(&m_ready[warp & 3]);    // its phases count tiles, whoever is active
         }
-        if (edge && (MODE == KEYS || x == 0)) {
+        if (edge && (MODE != ROWS || x == 0)) {
           // values past the last token count as zero, and so does a non-finite
           // value of a new token here (added at the item's end)
-          const uint32_t n = seq0 + v_place(i, cnt);
+          const uint32_t n = seq0 + v_place<C::AHEAD>(i, cnt);
+          // SHARED: S runs so far ahead that the values of two tiles before may
+          // still be on their way to this slot; a wait for a phase is only one
+          // once the phase before it is over
+          if (MODE == SHARED && i >= 2) wait(&o_step[(tile0 + i) & 1u], ((tile0 + i - 2) >> 1) & 1u);
           wait(&full[n % SLOTS], (n / SLOTS) & 1u);
           if (!ok) break;
           clean_values<BF16, D>(ring + (n % SLOTS) * C::SLOT, HB, k0, 0, TKT, s.r.ctx, s.r.len, lrow,
@@ -1007,20 +1074,21 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_full[x]);
+        if (lane == 0) ptx::mbar_arrive(&p_full[buf]);
       }
       // ---- the item's part is complete
       wait(&o_full, o_phase);
       o_phase ^= 1u;
       seq0 += 2u * cnt;
-      if constexpr (MODE == KEYS) s_ml[x][lrow] = make_float2(m, l);
+      tile0 += cnt;
+      if constexpr (MODE != ROWS) s_ml[x][lrow] = make_float2(m, l);
       ptx::named_sync(1, 256);
       const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
       const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
       const int64_t slot = 2 * int64_t(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
       if (ok && active) {
         float f0 = 1.f, f1 = 0.f;
-        if constexpr (MODE == KEYS) {
+        if constexpr (MODE != ROWS) {
           const float2 y = s_ml[x ^ 1][lrow];
           const float mm = fmaxf(m, y.x);
           f0 = mm == -INFINITY ? 0.f : ex2(m - mm);
@@ -1036,8 +1104,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = (int64_t(s.r.row0) + tok) * a.Hq + s.h * a.group + (r0 + my - tok * a.group);
         // KEYS: this warpgroup's half of the columns from both accumulators;
-        // ROWS: all columns of its rows; COLS: its columns
-        constexpr int NC = MODE == KEYS ? D / 2 : DV;
+        // SHARED: its half, which already refers to the larger maximum; ROWS:
+        // all columns of its rows
+        constexpr int NC = MODE == ROWS ? D : D / 2;
         const int col0 = MODE == ROWS ? 0 : x * NC;
 #pragma unroll 1
         for (int c = 0; c < NC / 32; ++c) {
@@ -1056,7 +1125,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
               for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(u[e]) * f1;
             }
           } else {
-            ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, u);
+            ptx::tmem_ld_32x32b_x32(o_addr + col0 + 32 * c, u);
             tmem_ld_wait_for(u);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
@@ -1264,7 +1333,7 @@ Choice choose(int64_t rows, int64_t D) {
   const int ctas = D == 256 ? 1 : 2;
   if (rows <= 8) return {1, 0, 8, ctas};
   if (rows <= 16) return {2, 0, 16, ctas};
-  if (D == 256) return {0, COLS, 128, 1};
+  if (D == 256) return {0, SHARED, 128, 1};
   return rows <= 128 ? Choice{0, KEYS, 128, 1} : Choice{0, ROWS, 256, 1};
 }
 
@@ -1325,7 +1394,7 @@ cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st)
   if (c.nt == 1) return launch_rows<BF16, D, 1>(call, a, st);
   if (c.nt == 2) return launch_rows<BF16, D, 2>(call, a, st);
   if constexpr (D == 256) {
-    return launch_tile<BF16, D, COLS>(call, a, st);
+    return launch_tile<BF16, D, SHARED>(call, a, st);
   } else {
     return c.mode == KEYS ? launch_tile<BF16, D, KEYS>(call, a, st)
                           : launch_tile<BF16, D, ROWS>(call, a, st);
