@@ -2,7 +2,9 @@
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``ternary_weight_linear_block_gb300/libtern.so``.  No cmake, no torch
-extension machinery: the library has a plain C ABI (include/tern.h).
+extension machinery: the library has a plain C ABI (include/tern.h).  Beside it
+the host compiler builds ``_kvcall.so``, the Python calls of kv.py (CPython's
+C API, csrc/kvcall.c), which takes the library's entry points by address.
 """
 
 from __future__ import annotations
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtern.so")
+EXT = os.path.join(PKG, "_kvcall.so")
 SOURCES = ["tern_abi.cu", "fwht.cu", "pack.cu", "gemv.cu", "gemm.cu", "noalloc.cu", "kv.cu",
            "attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,10 +51,10 @@ def _inputs():
 
 
 def is_stale() -> bool:
-    """True when libtern.so is missing or older than any of its sources."""
-    if not os.path.exists(LIB):
+    """True when libtern.so or _kvcall.so is missing or older than any source."""
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    built = os.path.getmtime(LIB)
+    built = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return any(os.path.getmtime(f) > built for f in _inputs())
 
 
@@ -73,8 +77,18 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
         rc, out = _run(cmd)
         return src, obj, rc, out
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        results = list(ex.map(compile_one, SOURCES))
+    def compile_ext():
+        cc = next((c for c in (os.environ.get("CC"), shutil.which("gcc"), shutil.which("cc")) if c), None)
+        if cc is None:
+            raise RuntimeError("no C compiler found")
+        src = "kvcall.c"
+        cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I",
+               os.path.join(ROOT, "include"), os.path.join(CSRC, src), "-o", EXT + ".tmp"]
+        return (src, None, *_run(cmd))
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(compile_ext)
+        results = list(ex.map(compile_one, SOURCES)) + [ext.result()]
     failed = [r for r in results if r[2] != 0]
     for src, _, rc, out in results:
         if verbose or rc != 0 or ptxas_info:
@@ -82,12 +96,13 @@ def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(r[0] for r in failed))
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[r[1] for r in results]]
+    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *[r[1] for r in results if r[1]]]
     rc, out = _run(cmd)
     if rc != 0:
         sys.stderr.write(out)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    os.replace(EXT + ".tmp", EXT)
     return LIB
 
 

@@ -89,6 +89,7 @@ template <int D, int NT>
 struct Rows {
   static constexpr int RT = 8 * NT;
   static constexpr int PAD = D == 64 ? 4 : 3;             // an item's cost beside its tiles
+  static constexpr int LEAST = PAD + 1;                   // places of a CTA's piece at least
   static constexpr int THREADS = (NW + 2) * 32;           // and a producer each of K and V
   static constexpr int STAGE = 2 * TK * D * 2;            // keys and values of a tile
   static constexpr int CTAS = D < 256 ? 2 : 1;            // per SM
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   }
   pdl_wait();
   pdl_launch_dependents();
-  const Piece piece = find_piece<TK, RT, C::PAD, THREADS>(a, scratch);   // synchronises the CTA
+  const Piece piece = find_piece<TK, RT, C::PAD, C::LEAST, THREADS>(a, scratch);   // synchronises the CTA
   if (piece.lo >= piece.hi) return;
 
   if (warp >= NW) {
@@ -225,27 +226,31 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
     };
     uint64_t word0 = 0;      // lane r: of the mask of the item's row r
     const auto rows_of = [&] { return min(RT, s.r.n * a.group - s.rt * RT); };
-    // the item's description and queries, or (none) the end
-    const auto post = [&](bool item) {
+    // the item's queries, once the one before needs its own no more
+    const auto post_queries = [&] {
       ok = give_up(ptx::mbar_wait_warp(&q_empty, q_phase, abort_flag, WAIT_LIMIT));
       if (!ok) return;
       q_phase ^= 1u;
       ++q_issued;
-      const int r0 = s.rt * RT;
-      const int rows = item ? rows_of() : 0;
-      if (lane < rows) {
-        const int tok = div_group(a, r0 + lane);
+      const int r = s.rt * RT + lane;
+      if (lane < rows_of()) {
+        const int tok = div_group(a, r);
         ptx::bulk_load(sq + lane * C::QLD,
                        a.q + (s.r.row0 + int64_t(tok)) * a.q_token +
-                           int64_t(s.h * a.group + (r0 + lane - tok * a.group)) * a.q_head,
+                           int64_t(s.h * a.group + (r - tok * a.group)) * a.q_head,
                        D * 2, &q_full);
-        s_word0[lane] = word0;
       }
+    };
+    // what the item is, or (none) that there is no further one
+    const auto post = [&](bool item) {
+      const int rows = item ? rows_of() : 0;
+      if (lane < rows) s_word0[lane] = word0;
       if (lane == 0) {
         const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
         const int first = whole ? 0 : cta_of(piece, s.first);
-        s_part = Part{s.b, s.h, r0, rows, s.r.row0, s.r.ctx, s.r.n, s.r.len, s.t0, item ? s.t1 : s.t0,
-                      whole, s.t0 == 0, first, whole ? 0 : cta_of(piece, s.end - 1) - first, {0, 0}};
+        s_part = Part{s.b, s.h, s.rt * RT, rows, s.r.row0, s.r.ctx, s.r.n, s.r.len, s.t0,
+                      item ? s.t1 : s.t0, whole, s.t0 == 0, first,
+                      whole ? 0 : cta_of(piece, s.end - 1) - first, {0, 0}};
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(rows) * D * 2);
@@ -254,6 +259,13 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       int page = page_at<TK>(a, s, s.t0, box_shift, lane);
       if (!vals && a.mask != nullptr && lane < rows_of())
         word0 = a.mask[(s.r.row0 + int64_t(div_group(a, s.rt * RT + lane))) * a.mask_words];
+      // the queries go first where their place is free (a CTA's first item:
+      // they are on their way while the page numbers are), else after a tile
+      bool posted = vals;
+      if (!vals && __all_sync(~0u, ptx::mbar_test_wait(&q_empty, q_phase))) {
+        post_queries();
+        posted = true;
+      }
       for (int t = s.t0; t < s.t1 && ok; ++t) {
         const int ahead = t + 1 < s.t1 ? page_at<TK>(a, s, t + 1, box_shift, lane) : 0;
         ok = give_up(ptx::mbar_wait_warp(&empty[st], phase ^ 1u, abort_flag, WAIT_LIMIT));
@@ -266,10 +278,16 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
           st = 0;
           phase ^= 1u;
         }
-        if (!vals && t == s.t0) post(true);
+        if (!vals && t == s.t0) {
+          if (!posted) post_queries();
+          if (ok) post(true);
+        }
       }
     }
-    if (ok && !vals) post(false);
+    if (ok && !vals) {
+      ok = give_up(ptx::mbar_wait_warp(&q_empty, q_phase, abort_flag, WAIT_LIMIT));
+      if (ok) post(false);
+    }
     if (!ok) {   // let the copies in flight land before the CTA exits
       const long back = issued < C::STAGES ? issued : C::STAGES;
       for (long i = 0; i < back; ++i) {
@@ -565,6 +583,7 @@ struct Tile {
   static constexpr int TKT = D == 256 ? 64 : 128;        // keys of a tile
   static constexpr int RT = MODE == ROWS ? 256 : 128;
   static constexpr int PAD = D == 64 ? 3 : 2;             // an item's cost beside its tiles
+  static constexpr int LEAST = PAD + 1;                   // places of a CTA's piece at least
   static constexpr int SLOT = TKT * D * 2;
   static constexpr int QB = 128 * D * 2;                 // one Q tile
   static constexpr int QBYTES = MODE == ROWS ? 2 * QB : QB;
@@ -720,7 +739,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   ptx::tc_fence_before();
   pdl_wait();
   pdl_launch_dependents();
-  const Piece piece = find_piece<TKT, RT, C::PAD, TILE_THREADS>(a, scratch);   // synchronises the CTA
+  const Piece piece = find_piece<TKT, RT, C::PAD, C::LEAST, TILE_THREADS>(a, scratch);   // synchronises the CTA
   ptx::tc_fence_after();
   const uint32_t tmem = s_tmem;
   if (tid == 128) a.items[blockIdx.x].follow = 0;   // the thread that may set it below

@@ -103,7 +103,7 @@ struct PieceScratch {
 };
 
 // Every thread of a CTA of NT threads (it synchronises them).
-template <int TK, int RT, int PAD, int NT>
+template <int TK, int RT, int PAD, int LEAST, int NT>
 __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = NT / 32;
@@ -137,7 +137,9 @@ __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) 
   };
   for (int base = 0; base < a.B; base += NT) round(base);
   p.total = carry;
-  p.ctas = static_cast<int>(min(int64_t(gridDim.x), p.total));
+  // no more CTAs than have LEAST places each: a part smaller than that costs
+  // more in starting and joining than it saves
+  p.ctas = static_cast<int>(min(int64_t(gridDim.x), max(quot(p.total, LEAST), min(p.total, int64_t(1)))));
   p.b = 0;
   p.base = 0;
   p.lo = p.hi = 0;
@@ -444,24 +446,41 @@ __device__ __forceinline__ void join_pieces(const Args& a, const Item (&items)[2
   // on, since every column's thread reads the piece's.
   const auto add_up = [&](const Item& it, int i0, int i1, int step, bool out) {
     const int64_t sums = step > 1 ? 2 * int64_t(grid) : 0;
+    // a thread has W groups of four columns of a row: with 16 rows or fewer
+    // nearly everything is read at once
+    constexpr int W = 4, CG = D / 4 / W;
 #pragma unroll 1
-    for (int p = tid; p < it.rows * (D / 4); p += N) {
-      const int d4 = p / it.rows, r = p - d4 * it.rows;
+    for (int p = tid; p < it.rows * CG; p += N) {
+      const int c = p / it.rows, r = p - c * it.rows;
       float m = -INFINITY, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 o[W];
+#pragma unroll
+      for (int k = 0; k < W; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
       for (int i = i0; i < i1; i += step) {
         const int64_t slot = slot_of(it, i);
         const float2 ml = __ldcg(a.part_ml + (sums + slot) * RT + r);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + d4) * RT + r) * 4));
-        add_piece(m, l, o, ml, x);
+        float4 x[W];
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + ((slot * (D / 4) + c + k * CG) * RT + r) * 4));
+        const float m0 = m, l0 = l;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+          m = m0;
+          l = l0;
+          add_piece(m, l, o[k], ml, x[k]);
+        }
       }
       if (out) {
-        write_joined<BF16, D>(a, it, r, d4, m, l, o);
+#pragma unroll
+        for (int k = 0; k < W; ++k) write_joined<BF16, D>(a, it, r, c + k * CG, m, l, o[k]);
       } else {
         const int64_t slot = slot_of(it, i0);
-        *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + d4) * RT + r) * 4) = o;
-        if (d4 == 0) a.part_ml[(2 * int64_t(grid) + slot) * RT + r] = make_float2(m, l);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+          *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + c + k * CG) * RT + r) * 4) = o[k];
+        if (c == 0) a.part_ml[(2 * int64_t(grid) + slot) * RT + r] = make_float2(m, l);
       }
     }
   };

@@ -17,6 +17,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
+import os
 from typing import NamedTuple, Sequence
 
 import torch
@@ -31,37 +34,32 @@ def _check(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _ints(t: torch.Tensor, name: str, dtype=torch.int32, ndim: int = 1):
-    if not (t.is_cuda and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()):
-        raise ValueError(f"{name}: expected a contiguous {ndim}-D CUDA tensor of {dtype}")
+_calls = None
 
 
-def _table(t: torch.Tensor, b: int):
-    """Row stride and width of a block table (rows may be longer than the part in use)."""
-    if t.is_cuda and t.dtype is torch.int32 and t.dim() == 2:
-        rows, width = t.shape
-        stride, one = t.stride()
-        if rows == b and (one == 1 or width <= 1) and (stride >= width or b <= 1):
-            return (stride if b > 1 else max(width, 1)), width
-    raise ValueError("table: expected an int32 CUDA tensor [requests, width], rows dense")
+def _native():
+    """The calls' checks and marshalling (csrc/kvcall.c, built with the library):
+    in Python they cost more host time at decode sizes than the launch."""
+    global _calls
+    if _calls is None:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_kvcall.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"_kvcall.so not built ({path}); run "
+                               "ternary_weight_linear_block_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_kvcall", path)
+        spec = importlib.util.spec_from_file_location("_kvcall", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        lib = B.lib()
+        names = ("tern_kv_plan", "tern_kv_write", "tern_tree_attention", "tern_kv_commit")
+        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
+                    torch.int32, torch.int64, torch.float32)
+        _calls = module
+    return _calls
 
 
-def _heads(t: torch.Tensor, heads: int, dim: int, dtype, name: str):
-    """Row and head strides of [rows, heads, dim], e.g. a slice of the qkv linear's output."""
-    if t.is_cuda and t.dtype is dtype and t.dim() == 3:
-        rows, h, d = t.shape
-        row, head, one = t.stride()
-        if h == heads and d == dim and one == 1:
-            return (row if rows > 1 else heads * dim), (head if heads > 1 else dim)
-    raise ValueError(f"{name}: expected a CUDA tensor [rows, {heads}, {dim}] of {dtype}, "
-                     "dense along the last axis")
-
-
-def _done(name: str, status: int):
-    """The entry points are called without the wrappers of ``binding``: at decode
-    sizes the wrappers would cost as much host time as the launch."""
-    if status:
-        raise B.TernError(name, status)
+def _failed(name: str, status: int):
+    raise B.TernError(name, status)
 
 
 @functools.lru_cache(maxsize=None)
@@ -134,48 +132,25 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
     those it has are taken from ``free_pages`` (from index free_head[0] on)
     and written into ``table`` in place.  ``capacity`` rows are planned;
     ``plan`` gives the outputs' buffers.  info[3] says what did not fit."""
-    b = ctx_len.shape[0]
-    _ints(ctx_len, "ctx_len")
-    _ints(new_len, "new_len")
-    _ints(free_pages, "free_pages")
-    _check(new_len.shape[0] == b, "new_len: expected as many requests as ctx_len")
-    stride, width = _table(table, b)
-    if free_head is not None:
-        _check(free_head.is_cuda and free_head.dtype == torch.int32 and free_head.numel() == 1,
-               "free_head: expected one int32 on the GPU")
     if plan is None:
         if stream is None:
-            plan = KVPlan.empty(b, capacity, ctx_len.device)
+            plan = KVPlan.empty(ctx_len.shape[0], capacity, ctx_len.device)
         else:
             with _on(stream):
-                plan = KVPlan.empty(b, capacity, ctx_len.device)
-    else:
-        _ints(plan.row_start, "plan.row_start")
-        _ints(plan.slots, "plan.slots", torch.int64)
-        for name in ("positions", "request", "info"):
-            _ints(getattr(plan, name), f"plan.{name}")
-        _check(plan.row_start.shape[0] == b + 1 and plan.info.shape[0] == 4 and
-               all(t.shape[0] >= capacity for t in plan[1:4]), "plan: buffers too small")
-    row_start, slots, positions, request, info = plan
-    _done("tern_kv_plan", B.lib().tern_kv_plan(
-        ctx_len.data_ptr(), new_len.data_ptr(), b, page_size, table.data_ptr(), stride, width,
-        free_pages.data_ptr(), free_pages.shape[0],
-        None if free_head is None else free_head.data_ptr(), row_start.data_ptr(), capacity,
-        slots.data_ptr(), positions.data_ptr(), request.data_ptr(), info.data_ptr(),
-        B._stream(stream)))
+                plan = KVPlan.empty(ctx_len.shape[0], capacity, ctx_len.device)
+    st = (_calls or _native()).plan(ctx_len, new_len, table, free_pages, free_head, page_size,
+                                    capacity, *plan, B._stream(stream))
+    if st:
+        _failed("tern_kv_plan", st)
     return plan
 
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
     """Rows of keys and values [T, heads, dim] into the cache's slots (-1: skipped)."""
-    kt, kh = _heads(k, cache.heads, cache.dim, cache.dtype, "k")
-    vt, vh = _heads(v, cache.heads, cache.dim, cache.dtype, "v")
-    _ints(slots, "slots", torch.int64)
-    t = k.shape[0]
-    _check(v.shape[0] == t and slots.shape[0] >= t, "v, slots: expected as many rows as k")
-    _done("tern_kv_write", B.lib().tern_kv_write(
-        cache.address, k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), t,
-        B._stream(stream)))
+    st = (_calls or _native()).write(cache.address, cache.dtype, cache.heads, cache.dim, k, v, slots,
+                                     B._stream(stream))
+    if st:
+        _failed("tern_kv_write", st)
 
 
 def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len: torch.Tensor,
@@ -190,26 +165,8 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
     sees 0 .. i).  Returns out [T, query heads, dim], and with ``return_lse``
     also the logarithm of each row's sum of exponentials (fp32 [T, query heads]).
     A row that sees nothing is 0, its lse -infinity."""
-    b = ctx_len.shape[0]
     t, hq, _ = q.shape
     heads, dim, dtype = cache.heads, cache.dim, cache.dtype
-    qt, qh = _heads(q, hq, dim, dtype, "q")
-    _check(hq > 0 and hq % heads == 0, "q: expected a multiple of the cache's heads")
-    _ints(ctx_len, "ctx_len")
-    _ints(row_start, "row_start")
-    _check(row_start.shape[0] == b + 1, "row_start: expected one more entry than requests")
-    stride, width = _table(table, b)
-    words = 0
-    if mask is not None:
-        _ints(mask, "mask", torch.int64, 2)
-        rows, words = mask.shape
-        _check(rows >= t and words > 0, "mask: expected [rows, words]")
-    if out is not None:
-        _check(out.is_cuda and out.dtype is dtype and out.shape == (t, hq, dim) and
-               out.is_contiguous(), "out: expected a contiguous [rows, query heads, dim]")
-    if lse is not None:
-        _check(lse.is_cuda and lse.dtype is torch.float32 and lse.shape == (t, hq) and
-               lse.is_contiguous(), "lse: expected a contiguous fp32 [rows, query heads]")
     if stream is not None and (out is None or ws is None or (return_lse and lse is None)):
         with _on(stream):          # what is allocated here belongs to that stream
             return tree_attention(q, cache, table, ctx_len, row_start, max_new, mask, scale, out,
@@ -218,15 +175,15 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
         out = torch.empty((t, hq, dim), dtype=dtype, device=cache.device)
     if return_lse and lse is None:
         lse = torch.empty((t, hq), dtype=torch.float32, device=cache.device)
-    nb = _workspace_bytes(max_new, hq, heads, dim)
     if ws is None:
         ws = B.Workspace(cache.device)
-    buf = ws.head(nb, B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
-    _done("tern_tree_attention", B.lib().tern_tree_attention(
-        q.data_ptr(), qt, qh, cache.address, table.data_ptr(), stride, width, ctx_len.data_ptr(),
-        row_start.data_ptr(), None if mask is None else mask.data_ptr(), words, b, t, hq, max_new,
-        dim ** -0.5 if scale is None else scale, out.data_ptr(),
-        None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), B._stream(stream)))
+    buf = ws.head(_workspace_bytes(max_new, hq, heads, dim), B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
+    st = (_calls or _native()).attention(
+        cache.address, dtype, heads, dim, q, table, ctx_len, row_start, max_new, mask,
+        dim ** -0.5 if scale is None else scale, out, lse, buf.data_ptr(), buf.numel(),
+        B._stream(stream))
+    if st:
+        _failed("tern_tree_attention", st)
     return (out, lse) if return_lse else out
 
 
@@ -239,26 +196,16 @@ def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len:
     path has to increase; it is cut where it does not."""
     if isinstance(caches, KVCache):
         caches = (caches,)
-    _check(len(caches) > 0, "caches: expected at least one")
-    b = ctx_len.shape[0]
-    _ints(ctx_len, "ctx_len")
-    _ints(path_len, "path_len")
-    _ints(path, "path", torch.int32, 2)
-    _check(path.shape[0] == b and path_len.shape[0] == b, "path, path_len: expected a row each request")
-    stride, width = _table(table, b)
     if ctx_out is None:
         if stream is None:
-            ctx_out = torch.empty(b, dtype=torch.int32, device=ctx_len.device)
+            ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
         else:
             with _on(stream):
-                ctx_out = torch.empty(b, dtype=torch.int32, device=ctx_len.device)
-    else:
-        _ints(ctx_out, "ctx_out")
-        _check(ctx_out.shape[0] == b, "ctx_out: expected as many requests as ctx_len")
-    _done("tern_kv_commit", B.lib().tern_kv_commit(
-        b"".join([c.desc_bytes for c in caches]), len(caches), table.data_ptr(), stride, width,
-        ctx_len.data_ptr(), path.data_ptr(), path.shape[1], path_len.data_ptr(),
-        ctx_out.data_ptr(), b, B._stream(stream)))
+                ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
+    st = (_calls or _native()).commit(b"".join([c.desc_bytes for c in caches]), len(caches), table,
+                                      ctx_len, path, path_len, ctx_out, B._stream(stream))
+    if st:
+        _failed("tern_kv_commit", st)
     return ctx_out
 
 
