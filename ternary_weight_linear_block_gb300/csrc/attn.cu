@@ -202,7 +202,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
   }
   pdl_wait();
   pdl_launch_dependents();
-  const Piece piece = find_piece<TK, RT, C::PAD, C::LEAST, THREADS>(a, scratch);   // synchronises the CTA
+  const Piece piece = find_piece<TK, C::PAD, C::LEAST, THREADS>(a, scratch);   // synchronises the CTA
   if (piece.lo >= piece.hi) return;
 
   if (warp >= NW) {
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
     // by themselves, that was a third of a short item's time.
     const bool vals = warp > NW;
     const CUtensorMap* map = vals ? &tm_v : &tm_k;
-    Walk<TK, RT, C::PAD> walk(a, piece);
+    Walk<TK, C::PAD> walk(a, piece);
     Seg s{};
     int st = 0;
     uint32_t phase = 0, q_phase = 1;
@@ -288,18 +288,17 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       ok = give_up(ptx::mbar_wait_warp(&q_empty, q_phase, abort_flag, WAIT_LIMIT));
       if (ok) post(false);
     }
-    if (!ok) {   // let the copies in flight land before the CTA exits
-      const long back = issued < C::STAGES ? issued : C::STAGES;
-      for (long i = 0; i < back; ++i) {
-        if (--st < 0) {
-          st = C::STAGES - 1;
-          phase ^= 1u;
-        }
-        if (!ptx::mbar_wait_bounded(&full[st], phase, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
+    // something gave up: the copies land before the CTA exits
+    const long back = ok && !*abort_flag ? 0 : issued < C::STAGES ? issued : C::STAGES;
+    for (long i = 0; i < back; ++i) {
+      if (--st < 0) {
+        st = C::STAGES - 1;
+        phase ^= 1u;
       }
-      if (q_issued > 0 && !ptx::mbar_wait_bounded(&q_full, q_phase, WAIT_LIMIT))
-        atomicOr(&g_attn_error, ERR_DRAIN);
+      if (!ptx::mbar_wait_bounded(&full[st], phase, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
     }
+    if (q_issued > 0 && (!ok || *abort_flag) && !ptx::mbar_wait_bounded(&q_full, q_phase, WAIT_LIMIT))
+      atomicOr(&g_attn_error, ERR_DRAIN);
     return;
   }
 
@@ -386,70 +385,72 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
       if (!ok) break;
       const uint32_t kbase = ring_u + st * C::STAGE;
       const uint32_t vbase = kbase + HALVES * HB;
-      if (edge) {
-        clean_values<BF16, D>(ring + st * C::STAGE + HALVES * HB, HB, t * TK, warp * 16,
-                              warp * 16 + 16, s.ctx, s.len, lane, 32, s_bad, &s_any_bad);
-        __syncwarp();
-      }
-      float c[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        uint32_t x[4];
-        const int chunk = (k & 3) * 2 + k_chunk;
-        ldsm_x4(kbase + (k >> 2) * HB + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), x);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816<BF16>(c[n], x, qf[k][n][0], qf[k][n][1]);
-      }
-      // c[n]: keys lane / 4 and + 8, rows row_c and + 1
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          c[n][e] *= a.scale_log2;
-          if (edge && !((vis[n][e & 1] >> (row_b + (e >> 1) * 8)) & 1)) c[n][e] = -INFINITY;
+      if (k0 < s.len || k0 == 0) {     // else past the last token: nothing to add
+        if (edge) {
+          clean_values<BF16, D>(ring + st * C::STAGE + HALVES * HB, HB, t * TK, warp * 16,
+                                warp * 16 + 16, s.ctx, s.len, lane, 32, s_bad, &s_any_bad);
+          __syncwarp();
         }
-      float al[NT][2];
-      bool moved = false;
-      uint32_t p[NT][2];
+        float c[NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float ms[2];
+        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(c[n][e], c[n][e + 2]);
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-          const float mn = fmaxf(m[n][e], x);
-          ms[e] = mn == -INFINITY ? 0.f : mn;
-          al[n][e] = ex2(m[n][e] - ms[e]);
-          moved |= mn != m[n][e];
-          m[n][e] = mn;
+        for (int k = 0; k < KS; ++k) {
+          uint32_t x[4];
+          const int chunk = (k & 3) * 2 + k_chunk;
+          ldsm_x4(kbase + (k >> 2) * HB + k_row * 128 + ((chunk ^ (k_row & 7)) << 4), x);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<BF16>(c[n], x, qf[k][n][0], qf[k][n][1]);
+        }
+        // c[n]: keys lane / 4 and + 8, rows row_c and + 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            c[n][e] *= a.scale_log2;
+            if (edge && !((vis[n][e & 1] >> (row_b + (e >> 1) * 8)) & 1)) c[n][e] = -INFINITY;
+          }
+        float al[NT][2];
+        bool moved = false;
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float ms[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaxf(c[n][e], c[n][e + 2]);
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            const float mn = fmaxf(m[n][e], x);
+            ms[e] = mn == -INFINITY ? 0.f : mn;
+            al[n][e] = ex2(m[n][e] - ms[e]);
+            moved |= mn != m[n][e];
+            m[n][e] = mn;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[n][e] = ex2(c[n][e] - ms[e & 1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) l[n][e] = l[n][e] * al[n][e] + (c[n][e] + c[n][e + 2]);
+          p[n][0] = movm(pack2<BF16>(c[n][0], c[n][1]));
+          p[n][1] = movm(pack2<BF16>(c[n][2], c[n][3]));
+        }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+          for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[i][n][e] *= al[n][e & 1];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[n][e] = ex2(c[n][e] - ms[e & 1]);
+        for (int i = 0; i < KS; ++i) {
+          uint32_t x[4];
+          const int chunk = (i & 3) * 2 + v_chunk;
+          ldsm_x4_t(vbase + (i >> 2) * HB + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), x);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) l[n][e] = l[n][e] * al[n][e] + (c[n][e] + c[n][e + 2]);
-        p[n][0] = movm(pack2<BF16>(c[n][0], c[n][1]));
-        p[n][1] = movm(pack2<BF16>(c[n][2], c[n][3]));
-      }
-      if (__any_sync(~0u, moved)) {
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][n][e] *= al[n][e & 1];
-      }
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        uint32_t x[4];
-        const int chunk = (i & 3) * 2 + v_chunk;
-        ldsm_x4_t(vbase + (i >> 2) * HB + v_row * 128 + ((chunk ^ (v_row & 7)) << 4), x);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) mma16816<BF16>(o[i][n], x, p[n][0], p[n][1]);
+          for (int n = 0; n < NT; ++n) mma16816<BF16>(o[i][n], x, p[n][0], p[n][1]);
+        }
       }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&empty[st]);
@@ -553,7 +554,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 
 // ------------------------------------------------------------------ tile kernel
 //
-// Up to 128 or 256 rows an item on tcgen05: S = Q K^T with 128 rows on the M
+// Up to 128 or 256 rows an item (whole tokens: 128 / group of them a stream)
+// on tcgen05: S = Q K^T with 128 rows on the M
 // side, the accumulator in tensor memory; a thread reads one row of S, writes
 // the row's probabilities over it as 16-bit values, and out += P V takes P
 // from tensor memory and V from the ring as its pages hold it (columns of V
@@ -677,6 +679,11 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return d;
 }
 
+__device__ __forceinline__ void turn_signs(uint32_t (&v)[2][32]) {
+#pragma unroll
+  for (int e = 0; e < 64; ++e) v[e >> 5][e & 31] ^= 0x80000000u;
+}
+
 // Scores that a row does not see.
 __device__ __forceinline__ void mask_out(uint32_t (&v)[32], uint32_t vis) {
 #pragma unroll
@@ -687,7 +694,8 @@ __device__ __forceinline__ void mask_out(uint32_t (&v)[32], uint32_t vis) {
 template <bool BF16, int D, int MODE>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Args a) {
+                     const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ Args a) {
   using C = Tile<D, MODE>;
   constexpr int TKT = C::TKT, RT = C::RT, SLOTS = C::SLOTS, NS = C::NS;
   constexpr int HALVES = D / 64;
@@ -731,6 +739,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     ptx::mbar_fence_init();
     ptx::prefetch_tmap(&tm_k);
     ptx::prefetch_tmap(&tm_v);
+    ptx::prefetch_tmap(&tm_q);
   }
   if (warp == 2) {
     ptx::tmem_alloc(&s_tmem, 512);
@@ -739,11 +748,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   ptx::tc_fence_before();
   pdl_wait();
   pdl_launch_dependents();
-  const Piece piece = find_piece<TKT, RT, C::PAD, C::LEAST, TILE_THREADS>(a, scratch);   // synchronises the CTA
+  const Piece piece = find_piece<TKT, C::PAD, C::LEAST, TILE_THREADS>(a, scratch);   // synchronises the CTA
   ptx::tc_fence_after();
   const uint32_t tmem = s_tmem;
   if (tid == 128) a.items[blockIdx.x].follow = 0;   // the thread that may set it below
-  Walk<TKT, RT, C::PAD> walk(a, piece);
+  const int stream_rows = MODE == ROWS ? a.tile_rows / 2 : a.tile_rows;   // at most 128
+  Walk<TKT, C::PAD> walk(a, piece);
   Seg s{};
 
   if (warp == 0 || warp == 3) {
@@ -773,10 +783,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       }
       seq0 += 2u * cnt;
     }
-    if (!ok)   // let the copies in flight land before the CTA exits
-      for (int sl = 0; sl < SLOTS; ++sl)
-        if (((mine >> sl) & 1u) && !ptx::mbar_wait_bounded(&full[sl], (parity >> sl) & 1u, WAIT_LIMIT))
-          atomicOr(&g_attn_error, ERR_DRAIN);
+    // something gave up: the copies land before the CTA exits
+    for (int sl = 0; (!ok || *abort_flag) && sl < SLOTS; ++sl)
+      if (((mine >> sl) & 1u) && !ptx::mbar_wait_bounded(&full[sl], (parity >> sl) & 1u, WAIT_LIMIT))
+        atomicOr(&g_attn_error, ERR_DRAIN);
   } else if (warp == 1) {
     // ---------------- MMA issuer: the whole warp waits and counts, one elected
     // lane issues.  Counters are made uniform over the warp (shuffles, votes),
@@ -827,10 +837,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         p_phase ^= 1u << x;
         if (!ok) return;
         const uint64_t dv = v_desc + sv * (C::SLOT >> 4);
+        // steps of 16 keys up to the request's last
+        const int steps = __shfl_sync(~0u, (s.r.len - (s.t0 + i) * TKT + 15) >> 4, 0);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TKT / 16; ++k)
-            ptx::mma_f16_ts(tm + C::O_COL + (MODE == SHARED ? 0 : 128 * x),
+            if (k == 0 || k < steps) ptx::mma_f16_ts(tm + C::O_COL + (MODE == SHARED ? 0 : 128 * x),
                             tm + C::S_COL + C::S_STEP * x + k * 8, dv + k * (2048 >> 4),
                             idesc<BF16>(D, true), (!first || k > 0) ? 1u : 0u);
           if (MODE == SHARED) ptx::mma_commit(&o_step[(tile0 + i) & 1u]);
@@ -863,11 +875,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           if (i + 1 < cnt) step(i + 1, i + 3, 1, i == 0, true, true);
         }
       } else {
-        begin(0, 0, true, false);
-        begin(0, 1, false, true);
+        const bool two = __any_sync(~0u, s.r.n * a.group - s.rt * a.tile_rows > stream_rows);
+        begin(0, 0, true, !two);
+        if (two) begin(0, 1, false, true);
         for (int i = 0; i < cnt && ok; ++i) {
-          step(i, i + 1, 0, i == 0, true, false);
-          step(i, i + 1, 1, i == 0, false, true);
+          step(i, i + 1, 0, i == 0, true, !two);
+          if (two) step(i, i + 1, 1, i == 0, false, true);
         }
       }
       if (ok && elect_one()) ptx::mma_commit(&o_full);
@@ -879,46 +892,31 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     __syncwarp();
     if (!ptx::mbar_wait_bounded(&done, 0, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
   } else if (warp == 2) {
-    // ---------------- queries: an item's rows, swizzled as TMA would, as soon
-    // as the item before needs its own no more.  Rows past the item's last
-    // keep what was there: they reach only their own rows of S.
+    // ---------------- queries: an item's rows, as soon as the item before
+    // needs its own no more.  A stream's rows are whole tokens with the heads
+    // of the group, which is how a box of [tokens][heads][64 values] lies in
+    // shared memory.  Rows past the request's last token are another's or
+    // zero: they reach only their own rows of S.
     bool ok = true;
     uint32_t parity = 1;
+    const int tokens = stream_rows / a.group;
     while (ok && walk.next(s)) {
-      const int r0 = s.rt * RT;
-      const int rows = min(RT, s.r.n * a.group - r0);
       ok = ptx::mbar_wait_warp(&q_empty, parity, abort_flag, WAIT_LIMIT);
       if (!ok) {
         if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
         break;
       }
       parity ^= 1u;
-      const auto place = [&](int i) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        return sq + (r >> 7) * C::QB + (c >> 3) * (128 * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
-      };
-#pragma unroll 4
-      for (int i = lane; i < rows * (D / 8); i += 32) {
-        const int g = r0 + i / (D / 8);
-        const int token = div_group(a, g);
-        const uint16_t* q = a.q + (s.r.row0 + int64_t(token)) * a.q_token +
-                            int64_t(s.h * a.group + (g - token * a.group)) * a.q_head + i % (D / 8) * 8;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(place(i))),
-                     "l"(q)
-                     : "memory");
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (a.scale_log2 < 0.f)    // the softmax takes the scale's absolute value
-        for (int i = lane; i < rows * (D / 8); i += 32) {
-          uint4* at = reinterpret_cast<uint4*>(place(i));
-          const uint4 v = *at;
-          constexpr uint32_t F = 0x80008000u;
-          *at = make_uint4(v.x ^ F, v.y ^ F, v.z ^ F, v.w ^ F);
-        }
-      ptx::fence_proxy_async_smem();
+      const bool two = MODE == ROWS && s.r.n * a.group - s.rt * a.tile_rows > stream_rows;
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(stream_rows) * D * (two ? 4 : 2));
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&q_full);
+      const int x = lane / HALVES, half = lane % HALVES;
+      if (x < (two ? 2 : 1))
+        ptx::tma_load_3d(sq + x * C::QB + half * (128 * 128), &tm_q, &q_full, half * 64,
+                         s.h * a.group, s.r.row0 + (s.rt * (MODE == ROWS ? 2 : 1) + x) * tokens);
     }
+    if (!ptx::mbar_wait_bounded(&q_full, parity, WAIT_LIMIT)) atomicOr(&g_attn_error, ERR_DRAIN);
   } else if (warp >= 4) {
     // ---------------- softmax and output: warpgroup x has stream x, a thread
     // one row of it
@@ -929,8 +927,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t o_addr = tmem + C::O_COL + (MODE == SHARED ? 0 : 128 * x) + lane_addr;
     const int wid = tid - 128;                         // 0 .. 255
     // the maximum is taken of the products themselves, so the scale must not
-    // be negative (the queries' signs are turned as they are loaded) nor zero
+    // be negative (the products' signs are turned instead) nor zero
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    const bool turned = a.scale_log2 < 0.f;
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
     uint32_t tile0 = 0;                                // tiles of the items before
@@ -942,19 +941,23 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     };
     while (walk.next(s)) {
       const int rows_all = s.r.n * a.group;
-      const int r0 = s.rt * RT;
-      const int rows = min(RT, rows_all - r0);
+      const int r0 = s.rt * a.tile_rows;
+      const int rows = min(a.tile_rows, rows_all - r0);
       const int cnt = s.t1 - s.t0;
-      const int my = (MODE == ROWS ? 128 * x : 0) + lrow;      // row of the item
-      const bool active = (MODE == ROWS ? 128 * x : 0) + (warp & 3) * 32 < rows;
-      const int tok = my < rows ? div_group(a, r0 + my) : 0;
+      // row of the item, of which the stream has some from `base` on
+      const int base = MODE == ROWS ? stream_rows * x : 0;
+      const bool has = lrow < stream_rows && base + lrow < rows;
+      const int my = base + lrow;
+      const bool active = base + (warp & 3) * 32 < rows;
+      const int tok = has ? div_group(a, r0 + my) : 0;
       const uint64_t* mw = a.mask != nullptr ? a.mask + (s.r.row0 + int64_t(tok)) * a.mask_words : nullptr;
       const uint64_t word0 = first_word(a, mw);
       float m = -INFINITY, l = 0.f;
       bool any = false;
       // KEYS: the stream's tiles are those of its parity; SHARED: the same,
       // counted on over the items
-      for (int i = MODE == ROWS ? 0 : MODE == KEYS ? x : (tile0 + x) & 1; i < cnt;
+      // (ROWS: a stream without rows has no S either)
+      for (int i = MODE == ROWS ? (base < rows ? 0 : cnt) : MODE == KEYS ? x : (tile0 + x) & 1; i < cnt;
            i += MODE == ROWS ? 1 : 2) {
         const int buf = MODE == SHARED ? (tile0 + i) % NS : x;
         if constexpr (MODE == SHARED) {
@@ -983,6 +986,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 32, v[1]);
             tmem_ld_wait_for(v[0]);
             tmem_ld_wait_for(v[1]);
+            if (turned) turn_signs(v);
             if (edge) {
               const uint64_t bits = TKT == 64 || c == 0 ? vis[0] : vis[TKT / 64 - 1];
               mask_out(v[0], static_cast<uint32_t>(bits));
@@ -1051,6 +1055,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             // P's columns 16 c .. overwrite columns of S that were read before
             tmem_ld_wait_for(v[0]);
             tmem_ld_wait_for(v[1]);
+            if (turned) turn_signs(v);
             if (edge) {
               const uint64_t bits = TKT == 64 || c == 0 ? vis[0] : vis[TKT / 64 - 1];
               mask_out(v[0], static_cast<uint32_t>(bits));
@@ -1088,7 +1093,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           if (MODE == SHARED && i >= 2) wait(&o_step[(tile0 + i) & 1u], ((tile0 + i - 2) >> 1) & 1u);
           wait(&full[n % SLOTS], (n / SLOTS) & 1u);
           if (!ok) break;
-          clean_values<BF16, D>(ring + (n % SLOTS) * C::SLOT, HB, k0, 0, TKT, s.r.ctx, s.r.len, lrow,
+          clean_values<BF16, D>(ring + (n % SLOTS) * C::SLOT, HB, k0, 0,
+                                min(TKT, (max(s.r.len - k0, 1) + 15) & ~15), s.r.ctx, s.r.len, lrow,
                                 128, s_bad, &s_any_bad);
         }
         ptx::tc_fence_before();
@@ -1149,7 +1155,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
           }
-          if (my < rows) {
+          if (has) {
             const int d = col0 + 32 * c;
             if (whole) {
 #pragma unroll
@@ -1174,7 +1180,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                             a.part_o + ((slot * (D / 4) + d / 4) * RT + my) * 4, 4 * RT);
           }
         }
-        if (my < rows && (MODE == ROWS || x == 0)) {
+        if (has && (MODE == ROWS || x == 0)) {
           if (!whole)
             a.part_ml[slot * RT + my] = make_float2(m, l);
           else if (a.lse != nullptr)
@@ -1327,6 +1333,22 @@ bool make_map(CUtensorMap* map, const tern_kv_cache& c, void* base, int rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_query_map(CUtensorMap* map, const TreeAttnCall& call, int tokens, int group) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(call.cache.dim), static_cast<cuuint64_t>(call.Hq),
+                              static_cast<cuuint64_t>(call.T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(call.q_head_stride) * 2,
+                                 static_cast<cuuint64_t>(call.q_token_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const auto type = call.cache.dtype == TERN_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return enc(map, type, 3, const_cast<void*>(call.q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The workspace: arrival counters, which are zero between calls, then the
 // pieces.
 struct Ws {
@@ -1348,12 +1370,13 @@ struct Choice {
   int mode;       // tile kernel
   int rt, ctas;
 };
-Choice choose(int64_t rows, int64_t D) {
+Choice choose(int64_t max_new, int64_t group, int64_t D) {
+  const int64_t rows = max_new * group;
   const int ctas = D == 256 ? 1 : 2;
   if (rows <= 8) return {1, 0, 8, ctas};
-  if (rows <= 16) return {2, 0, 16, ctas};
+  if (rows <= 16 || group > 128) return {2, 0, 16, ctas};   // the tile kernel takes whole tokens
   if (D == 256) return {0, SHARED, 128, 1};
-  return rows <= 128 ? Choice{0, KEYS, 128, 1} : Choice{0, ROWS, 256, 1};
+  return rows <= 128 / group * group ? Choice{0, KEYS, 128, 1} : Choice{0, ROWS, 256, 1};
 }
 
 cudaError_t set_up(const TreeAttnCall& call, int keys, int grid, int rt, Args& a, CUtensorMap& tk,
@@ -1367,6 +1390,7 @@ cudaError_t set_up(const TreeAttnCall& call, int keys, int grid, int rt, Args& a
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.arrived = reinterpret_cast<int*>(ws);
   a.items = reinterpret_cast<Item*>(ws + w.items);
+  a.tile_rows = rt;
   return cudaSuccess;
 }
 
@@ -1401,7 +1425,12 @@ cudaError_t launch_tile(const TreeAttnCall& call, Args a, cudaStream_t st) {
   CUtensorMap tk, tv;
   e = set_up(call, C::TKT, grid, C::RT, a, tk, tv);
   if (e != cudaSuccess) return e;
-  e = launch(attn_tile_kernel<BF16, D, MODE>, dim3(grid), dim3(TILE_THREADS), C::SMEM, st, tk, tv, a);
+  // the queries as [T][Hq][D]: boxes of a stream's tokens and the group's heads
+  const int tokens = 128 / a.group;
+  a.tile_rows = tokens * a.group * (MODE == ROWS ? 2 : 1);
+  CUtensorMap tq;
+  if (!make_query_map(&tq, call, tokens, a.group)) return cudaErrorInvalidValue;
+  e = launch(attn_tile_kernel<BF16, D, MODE>, dim3(grid), dim3(TILE_THREADS), C::SMEM, st, tk, tv, tq, a);
   if (e != cudaSuccess) return e;
   return launch(combine_kernel<BF16, D>, dim3(4 * kv_sm_count()), dim3(JOIN_THREADS), 0, st, a, C::RT,
                 grid);
@@ -1409,7 +1438,7 @@ cudaError_t launch_tile(const TreeAttnCall& call, Args a, cudaStream_t st) {
 
 template <bool BF16, int D>
 cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st) {
-  const Choice c = choose(call.max_new * a.group, D);
+  const Choice c = choose(call.max_new, a.group, D);
   if (c.nt == 1) return launch_rows<BF16, D, 1>(call, a, st);
   if (c.nt == 2) return launch_rows<BF16, D, 2>(call, a, st);
   if constexpr (D == 256) {
@@ -1423,7 +1452,7 @@ cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st)
 }  // namespace
 
 size_t tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
-  const Choice c = choose(max_new * (Hq / H), D);
+  const Choice c = choose(max_new, Hq / H, D);
   return ws_layout(std::min(kv_sm_count() * c.ctas, MAX_GRID), c.rt, D).bytes;
 }
 

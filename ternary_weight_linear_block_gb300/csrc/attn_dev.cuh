@@ -43,6 +43,7 @@ struct Args {
   int64_t page_stride, token_stride, head_stride;
   int width, pages, page_shift, mask_words, B, T, H, group, Hq;
   uint32_t group_mul;       // 2^32 / group + 1, or 0 (div_group)
+  int tile_rows;            // rows of an item, RT or (tile kernel) whole tokens of it
   float scale_log2;
 };
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ int64_t line_of(const Args& a, const Req& r) {
   return r.n > 0 ? int64_t(a.H) * r.rts * (r.tiles + PAD) : 0;
 }
 
-template <int TK, int RT>
+template <int TK>
 __device__ __forceinline__ Req load_req(const Args& a, int b) {
   Req r;
   const int s0 = a.row_start[b], s1 = a.row_start[b + 1];
@@ -75,7 +76,8 @@ __device__ __forceinline__ Req load_req(const Args& a, int b) {
   r.ctx = min(max(a.ctx_len[b], 0), cap);
   r.len = static_cast<int>(min(int64_t(r.ctx) + r.n, int64_t(cap)));
   r.tiles = r.n > 0 ? max((r.len + TK - 1) / TK, 1) : 0;
-  r.rts = static_cast<int>((uint32_t(r.n) * uint32_t(a.group) + RT - 1) / RT);   // below 2^28 rows
+  const uint32_t rt = a.tile_rows;
+  r.rts = static_cast<int>((uint32_t(r.n) * uint32_t(a.group) + rt - 1) / rt);   // below 2^28 rows
   return r;
 }
 
@@ -103,7 +105,7 @@ struct PieceScratch {
 };
 
 // Every thread of a CTA of NT threads (it synchronises them).
-template <int TK, int RT, int PAD, int LEAST, int NT>
+template <int TK, int PAD, int LEAST, int NT>
 __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int W = NT / 32;
@@ -115,7 +117,7 @@ __device__ __forceinline__ Piece find_piece(const Args& a, PieceScratch<NT>& s) 
     const int b = base + tid;
     mine = 0;
     if (b < a.B) {
-      r = load_req<TK, RT>(a, b);
+      r = load_req<TK>(a, b);
       mine = line_of<PAD>(a, r);
     }
     int64_t x = mine;
@@ -182,7 +184,7 @@ struct Seg {
 };
 
 // Steps through a piece item by item.  Each role of a CTA walks on its own.
-template <int TK, int RT, int PAD>
+template <int TK, int PAD>
 struct Walk {
   const Args& a;
   int64_t w, hi, base;
@@ -197,7 +199,7 @@ struct Walk {
       while (w - base >= size) {   // the line covers w: a request with tiles follows
         base += size;
         ++b;
-        r = load_req<TK, RT>(a, b);
+        r = load_req<TK>(a, b);
         size = line_of<PAD>(a, r);
       }
       const int64_t off = w - base;

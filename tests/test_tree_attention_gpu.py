@@ -211,6 +211,18 @@ def test_cached_keys_that_are_not_finite_reach_every_row():
     assert torch.isnan(out).all() and torch.isnan(lse).all()
 
 
+@pytest.mark.parametrize("group", [3, 5, 7, 12, 130])
+def test_groups_that_do_not_divide_a_tile(group):
+    c = Case([150, 9], [31, 12] if group < 100 else [2, 1], 2, group, 64, 32, BF, seed=group)
+    check(c.run(), c.reference())
+
+
+@pytest.mark.parametrize("dim,new", [(64, 60), (128, 11), (128, 40), (256, 12)])
+def test_negative_scale(dim, new):
+    c = Case([300, 70], [new, 2], 2, 4, dim, 16, HF, scale=-0.15, seed=dim)
+    check(c.run(), c.reference())
+
+
 def test_scores_far_apart_and_negative_scale():
     c = Case([600, 40], [7, 3], 2, 2, 128, 16, BF, scale=3.0)
     check(c.run(), c.reference())
