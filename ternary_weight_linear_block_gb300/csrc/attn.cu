@@ -562,15 +562,17 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // along the MMA's N side: the MN-major operand).  Keys and values arrive in a
 // ring of slots in the order K0 K1 V0 K2 V1 K3 ...
 //
-// Two streams, each with its S, its out accumulator and a warpgroup, so that
-// one stream's softmax runs beside the other's MMAs:
-//   KEYS  rows <= 128:  the streams take the even and the odd key tiles
-//   ROWS  rows <= 256:  each has 128 rows; a key tile serves both
-//   SHARED head size 256, whose accumulator of 256 columns fits tensor memory
-//         once: the warpgroups take the tiles in turn and share it.  A row's
-//         reference maximum goes from one to the other through shared memory,
-//         tile by tile, and whoever has to move it waits for the MMA before
-//         and rescales.  S has three buffers and runs two tiles ahead.
+// Two warpgroups, so that one's softmax runs beside the MMAs for the other:
+//   SHARED rows <= 128: they take the key tiles in turn and share the out
+//          accumulator.  A row's reference maximum goes from one to the other
+//          through shared memory, tile by tile, and whoever has to move it
+//          waits for the MMA before and rescales.  S has three buffers and
+//          runs two tiles ahead.  (An accumulator for each, joined at the end,
+//          measured the same with head size 128 and 64; with 256 columns it
+//          does not fit, and a half of the columns for each, S computed twice,
+//          took 109 us against 82 on 8 requests of 20003 keys.)
+//   ROWS   rows <= 256, head size 64 or 128: each has 128 rows with their own
+//          S and accumulator (a stream); a key tile serves both.
 // The maximum that a row's exponents refer to only moves when it grows by
 // more than 2^8: until then nothing is rescaled (probabilities up to 256 are
 // as exact in the 16-bit types, and sums are in 32 bits), so the pass over
@@ -578,7 +580,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // whole warps of them skip the softmax.
 
 constexpr int TILE_THREADS = 384;   // K producer, MMA, TMEM, V producer; two warpgroups
-enum Mode { KEYS, ROWS, SHARED };
+enum Mode { SHARED, ROWS };
 
 template <int D, int MODE>
 struct Tile {
@@ -596,7 +598,7 @@ struct Tile {
   static constexpr int NS = MODE == SHARED ? 3 : 2;      // buffers of S
   static constexpr int S_STEP = MODE == SHARED ? TKT : 128;
   // accumulators: stream x at O_COL + 128 x; SHARED: one
-  static constexpr uint32_t S_COL = 0, O_COL = 256;
+  static constexpr uint32_t S_COL = 0, O_COL = MODE == SHARED && D < 256 ? 384 : 256;
   static_assert(SLOTS >= 4, "ring");
 };
 
@@ -867,13 +869,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           step(i, cnt, (tile0 + i) % NS, i == 0, true, true);
         }
         tile0 += cnt;
-      } else if constexpr (MODE == KEYS) {
-        begin(0, 0, true, true);
-        if (cnt > 1) begin(1, 1, true, true);
-        for (int i = 0; i < cnt && ok; i += 2) {
-          step(i, i + 2, 0, i == 0, true, true);
-          if (i + 1 < cnt) step(i + 1, i + 3, 1, i == 0, true, true);
-        }
       } else {
         const bool two = __any_sync(~0u, s.r.n * a.group - s.rt * a.tile_rows > stream_rows);
         begin(0, 0, true, !two);
@@ -954,10 +949,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       const uint64_t word0 = first_word(a, mw);
       float m = -INFINITY, l = 0.f;
       bool any = false;
-      // KEYS: the stream's tiles are those of its parity; SHARED: the same,
-      // counted on over the items
+      // SHARED: the tiles of this warpgroup's parity, counted over all items
       // (ROWS: a stream without rows has no S either)
-      for (int i = MODE == ROWS ? (base < rows ? 0 : cnt) : MODE == KEYS ? x : (tile0 + x) & 1; i < cnt;
+      for (int i = MODE == SHARED ? (tile0 + x) & 1 : base < rows ? 0 : cnt; i < cnt;
            i += MODE == ROWS ? 1 : 2) {
         const int buf = MODE == SHARED ? (tile0 + i) % NS : x;
         if constexpr (MODE == SHARED) {
@@ -1083,7 +1077,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         } else if (MODE == SHARED && lane == 0) {
           ptx::mbar_arrive(&m_ready[warp & 3]);    // its phases count tiles, whoever is active
         }
-        if (edge && (MODE != ROWS || x == 0)) {
+        if (edge && (MODE == SHARED || x == 0)) {
           // values past the last token count as zero, and so does a non-finite
           // value of a new token here (added at the item's end)
           const uint32_t n = seq0 + v_place<C::AHEAD>(i, cnt);
@@ -1106,55 +1100,32 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       o_phase ^= 1u;
       seq0 += 2u * cnt;
       tile0 += cnt;
-      if constexpr (MODE != ROWS) s_ml[x][lrow] = make_float2(m, l);
+      if constexpr (MODE == SHARED) s_ml[x][lrow] = make_float2(m, l);
       ptx::named_sync(1, 256);
       const bool any_bad = *reinterpret_cast<volatile int*>(&s_any_bad) != 0;
       const bool whole = s.t0 == 0 && s.t1 == s.r.tiles;
       const int64_t slot = 2 * int64_t(blockIdx.x) + (s.t0 == 0 ? 1 : 0);
       if (ok && active) {
-        float f0 = 1.f, f1 = 0.f;
-        if constexpr (MODE != ROWS) {
+        if constexpr (MODE == SHARED) {      // the sums of both warpgroups' tiles
           const float2 y = s_ml[x ^ 1][lrow];
           const float mm = fmaxf(m, y.x);
-          f0 = mm == -INFINITY ? 0.f : ex2(m - mm);
-          f1 = mm == -INFINITY ? 0.f : ex2(y.x - mm);
-          l = l * f0 + y.y * f1;
+          l = l * (mm == -INFINITY ? 0.f : ex2(m - mm)) + y.y * (mm == -INFINITY ? 0.f : ex2(y.x - mm));
           m = mm;
-          if (x == 1) {        // f0 is stream 0's
-            const float z = f0;
-            f0 = f1;
-            f1 = z;
-          }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = (int64_t(s.r.row0) + tok) * a.Hq + s.h * a.group + (r0 + my - tok * a.group);
-        // KEYS: this warpgroup's half of the columns from both accumulators;
-        // SHARED: its half, which already refers to the larger maximum; ROWS:
-        // all columns of its rows
+        // SHARED: this warpgroup's half of the columns, which refer to the larger
+        // maximum already; ROWS: all columns of its rows
         constexpr int NC = MODE == ROWS ? D : D / 2;
         const int col0 = MODE == ROWS ? 0 : x * NC;
 #pragma unroll 1
         for (int c = 0; c < NC / 32; ++c) {
           float o[32];
           uint32_t u[32];
-          if constexpr (MODE == KEYS) {
-            const uint32_t base = tmem + C::O_COL + lane_addr + col0 + 32 * c;
-            ptx::tmem_ld_32x32b_x32(base, u);
-            tmem_ld_wait_for(u);
+          ptx::tmem_ld_32x32b_x32(o_addr + col0 + 32 * c, u);
+          tmem_ld_wait_for(u);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]) * f0;
-            if (cnt > 1) {
-              ptx::tmem_ld_32x32b_x32(base + 128, u);
-              tmem_ld_wait_for(u);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(u[e]) * f1;
-            }
-          } else {
-            ptx::tmem_ld_32x32b_x32(o_addr + col0 + 32 * c, u);
-            tmem_ld_wait_for(u);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
-          }
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
           if (has) {
             const int d = col0 + 32 * c;
             if (whole) {
@@ -1375,8 +1346,8 @@ Choice choose(int64_t max_new, int64_t group, int64_t D) {
   const int ctas = D == 256 ? 1 : 2;
   if (rows <= 8) return {1, 0, 8, ctas};
   if (rows <= 16 || group > 128) return {2, 0, 16, ctas};   // the tile kernel takes whole tokens
-  if (D == 256) return {0, SHARED, 128, 1};
-  return rows <= 128 / group * group ? Choice{0, KEYS, 128, 1} : Choice{0, ROWS, 256, 1};
+  if (D == 256 || rows <= 128 / group * group) return {0, SHARED, 128, 1};
+  return {0, ROWS, 256, 1};
 }
 
 cudaError_t set_up(const TreeAttnCall& call, int keys, int grid, int rt, Args& a, CUtensorMap& tk,
@@ -1444,8 +1415,8 @@ cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st)
   if constexpr (D == 256) {
     return launch_tile<BF16, D, SHARED>(call, a, st);
   } else {
-    return c.mode == KEYS ? launch_tile<BF16, D, KEYS>(call, a, st)
-                          : launch_tile<BF16, D, ROWS>(call, a, st);
+    return c.mode == ROWS ? launch_tile<BF16, D, ROWS>(call, a, st)
+                          : launch_tile<BF16, D, SHARED>(call, a, st);
   }
 }
 
