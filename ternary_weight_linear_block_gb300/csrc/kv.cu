@@ -16,13 +16,14 @@ namespace {
 // Two sums over the requests carry everything: the rows before request b
 // (its row start) and the further pages taken before it.  Every CTA adds
 // them up for itself (B is at most 16384 lengths, read from L2) and keeps
-// both sums in shared memory, so one launch is enough and no CTA waits for
-// another; a row or a page then finds its request by bisection.  Bound: the
-// launch and two dependent round trips to L2 up to about 100,000 rows, then
-// the 16 bytes written for each row.
+// both, and the cached lengths, in shared memory, so one launch is enough and
+// no CTA waits for another; a row or a page then finds its request by
+// bisection and has one number to read, its page.  Bound: the launch and two
+// dependent round trips to L2 up to about 100,000 rows, then the 16 bytes
+// written for each row.
 
 constexpr int PLAN_THREADS = 512;
-constexpr int PLAN_ROWS = 4;   // consecutive rows of one thread: 16-byte stores
+constexpr int PLAN_REQS = 2;   // consecutive requests of one thread in a round of the sums
 
 struct PlanArgs {
   const int32_t* ctx_len;
@@ -39,54 +40,66 @@ struct PlanArgs {
   int B, shift, width, n_free, capacity;
 };
 
-struct Need {
-  int64_t rows;   // new tokens
-  int64_t pages;  // further pages
-  int held;       // pages of the cached tokens
-  int flags;
-};
-
-__device__ __forceinline__ Need need_of(const PlanArgs& a, int b) {
-  const int c0 = a.ctx_len[b], n0 = a.new_len[b];
-  Need r;
-  r.flags = (c0 < 0 || n0 < 0) ? 8 : 0;
-  const int64_t c = max(c0, 0), n = max(n0, 0), page = int64_t(1) << a.shift;
-  const int64_t held = (c + page - 1) >> a.shift, all = (c + n + page - 1) >> a.shift;
-  if (all > a.width) r.flags |= 2;
-  r.rows = n;
-  r.held = static_cast<int>(held < a.width ? held : a.width);
-  r.pages = (all < a.width ? all : a.width) - r.held;
-  return r;
+// Pages that c cached tokens hold, in a table row of `width`.
+__device__ __forceinline__ int held_pages(const PlanArgs& a, int c) {
+  const int64_t held = (int64_t(c) + (int64_t(1) << a.shift) - 1) >> a.shift;
+  return static_cast<int>(held < a.width ? held : a.width);
 }
 
-// Largest b with start[b] <= x (start[0] = 0, not decreasing, B entries).
-__device__ __forceinline__ int request_of(const int* start, int B, int x) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= x) lo = mid; else hi = mid;
+// For each of N numbers the largest b with start[b] <= x (start[0] = 0, not
+// decreasing, B entries): side by side, as every step waits for shared memory.
+template <int N>
+__device__ __forceinline__ void requests_of(const int* start, int B, const int (&x)[N], int (&b)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) b[i] = 0;
+  int step = 1;
+  while (step < B) step <<= 1;
+  for (step >>= 1; step > 0; step >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {      // without branches, or the reads do not overlap
+      const int at = b[i] + step;
+      const int first = start[min(at, B)];
+      b[i] = (at < B) & (first <= x[i]) ? at : b[i];
+    }
   }
-  return lo;
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+// A warp has 32 ROWS consecutive rows, 32 at a time, so that its stores are
+// whole lines (a thread with consecutive rows of its own wrote half sectors:
+// 12.1 us for 1.17 million rows).  Four, so that a step's rows use many
+// threads; eight once four would not fit the GPU in one wave (two CTAs an SM).
+template <int ROWS>
+__global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_constant__ PlanArgs a) {
   extern __shared__ int s_sums[];
-  int* s_row = s_sums;              // [B + 1] rows before request b
-  int* s_page = s_sums + a.B + 1;   // [B + 1] further pages before it
+  int* s_row = s_sums;                   // [B + 1] rows before request b
+  int* s_page = s_row + a.B + 1;         // [B + 1] further pages before it
+  int* s_ctx = s_page + a.B + 1;         // [B] cached tokens
   __shared__ int64_t s_warp[2][PLAN_THREADS / 32];
-  __shared__ int64_t s_carry[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
+  const int head0 = a.free_head != nullptr ? *a.free_head : 0;   // on its way with the lengths
 
   int64_t rows0 = 0, pages0 = 0;
   int flags = 0;
-  for (int base = 0; base < a.B; base += PLAN_THREADS) {
-    const int b = base + tid;
-    Need w{0, 0, 0, 0};
-    if (b < a.B) w = need_of(a, b);
-    flags |= w.flags;
-    int64_t rows = w.rows, pages = w.pages;
+  for (int base = 0; base < a.B; base += PLAN_THREADS * PLAN_REQS) {
+    int64_t n[PLAN_REQS], more[PLAN_REQS], rows = 0, pages = 0;
+    const int b0 = base + tid * PLAN_REQS;
+#pragma unroll
+    for (int i = 0; i < PLAN_REQS; ++i) {
+      const int b = b0 + i;
+      const int cl = b < a.B ? a.ctx_len[b] : 0, nl = b < a.B ? a.new_len[b] : 0;
+      const int c = max(cl, 0);
+      if (cl < 0 || nl < 0) flags |= 8;
+      n[i] = max(nl, 0);
+      const int64_t all = (int64_t(c) + n[i] + (int64_t(1) << a.shift) - 1) >> a.shift;
+      if (all > a.width) flags |= 2;
+      more[i] = (all < a.width ? all : a.width) - held_pages(a, c);
+      rows += n[i];
+      pages += more[i];
+      if (b < a.B) s_ctx[b] = c;
+    }
+    const int64_t mine_r = rows, mine_p = pages;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t r = __shfl_up_sync(~0u, rows, d), p = __shfl_up_sync(~0u, pages, d);
@@ -95,107 +108,105 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
         pages += p;
       }
     }
+    __syncthreads();
     if (lane == 31) {
       s_warp[0][warp] = rows;
       s_warp[1][warp] = pages;
     }
     __syncthreads();
-    int64_t before_r = rows0, before_p = pages0;
-    for (int w2 = 0; w2 < warp; ++w2) {
-      before_r += s_warp[0][w2];
-      before_p += s_warp[1][w2];
+    int64_t before_r = rows0 + rows - mine_r, before_p = pages0 + pages - mine_p;
+#pragma unroll
+    for (int w = 0; w < PLAN_THREADS / 32; ++w) {
+      const int64_t r = s_warp[0][w], p = s_warp[1][w];
+      if (w < warp) {
+        before_r += r;
+        before_p += p;
+      }
+      rows0 += r;
+      pages0 += p;
     }
-    rows += before_r;
-    pages += before_p;
-    if (b < a.B) {   // sums past 2^31 stay at its end: they are past every row asked for
-      s_row[b + 1] = static_cast<int>(min(rows, int64_t(INT32_MAX)));
-      s_page[b + 1] = static_cast<int>(min(pages, int64_t(INT32_MAX)));
+#pragma unroll
+    for (int i = 0; i < PLAN_REQS; ++i) {
+      before_r += n[i];
+      before_p += more[i];
+      if (b0 + i < a.B) {   // sums past 2^31 stay at its end: past every row asked for
+        s_row[b0 + i + 1] = static_cast<int>(min(before_r, int64_t(INT32_MAX)));
+        s_page[b0 + i + 1] = static_cast<int>(min(before_p, int64_t(INT32_MAX)));
+      }
     }
-    if (tid == PLAN_THREADS - 1) {
-      s_carry[0] = rows;
-      s_carry[1] = pages;
-    }
-    __syncthreads();
-    rows0 = s_carry[0];
-    pages0 = s_carry[1];
   }
   if (tid == 0) s_row[0] = s_page[0] = 0;
-  const int any_flags = __syncthreads_or(flags & 2) ? 2 : 0;
-  const int neg_flags = __syncthreads_or(flags & 8) ? 8 : 0;
-  const int head = a.free_head != nullptr ? min(max(*a.free_head, 0), a.n_free) : 0;
+  const int head = min(max(head0, 0), a.n_free);
   const int64_t avail = a.n_free - head;
-  const int total = s_row[a.B];
-  const int pages_all = s_page[a.B];
-
   if (blockIdx.x == 0) {
+    const int too_long = __syncthreads_or(flags & 2) ? 2 : 0;
+    const int negative = __syncthreads_or(flags & 8) ? 8 : 0;
     for (int b = tid; b <= a.B; b += PLAN_THREADS) a.row_start[b] = s_row[b];
     if (tid == 0) {
       const int taken = static_cast<int>(min(pages0, avail));
-      a.info[0] = total;
+      a.info[0] = s_row[a.B];
       a.info[1] = taken;
       a.info[2] = head + taken;
-      a.info[3] = any_flags | neg_flags | (pages0 > avail ? 1 : 0) | (rows0 > a.capacity ? 4 : 0);
+      a.info[3] = too_long | negative | (pages0 > avail ? 1 : 0) | (rows0 > a.capacity ? 4 : 0);
     }
+  } else {
+    __syncthreads();
   }
+  const int total = s_row[a.B];
+  const int pages_all = s_page[a.B];
 
-  const int64_t threads = int64_t(gridDim.x) * PLAN_THREADS;
-  const int64_t me = int64_t(blockIdx.x) * PLAN_THREADS + tid;
-  // the further pages into the table
-  for (int64_t p = me; p < pages_all; p += threads) {
-    const int b = request_of(s_page, a.B, static_cast<int>(p));
-    const Need w = need_of(a, b);
-    const int64_t at = w.held + (p - s_page[b]);
-    if (at < a.width) a.table[b * a.table_stride + at] = p < avail ? a.free_pages[head + p] : -1;
-  }
   // the rows
-  for (int64_t q = me; q * PLAN_ROWS < a.capacity; q += threads) {
-    const int r0 = static_cast<int>(q * PLAN_ROWS);
-    int64_t slot[PLAN_ROWS];
-    int pos[PLAN_ROWS], req[PLAN_ROWS];
-    int b = r0 < total ? request_of(s_row, a.B, r0) : a.B;
-    int known = -1, c = 0, held = 0;
+  const int64_t warps = int64_t(gridDim.x) * (PLAN_THREADS / 32);
+  for (int64_t w = int64_t(blockIdx.x) * (PLAN_THREADS / 32) + warp; w * (32 * ROWS) < a.capacity;
+       w += warps) {
+    int row[ROWS], b[ROWS], page[ROWS];
+    int64_t p[ROWS];
 #pragma unroll
-    for (int i = 0; i < PLAN_ROWS; ++i) {
-      const int r = r0 + i;
-      slot[i] = -1;
-      pos[i] = 0;
-      req[i] = -1;
-      if (r < total && r < a.capacity) {
-        while (b + 1 < a.B && s_row[b + 1] <= r) ++b;
-        if (b != known) {
-          known = b;
-          c = max(a.ctx_len[b], 0);
-          held = need_of(a, b).held;
-        }
-        const int64_t p = int64_t(c) + (r - s_row[b]);
-        const int64_t at = p >> a.shift;
-        int page = -1;
-        if (at < held) {
-          page = a.table[b * a.table_stride + at];
-        } else if (at < a.width) {
-          const int64_t taken = s_page[b] + (at - held);
-          if (taken < avail) page = a.free_pages[head + taken];
-        }
-        if (page >= 0) slot[i] = (int64_t(page) << a.shift) + (p & ((int64_t(1) << a.shift) - 1));
-        pos[i] = static_cast<int>(min(p, int64_t(INT32_MAX)));
-        req[i] = b;
-      }
-    }
-    if (r0 + PLAN_ROWS <= a.capacity) {
-      *reinterpret_cast<longlong2*>(a.slots + r0) = make_longlong2(slot[0], slot[1]);
-      *reinterpret_cast<longlong2*>(a.slots + r0 + 2) = make_longlong2(slot[2], slot[3]);
-      *reinterpret_cast<int4*>(a.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(a.request + r0) = make_int4(req[0], req[1], req[2], req[3]);
+    for (int i = 0; i < ROWS; ++i) row[i] = static_cast<int>(min(w * (32 * ROWS) + i * 32 + lane, int64_t(INT32_MAX)));
+    // long requests: the warp's first and last rows have the same one
+    const int ends[2] = {static_cast<int>(w * (32 * ROWS)),
+                         static_cast<int>(min(w * (32 * ROWS) + 32 * ROWS - 1, int64_t(INT32_MAX)))};
+    int of[2];
+    requests_of<2>(s_row, a.B, ends, of);
+    if (of[0] == of[1]) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) b[i] = of[0];
     } else {
+      requests_of<ROWS>(s_row, a.B, row, b);
+    }
 #pragma unroll
-      for (int i = 0; i < PLAN_ROWS; ++i) {
-        if (r0 + i < a.capacity) {
-          a.slots[r0 + i] = slot[i];
-          a.positions[r0 + i] = pos[i];
-          a.request[r0 + i] = req[i];
-        }
+    for (int i = 0; i < ROWS; ++i) {
+      // one address each and no branches, so that all the reads are on their
+      // way together
+      const int bi = min(b[i], a.B - 1);
+      const bool in = (row[i] < total) & (row[i] < a.capacity);
+      const int c = bi >= 0 ? s_ctx[bi] : 0, held = held_pages(a, c);
+      const int start = bi >= 0 ? s_row[bi] : 0, more = bi >= 0 ? s_page[bi] : 0;
+      p[i] = in ? int64_t(c) + (row[i] - start) : 0;
+      const int64_t at = p[i] >> a.shift, taken = more + (at - held);
+      const bool known = at < held;
+      const int32_t* from = known ? a.table + bi * a.table_stride + at : a.free_pages + head + taken;
+      page[i] = in & (known | ((at < a.width) & (taken < avail))) ? __ldg(from) : -1;
+      b[i] = in ? bi : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (row[i] < a.capacity) {
+        a.slots[row[i]] = page[i] < 0 ? -1 : (int64_t(page[i]) << a.shift) +
+                                                 (p[i] & ((int64_t(1) << a.shift) - 1));
+        a.positions[row[i]] = static_cast<int>(min(p[i], int64_t(INT32_MAX)));
+        a.request[row[i]] = b[i];
       }
     }
+  }
+  // the further pages into the table (entries that no row reads)
+  const int64_t threads = int64_t(gridDim.x) * PLAN_THREADS;
+  for (int64_t q = int64_t(blockIdx.x) * PLAN_THREADS + tid; q < pages_all; q += threads) {
+    const int x[1] = {static_cast<int>(q)};
+    int b[1];
+    requests_of<1>(s_page, a.B, x, b);
+    const int64_t at = held_pages(a, s_ctx[b[0]]) + (q - s_page[b[0]]);
+    if (at < a.width) a.table[b[0] * a.table_stride + at] = q < avail ? a.free_pages[head + q] : -1;
   }
 }
 
@@ -352,20 +363,28 @@ cudaError_t launch_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64
                            int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
                            cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  const size_t smem = static_cast<size_t>(2 * (B + 1)) * sizeof(int);
+  const size_t smem = static_cast<size_t>(3 * B + 2) * sizeof(int);
   const cudaError_t e = once_per_device(attr_done, [] {
-    return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                2 * (16384 + 1) * static_cast<int>(sizeof(int)));
+    constexpr int most = (3 * 16384 + 2) * static_cast<int>(sizeof(int));
+    const cudaError_t e4 =
+        cudaFuncSetAttribute(plan_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return e4 != cudaSuccess ? e4 : cudaFuncSetAttribute(
+        plan_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   });
   if (e != cudaSuccess) return e;
   PlanArgs a{ctx_len, new_len, table, free_pages, free_head, row_start, slots, positions, request,
              info, table_stride, static_cast<int>(B), log2_of(page_size),
              static_cast<int>(table_width), static_cast<int>(n_free), static_cast<int>(capacity)};
-  const int64_t per_block = PLAN_THREADS * PLAN_ROWS;
-  const int64_t blocks = std::min<int64_t>((capacity + per_block - 1) / per_block,
-                                           int64_t(4) * kv_sm_count());
-  return launch(plan_kernel, dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))),
-                dim3(PLAN_THREADS), smem, st, a);
+  const int64_t wave = int64_t(2) * kv_sm_count();
+  const auto blocks_of = [&](int rows) {
+    const int64_t per_block = int64_t(PLAN_THREADS) * rows;
+    return std::min(std::max<int64_t>((capacity + per_block - 1) / per_block, 1), wave);
+  };
+  if (blocks_of(4) < wave)
+    return launch(plan_kernel<4>, dim3(static_cast<unsigned>(blocks_of(4))), dim3(PLAN_THREADS), smem,
+                  st, a);
+  return launch(plan_kernel<8>, dim3(static_cast<unsigned>(blocks_of(8))), dim3(PLAN_THREADS), smem,
+                st, a);
 }
 
 cudaError_t launch_kv_write(const tern_kv_cache& c, const void* k, const void* v, int64_t k_token,
