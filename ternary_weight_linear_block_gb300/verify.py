@@ -1,0 +1,136 @@
+"""Verification of drafted-token trees through attention blocks of ternary linears.
+
+``VerifyStack`` runs one step of speculative decoding over a stack of blocks
+(qkv linear, paged attention, output linear): the step's pages and slots are
+planned on the GPU, every block writes its new keys and values and attends
+over the cache, and once the caller knows the accepted paths, ``commit``
+makes them contiguous in all blocks at once.  Norms, the MLP and sampling
+belong to the model around it; here a block's output is added to its input.
+
+``python -m ternary_weight_linear_block_gb300.verify`` runs a small stack of
+random weights: a prompt, then steps that verify a tree for each request.
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import binding as B
+from . import kv
+
+
+@dataclass
+class Block:
+    """One attention block: qkv [(heads + 2 kv_heads) dim, hidden] and output
+    [hidden, heads dim] ternary layers, and its cache."""
+    qkv: B.PackedLayer
+    out: B.PackedLayer
+    cache: kv.KVCache
+
+    def __post_init__(self):
+        self.heads = self.out.k // self.cache.dim
+        if self.qkv.n != (self.heads + 2 * self.cache.heads) * self.cache.dim or \
+                self.out.k != self.heads * self.cache.dim or self.qkv.k != self.out.n:
+            raise ValueError("qkv, out: sizes do not belong together")
+
+
+class VerifyStack:
+    """Blocks that share block tables and lengths.  ``table`` int32 [requests,
+    width] and ``ctx_len`` int32 [requests] start empty; pages come from the
+    cache's own, in order."""
+
+    def __init__(self, blocks: list[Block], requests: int, width: int):
+        self.blocks = blocks
+        cache = blocks[0].cache
+        dev = cache.device
+        self.requests, self.page_size = requests, cache.page_size
+        self.table = torch.full((requests, width), -1, dtype=torch.int32, device=dev)
+        self.ctx_len = torch.zeros(requests, dtype=torch.int32, device=dev)
+        self.free_pages = torch.arange(cache.pages, dtype=torch.int32, device=dev)
+        self.free_head = torch.zeros(1, dtype=torch.int32, device=dev)
+        # the linears' and the attention's workspaces: the attention leaves
+        # partial sums behind, which the linears would have to zero again
+        self.ws_linear, self.ws_attention = B.Workspace(dev), B.Workspace(dev)
+        self.plan = None
+
+    def step(self, x: torch.Tensor, new_len: torch.Tensor, max_new: int,
+             mask: torch.Tensor | None = None) -> torch.Tensor:
+        """Hidden states [rows, hidden] of the new tokens through all blocks;
+        new_len int32 [requests] rows each (``max_new`` at most), masked as
+        kv.tree_attention's ``mask``.  The tokens stay drafts until commit."""
+        rows = x.shape[0]
+        self.plan = kv.kv_plan(self.ctx_len, new_len, self.table, self.free_pages, self.page_size,
+                               rows, free_head=self.free_head)
+        # a request's table keeps the pages of drafts that are not accepted:
+        # planning the next step from the same lengths would take them again,
+        # so the head only moves when pages were taken, in commit
+        for block in self.blocks:
+            x = x + self.block(block, x, max_new, mask)
+        return x
+
+    def block(self, block: Block, x: torch.Tensor, max_new: int, mask) -> torch.Tensor:
+        cache, p = block.cache, self.plan
+        qkv = B.forward(block.qkv, x, ws=self.ws_linear)
+        q, k, v = (t.unflatten(1, (-1, cache.dim)) for t in qkv.split(
+            [block.heads * cache.dim, cache.heads * cache.dim, cache.heads * cache.dim], dim=1))
+        kv.kv_write(cache, k, v, p.slots)
+        a = kv.tree_attention(q, cache, self.table, self.ctx_len, p.row_start, max_new, mask=mask,
+                              ws=self.ws_attention)
+        return B.forward(block.out, a.flatten(1), ws=self.ws_linear)
+
+    def commit(self, path: torch.Tensor, path_len: torch.Tensor) -> torch.Tensor:
+        """Keep the accepted path of every request (kv.kv_commit), in all
+        blocks; returns the new lengths."""
+        self.ctx_len = kv.kv_commit([b.cache for b in self.blocks], self.table, self.ctx_len, path,
+                                    path_len)
+        self.free_head = self.plan.info[2:3]
+        return self.ctx_len
+
+
+def random_stack(layers: int, hidden: int, heads: int, kv_heads: int, dim: int, pages: int,
+                 page_size: int, requests: int, width: int, seed: int = 0,
+                 device="cuda") -> VerifyStack:
+    """A stack of random ternary blocks (for examples and tests)."""
+    gen = torch.Generator(device=device).manual_seed(seed)
+
+    def linear(n, k):
+        codes = torch.randint(-1, 2, (n, k), generator=gen, device=device, dtype=torch.int8)
+        scales = (0.02 * torch.rand(n, k // 128, generator=gen, device=device) + 0.005).half()
+        return B.pack_layer(codes, scales)
+
+    return VerifyStack([Block(linear((heads + 2 * kv_heads) * dim, hidden), linear(hidden, heads * dim),
+                              kv.KVCache.empty(pages, page_size, kv_heads, dim, device=device))
+                        for _ in range(layers)], requests, width)
+
+
+def main():
+    requests, hidden, tree = 2, 5120, [-1, 0, 0, 1, 1, 2, 3]
+    stack = random_stack(layers=2, hidden=hidden, heads=40, kv_heads=20, dim=128, pages=64,
+                         page_size=16, requests=requests, width=32)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def states(rows):
+        return torch.randn(rows, hidden, generator=gen, device="cuda").to(torch.bfloat16)
+
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    prompt = [100, 37]                                   # a prompt is a chain whose tokens all stay
+    stack.step(states(sum(prompt)), ints(prompt), max(prompt))
+    stack.commit(ints([list(range(max(prompt)))] * requests), ints(prompt))
+    mask = kv.ancestor_masks(tree).repeat(requests, 1)
+    for accepted in ([0, 1, 3, 6], [0, 2]), ([0], [0, 1, 4]):
+        y = stack.step(states(requests * len(tree)), ints([len(tree)] * requests), len(tree), mask)
+        path = torch.zeros((requests, 4), dtype=torch.int32)
+        for b, p in enumerate(accepted):
+            path[b, :len(p)] = torch.tensor(p)
+        lengths = stack.commit(path.cuda(), ints([len(p) for p in accepted]))
+        B.tern_check()
+        print(f"verified {tuple(y.shape)} drafts, kept {[len(p) for p in accepted]}, "
+              f"lengths now {lengths.tolist()}, finite: {bool(torch.isfinite(y).all())}")
+
+
+if __name__ == "__main__":
+    main()
