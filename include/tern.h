@@ -565,8 +565,12 @@ typedef struct {
  *   ctx_len, new_len  int32 [B]: cached and new tokens (a negative length
  *                     counts as 0 and sets flag 8)
  *   table             int32 [B][table_width], rows table_stride apart, in
- *                     and out: entries below ceil(ctx_len / P) are kept, the
- *                     new tokens' further pages are written behind them
+ *                     and out: the pages that the new tokens need beyond
+ *                     those held are written behind them
+ *   held              int32 [B] or NULL: entries of each table row that are
+ *                     pages already (the pages of drafts that were not kept
+ *                     stay in the row and serve the next step); NULL:
+ *                     ceil(ctx_len / P).  Entries below are kept
  *   free_pages        int32 [n_free]: pages not in use; pages are taken from
  *                     index *free_head on (NULL: 0), in request order
  *   free_head         int32 [1] or NULL
@@ -576,19 +580,20 @@ typedef struct {
  *                               where a token has no page
  *   positions  int32 [capacity] position of every row (0 past the last)
  *   request    int32 [capacity] request of every row (-1 past the last)
+ *   held_out   int32 [B] or NULL  held, and the pages taken
  *   info       int32 [4]       rows in all, pages taken, the next free_head,
  *                              flags: 1 free pages ran out (the table gets
  *                              -1), 2 a request longer than its table row,
  *                              4 more rows than capacity, 8 a negative length
  * No output may overlap an input other than the table.
  * Requirements: page_size a power of two, 1 <= page_size <= 65536;
- * 0 <= B <= 16384; capacity, n_free < 2^31; table_width * page_size < 2^31. */
+ * 0 <= B <= 8192; capacity, n_free < 2^31; table_width * page_size < 2^31. */
 tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
                          int64_t page_size, int32_t* table, int64_t table_stride,
-                         int64_t table_width, const int32_t* free_pages, int64_t n_free,
-                         const int32_t* free_head, int32_t* row_start, int64_t capacity,
-                         int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
-                         void* stream);
+                         int64_t table_width, const int32_t* held, const int32_t* free_pages,
+                         int64_t n_free, const int32_t* free_head, int32_t* row_start,
+                         int64_t capacity, int64_t* slots, int32_t* positions, int32_t* request,
+                         int32_t* held_out, int32_t* info, void* stream);
 
 /* tern_kv_write -- rows of keys and values into the cache's slots.
  *   k, v   [T][H][D] of the cache's type; rows token_stride and heads

@@ -81,8 +81,8 @@ _SIGS = {
     "tern_gemv_decode_noalloc": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p]),
     "tern_linear_decode": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _p, _p, _sz, _p]),
     "tern_gemv_decode_f32": (ctypes.c_int, [_p, _p, _i64, _i64, _i64, _p, _p, _sz, _p]),
-    "tern_kv_plan": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _p, _i64, _p,
-                                    _p, _p, _p, _p]),
+    "tern_kv_plan": (ctypes.c_int, [_p, _p, _i64, _i64, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i64,
+                                    _p, _p, _p, _p, _p, _p]),
     "tern_kv_write": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _i64, _p]),
     "tern_kv_commit": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p]),
     "tern_tree_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
@@ -288,13 +288,13 @@ def _desc(cache):
     return ctypes.addressof(cache) if isinstance(cache, ctypes.Structure) else cache
 
 
-def tern_kv_plan(ctx_len, new_len, b, page_size, table, table_stride, table_width, free_pages,
-                 n_free, free_head, row_start, capacity, slots, positions, request, info,
+def tern_kv_plan(ctx_len, new_len, b, page_size, table, table_stride, table_width, held, free_pages,
+                 n_free, free_head, row_start, capacity, slots, positions, request, held_out, info,
                  stream=None):
     return _call("tern_kv_plan", _ptr(ctx_len), _ptr(new_len), b, page_size, _ptr(table),
-                 table_stride, table_width, _ptr(free_pages), n_free, _ptr(free_head),
+                 table_stride, table_width, _ptr(held), _ptr(free_pages), n_free, _ptr(free_head),
                  _ptr(row_start), capacity, _ptr(slots), _ptr(positions), _ptr(request),
-                 _ptr(info), _stream(stream))
+                 _ptr(held_out), _ptr(info), _stream(stream))
 
 
 def tern_kv_write(cache, k, v, k_token_stride, k_head_stride, v_token_stride, v_head_stride, slots,

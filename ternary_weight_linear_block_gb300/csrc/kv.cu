@@ -15,8 +15,8 @@ namespace {
 //
 // Two sums over the requests carry everything: the rows before request b
 // (its row start) and the further pages taken before it.  Every CTA adds
-// them up for itself (B is at most 16384 lengths, read from L2) and keeps
-// both, and the cached lengths, in shared memory, so one launch is enough and
+// them up for itself (B is at most 8192 lengths, read from L2) and keeps both,
+// the cached lengths and the pages held in shared memory, so one launch is enough and
 // no CTA waits for another; a row or a page then finds its request by
 // bisection and has one number to read, its page.  Bound: the launch and two
 // dependent round trips to L2 up to about 100,000 rows, then the 16 bytes
@@ -29,22 +29,18 @@ struct PlanArgs {
   const int32_t* ctx_len;
   const int32_t* new_len;
   int32_t* table;
+  const int32_t* held;
   const int32_t* free_pages;
   const int32_t* free_head;
   int32_t* row_start;
   int64_t* slots;
   int32_t* positions;
   int32_t* request;
+  int32_t* held_out;
   int32_t* info;
   int64_t table_stride;
   int B, shift, width, n_free, capacity;
 };
-
-// Pages that c cached tokens hold, in a table row of `width`.
-__device__ __forceinline__ int held_pages(const PlanArgs& a, int c) {
-  const int64_t held = (int64_t(c) + (int64_t(1) << a.shift) - 1) >> a.shift;
-  return static_cast<int>(held < a.width ? held : a.width);
-}
 
 // For each of N numbers the largest b with start[b] <= x (start[0] = 0, not
 // decreasing, B entries): side by side, as every step waits for shared memory.
@@ -74,6 +70,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
   int* s_row = s_sums;                   // [B + 1] rows before request b
   int* s_page = s_row + a.B + 1;         // [B + 1] further pages before it
   int* s_ctx = s_page + a.B + 1;         // [B] cached tokens
+  int* s_held = s_ctx + a.B;             // [B] pages in the table row
   __shared__ int64_t s_warp[2][PLAN_THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -92,12 +89,20 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
       const int c = max(cl, 0);
       if (cl < 0 || nl < 0) flags |= 8;
       n[i] = max(nl, 0);
-      const int64_t all = (int64_t(c) + n[i] + (int64_t(1) << a.shift) - 1) >> a.shift;
+      const int64_t up = (int64_t(1) << a.shift) - 1;
+      const int64_t all = (int64_t(c) + n[i] + up) >> a.shift;
+      int64_t held = (int64_t(c) + up) >> a.shift;
+      if (a.held != nullptr) held = b < a.B ? max(a.held[b], 0) : 0;
+      held = held < a.width ? held : a.width;
       if (all > a.width) flags |= 2;
-      more[i] = (all < a.width ? all : a.width) - held_pages(a, c);
+      more[i] = max((all < a.width ? all : a.width) - held, int64_t(0));
       rows += n[i];
       pages += more[i];
-      if (b < a.B) s_ctx[b] = c;
+      if (b < a.B) {
+        s_ctx[b] = c;
+        s_held[b] = static_cast<int>(held);
+        if (a.held_out != nullptr && blockIdx.x == 0) a.held_out[b] = static_cast<int>(held + more[i]);
+      }
     }
     const int64_t mine_r = rows, mine_p = pages;
 #pragma unroll
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
       // way together
       const int bi = min(b[i], a.B - 1);
       const bool in = (row[i] < total) & (row[i] < a.capacity);
-      const int c = bi >= 0 ? s_ctx[bi] : 0, held = held_pages(a, c);
+      const int c = bi >= 0 ? s_ctx[bi] : 0, held = bi >= 0 ? s_held[bi] : 0;
       const int start = bi >= 0 ? s_row[bi] : 0, more = bi >= 0 ? s_page[bi] : 0;
       p[i] = in ? int64_t(c) + (row[i] - start) : 0;
       const int64_t at = p[i] >> a.shift, taken = more + (at - held);
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
     const int x[1] = {static_cast<int>(q)};
     int b[1];
     requests_of<1>(s_page, a.B, x, b);
-    const int64_t at = held_pages(a, s_ctx[b[0]]) + (q - s_page[b[0]]);
+    const int64_t at = s_held[b[0]] + (q - s_page[b[0]]);
     if (at < a.width) a.table[b[0] * a.table_stride + at] = q < avail ? a.free_pages[head + q] : -1;
   }
 }
@@ -358,22 +363,22 @@ int kv_sm_count() {
 
 cudaError_t launch_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
                            int64_t page_size, int32_t* table, int64_t table_stride,
-                           int64_t table_width, const int32_t* free_pages, int64_t n_free,
-                           const int32_t* free_head, int32_t* row_start, int64_t capacity,
-                           int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
-                           cudaStream_t st) {
+                           int64_t table_width, const int32_t* held, const int32_t* free_pages,
+                           int64_t n_free, const int32_t* free_head, int32_t* row_start,
+                           int64_t capacity, int64_t* slots, int32_t* positions, int32_t* request,
+                           int32_t* held_out, int32_t* info, cudaStream_t st) {
   static std::atomic<unsigned long long> attr_done{0};
-  const size_t smem = static_cast<size_t>(3 * B + 2) * sizeof(int);
+  const size_t smem = static_cast<size_t>(4 * B + 2) * sizeof(int);
   const cudaError_t e = once_per_device(attr_done, [] {
-    constexpr int most = (3 * 16384 + 2) * static_cast<int>(sizeof(int));
+    constexpr int most = (4 * 8192 + 2) * static_cast<int>(sizeof(int));
     const cudaError_t e4 =
         cudaFuncSetAttribute(plan_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     return e4 != cudaSuccess ? e4 : cudaFuncSetAttribute(
         plan_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   });
   if (e != cudaSuccess) return e;
-  PlanArgs a{ctx_len, new_len, table, free_pages, free_head, row_start, slots, positions, request,
-             info, table_stride, static_cast<int>(B), log2_of(page_size),
+  PlanArgs a{ctx_len, new_len, table, held, free_pages, free_head, row_start, slots, positions,
+             request, held_out, info, table_stride, static_cast<int>(B), log2_of(page_size),
              static_cast<int>(table_width), static_cast<int>(n_free), static_cast<int>(capacity)};
   const int64_t wave = int64_t(2) * kv_sm_count();
   const auto blocks_of = [&](int rows) {

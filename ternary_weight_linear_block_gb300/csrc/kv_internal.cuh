@@ -12,10 +12,10 @@ namespace tern {
 int kv_sm_count();
 cudaError_t launch_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
                            int64_t page_size, int32_t* table, int64_t table_stride,
-                           int64_t table_width, const int32_t* free_pages, int64_t n_free,
-                           const int32_t* free_head, int32_t* row_start, int64_t capacity,
-                           int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
-                           cudaStream_t st);
+                           int64_t table_width, const int32_t* held, const int32_t* free_pages,
+                           int64_t n_free, const int32_t* free_head, int32_t* row_start,
+                           int64_t capacity, int64_t* slots, int32_t* positions, int32_t* request,
+                           int32_t* held_out, int32_t* info, cudaStream_t st);
 cudaError_t launch_kv_write(const tern_kv_cache& c, const void* k, const void* v, int64_t k_token,
                             int64_t k_head, int64_t v_token, int64_t v_head, const int64_t* slots,
                             int64_t T, cudaStream_t st);

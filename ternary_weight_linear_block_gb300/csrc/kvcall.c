@@ -14,8 +14,9 @@ static PyObject *s_is_cuda, *s_dtype, *s_shape, *s_stride, *s_data_ptr;
 static PyObject *t_int32, *t_int64, *t_float32;   /* torch's types */
 
 typedef tern_status (*plan_fn)(const int32_t*, const int32_t*, int64_t, int64_t, int32_t*, int64_t,
-                               int64_t, const int32_t*, int64_t, const int32_t*, int32_t*, int64_t,
-                               int64_t*, int32_t*, int32_t*, int32_t*, void*);
+                               int64_t, const int32_t*, const int32_t*, int64_t, const int32_t*,
+                               int32_t*, int64_t, int64_t*, int32_t*, int32_t*, int32_t*, int32_t*,
+                               void*);
 typedef tern_status (*write_fn)(const tern_kv_cache*, const void*, const void*, int64_t, int64_t,
                                 int64_t, int64_t, const int64_t*, int64_t, void*);
 typedef tern_status (*attn_fn)(const void*, int64_t, int64_t, const tern_kv_cache*, const int32_t*,
@@ -151,11 +152,11 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* plan(ctx_len, new_len, table, free_pages, free_head or None, page_size, capacity,
- *      row_start, slots, positions, request, info, stream) */
+ *      row_start, slots, positions, request, info, held or None, held_out or None, stream) */
 static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  Tensor ctx, new_len, table, free_pages, head, start, slots, pos, req, info;
+  Tensor ctx, new_len, table, free_pages, head, start, slots, pos, req, info, held, held_out;
   int64_t stride;
-  if (!counted(n, 13) || !read_dense(a[0], t_int32, 1, "ctx_len", &ctx) ||
+  if (!counted(n, 15) || !read_dense(a[0], t_int32, 1, "ctx_len", &ctx) ||
       !read_dense(a[1], t_int32, 1, "new_len", &new_len) ||
       !read_table(a[2], ctx.shape[0], &table, &stride) ||
       !read_dense(a[3], t_int32, 1, "free_pages", &free_pages) ||
@@ -171,15 +172,20 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (!read_dense(a[4], t_int32, 1, "free_head", &head)) return NULL;
     if (head.shape[0] != 1) return refuse("free_head: expected one number"), NULL;
   }
-  void* stream = PyLong_AsVoidPtr(a[12]);
+  held.p = held_out.p = NULL;
+  if (a[12] != Py_None && !read_dense(a[12], t_int32, 1, "held", &held)) return NULL;
+  if (a[13] != Py_None && !read_dense(a[13], t_int32, 1, "held_out", &held_out)) return NULL;
+  void* stream = PyLong_AsVoidPtr(a[14]);
   if (PyErr_Occurred()) return NULL;
+  if ((held.p != NULL && held.shape[0] != b) || (held_out.p != NULL && held_out.shape[0] != b))
+    return refuse("held, held_out: expected as many requests as ctx_len"), NULL;
   if (new_len.shape[0] != b) return refuse("new_len: expected as many requests as ctx_len"), NULL;
   if (start.shape[0] != b + 1 || info.shape[0] != 4 || slots.shape[0] < capacity ||
       pos.shape[0] < capacity || req.shape[0] < capacity)
     return refuse("plan: buffers too small"), NULL;
   return PyLong_FromLong(f_plan(ctx.p, new_len.p, b, page, table.p, stride, table.shape[1],
-                                free_pages.p, free_pages.shape[0], head.p, start.p, capacity,
-                                slots.p, pos.p, req.p, info.p, stream));
+                                held.p, free_pages.p, free_pages.shape[0], head.p, start.p,
+                                capacity, slots.p, pos.p, req.p, held_out.p, info.p, stream));
 }
 
 /* write(cache address, dtype, heads, dim, k, v, slots, stream) */

@@ -452,24 +452,26 @@ tern_status tern_check(void* stream) {
 
 tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
                          int64_t page_size, int32_t* table, int64_t table_stride,
-                         int64_t table_width, const int32_t* free_pages, int64_t n_free,
-                         const int32_t* free_head, int32_t* row_start, int64_t capacity,
-                         int64_t* slots, int32_t* positions, int32_t* request, int32_t* info,
-                         void* stream) {
+                         int64_t table_width, const int32_t* held, const int32_t* free_pages,
+                         int64_t n_free, const int32_t* free_head, int32_t* row_start,
+                         int64_t capacity, int64_t* slots, int32_t* positions, int32_t* request,
+                         int32_t* held_out, int32_t* info, void* stream) {
   if (B < 0 || capacity < 0 || n_free < 0) return TERN_ERR_INVALID_ARG;
-  if (!pow2(page_size) || page_size > 65536 || B > 16384 || capacity >= (int64_t(1) << 31) ||
+  if (!pow2(page_size) || page_size > 65536 || B > 8192 || capacity >= (int64_t(1) << 31) ||
       n_free >= (int64_t(1) << 31) || !table_ok(table_stride, table_width, page_size))
     return TERN_ERR_SHAPE;
   if (row_start == nullptr || info == nullptr ||
       (B > 0 && (ctx_len == nullptr || new_len == nullptr)) ||
       (B > 0 && table_width > 0 && table == nullptr) || (n_free > 0 && free_pages == nullptr) ||
+      (held != nullptr && held == held_out) ||
       (capacity > 0 && (slots == nullptr || positions == nullptr || request == nullptr)))
     return TERN_ERR_INVALID_ARG;
   if (!aligned16(slots) || !aligned16(positions) || !aligned16(request)) return TERN_ERR_ALIGN;
   if (!device_supported()) return TERN_ERR_UNSUPPORTED;
   return from_cuda(launch_kv_plan(ctx_len, new_len, B, page_size, table, table_stride, table_width,
-                                  free_pages, n_free, free_head, row_start, capacity, slots,
-                                  positions, request, info, static_cast<cudaStream_t>(stream)));
+                                  held, free_pages, n_free, free_head, row_start, capacity, slots,
+                                  positions, request, held_out, info,
+                                  static_cast<cudaStream_t>(stream)));
 }
 
 tern_status tern_kv_write(const tern_kv_cache* cache, const void* k, const void* v,

@@ -126,12 +126,17 @@ class KVPlan(NamedTuple):
 def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
             free_pages: torch.Tensor, page_size: int, capacity: int,
             free_head: torch.Tensor | None = None, plan: KVPlan | None = None,
+            held: torch.Tensor | None = None, held_out: torch.Tensor | None = None,
             stream=None) -> KVPlan:
     """Block tables and slot maps of one step: request b gets new_len[b] rows
     behind its ctx_len[b] cached tokens; the pages that they need beyond
     those it has are taken from ``free_pages`` (from index free_head[0] on)
     and written into ``table`` in place.  ``capacity`` rows are planned;
-    ``plan`` gives the outputs' buffers.  info[3] says what did not fit."""
+    ``plan`` gives the outputs' buffers.  info[3] says what did not fit.
+
+    A request has the pages of its cached tokens, or ``held`` int32
+    [requests] of them: the pages of drafts that were not kept stay in its
+    table row, and ``held_out`` (another tensor) says how many it has now."""
     if plan is None:
         if stream is None:
             plan = KVPlan.empty(ctx_len.shape[0], capacity, ctx_len.device)
@@ -139,7 +144,7 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
             with _on(stream):
                 plan = KVPlan.empty(ctx_len.shape[0], capacity, ctx_len.device)
     st = (_calls or _native()).plan(ctx_len, new_len, table, free_pages, free_head, page_size,
-                                    capacity, *plan, B._stream(stream))
+                                    capacity, *plan, held, held_out, B._stream(stream))
     if st:
         _failed("tern_kv_plan", st)
     return plan

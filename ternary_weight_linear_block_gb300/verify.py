@@ -39,7 +39,7 @@ class Block:
 class VerifyStack:
     """Blocks that share block tables and lengths.  ``table`` int32 [requests,
     width] and ``ctx_len`` int32 [requests] start empty; pages come from the
-    cache's own, in order."""
+    cache's own, in order, and stay with their request."""
 
     def __init__(self, blocks: list[Block], requests: int, width: int):
         self.blocks = blocks
@@ -50,6 +50,9 @@ class VerifyStack:
         self.ctx_len = torch.zeros(requests, dtype=torch.int32, device=dev)
         self.free_pages = torch.arange(cache.pages, dtype=torch.int32, device=dev)
         self.free_head = torch.zeros(1, dtype=torch.int32, device=dev)
+        # pages in each table row, of this step and the next
+        self.held, self.held_next = (torch.zeros(requests, dtype=torch.int32, device=dev)
+                                     for _ in range(2))
         # the linears' and the attention's workspaces: the attention leaves
         # partial sums behind, which the linears would have to zero again
         self.ws_linear, self.ws_attention = B.Workspace(dev), B.Workspace(dev)
@@ -62,10 +65,10 @@ class VerifyStack:
         kv.tree_attention's ``mask``.  The tokens stay drafts until commit."""
         rows = x.shape[0]
         self.plan = kv.kv_plan(self.ctx_len, new_len, self.table, self.free_pages, self.page_size,
-                               rows, free_head=self.free_head)
-        # a request's table keeps the pages of drafts that are not accepted:
-        # planning the next step from the same lengths would take them again,
-        # so the head only moves when pages were taken, in commit
+                               rows, free_head=self.free_head, held=self.held,
+                               held_out=self.held_next)
+        self.held, self.held_next = self.held_next, self.held
+        self.free_head = self.plan.info[2:3]
         for block in self.blocks:
             x = x + self.block(block, x, max_new, mask)
         return x
@@ -85,7 +88,6 @@ class VerifyStack:
         blocks; returns the new lengths."""
         self.ctx_len = kv.kv_commit([b.cache for b in self.blocks], self.table, self.ctx_len, path,
                                     path_len)
-        self.free_head = self.plan.info[2:3]
         return self.ctx_len
 
 

@@ -39,12 +39,13 @@ def st(fn, *args):
 
 def test_plan_arguments():
     def p(ctx=FAKE, new=FAKE, b=4, page=16, table=FAKE, stride=8, width=8, free=FAKE, n_free=10,
-          head=None, start=FAKE, cap=64, slots=FAKE, pos=FAKE, req=FAKE, info=FAKE):
-        return st("tern_kv_plan", ctx, new, b, page, table, stride, width, free, n_free, head, start,
-                  cap, slots, pos, req, info, None)
+          head=None, start=FAKE, cap=64, slots=FAKE, pos=FAKE, req=FAKE, info=FAKE, held=None,
+          held_out=None):
+        return st("tern_kv_plan", ctx, new, b, page, table, stride, width, held, free, n_free, head,
+                  start, cap, slots, pos, req, held_out, info, None)
     for bad, want in [(dict(b=-1), INVALID), (dict(cap=-1), INVALID), (dict(n_free=-1), INVALID),
                       (dict(page=0), SHAPE), (dict(page=24), SHAPE), (dict(page=1 << 17), SHAPE),
-                      (dict(b=16385), SHAPE), (dict(cap=1 << 31), SHAPE), (dict(n_free=1 << 31), SHAPE),
+                      (dict(b=8193), SHAPE), (dict(held=FAKE, held_out=FAKE), INVALID), (dict(cap=1 << 31), SHAPE), (dict(n_free=1 << 31), SHAPE),
                       (dict(stride=7), SHAPE), (dict(width=-1), SHAPE),
                       (dict(width=1 << 28, stride=1 << 28), SHAPE), (dict(ctx=None), INVALID),
                       (dict(new=None), INVALID), (dict(table=None), INVALID), (dict(free=None), INVALID),
@@ -116,8 +117,8 @@ def test_valid_calls_without_gpu_are_unsupported():
     kept = cache()
     c = ctypes.addressof(kept)
     nb = B.tern_tree_attention_workspace_bytes(8, 4, 2, 64)
-    assert st("tern_kv_plan", FAKE, FAKE, 4, 16, FAKE, 8, 8, FAKE, 10, None, FAKE, 64, FAKE, FAKE, FAKE,
-              FAKE, None) == UNSUPPORTED
+    assert st("tern_kv_plan", FAKE, FAKE, 4, 16, FAKE, 8, 8, None, FAKE, 10, None, FAKE, 64, FAKE, FAKE,
+              FAKE, None, FAKE, None) == UNSUPPORTED
     assert st("tern_kv_write", c, FAKE, FAKE, 128, 64, 128, 64, FAKE, 3, None) == UNSUPPORTED
     assert st("tern_kv_commit", c, 1, FAKE, 8, 8, FAKE, FAKE, 4, FAKE, FAKE + 64, 2, None) == UNSUPPORTED
     assert st("tern_tree_attention", FAKE, 256, 64, c, FAKE, 8, 8, FAKE, FAKE, None, 0, 2, 9, 4, 8, 0.125,

@@ -78,6 +78,18 @@ def test_plan_of_no_requests():
     assert got.info.tolist() == [0, 0, 0, 0]
 
 
+def test_plan_with_pages_held_from_a_step_before():
+    """A request that kept few of its drafts has pages to spare; one has fewer than its tokens."""
+    table = torch.tensor([[3, 4, 5, -1], [6, -1, -1, -1], [7, 8, -1, -1]], dtype=torch.int32, device="cuda")
+    held, out = ints([3, 1, 2]), poison(torch.empty(3, dtype=torch.int32, device="cuda"))
+    got = kv.kv_plan(ints([18, 16, 33]), ints([9, 1, 2]), table, ints([20, 21, 22]), 16, 12, held=held,
+                     held_out=out)
+    assert table.tolist() == [[3, 4, 5, -1], [6, 20, -1, -1], [7, 8, 21, -1]]
+    assert out.tolist() == [3, 2, 3] and got.info.tolist() == [12, 2, 2, 0]
+    want = [4 * 16 + i for i in range(2, 11)] + [20 * 16] + [21 * 16 + 1, 21 * 16 + 2]
+    assert got.slots.tolist() == want
+
+
 def test_plan_is_the_next_steps_free_head():
     free = ints([9, 8, 7, 6, 5])
     table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")

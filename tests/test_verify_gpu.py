@@ -36,6 +36,7 @@ def test_verification_steps():
     s.step(states(sum(prompt)), ints(prompt), max(prompt))
     s.commit(ints([list(range(70))] * requests), ints(prompt))
     assert s.ctx_len.tolist() == prompt
+    taken = [-(-p // page) for p in prompt]
     ctx, accepted = prompt, [[0, 2, 4], [0], [0, 1, 3]]
     trees = [[-1, 0, 0, 1, 2], [-1, 0, 1, 2, 3], [-1, 0, 0, 1, 1]]
     mask = torch.cat([kv.ancestor_masks(t) for t in trees])
@@ -48,6 +49,9 @@ def test_verification_steps():
         table = s.table.tolist()
         used = [p for b in range(requests) for p in table[b][:-(-(ctx[b] + 5) // page)]]
         assert len(set(used)) == len(used) and min(used) >= 0
+        # pages of drafts that were not kept are used again: none are taken twice
+        taken = [max(h, -(-(c + 5) // page)) for h, c in zip(taken, ctx)]
+        assert s.held.tolist() == taken and s.free_head.tolist() == [sum(taken)]
         # the first block's attention against its 64-bit statement
         block = s.blocks[0]
         qkv = B.forward(block.qkv, x, ws=s.ws_linear)
