@@ -1189,6 +1189,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 // would otherwise leave most blocks without work.  Bound by the launch and
 // three round trips to L2, with many rows by L2's rate.
 constexpr int JOIN_THREADS = 256, JOIN_GROUPS = 8;
+static_assert(JOIN_THREADS == 1 << 8 && JOIN_THREADS / JOIN_GROUPS == 1 << 5, "passes");
 // Room for the arrival counters of this many CTAs (two an SM).
 constexpr int MAX_GRID = TERN_TREE_ATTENTION_ZERO_BYTES / (3 * sizeof(int));
 
@@ -1196,19 +1197,20 @@ template <bool BF16, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) combine_kernel(const Args a, int rt, int ctas) {
   __shared__ float4 s_o[JOIN_THREADS];
   __shared__ float2 s_ml[JOIN_THREADS];
-  __shared__ int s_first[MAX_GRID + 1];     // passes before each CTA's item
+  __shared__ Item s_item[MAX_GRID];
+  __shared__ int s_first[MAX_GRID];         // passes before each CTA's item
   __shared__ int s_warp[JOIN_THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31;
-  const auto groups_of = [](int follow) { return follow + 1 < JOIN_GROUPS ? 1 : JOIN_GROUPS; };
   pdl_wait();
   pdl_launch_dependents();
   int total = 0;
   for (int base = 0; base < ctas; base += JOIN_THREADS) {
     int n = 0;
     if (base + tid < ctas) {
-      const int follow = a.items[base + tid].follow;
-      const int width = JOIN_THREADS / groups_of(follow);
-      if (follow > 0) n = (a.items[base + tid].rows * (D / 4) + width - 1) / width;
+      const Item it = a.items[base + tid];
+      s_item[base + tid] = it;
+      const int shift = it.follow + 1 < JOIN_GROUPS ? 8 : 5;      // log2 of a pass's places
+      if (it.follow > 0) n = (it.rows * (D / 4) + (1 << shift) - 1) >> shift;
     }
     int x = n;
 #pragma unroll
@@ -1232,9 +1234,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) combine_kernel(const Args a, int
       const int mid = (lo + hi) >> 1;
       if (s_first[mid] <= u) lo = mid; else hi = mid;
     }
-    const Item it = a.items[lo];
-    const int groups = groups_of(it.follow), width = JOIN_THREADS / groups;
-    const int p = tid % width, g = tid / width;
+    const Item it = s_item[lo];
+    const int groups = it.follow + 1 < JOIN_GROUPS ? 1 : JOIN_GROUPS;
+    const int shift = groups == 1 ? 8 : 5, width = 1 << shift;
+    const int p = tid & (width - 1), g = tid >> shift;
     const int place = (u - s_first[lo]) * width + p;
     const bool in = place < it.rows * (D / 4);
     const int d4 = place / it.rows, r = place - d4 * it.rows;
