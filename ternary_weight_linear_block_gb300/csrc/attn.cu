@@ -653,6 +653,15 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]),
+                 "+r"(v[6]), "+r"(v[7]), "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]),
+                 "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -679,11 +688,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "=l"(reinterpret_cast<uint64_t&>(d))
       : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
   return d;
-}
-
-__device__ __forceinline__ void turn_signs(uint32_t (&v)[2][32]) {
-#pragma unroll
-  for (int e = 0; e < 64; ++e) v[e >> 5][e & 31] ^= 0x80000000u;
 }
 
 // Scores that a row does not see.
@@ -809,6 +813,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint64_t k_desc = ptx::sw128_kmajor_desc(ptx::smem_u32(ring));
     const uint64_t v_desc = sw128_mn_desc(ptx::smem_u32(ring), HB);
     const uint32_t tm = __shfl_sync(~0u, tmem, 0);
+    // a negative scale turns the queries' signs
+    const uint32_t s_idesc = idesc<BF16>(TKT, false) | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
     while (ok && __any_sync(~0u, walk.next(s))) {
       const int cnt = __shfl_sync(~0u, s.t1 - s.t0, 0);
       // S of stream x from the keys in slot sl (one lane): 16 values further
@@ -820,7 +826,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           ptx::mma_f16_ss(tm + C::S_COL + C::S_STEP * x,
-                          da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)), db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), idesc<BF16>(TKT, false), k > 0);
+                          da + ((k >> 2) * (128 * 128 >> 4) + 2 * (k & 3)),
+                          db + ((k >> 2) * (HB >> 4) + 2 * (k & 3)), s_idesc, k > 0);
         if (last) ptx::mma_commit(&empty[sl]);
         ptx::mma_commit(&s_full[x]);
         if (last && i == cnt - 1) ptx::mma_commit(&q_empty);   // the item's queries were read
@@ -845,7 +852,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 #pragma unroll
           for (int k = 0; k < TKT / 16; ++k)
             if (k == 0 || k < steps) ptx::mma_f16_ts(tm + C::O_COL + (MODE == SHARED ? 0 : 128 * x),
-                            tm + C::S_COL + C::S_STEP * x + k * 8, dv + k * (2048 >> 4),
+                            tm + C::S_COL + C::S_STEP * x + TKT / 2 + k * 8, dv + k * (2048 >> 4),
                             idesc<BF16>(D, true), (!first || k > 0) ? 1u : 0u);
           if (MODE == SHARED) ptx::mma_commit(&o_step[(tile0 + i) & 1u]);
           if (last) ptx::mma_commit(&empty[sv]);
@@ -922,9 +929,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t o_addr = tmem + C::O_COL + (MODE == SHARED ? 0 : 128 * x) + lane_addr;
     const int wid = tid - 128;                         // 0 .. 255
     // the maximum is taken of the products themselves, so the scale must not
-    // be negative (the products' signs are turned instead) nor zero
+    // be negative (the MMA turns the queries' signs instead) nor zero
     const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
-    const bool turned = a.scale_log2 < 0.f;
     bool ok = true;
     uint32_t seq0 = 0, s_phase = 0, o_phase = 0;
     uint32_t tile0 = 0;                                // tiles of the items before
@@ -971,7 +977,8 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (!ok) break;
         if (active) {
           // a row of S is read twice, 64 columns at a time: held whole it would
-          // not fit the registers
+          // not fit the registers.  The last 64 of the first pass are the first
+          // of the second, so P starts in the upper half of S.
           uint32_t v[2][32];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
@@ -980,7 +987,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 32, v[1]);
             tmem_ld_wait_for(v[0]);
             tmem_ld_wait_for(v[1]);
-            if (turned) turn_signs(v);
             if (edge) {
               const uint64_t bits = TKT == 64 || c == 0 ? vis[0] : vis[TKT / 64 - 1];
               mask_out(v[0], static_cast<uint32_t>(bits));
@@ -991,8 +997,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
               mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(v[e >> 5][e & 31]),
                                                                __uint_as_float(v[e >> 5][(e & 31) + 1])));
           }
-          ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
-          ptx::tmem_ld_32x32b_x32(s_addr + 32, v[1]);
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
           float f = 1.f;            // of this thread's sum
           bool move = false;        // of the accumulator, by `fo`
@@ -1026,34 +1030,28 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           }
           if (move) {
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              ptx::tmem_ld_32x32b_x32(o_addr + 32 * c, o);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              ptx::tmem_ld_32x32b_x16(o_addr + 16 * c, o);
               tmem_ld_wait_for(o);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  w[e] = __float_as_uint(__uint_as_float(o[16 * h + e]) * fo);
-                tmem_st_x16(o_addr + 32 * c + 16 * h, w);
-              }
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
+              tmem_st_x16(o_addr + 16 * c, o);
             }
           }
           any = true;
           const float ms = m == -INFINITY ? 0.f : m;
           const float2 sc2 = make_float2(scale, scale), ms2 = make_float2(-ms, -ms);
           float2 sum[4] = {};
-#pragma unroll 1
-          for (int c = 0; c < TKT / 32; c += 2) {
-            // P's columns 16 c .. overwrite columns of S that were read before
-            tmem_ld_wait_for(v[0]);
-            tmem_ld_wait_for(v[1]);
-            if (turned) turn_signs(v);
-            if (edge) {
-              const uint64_t bits = TKT == 64 || c == 0 ? vis[0] : vis[TKT / 64 - 1];
-              mask_out(v[0], static_cast<uint32_t>(bits));
-              mask_out(v[1], static_cast<uint32_t>(bits >> 32));
+#pragma unroll
+          for (int c = TKT / 32 - 2; c >= 0; c -= 2) {
+            if (c < TKT / 32 - 2) {
+              tmem_ld_wait_for(v[0]);
+              tmem_ld_wait_for(v[1]);
+              if (edge) {
+                mask_out(v[0], static_cast<uint32_t>(vis[0]));
+                mask_out(v[1], static_cast<uint32_t>(vis[0] >> 32));
+              }
             }
             uint32_t w[2][16];
 #pragma unroll
@@ -1064,12 +1062,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
               sum[e & 3] = add2(sum[e & 3], p);
               w[e >> 4][e & 15] = pack2<BF16>(p.x, p.y);
             }
-            if (c + 2 < TKT / 32) {
-              ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 64, v[0]);
-              ptx::tmem_ld_32x32b_x32(s_addr + 32 * c + 96, v[1]);
+            if (c > 0) {
+              ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
+              ptx::tmem_ld_32x32b_x32(s_addr + 32, v[1]);
             }
-            tmem_st_x16(s_addr + 16 * c, w[0]);
-            tmem_st_x16(s_addr + 16 * c + 16, w[1]);
+            tmem_st_x16(s_addr + TKT / 2 + 16 * c, w[0]);
+            tmem_st_x16(s_addr + TKT / 2 + 16 * c + 16, w[1]);
           }
           const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           l = l * f + (all.x + all.y);
@@ -1119,18 +1117,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         constexpr int NC = MODE == ROWS ? D : D / 2;
         const int col0 = MODE == ROWS ? 0 : x * NC;
 #pragma unroll 1
-        for (int c = 0; c < NC / 32; ++c) {
-          float o[32];
-          uint32_t u[32];
-          ptx::tmem_ld_32x32b_x32(o_addr + col0 + 32 * c, u);
+        for (int c = 0; c < NC / 16; ++c) {
+          uint32_t u[16];
+          ptx::tmem_ld_32x32b_x16(o_addr + col0 + 16 * c, u);
           tmem_ld_wait_for(u);
+          float o[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(u[e]);
           if (has) {
-            const int d = col0 + 32 * c;
+            const int d = col0 + 16 * c;
             if (whole) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < 2; ++e) {
                 uint4 w;
                 w.x = pack2<BF16>(o[8 * e] * inv, o[8 * e + 1] * inv);
                 w.y = pack2<BF16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
@@ -1141,12 +1139,12 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             } else {
               float* po = a.part_o + ((slot * (D / 4) + d / 4) * RT + my) * 4;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < 4; ++e)
                 *reinterpret_cast<float4*>(po + 4 * RT * e) =
                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             }
             if (any_bad)
-              add_bad<BF16>(a, s_bad, s.b, s.h, s.r.ctx, s.r.n, s.r.row0, tok, d, 32,
+              add_bad<BF16>(a, s_bad, s.b, s.h, s.r.ctx, s.r.n, s.r.row0, tok, d, 16,
                             whole ? a.out + at * D + d : nullptr,
                             a.part_o + ((slot * (D / 4) + d / 4) * RT + my) * 4, 4 * RT);
           }
