@@ -88,7 +88,10 @@ constexpr int NW = 4;              // warps that share a tile's keys, 16 each
 template <int D, int NT>
 struct Rows {
   static constexpr int RT = 8 * NT;
-  static constexpr int PAD = D == 64 ? 4 : 3;             // an item's cost beside its tiles
+  // an item's cost beside its tiles, which also bounds a piece (LEAST).  8 heads
+  // of 128, 16 rows: 2 requests of 20000 keys 35.7 us with 1, 32.6 with 3, 29.9
+  // with 6, but 1 of 1000 keys 14.5 with 3 and 17.8 with 6
+  static constexpr int PAD = D == 64 ? 4 : 3;
   static constexpr int LEAST = PAD + 1;                   // places of a CTA's piece at least
   static constexpr int THREADS = (NW + 2) * 32;           // and a producer each of K and V
   static constexpr int STAGE = 2 * TK * D * 2;            // keys and values of a tile
@@ -571,8 +574,8 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 //          measured the same with head size 128 and 64; with 256 columns it
 //          does not fit, and a half of the columns for each, S computed twice,
 //          took 109 us against 82 on 8 requests of 20003 keys.)
-//   ROWS   rows <= 256, head size 64 or 128: each has 128 rows with their own
-//          S and accumulator (a stream); a key tile serves both.
+//   ROWS   rows <= 256, head size 128: each has 128 rows with their own S and
+//          accumulator (a stream); a key tile serves both.
 // The maximum that a row's exponents refer to only moves when it grows by
 // more than 2^8: until then nothing is rescaled (probabilities up to 256 are
 // as exact in the 16-bit types, and sums are in 32 bits), so the pass over
@@ -586,7 +589,9 @@ template <int D, int MODE>
 struct Tile {
   static constexpr int TKT = D == 256 ? 64 : 128;        // keys of a tile
   static constexpr int RT = MODE == ROWS ? 256 : 128;
-  static constexpr int PAD = D == 64 ? 3 : 2;             // an item's cost beside its tiles
+  // an item's cost beside its tiles: 16 requests of 4099 keys, 16 heads of 64:
+  // 51.2 us with 1, 47.6 with 3, 48.9 with 6
+  static constexpr int PAD = D == 64 ? 3 : 2;
   static constexpr int LEAST = PAD + 1;                   // places of a CTA's piece at least
   static constexpr int SLOT = TKT * D * 2;
   static constexpr int QB = 128 * D * 2;                 // one Q tile
@@ -1336,7 +1341,20 @@ Ws ws_layout(int64_t grid, int64_t rt, int64_t D) {
 }
 
 // Which kernel serves requests of up to `rows` rows on a key head, as its
-// rows an item and its CTAs an SM.
+// rows an item and its CTAs an SM.  8 key heads, device time:
+//   16 rows, 16 requests of 1000 keys / 1 of 100000: rows kernel 14.8 / 44.4 us
+//     with head size 64, 20.1 / 74.7 with 128, 31.8 / 136 with 256; tile kernel
+//     18.5 / 44.6, 21.1 / 72.7, 24.0 / 127.  Over 26 sizes from 3 to 20000 keys
+//     the tile kernel takes 1.15 of the rows kernel's time with head size 64,
+//     0.99 with 128, 0.80 with 256 (and 1.16 with 256 and 1, 4 and 8 rows).
+//   256 rows, 16 requests of 6000 keys / 4 of 30000: ROWS 58.9 / 75.2 us with
+//     head size 64, 75.5 / 96.1 with 128; SHARED twice, the second reading the
+//     keys from L2 where it keeps pace, 59.7 / 81.1 and 88.9 / 133.  144 rows:
+//     56.2 / 64.8 and 70.3 / 77.6 against 45.8 / 52.4 and 67.6 / 71.7; over
+//     nine counts of rows from 144 to 512 SHARED takes 0.96 of ROWS's time with
+//     head size 64 and 1.11 of it with 128.
+// The tile kernel takes whole tokens, so a group above 128 heads is the rows
+// kernel's.
 struct Choice {
   int nt;         // rows kernel: eights of rows; 0: tile kernel
   int mode;       // tile kernel
@@ -1346,8 +1364,8 @@ Choice choose(int64_t max_new, int64_t group, int64_t D) {
   const int64_t rows = max_new * group;
   const int ctas = D == 256 ? 1 : 2;
   if (rows <= 8) return {1, 0, 8, ctas};
-  if (rows <= 16 || group > 128) return {2, 0, 16, ctas};   // the tile kernel takes whole tokens
-  if (D == 256 || rows <= 128 / group * group) return {0, SHARED, 128, 1};
+  if ((rows <= 16 && D < 256) || group > 128) return {2, 0, 16, ctas};
+  if (D != 128 || rows <= 128 / group * group) return {0, SHARED, 128, 1};
   return {0, ROWS, 256, 1};
 }
 
@@ -1413,7 +1431,7 @@ cudaError_t launch_dim(const TreeAttnCall& call, const Args& a, cudaStream_t st)
   const Choice c = choose(call.max_new, a.group, D);
   if (c.nt == 1) return launch_rows<BF16, D, 1>(call, a, st);
   if (c.nt == 2) return launch_rows<BF16, D, 2>(call, a, st);
-  if constexpr (D == 256) {
+  if constexpr (D != 128) {
     return launch_tile<BF16, D, SHARED>(call, a, st);
   } else {
     return c.mode == ROWS ? launch_tile<BF16, D, ROWS>(call, a, st)
