@@ -573,7 +573,8 @@ typedef struct {
  *                     ceil(ctx_len / P).  Entries below are kept
  *   free_pages        int32 [n_free]: pages not in use; pages are taken from
  *                     index *free_head on (NULL: 0), in request order
- *   free_head         int32 [1] or NULL
+ *   free_head         int32 [1] or NULL; not this call's info[2] (take turns
+ *                     with two infos)
  * outputs:
  *   row_start  int32 [B + 1]   first row of each request
  *   slots      int64 [capacity] slot of every row; -1 past the last row and

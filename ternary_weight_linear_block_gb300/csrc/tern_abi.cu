@@ -464,6 +464,7 @@ tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t
       (B > 0 && (ctx_len == nullptr || new_len == nullptr)) ||
       (B > 0 && table_width > 0 && table == nullptr) || (n_free > 0 && free_pages == nullptr) ||
       (held != nullptr && held == held_out) ||
+      (free_head != nullptr && free_head >= info && free_head < info + 4) ||
       (capacity > 0 && (slots == nullptr || positions == nullptr || request == nullptr)))
     return TERN_ERR_INVALID_ARG;
   if (!aligned16(slots) || !aligned16(positions) || !aligned16(request)) return TERN_ERR_ALIGN;

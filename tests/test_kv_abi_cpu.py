@@ -54,6 +54,13 @@ def test_plan_arguments():
         assert p(**bad) == want, bad
 
 
+def test_plan_refuses_its_own_next_head():
+    # every CTA reads free_head while one writes info
+    for head in (FAKE, FAKE + 8, FAKE + 12):
+        assert st("tern_kv_plan", FAKE, FAKE, 4, 16, FAKE, 8, 8, None, FAKE, 10, head, FAKE, 64, FAKE, FAKE,
+                  FAKE, None, FAKE, None) == INVALID, head
+
+
 def test_write_arguments():
     def w(c=None, k=FAKE, v=FAKE, s=(128, 64, 128, 64), slots=FAKE, t=3):
         c = c or cache()             # kept alive while its address is in use
