@@ -16,13 +16,16 @@ namespace {
 // Two sums over the requests carry everything: the rows before request b
 // (its row start) and the further pages taken before it.  Every CTA adds
 // them up for itself (B is at most 8192 lengths, read from L2) and keeps both,
-// the cached lengths and the pages held in shared memory, so one launch is enough and
-// no CTA waits for another; a row or a page then finds its request by
-// bisection and has one number to read, its page.  Bound: the launch and two
-// dependent round trips to L2 up to about 100,000 rows, then the 16 bytes
-// written for each row.
+// the cached lengths and the pages held in shared memory, so one launch is
+// enough and no CTA waits for another; a row or a page then finds its request
+// by bisection and has one number to read, its page.  Bound: the launch and
+// two dependent round trips to L2 (16 requests, 204 rows: 4.3 us on the
+// device), then the steps of the bisections before the 16 bytes written for
+// each row (1024 requests, 1.17 million rows: 12.7 us, 1.5 TB/s; written at
+// copy rate the rows would take 2.8).
 
 constexpr int PLAN_THREADS = 512;
+constexpr int PLAN_ROWS = 4;   // rows of one thread
 constexpr int PLAN_REQS = 2;   // consecutive requests of one thread in a round of the sums
 
 struct PlanArgs {
@@ -61,11 +64,11 @@ __device__ __forceinline__ void requests_of(const int* start, int B, const int (
 }
 
 // A warp has 32 ROWS consecutive rows, 32 at a time, so that its stores are
-// whole lines (a thread with consecutive rows of its own wrote half sectors:
-// 12.1 us for 1.17 million rows).  Four, so that a step's rows use many
-// threads; eight once four would not fit the GPU in one wave (two CTAs an SM).
-template <int ROWS>
+// whole lines.  Four: with eight, fewer threads wait for as many bisections
+// (204 rows 5.3 us against 4.6, 80000 rows 7.1 against 5.3, 1.17 million 13.3
+// against 12.7).
 __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_constant__ PlanArgs a) {
+  constexpr int ROWS = PLAN_ROWS;
   extern __shared__ int s_sums[];
   int* s_row = s_sums;                   // [B + 1] rows before request b
   int* s_page = s_row + a.B + 1;         // [B + 1] further pages before it
@@ -219,7 +222,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
 //
 // A copy of 16-byte chunks to slots: `tpt` threads (a power of two) share a
 // row, so that a few rows still use many threads and many rows keep a warp's
-// accesses in one row.  Bound: the rows read and written once.
+// accesses in one row.  Bound: the rows read and written once (95601 rows of
+// 8 heads of 128: 784 MB in 122 us, 6.4 TB/s, 0.95 of a copy's rate; 16 rows of
+// 20 heads: 1.8 us, the launch).
 
 constexpr int COPY_THREADS = 256;
 
@@ -269,8 +274,9 @@ __global__ void __launch_bounds__(COPY_THREADS) write_kernel(const WriteArgs a) 
 // after it was read as a source (path[j'] = j needs j' <= j), and a later
 // source path[j'] > path[j] >= j is never a row already written.  So loads
 // may run ahead of stores and no thread waits for another.  Bound: the
-// moved rows read and written once; at decode sizes the launch and three
-// dependent round trips (path, table, rows).
+// moved rows read and written once (61 requests of up to 64 drafts, 16 layers:
+// 452 MB in 73 us, 6.2 TB/s); at decode sizes the launch and three dependent
+// round trips (path, table, rows: 2 requests, 16 layers 5.1 us).
 
 constexpr int MAX_PATH = 256;
 constexpr int COMMIT_LAYERS = 64;   // layers of one launch: their pointers are kernel arguments
@@ -371,25 +377,16 @@ cudaError_t launch_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64
   const size_t smem = static_cast<size_t>(4 * B + 2) * sizeof(int);
   const cudaError_t e = once_per_device(attr_done, [] {
     constexpr int most = (4 * 8192 + 2) * static_cast<int>(sizeof(int));
-    const cudaError_t e4 =
-        cudaFuncSetAttribute(plan_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    return e4 != cudaSuccess ? e4 : cudaFuncSetAttribute(
-        plan_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   });
   if (e != cudaSuccess) return e;
   PlanArgs a{ctx_len, new_len, table, held, free_pages, free_head, row_start, slots, positions,
              request, held_out, info, table_stride, static_cast<int>(B), log2_of(page_size),
              static_cast<int>(table_width), static_cast<int>(n_free), static_cast<int>(capacity)};
-  const int64_t wave = int64_t(2) * kv_sm_count();
-  const auto blocks_of = [&](int rows) {
-    const int64_t per_block = int64_t(PLAN_THREADS) * rows;
-    return std::min(std::max<int64_t>((capacity + per_block - 1) / per_block, 1), wave);
-  };
-  if (blocks_of(4) < wave)
-    return launch(plan_kernel<4>, dim3(static_cast<unsigned>(blocks_of(4))), dim3(PLAN_THREADS), smem,
-                  st, a);
-  return launch(plan_kernel<8>, dim3(static_cast<unsigned>(blocks_of(8))), dim3(PLAN_THREADS), smem,
-                st, a);
+  const int64_t per_block = int64_t(PLAN_THREADS) * PLAN_ROWS;
+  const int64_t blocks = std::min(std::max<int64_t>((capacity + per_block - 1) / per_block, 1),
+                                  int64_t(2) * kv_sm_count());
+  return launch(plan_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PLAN_THREADS), smem, st, a);
 }
 
 cudaError_t launch_kv_write(const tern_kv_cache& c, const void* k, const void* v, int64_t k_token,
@@ -401,6 +398,8 @@ cudaError_t launch_kv_write(const tern_kv_cache& c, const void* k, const void* v
               c.pages * c.page_size, static_cast<int>(c.heads * c.dim / 8), log2_of(c.dim / 8),
               log2_of(c.page_size), 0};
   // one chunk a thread while that fits the GPU once, at most a warp a row beyond
+  // (a warp a row always: 16 rows of 20 heads 4.0 us against 1.9; one chunk a
+  // thread always: 95601 rows of 8 heads 126 us against 122)
   const int64_t room = int64_t(kv_sm_count()) * 2048;
   int shift = 0;
   while (shift < 8 && (2 << shift) <= a.chunks && (shift < 5 || (T << (shift + 1)) <= room)) ++shift;
