@@ -15,6 +15,12 @@
 // on the 16 side and 8 rows on the other: one to eight rows cost one
 // instruction of a tile, not two of which half is padding, and each
 // ldmatrix of keys or values serves all the rows.
+// Bound: the keys and values, read once (64 requests of up to 16001 keys, 8
+// heads of 128, 4 query heads on each: 2.63 GB in 395 us, 6.65 TB/s, 0.98 of a
+// copy's rate); small calls start, find their piece and join for about 9 us
+// (16 requests of up to 700 keys, 20 heads of 128: 70 MB in 16.4 us, of which
+// 10.3 at copy rate; 4 requests of 3 keys, heads of 64, 7.2 us).  A second kernel that joins
+// the pieces, in place of the last CTA to arrive, took 22.6 us against 19.7.
 #include <algorithm>
 
 #include "attn_dev.cuh"
@@ -581,6 +587,21 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // as exact in the 16-bit types, and sums are in 32 bits), so the pass over
 // the accumulator is rare.  Rows past the item's last cost their MMAs alone:
 // whole warps of them skip the softmax.
+//
+// Bound: keys and values up to about 64 rows of head size 128 (a context of 131001 keys, 16
+// drafts, 8 heads of 128, 64 rows on each: 537 MB in 89.5 us, 6.0 TB/s, 0.88 of
+// a copy's rate).  Otherwise each tile's chain of S, its softmax and P V, which
+// two streams only partly hide from each other (4 requests of 64 drafts over up
+// to 32768 keys, 512 rows on each of 8 heads: 154 us, 940 TFLOP/s, 0.51 of the
+// matrix rate; 8 requests of 29 drafts over up to 20003 keys, 232 rows on each of
+// 2 heads of 256: 77 us, 540 TFLOP/s; 16 requests of 23 drafts over up to 4099
+// keys, 16 heads of 64: 47 us, 3.9 TB/s).  A tile of 128 rows and keys took a
+// stream 3800 cycles when the first of these was 167 us: 1320 until S is there,
+// 500 for the maximum, 1380 for the reference, the exponentials and P, the rest
+// in handing over.  Measured and slower (512 rows): the streams' softmax in turns 257 us against 247 at
+// that step; four warpgroups, two threads a row, 183 against 167; 64-key tiles
+// with S two ahead 217; P V in two halves while the second is still exponents
+// 171.  For 64-wide heads two CTAs an SM took 66 us against 50.
 
 constexpr int TILE_THREADS = 384;   // K producer, MMA, TMEM, V producer; two warpgroups
 enum Mode { SHARED, ROWS };
@@ -1190,7 +1211,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
 // order.  The blocks share the passes of all items (each adds up for itself
 // where they lie), because a few items with many pieces and many with few
 // would otherwise leave most blocks without work.  Bound by the launch and
-// three round trips to L2, with many rows by L2's rate.
+// three round trips to L2, with many rows by L2's rate.  Joined by the last
+// CTA to arrive, as the rows kernel does, these items cost more: a context of
+// 131001 keys 111 us against 94, 512 rows a key head 198 against 170.
 constexpr int JOIN_THREADS = 256, JOIN_GROUPS = 8;
 static_assert(JOIN_THREADS == 1 << 8 && JOIN_THREADS / JOIN_GROUPS == 1 << 5, "passes");
 // Room for the arrival counters of this many CTAs (two an SM).
