@@ -588,22 +588,24 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // the accumulator is rare.  Rows past the item's last cost their MMAs alone:
 // whole warps of them skip the softmax.
 //
-// Bound: keys and values up to about 64 rows of head size 128 (a context of 131001 keys, 16
-// drafts, 8 heads of 128, 64 rows on each: 537 MB in 89.5 us, 6.0 TB/s, 0.88 of
-// a copy's rate).  Otherwise each tile's chain of S, its softmax and P V, which
-// two streams only partly hide from each other (4 requests of 64 drafts over up
-// to 32768 keys, 512 rows on each of 8 heads: 154 us, 940 TFLOP/s, 0.51 of the
-// matrix rate; 8 requests of 29 drafts over up to 20003 keys, 232 rows on each of
-// 2 heads of 256: 77 us, 540 TFLOP/s; 16 requests of 23 drafts over up to 4099
-// keys, 16 heads of 64: 47 us, 3.9 TB/s).  A tile of 128 rows and keys took a
-// stream 3800 cycles when the first of these was 167 us: 1320 until S is there,
-// 500 for the maximum, 1380 for the reference, the exponentials and P, the rest
-// in handing over.  Measured and slower (512 rows): the streams' softmax in turns 257 us against 247 at
-// that step; four warpgroups, two threads a row, 183 against 167; 64-key tiles
-// with S two ahead 217; P V in two halves while the second is still exponents
-// 171.  For 64-wide heads two CTAs an SM took 66 us against 50.
+// Bound: keys and values up to about 64 rows of head size 128 (a context of
+// 131001 keys, 16 drafts, 8 heads of 128, 64 rows on each: 537 MB in 89.5 us,
+// 6.0 TB/s, 0.88 of a copy's rate).  Above that each tile's chain of S, its
+// softmax and P V, which two streams only partly hide from each other (4
+// requests of 64 drafts over up to 32768 keys, 512 rows on each of 8 heads:
+// 154 us, 940 TFLOP/s, 0.51 of the matrix rate; 8 requests of 29 drafts over up
+// to 20003 keys, 232 rows on each of 2 heads of 256: 77 us, 540 TFLOP/s).  Short
+// items are bound by filling and draining each part (16 requests of 23 drafts
+// over up to 4099 keys, 16 heads of 64: 47 us, 3.9 TB/s).
+// A tile of 128 rows and keys took a stream 3800 cycles when the first of these
+// chains was 167 us: 1320 until S is there, 500 for the maximum, 1380 for the
+// reference, the exponentials and P, the rest in handing over.  Measured and
+// slower (512 rows): the streams' softmax in turns 257 us against 247 at that
+// step; four warpgroups, two threads a row, 183 against 167; 64-key tiles with
+// S two ahead 217; P V in two halves while the second is still exponents 171.
+// For 64-wide heads two CTAs an SM took 66 us against 50.
 
-constexpr int TILE_THREADS = 384;   // K producer, MMA, TMEM, V producer; two warpgroups
+constexpr int TILE_THREADS = 384;   // K producer, MMA, queries, V producer; two warpgroups
 enum Mode { SHARED, ROWS };
 
 template <int D, int MODE>
