@@ -437,10 +437,10 @@ class Workspace:
         return self.buf
 
     def head(self, nbytes: int, zero: int, stream=None) -> torch.Tensor:
-        """The buffer of at least ``nbytes`` bytes whose first ``zero`` bytes are
-        zero and stay so, for tern_tree_attention (which leaves partial sums
-        behind them)."""
-        self._ensure(nbytes)
+        """The buffer of at least ``nbytes`` bytes, and at least ``zero``, of
+        which the first ``zero`` are zero and stay so, for
+        tern_tree_attention (which leaves partial sums behind them)."""
+        self._ensure(max(nbytes, zero))
         if self.clean < zero:
             tern_workspace_init(self.buf, zero, stream)
         self.clean = zero

@@ -181,13 +181,14 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
         out = torch.empty((t, hq, dim), dtype=dtype, device=cache.device)
     if return_lse and lse is None:
         lse = torch.empty((t, hq), dtype=torch.float32, device=cache.device)
-    if ws is None:
-        ws = B.Workspace(cache.device)
-    buf = ws.head(_workspace_bytes(max_new, hq, heads, dim), B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
+    need, at, size = _workspace_bytes(max_new, hq, heads, dim), 0, 0
+    if need:      # none: there are no new tokens, or the call below refuses what it gets
+        buf = (B.Workspace(cache.device) if ws is None else ws).head(
+            need, B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
+        at, size = buf.data_ptr(), buf.numel()
     st = (_calls or _native()).attention(
         cache.address, dtype, heads, dim, q, table, ctx_len, row_start, max_new, mask,
-        dim ** -0.5 if scale is None else scale, out, lse, buf.data_ptr(), buf.numel(),
-        B._stream(stream))
+        dim ** -0.5 if scale is None else scale, out, lse, at, size, B._stream(stream))
     if st:
         _failed("tern_tree_attention", st)
     return (out, lse) if return_lse else out
