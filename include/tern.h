@@ -581,7 +581,8 @@ typedef struct {
  *                               where a token has no page
  *   positions  int32 [capacity] position of every row (0 past the last)
  *   request    int32 [capacity] request of every row (-1 past the last)
- *   held_out   int32 [B] or NULL  held, and the pages taken
+ *   held_out   int32 [B] or NULL  held, and the pages that it got (fewer than
+ *                              it needs where the free pages ran out)
  *   info       int32 [4]       rows in all, pages taken, the next free_head,
  *                              flags: 1 free pages ran out (the table gets
  *                              -1), 2 a request longer than its table row,

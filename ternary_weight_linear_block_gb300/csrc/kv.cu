@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
   pdl_wait();
   pdl_launch_dependents();
   const int head0 = a.free_head != nullptr ? *a.free_head : 0;   // on its way with the lengths
+  const int head = min(max(head0, 0), a.n_free);
+  const int64_t avail = a.n_free - head;
 
   int64_t rows0 = 0, pages0 = 0;
   int flags = 0;
@@ -104,7 +106,6 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
       if (b < a.B) {
         s_ctx[b] = c;
         s_held[b] = static_cast<int>(held);
-        if (a.held_out != nullptr && blockIdx.x == 0) a.held_out[b] = static_cast<int>(held + more[i]);
       }
     }
     const int64_t mine_r = rows, mine_p = pages;
@@ -135,6 +136,9 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
     }
 #pragma unroll
     for (int i = 0; i < PLAN_REQS; ++i) {
+      // held: what it has and what it gets of the free pages, which may run out
+      if (a.held_out != nullptr && blockIdx.x == 0 && b0 + i < a.B)
+        a.held_out[b0 + i] = s_held[b0 + i] + static_cast<int>(min(max(avail - before_p, int64_t(0)), more[i]));
       before_r += n[i];
       before_p += more[i];
       if (b0 + i < a.B) {   // sums past 2^31 stay at its end: past every row asked for
@@ -144,8 +148,6 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
     }
   }
   if (tid == 0) s_row[0] = s_page[0] = 0;
-  const int head = min(max(head0, 0), a.n_free);
-  const int64_t avail = a.n_free - head;
   if (blockIdx.x == 0) {
     const int too_long = __syncthreads_or(flags & 2) ? 2 : 0;
     const int negative = __syncthreads_or(flags & 8) ? 8 : 0;
