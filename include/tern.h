@@ -644,6 +644,10 @@ tern_status tern_kv_commit(const tern_kv_cache* caches, int64_t layers, const in
  *              (tern_workspace_init); a call leaves them zero.  Calls that may
  *              run at the same time need a workspace each; after a timeout
  *              (tern_check) the bytes must be zeroed again
+ * Scores, maxima, sums and lse are held in 32 bits.  The softmax's
+ * probabilities are rounded to the cache's type for their product with the
+ * values, relatively (in fp16 those below 2^-21 of the row's largest by up to
+ * 2^-32 of it), and out is rounded to it once more.
  * A row that sees nothing (or only scores of -infinity) has out = 0 and
  * lse = -infinity.  What a row does not see has no influence on it: masked
  * keys and values may hold infinities or NaN, and the cache past a request's

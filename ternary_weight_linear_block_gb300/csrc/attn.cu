@@ -5,7 +5,9 @@
 //   out = sum 2^(t_j - m) v_j / l,  lse = (m + log2 l) ln 2,
 // kept over the tiles of a piece as (m, l, unnormalised out) in 32 bits and
 // rescaled where m grows.  The probabilities are rounded to the cache's type
-// for the second product, as its values are; l sums them unrounded.
+// for the second product, as its values are (the matrix instructions take both
+// operands in one type, and splitting a probability into two would double that
+// product); l sums them unrounded.  m is less than the maximum by kLift.
 //
 // attn_rows_kernel: up to 16 rows an item, tiles of 64 keys.  A producer warp
 // copies each page's part of a tile with TMA into a ring; four warps take 16
@@ -431,7 +433,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-            const float mn = fmaxf(m[n][e], x);
+            const float mn = fmaxf(m[n][e], x - kLift<BF16>);
             ms[e] = mn == -INFINITY ? 0.f : mn;
             al[n][e] = ex2(m[n][e] - ms[e]);
             moved |= mn != m[n][e];
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
           *reinterpret_cast<uint2*>(a.out + at * D + d) =
               make_uint2(pack2<BF16>(x.x * inv, x.y * inv), pack2<BF16>(x.z * inv, x.w * inv));
           if (d == 0 && a.lse != nullptr)
-            a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+            a.lse[at] = ll == 0.f ? -INFINITY : lse_of<BF16>(mm, ll);
         } else {
           *reinterpret_cast<float4*>(a.part_o + ((slot * (D / 4) + d / 4) * RT + r) * 4) = x;
           if (d == 0) a.part_ml[slot * RT + r] = make_float2(mm, ll);
@@ -583,9 +585,9 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 //   ROWS   rows <= 256, head size 128: each has 128 rows with their own S and
 //          accumulator (a stream); a key tile serves both.
 // The maximum that a row's exponents refer to only moves when it grows by
-// more than 2^8: until then nothing is rescaled (probabilities up to 256 are
-// as exact in the 16-bit types, and sums are in 32 bits), so the pass over
-// the accumulator is rare.  Rows past the item's last cost their MMAs alone:
+// more than 2^8: until then nothing is rescaled (probabilities above one round
+// as others do, kLift leaves fp16 room for them, and sums are in 32 bits), so the
+// pass over the accumulator is rare.  Rows past the item's last cost their MMAs alone:
 // whole warps of them skip the softmax.
 //
 // Bound: keys and values up to about 64 rows of head size 128 (a context of
@@ -1025,7 +1027,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
               mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(v[e >> 5][e & 31]),
                                                                __uint_as_float(v[e >> 5][(e & 31) + 1])));
           }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale - kLift<BF16>;
           float f = 1.f;            // of this thread's sum
           bool move = false;        // of the accumulator, by `fo`
           float fo = 1.f;
@@ -1181,7 +1183,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           if (!whole)
             a.part_ml[slot * RT + my] = make_float2(m, l);
           else if (a.lse != nullptr)
-            a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            a.lse[at] = l == 0.f ? -INFINITY : lse_of<BF16>(m, l);
         }
       }
       if (!whole && s.t0 == 0 && wid == 0) {

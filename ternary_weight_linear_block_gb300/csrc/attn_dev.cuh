@@ -369,6 +369,24 @@ __device__ __noinline__ void add_bad(const Args& a, const unsigned int* s_bad, i
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// The reference that a row's exponents are taken from is its maximum less this
+// much: 2^7 is then the largest probability when the reference is set and 2^15
+// before it moves on.  fp16 has no numbers below 2^-24 and loses bits below
+// 2^-14, so that with the maximum itself a probability of 2^-24.6 counted half as
+// much again and one of 2^-25 nothing, beside a sum that had both; so it is off
+// by at most 2^-32 of the largest, or relatively as the type rounds.  bf16 has
+// the exponents of 32 bits.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+
+// lse of a row with a sum l > 0 referred to m (which is less by kLift than the
+// maximum).
+template <bool BF16>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  if constexpr (BF16) return (m + log2f(l)) * kLn2;
+  return ((m + kLift<BF16>) + log2f(l * (1.f / 128.f))) * kLn2;
+}
+
 // ------------------------------------------------------------------ join
 //
 // out = sum 2^(m_i - m) out_i / sum 2^(m_i - m) l_i over the pieces of an item
@@ -407,7 +425,7 @@ __device__ __forceinline__ void write_joined(const Args& a, const Item& it, int 
   *reinterpret_cast<uint2*>(a.out + at * D + d4 * 4) =
       make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
   if (d4 == 0 && a.lse != nullptr)
-    a.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    a.lse[at] = l == 0.f ? -INFINITY : lse_of<BF16>(m, l);
 }
 
 // The one or two items whose parts a CTA stored (the first and the last of its

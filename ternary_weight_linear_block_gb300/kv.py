@@ -170,7 +170,9 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
     whose bits are set in ``mask`` (int64 [T, words]; None: a chain, token i
     sees 0 .. i).  Returns out [T, query heads, dim], and with ``return_lse``
     also the logarithm of each row's sum of exponentials (fp32 [T, query heads]).
-    A row that sees nothing is 0, its lse -infinity."""
+    A row that sees nothing is 0, its lse -infinity.  The probabilities are
+    rounded to the cache's type for their product with the values; everything
+    else up to the output's own rounding is in 32 bits."""
     t, hq, _ = q.shape
     heads, dim, dtype = cache.heads, cache.dim, cache.dtype
     if stream is not None and (out is None or ws is None or (return_lse and lse is None)):
