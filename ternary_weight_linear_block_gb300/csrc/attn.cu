@@ -1499,7 +1499,9 @@ cudaError_t launch_tree_attention(const TreeAttnCall& call, cudaStream_t st) {
   a.H = static_cast<int>(c.heads);
   a.Hq = static_cast<int>(call.Hq);
   a.group = static_cast<int>(call.Hq / c.heads);
-  a.group_mul = a.group > 1 && a.group < 4096 ? static_cast<uint32_t>((uint64_t(1) << 32) / a.group + 1) : 0;
+  // exact for every row that T tokens can have: r group < 2^32 for r < T group
+  a.group_mul = a.group > 1 && call.T < (int64_t(1) << 32) / (int64_t(a.group) * a.group)
+                    ? static_cast<uint32_t>((uint64_t(1) << 32) / a.group + 1) : 0;
   a.scale_log2 = call.scale * 1.4426950408889634f;
   const bool bf = c.dtype == TERN_KV_BF16;
   if (c.dim == 64) return bf ? launch_dim<true, 64>(call, a, st) : launch_dim<false, 64>(call, a, st);

@@ -52,8 +52,9 @@ struct Req {
   int ctx, n, row0, len, tiles, rts;
 };
 
-// Row r of a request on a key head -> its new token.  r is below 256 group, so
-// the product with 2^32 / group + 1 is exact while group < 4096.
+// Row r of a request on a key head -> its new token.  r is below T group,
+// whatever the lengths on the GPU are, and the product with 2^32 / group + 1 is
+// exact while r group < 2^32: the host gives the factor only then.
 __device__ __forceinline__ int div_group(const Args& a, int r) {
   if (a.group_mul != 0) return static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.group_mul));
   return a.group == 1 ? r : r / a.group;
