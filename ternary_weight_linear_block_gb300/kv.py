@@ -70,7 +70,8 @@ def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int) -> int:
 def _on(stream):
     """Allocate on the stream that the call runs on."""
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream)
+        # the default stream's handle is 0, of which ExternalStream makes a new stream
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 
