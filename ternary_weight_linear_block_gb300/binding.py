@@ -12,6 +12,7 @@ outputs with torch and call the entry points in order.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -143,6 +144,14 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
+
+
+def _on(stream):
+    """Allocate on the stream that a call runs on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        # the default stream's handle is 0, of which ExternalStream makes a new stream
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _call(name, *args):
@@ -420,17 +429,19 @@ class Workspace:
         self.clean = 0        # leading bytes known to be zero
         _WORKSPACES.add(self)
 
-    def _ensure(self, nbytes: int) -> int:
+    def _ensure(self, nbytes: int, stream) -> int:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            # on the stream that uses it, which may still use the one that it replaces
+            with contextlib.nullcontext() if stream is None else _on(stream):
+                self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             self.clean = 0
         return nbytes
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         """The buffer with at least ``nbytes`` zero bytes, for tern_gemv_decode
         or tern_linear_decode."""
-        nbytes = self._ensure(nbytes)
+        nbytes = self._ensure(nbytes, stream)
         if self.clean < nbytes:
             tern_workspace_init(self.buf, self.buf.numel(), stream)
             self.clean = self.buf.numel()
@@ -440,7 +451,7 @@ class Workspace:
         """The buffer of at least ``nbytes`` bytes, and at least ``zero``, of
         which the first ``zero`` are zero and stay so, for
         tern_tree_attention (which leaves partial sums behind them)."""
-        self._ensure(max(nbytes, zero))
+        self._ensure(max(nbytes, zero), stream)
         if self.clean < zero:
             tern_workspace_init(self.buf, zero, stream)
         self.clean = zero
@@ -449,7 +460,7 @@ class Workspace:
     def scratch(self, nbytes: int, stream=None) -> torch.Tensor:
         """The buffer of at least ``nbytes`` bytes, any contents, for a GEMM
         (which leaves partial sums in it)."""
-        self._ensure(nbytes)
+        self._ensure(nbytes, stream)
         self.clean = 0
         return self.buf
 

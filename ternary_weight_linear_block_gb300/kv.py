@@ -67,14 +67,6 @@ def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int) -> int:
     return B.tern_tree_attention_workspace_bytes(max_new, hq, heads, dim)
 
 
-def _on(stream):
-    """Allocate on the stream that the call runs on."""
-    if not isinstance(stream, torch.cuda.Stream):
-        # the default stream's handle is 0, of which ExternalStream makes a new stream
-        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
-
-
 class KVCache:
     """Keys and values of one layer as pages: two tensors [pages, page_size,
     heads, dim] of bf16 or fp16 with the same strides (a permuted view of
@@ -143,7 +135,7 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
         if stream is None:
             plan = KVPlan.empty(ctx_len.shape[0], capacity, ctx_len.device)
         else:
-            with _on(stream):
+            with B._on(stream):
                 plan = KVPlan.empty(ctx_len.shape[0], capacity, ctx_len.device)
     st = (_calls or _native()).plan(ctx_len, new_len, table, free_pages, free_head, page_size,
                                     capacity, *plan, held, held_out, B._stream(stream))
@@ -177,7 +169,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
     t, hq, _ = q.shape
     heads, dim, dtype = cache.heads, cache.dim, cache.dtype
     if stream is not None and (out is None or ws is None or (return_lse and lse is None)):
-        with _on(stream):          # what is allocated here belongs to that stream
+        with B._on(stream):          # what is allocated here belongs to that stream
             return tree_attention(q, cache, table, ctx_len, row_start, max_new, mask, scale, out,
                                   return_lse, lse, ws)
     if out is None:
@@ -210,7 +202,7 @@ def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len:
         if stream is None:
             ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
         else:
-            with _on(stream):
+            with B._on(stream):
                 ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
     st = (_calls or _native()).commit(b"".join([c.desc_bytes for c in caches]), len(caches), table,
                                       ctx_len, path, path_len, ctx_out, B._stream(stream))
