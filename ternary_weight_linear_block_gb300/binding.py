@@ -438,13 +438,19 @@ class Workspace:
             self.clean = 0
         return nbytes
 
+    def _zero(self, nbytes: int, stream):
+        tern_workspace_init(self.buf, nbytes, stream)
+        # a zero-fill that is only captured runs with its graph, and not before
+        # a call that comes first
+        if not (self.buf.is_cuda and torch.cuda.is_current_stream_capturing()):
+            self.clean = nbytes
+
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         """The buffer with at least ``nbytes`` zero bytes, for tern_gemv_decode
         or tern_linear_decode."""
         nbytes = self._ensure(nbytes, stream)
         if self.clean < nbytes:
-            tern_workspace_init(self.buf, self.buf.numel(), stream)
-            self.clean = self.buf.numel()
+            self._zero(self.buf.numel(), stream)
         return self.buf
 
     def head(self, nbytes: int, zero: int, stream=None) -> torch.Tensor:
@@ -453,8 +459,8 @@ class Workspace:
         tern_tree_attention (which leaves partial sums behind them)."""
         self._ensure(max(nbytes, zero), stream)
         if self.clean < zero:
-            tern_workspace_init(self.buf, zero, stream)
-        self.clean = zero
+            self._zero(zero, stream)
+        self.clean = min(self.clean, zero)
         return self.buf
 
     def scratch(self, nbytes: int, stream=None) -> torch.Tensor:
