@@ -129,6 +129,18 @@ static int read_heads(PyObject* o, PyObject* dtype, int64_t heads, int64_t dim, 
   return 1;
 }
 
+/* Returns an entry point's status as a number.  It runs without the interpreter's
+ * lock: a launch waits where the stream's queue is full, e.g. behind a host
+ * callback that needs the lock. */
+#define RETURN_STATUS(call)          \
+  do {                               \
+    tern_status st_;                 \
+    Py_BEGIN_ALLOW_THREADS           \
+    st_ = (call);                    \
+    Py_END_ALLOW_THREADS             \
+    return PyLong_FromLong(st_);     \
+  } while (0)
+
 static int counted(Py_ssize_t got, Py_ssize_t want) {
   if (got == want) return 1;
   PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, got);
@@ -183,9 +195,9 @@ static PyObject* py_plan(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (start.shape[0] != b + 1 || info.shape[0] != 4 || slots.shape[0] < capacity ||
       pos.shape[0] < capacity || req.shape[0] < capacity)
     return refuse("plan: buffers too small"), NULL;
-  return PyLong_FromLong(f_plan(ctx.p, new_len.p, b, page, table.p, stride, table.shape[1],
-                                held.p, free_pages.p, free_pages.shape[0], head.p, start.p,
-                                capacity, slots.p, pos.p, req.p, held_out.p, info.p, stream));
+  RETURN_STATUS(f_plan(ctx.p, new_len.p, b, page, table.p, stride, table.shape[1],
+                       held.p, free_pages.p, free_pages.shape[0], head.p, start.p,
+                       capacity, slots.p, pos.p, req.p, held_out.p, info.p, stream));
 }
 
 /* write(cache address, dtype, heads, dim, k, v, slots, stream) */
@@ -203,7 +215,7 @@ static PyObject* py_write(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return NULL;
   if (v.shape[0] != k.shape[0] || slots.shape[0] < k.shape[0])
     return refuse("v, slots: expected as many rows as k"), NULL;
-  return PyLong_FromLong(f_write(cache, k.p, v.p, kr, kh, vr, vh, slots.p, k.shape[0], stream));
+  RETURN_STATUS(f_write(cache, k.p, v.p, kr, kh, vr, vh, slots.p, k.shape[0], stream));
 }
 
 /* attention(cache address, dtype, heads, dim, q, table, ctx_len, row_start, max_new,
@@ -244,9 +256,9 @@ static PyObject* py_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     if (lse.shape[0] != t || lse.shape[1] != hq)
       return refuse("lse: expected [rows, query heads]"), NULL;
   }
-  return PyLong_FromLong(f_attn(q.p, qr, qh, cache, table.p, stride, table.shape[1], ctx.p, start.p,
-                                mask.p, mask.shape[1], b, t, hq, max_new, (float)scale, out.p,
-                                lse.p, ws, ws_bytes, stream));
+  RETURN_STATUS(f_attn(q.p, qr, qh, cache, table.p, stride, table.shape[1], ctx.p, start.p,
+                       mask.p, mask.shape[1], b, t, hq, max_new, (float)scale, out.p,
+                       lse.p, ws, ws_bytes, stream));
 }
 
 /* commit(descriptions as bytes, layers, table, ctx_len, path, path_len, ctx_out, stream) */
@@ -269,9 +281,9 @@ static PyObject* py_commit(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   const int64_t b = ctx.shape[0];
   if (path.shape[0] != b || len.shape[0] != b || out.shape[0] != b)
     return refuse("path, path_len, ctx_out: expected a row each request"), NULL;
-  return PyLong_FromLong(f_commit((const tern_kv_cache*)PyBytes_AS_STRING(a[0]), layers, table.p,
-                                  stride, table.shape[1], ctx.p, path.p, path.shape[1], len.p,
-                                  out.p, b, stream));
+  RETURN_STATUS(f_commit((const tern_kv_cache*)PyBytes_AS_STRING(a[0]), layers, table.p,
+                         stride, table.shape[1], ctx.p, path.p, path.shape[1], len.p,
+                         out.p, b, stream));
 }
 
 static PyMethodDef methods[] = {
