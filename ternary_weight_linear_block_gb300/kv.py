@@ -53,7 +53,7 @@ def _native():
         lib = B.lib()
         names = ("tern_kv_plan", "tern_kv_write", "tern_tree_attention", "tern_kv_commit")
         module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
-                    torch.int32, torch.int64, torch.float32)
+                    torch.int32, torch.int64, torch.float32, torch._C._cuda_getDevice)
         _calls = module
     return _calls
 
@@ -63,7 +63,7 @@ def _failed(name: str, status: int):
 
 
 @functools.lru_cache(maxsize=None)
-def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int) -> int:
+def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int, index: int) -> int:
     return B.tern_tree_attention_workspace_bytes(max_new, hq, heads, dim)
 
 
@@ -79,7 +79,7 @@ class KVCache:
         _check(k.stride(3) == 1, "k, v: expected to be dense along the last axis")
         self.k, self.v = k, v
         self.pages, self.page_size, self.heads, self.dim = k.shape
-        self.dtype, self.device = k.dtype, k.device
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
         # an axis of length one may have any stride: give it one that passes
         ps, ts, hs = (k.stride(i) if k.shape[i] > 1 else self.page_size * self.heads * self.dim
                       for i in range(3))
@@ -146,8 +146,8 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
 
 def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
     """Rows of keys and values [T, heads, dim] into the cache's slots (-1: skipped)."""
-    st = (_calls or _native()).write(cache.address, cache.dtype, cache.heads, cache.dim, k, v, slots,
-                                     B._stream(stream))
+    st = (_calls or _native()).write(cache.address, cache.dtype, cache.heads, cache.dim,
+                                     cache.index, k, v, slots, B._stream(stream))
     if st:
         _failed("tern_kv_write", st)
 
@@ -176,13 +176,14 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
         out = torch.empty((t, hq, dim), dtype=dtype, device=cache.device)
     if return_lse and lse is None:
         lse = torch.empty((t, hq), dtype=torch.float32, device=cache.device)
-    need, at, size = _workspace_bytes(max_new, hq, heads, dim), 0, 0
+    need, at, size = _workspace_bytes(max_new, hq, heads, dim, cache.index), 0, 0
     if need:      # none: there are no new tokens, or the call below refuses what it gets
         buf = (B.Workspace(cache.device) if ws is None else ws).head(
             need, B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
+        _check(buf.get_device() == cache.index, "ws: expected a workspace on the cache's device")
         at, size = buf.data_ptr(), buf.numel()
     st = (_calls or _native()).attention(
-        cache.address, dtype, heads, dim, q, table, ctx_len, row_start, max_new, mask,
+        cache.address, dtype, heads, dim, cache.index, q, table, ctx_len, row_start, max_new, mask,
         dim ** -0.5 if scale is None else scale, out, lse, at, size, B._stream(stream))
     if st:
         _failed("tern_tree_attention", st)
@@ -198,14 +199,16 @@ def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len:
     path has to increase; it is cut where it does not."""
     if isinstance(caches, KVCache):
         caches = (caches,)
+    _check(len({c.index for c in caches}) == 1, "caches: expected one or more, on the same device")
     if ctx_out is None:
         if stream is None:
             ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
         else:
             with B._on(stream):
                 ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
-    st = (_calls or _native()).commit(b"".join([c.desc_bytes for c in caches]), len(caches), table,
-                                      ctx_len, path, path_len, ctx_out, B._stream(stream))
+    st = (_calls or _native()).commit(b"".join([c.desc_bytes for c in caches]), len(caches),
+                                      caches[0].index, table, ctx_len, path, path_len, ctx_out,
+                                      B._stream(stream))
     if st:
         _failed("tern_kv_commit", st)
     return ctx_out

@@ -21,7 +21,10 @@ class Tensor:
 
     def __init__(self, dtype, *shape, ptr=1 << 20):
         self.dtype, self.shape, self.ptr = dtype, tuple(shape), ptr
-        self.is_cuda = True
+        self.is_cuda, self.device = True, 0
+
+    def get_device(self):
+        return self.device
 
     def stride(self):
         out, step = [], 1
@@ -46,7 +49,8 @@ def calls(tmp_path):
     spec.loader.exec_module(module)
 
     def bind_to(name):
-        module.bind(*[ctypes.cast(getattr(ctypes.CDLL(None), name), ctypes.c_void_p).value] * 4, I32, I64, F32)
+        module.bind(*[ctypes.cast(getattr(ctypes.CDLL(None), name), ctypes.c_void_p).value] * 4, I32, I64, F32,
+                    lambda: 0)
         return module
     return bind_to
 
@@ -58,11 +62,15 @@ def plan_args(ptr=1 << 20):
 
 
 def write_args(ptr=1 << 20):
-    return [ptr, B16, 2, 64, Tensor(B16, 3, 2, 64), Tensor(B16, 3, 2, 64), Tensor(I64, 3), 0]
+    return [ptr, B16, 2, 64, 0, Tensor(B16, 3, 2, 64), Tensor(B16, 3, 2, 64), Tensor(I64, 3), 0]
+
+
+def commit_args():
+    return [bytes(80), 1, 0, Tensor(I32, 2, 4), Tensor(I32, 2), Tensor(I32, 2, 3), Tensor(I32, 2), Tensor(I32, 2), 0]
 
 
 def attention_args(ptr=1 << 20):
-    return [1 << 20, B16, 2, 64, Tensor(B16, 3, 4, 64, ptr=ptr), Tensor(I32, 2, 4), Tensor(I32, 2), Tensor(I32, 3), 2,
+    return [1 << 20, B16, 2, 64, 0, Tensor(B16, 3, 4, 64, ptr=ptr), Tensor(I32, 2, 4), Tensor(I32, 2), Tensor(I32, 3), 2,
             Tensor(I64, 3, 1), 0.125, Tensor(B16, 3, 4, 64), Tensor(F32, 3, 4), 1 << 20, 1 << 20, 0]
 
 
@@ -85,3 +93,29 @@ def test_other_threads_run_during_a_call(calls, name, args):
         stop.set()
         thread.join()
     assert last - first >= 0.3 and sum(first + 0.02 < t < last - 0.02 for t in ticks) >= 5
+
+
+@pytest.mark.parametrize("name,args", [("plan", plan_args), ("write", write_args), ("attention", attention_args),
+                                       ("commit", commit_args)])
+def test_what_is_on_another_device_is_refused(calls, name, args):
+    """Every tensor and the cache; the entry point (abs, which does nothing) is reached without one."""
+    call = getattr(calls("abs"), name)
+
+    def given():
+        a = args()
+        if name == "plan":
+            a[4], a[12], a[13] = Tensor(I32, 1), Tensor(I32, 2), Tensor(I32, 2)
+        return a
+    call(*given())
+    at = [i for i, x in enumerate(given()) if isinstance(x, Tensor)]
+    assert len(at) == {"plan": 12, "write": 3, "attention": 7, "commit": 5}[name]
+    for i in at:
+        a = given()
+        a[i].device = 1
+        with pytest.raises(ValueError, match="current device"):
+            call(*a)
+    if name != "plan":
+        a = given()
+        a[2 if name == "commit" else 4] = 1
+        with pytest.raises(ValueError, match="current device"):
+            call(*a)

@@ -51,7 +51,8 @@ def test_attention_calls_without_work_or_refused_use_no_workspace(zeroed, monkey
     monkeypatch.setattr(kv, "_native", lambda: SimpleNamespace(attention=lambda *a: seen.append(a) or 2))
     monkeypatch.setattr(kv, "_calls", None)
     monkeypatch.setattr(B, "_stream", lambda stream: 0)
-    cache = SimpleNamespace(heads=heads, dim=dim, dtype=torch.bfloat16, device=torch.device("cpu"), address=0)
+    cache = SimpleNamespace(heads=heads, dim=dim, dtype=torch.bfloat16, device=torch.device("cpu"), index=0,
+                            address=0)
     q, ints = torch.zeros(3, hq, dim, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
     out = torch.empty_like(q)
     for ws in (None, B.Workspace("cpu")):
