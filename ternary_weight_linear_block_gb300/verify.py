@@ -20,6 +20,12 @@ import torch
 from . import binding as B
 from . import kv
 
+MAX_NEW = 256      # new tokens of a request in one step, as tern_tree_attention takes them
+
+
+_FLAGS = {1: "the cache has no free pages left", 2: "a request is longer than its table row's pages",
+          4: "new_len has more rows than x", 8: "a negative length"}
+
 
 @dataclass
 class Block:
@@ -61,17 +67,33 @@ class VerifyStack:
     def step(self, x: torch.Tensor, new_len: torch.Tensor, max_new: int,
              mask: torch.Tensor | None = None) -> torch.Tensor:
         """Hidden states [rows, hidden] of the new tokens through all blocks;
-        new_len int32 [requests] rows each (``max_new`` at most), masked as
-        kv.tree_attention's ``mask``.  The tokens stay drafts until commit."""
-        rows = x.shape[0]
+        new_len int32 [requests] rows each (``max_new`` at most, which is 256
+        at most: a longer prompt goes in parts), masked as
+        kv.tree_attention's ``mask``.  The tokens stay drafts until commit.
+        Whether they all had a place, only ``check`` says."""
+        if max_new > MAX_NEW:
+            raise ValueError(f"max_new: expected {MAX_NEW} at most, longer prompts in parts")
         self.plan = kv.kv_plan(self.ctx_len, new_len, self.table, self.free_pages, self.page_size,
-                               rows, free_head=self.free_head, held=self.held,
+                               x.shape[0], free_head=self.free_head, held=self.held,
                                held_out=self.held_next)
-        self.held, self.held_next = self.held_next, self.held
-        self.free_head = self.plan.info[2:3]
         for block in self.blocks:
             x = x + self.block(block, x, max_new, mask)
+        # only now, so that after a call that was refused the next step plans
+        # with the same pages
+        self.held, self.held_next = self.held_next, self.held
+        self.free_head = self.plan.info[2:3]
         return x
+
+    def check(self):
+        """Raises if the last step's tokens did not all fit, or if a wait on
+        the GPU gave up (synchronises).  A token without a page is not
+        written, the step's other rows see it as a zero key, and commit cuts
+        a path there."""
+        B.tern_check()
+        flags = int(self.plan.info[3])
+        what = [name for bit, name in _FLAGS.items() if flags & bit]
+        if what:
+            raise RuntimeError("step: " + ", ".join(what))
 
     def block(self, block: Block, x: torch.Tensor, max_new: int, mask) -> torch.Tensor:
         cache, p = block.cache, self.plan
@@ -128,8 +150,8 @@ def main():
         path = torch.zeros((requests, 4), dtype=torch.int32)
         for b, p in enumerate(accepted):
             path[b, :len(p)] = torch.tensor(p)
+        stack.check()
         lengths = stack.commit(path.cuda(), ints([len(p) for p in accepted]))
-        B.tern_check()
         print(f"verified {tuple(y.shape)} drafts, kept {[len(p) for p in accepted]}, "
               f"lengths now {lengths.tolist()}, finite: {bool(torch.isfinite(y).all())}")
 
