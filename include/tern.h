@@ -579,7 +579,10 @@ typedef struct {
  *   row_start  int32 [B + 1]   first row of each request
  *   slots      int64 [capacity] slot of every row; -1 past the last row and
  *                               where a token has no page
- *   positions  int32 [capacity] position of every row (0 past the last)
+ *   positions  int32 [capacity] ctx_len + its index, the place of every row's
+ *                               token (0 past the last); of a chain's tokens
+ *                               also their position.  In a tree a token's
+ *                               position is ctx_len + the ancestors it has
  *   request    int32 [capacity] request of every row (-1 past the last)
  *   held_out   int32 [B] or NULL  held, and the pages that it got (fewer than
  *                              it needs where the free pages ran out)

@@ -104,7 +104,7 @@ class KVCache:
 class KVPlan(NamedTuple):
     row_start: torch.Tensor   # int32 [requests + 1]: first row of each request
     slots: torch.Tensor       # int64 [capacity]: where each row's keys and values go, -1: nowhere
-    positions: torch.Tensor   # int32 [capacity]: each row's position in its request
+    positions: torch.Tensor   # int32 [capacity]: each row's place in its request's cache (see kv_plan)
     request: torch.Tensor     # int32 [capacity]: each row's request, -1 past the last
     info: torch.Tensor        # int32 [4]: rows, pages taken, next free_head, flags
 
@@ -127,6 +127,11 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
     and written into ``table`` in place.  ``capacity`` rows are planned;
     ``plan`` gives the outputs' buffers.  info[2] is the next step's free_head
     (steps that reuse buffers take turns with two), info[3] says what did not fit.
+
+    ``positions`` are places in the cache, ctx_len + the row's index: of a
+    prompt's or a chain's tokens also their positions, e.g. for a rotary
+    embedding.  A tree's token has position ctx_len + tree_depths, which is
+    the place that kv_commit moves it to.
 
     A request has the pages of its cached tokens, or ``held`` int32
     [requests] of them: the pages of drafts that were not kept stay in its
@@ -226,3 +231,14 @@ def ancestor_masks(parents: Sequence[int], device="cuda") -> torch.Tensor:
     signed = [[((r >> (64 * w)) & (2 ** 64 - 1)) for w in range(words)] for r in rows]
     signed = [[x - 2 ** 64 if x >= 2 ** 63 else x for x in row] for row in signed]
     return torch.tensor(signed, dtype=torch.int64, device=device).reshape(len(parents), words)
+
+
+def tree_depths(parents: Sequence[int], device="cuda") -> torch.Tensor:
+    """How many ancestors each token of a drafted tree has, int32 [tokens]:
+    its position is this much behind the cached tokens.  ``parents`` as for
+    ancestor_masks."""
+    depths = []
+    for i, p in enumerate(parents):
+        _check(-1 <= p < i, "parents: expected -1 or an earlier token")
+        depths.append(depths[p] + 1 if p >= 0 else 0)
+    return torch.tensor(depths, dtype=torch.int32, device=device)

@@ -65,19 +65,33 @@ class VerifyStack:
         self.plan = None
 
     def step(self, x: torch.Tensor, new_len: torch.Tensor, max_new: int,
-             mask: torch.Tensor | None = None) -> torch.Tensor:
+             mask: torch.Tensor | None = None, depth: torch.Tensor | None = None,
+             rotate=None) -> torch.Tensor:
         """Hidden states [rows, hidden] of the new tokens through all blocks;
         new_len int32 [requests] rows each (``max_new`` at most, which is 256
         at most: a longer prompt goes in parts), masked as
         kv.tree_attention's ``mask``.  The tokens stay drafts until commit.
-        Whether they all had a place, only ``check`` says."""
+        Whether they all had a place, only ``check`` says.
+
+        ``rotate(q, k, positions)`` returns every block's queries [rows, heads,
+        dim] and keys [rows, kv_heads, dim] with their position in them (a
+        rotary embedding); positions are int32 [rows].  With a mask,
+        ``depth`` (kv.tree_depths of each request's tree, int32 [rows]) says
+        where the tokens stand; without one they are chains."""
+        rows = x.shape[0]
         if max_new > MAX_NEW:
             raise ValueError(f"max_new: expected {MAX_NEW} at most, longer prompts in parts")
+        if rotate is not None and mask is not None and (depth is None or depth.shape != (rows,)):
+            raise ValueError("depth: expected the depth of every row's token, as mask describes a tree")
         self.plan = kv.kv_plan(self.ctx_len, new_len, self.table, self.free_pages, self.page_size,
-                               x.shape[0], free_head=self.free_head, held=self.held,
+                               rows, free_head=self.free_head, held=self.held,
                                held_out=self.held_next)
+        if rotate is not None:
+            at = self.plan.positions
+            if depth is not None:
+                at = self.ctx_len[self.plan.request.clamp(min=0)] + depth
         for block in self.blocks:
-            x = x + self.block(block, x, max_new, mask)
+            x = x + self.block(block, x, max_new, mask, rotate and (lambda q, k: rotate(q, k, at)))
         # only now, so that after a call that was refused the next step plans
         # with the same pages
         self.held, self.held_next = self.held_next, self.held
@@ -95,11 +109,13 @@ class VerifyStack:
         if what:
             raise RuntimeError("step: " + ", ".join(what))
 
-    def block(self, block: Block, x: torch.Tensor, max_new: int, mask) -> torch.Tensor:
+    def block(self, block: Block, x: torch.Tensor, max_new: int, mask, rotate=None) -> torch.Tensor:
         cache, p = block.cache, self.plan
         qkv = B.forward(block.qkv, x, ws=self.ws_linear)
         q, k, v = (t.unflatten(1, (-1, cache.dim)) for t in qkv.split(
             [block.heads * cache.dim, cache.heads * cache.dim, cache.heads * cache.dim], dim=1))
+        if rotate is not None:
+            q, k = rotate(q, k)
         kv.kv_write(cache, k, v, p.slots)
         a = kv.tree_attention(q, cache, self.table, self.ctx_len, p.row_start, max_new, mask=mask,
                               ws=self.ws_attention)
@@ -129,6 +145,19 @@ def random_stack(layers: int, hidden: int, heads: int, kv_heads: int, dim: int, 
                         for _ in range(layers)], requests, width)
 
 
+def rotary(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, base: float = 1e6):
+    """A rotary embedding as VerifyStack.step's ``rotate`` (for the example; plain torch)."""
+    half = q.shape[-1] // 2
+    rate = base ** (-torch.arange(half, device=q.device) / half)
+    angle = positions[:, None, None] * rate
+    cos, sin = angle.cos(), angle.sin()
+
+    def turn(x):
+        a, b = x.float().chunk(2, dim=-1)
+        return torch.cat([a * cos - b * sin, a * sin + b * cos], -1).to(x.dtype)
+    return turn(q), turn(k)
+
+
 def main():
     requests, hidden, tree = 2, 5120, [-1, 0, 0, 1, 1, 2, 3]
     stack = random_stack(layers=2, hidden=hidden, heads=40, kv_heads=20, dim=128, pages=64,
@@ -142,11 +171,11 @@ def main():
         return torch.tensor(x, dtype=torch.int32, device="cuda")
 
     prompt = [100, 37]                                   # a prompt is a chain whose tokens all stay
-    stack.step(states(sum(prompt)), ints(prompt), max(prompt))
+    stack.step(states(sum(prompt)), ints(prompt), max(prompt), rotate=rotary)
     stack.commit(ints([list(range(max(prompt)))] * requests), ints(prompt))
-    mask = kv.ancestor_masks(tree).repeat(requests, 1)
+    mask, depth = kv.ancestor_masks(tree).repeat(requests, 1), kv.tree_depths(tree).repeat(requests)
     for accepted in ([0, 1, 3, 6], [0, 2]), ([0], [0, 1, 4]):
-        y = stack.step(states(requests * len(tree)), ints([len(tree)] * requests), len(tree), mask)
+        y = stack.step(states(requests * len(tree)), ints([len(tree)] * requests), len(tree), mask, depth, rotary)
         path = torch.zeros((requests, 4), dtype=torch.int32)
         for b, p in enumerate(accepted):
             path[b, :len(p)] = torch.tensor(p)
