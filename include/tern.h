@@ -591,8 +591,9 @@ typedef struct {
  *                              -1), 2 a request longer than its table row,
  *                              4 more rows than capacity, 8 a negative length
  * No output may overlap an input other than the table.
- * Requirements: page_size a power of two, 1 <= page_size <= 65536;
- * 0 <= B <= 8192; capacity, n_free < 2^31; table_width * page_size < 2^31. */
+ * Requirements: slots, positions and request 16-byte aligned; page_size
+ * a power of two, 1 <= page_size <= 65536; 0 <= B <= 8192; capacity, n_free
+ * < 2^31; table_width * page_size < 2^31. */
 tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
                          int64_t page_size, int32_t* table, int64_t table_stride,
                          int64_t table_width, const int32_t* held, const int32_t* free_pages,

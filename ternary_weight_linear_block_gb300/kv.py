@@ -125,7 +125,8 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
     behind its ctx_len[b] cached tokens; the pages that they need beyond
     those it has are taken from ``free_pages`` (from index free_head[0] on)
     and written into ``table`` in place.  ``capacity`` rows are planned;
-    ``plan`` gives the outputs' buffers.  info[2] is the next step's free_head
+    ``plan`` gives the outputs' buffers (slots, positions and request 16-byte
+    aligned).  info[2] is the next step's free_head
     (steps that reuse buffers take turns with two), info[3] says what did not fit.
 
     ``positions`` are places in the cache, ctx_len + the row's index: of a
