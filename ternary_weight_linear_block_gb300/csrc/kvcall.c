@@ -12,7 +12,7 @@
 
 static PyObject *s_is_cuda, *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
 static PyObject *t_int32, *t_int64, *t_float32;   /* torch's types */
-static PyObject* current_device;                   /* torch's, a callable */
+static PyObject* current_device;                   /* torch's, a callable; None: there is one device */
 
 typedef tern_status (*plan_fn)(const int32_t*, const int32_t*, int64_t, int64_t, int32_t*, int64_t,
                                int64_t, const int32_t*, const int32_t*, int64_t, const int32_t*,
@@ -36,7 +36,7 @@ typedef struct {
   void* p;
   int64_t shape[3], stride[3];
   int ndim;
-  long device;   /* -1: an argument that was not given */
+  long device;   /* -1: an argument that was not given, or there is one device */
 } Tensor;
 
 /* A dimension or stride tuple into out; its length, or -1. */
@@ -74,13 +74,16 @@ static int read_tensor(PyObject* o, PyObject* dtype, int ndim, const char* name,
   const int n = numbers(x, t->stride);
   Py_XDECREF(x);
   if (n < 0) return 0;
-  x = PyObject_CallMethodNoArgs(o, s_get_device);
-  if (x == NULL) return 0;
-  t->device = PyLong_AsLong(x);
-  Py_DECREF(x);
-  if (t->device < 0) {
-    if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%s: expected a device number", name);
-    return 0;
+  t->device = -1;
+  if (current_device != Py_None) {
+    x = PyObject_CallMethodNoArgs(o, s_get_device);
+    if (x == NULL) return 0;
+    t->device = PyLong_AsLong(x);
+    Py_DECREF(x);
+    if (t->device < 0) {
+      if (!PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%s: expected a device number", name);
+      return 0;
+    }
   }
   x = PyObject_CallMethodNoArgs(o, s_data_ptr);
   if (x == NULL) return 0;
@@ -154,6 +157,7 @@ static int read_heads(PyObject* o, PyObject* dtype, int64_t heads, int64_t dim, 
 /* Whether all of them are on the current device, the one of the call's stream:
  * a pointer to another's memory could fault in a kernel. */
 static int on_current_device(const Tensor* const* t, int n, long cache) {
+  if (current_device == Py_None) return 1;
   PyObject* x = PyObject_CallNoArgs(current_device);
   if (x == NULL) return 0;
   const long now = PyLong_AsLong(x);
@@ -177,7 +181,7 @@ static int counted(Py_ssize_t got, Py_ssize_t want) {
 
 static int64_t integer(PyObject* o) { return PyLong_AsLongLong(o); }
 
-/* bind(plan, write, attention, commit, int32, int64, float32, current device's callable) */
+/* bind(plan, write, attention, commit, int32, int64, float32, current device's callable or None) */
 static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (!counted(n, 8)) return NULL;
   f_plan = (plan_fn)PyLong_AsVoidPtr(a[0]);

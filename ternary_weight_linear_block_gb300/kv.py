@@ -53,9 +53,17 @@ def _native():
         lib = B.lib()
         names = ("tern_kv_plan", "tern_kv_write", "tern_tree_attention", "tern_kv_commit")
         module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
-                    torch.int32, torch.int64, torch.float32, torch._C._cuda_getDevice)
+                    torch.int32, torch.int64, torch.float32,
+                    torch._C._cuda_getDevice if _several_devices() else None)
         _calls = module
     return _calls
+
+
+@functools.cache
+def _several_devices() -> bool:
+    """Whether a CUDA tensor can be on another device than the current one; where it
+    cannot, asking costs a small call up to a microsecond for nothing."""
+    return torch.cuda.device_count() > 1
 
 
 def _failed(name: str, status: int):
@@ -205,7 +213,8 @@ def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len:
     path has to increase; it is cut where it does not."""
     if isinstance(caches, KVCache):
         caches = (caches,)
-    _check(len({c.index for c in caches}) == 1, "caches: expected one or more, on the same device")
+    _check(len(caches) > 0 and (not _several_devices() or len({c.index for c in caches}) == 1),
+           "caches: expected one or more, on the same device")
     if ctx_out is None:
         if stream is None:
             ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
