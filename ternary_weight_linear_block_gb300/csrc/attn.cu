@@ -18,11 +18,12 @@
 // instruction of a tile, not two of which half is padding, and each
 // ldmatrix of keys or values serves all the rows.
 // Bound: the keys and values, read once (64 requests of up to 16001 keys, 8
-// heads of 128, 4 query heads on each: 2.63 GB in 395 us, 6.65 TB/s, 0.98 of a
-// copy's rate); small calls start, find their piece and join for about 9 us
-// (16 requests of up to 700 keys, 20 heads of 128: 70 MB in 16.4 us, of which
-// 10.3 at copy rate; 4 requests of 3 keys, heads of 64, 7.2 us).  A second kernel that joins
-// the pieces, in place of the last CTA to arrive, took 22.6 us against 19.7.
+// heads of 128, 4 query heads on each: 2.63 GB in 397 us, 6.62 TB/s, 0.99 of a
+// copy's rate); a small call starts, finds its pieces and joins them beside that
+// (16 requests of up to 700 keys, 20 heads of 128: 70 MB in 21.8 us, of which
+// 10.5 at copy rate, and 16.3 where L2 has the keys; 4 requests of 3 keys, heads
+// of 64, 5.4 us).  A second kernel that joins the pieces, in place of the last CTA
+// to arrive, took 22.6 us against 19.7.
 #include <algorithm>
 
 #include "attn_dev.cuh"
@@ -97,7 +98,7 @@ template <int D, int NT>
 struct Rows {
   static constexpr int RT = 8 * NT;
   // an item's cost beside its tiles, which also bounds a piece (LEAST).  8 heads
-  // of 128, 16 rows: 2 requests of 20000 keys 35.7 us with 1, 32.6 with 3, 29.9
+  // of 128, 16 rows: 2 requests of up to 20000 keys 35.7 us with 1, 32.6 with 3, 29.9
   // with 6, but 1 of 1000 keys 14.5 with 3 and 17.8 with 6
   static constexpr int PAD = D == 64 ? 4 : 3;
   static constexpr int LEAST = PAD + 1;                   // places of a CTA's piece at least
@@ -581,7 +582,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 //          runs two tiles ahead.  (An accumulator for each, joined at the end,
 //          measured the same with head size 128 and 64; with 256 columns it
 //          does not fit, and a half of the columns for each, S computed twice,
-//          took 109 us against 82 on 8 requests of 20003 keys.)
+//          took 109 us against 82 on 8 requests of up to 20003 keys.)
 //   ROWS   rows <= 256, head size 128: each has 128 rows with their own S and
 //          accumulator (a stream); a key tile serves both.
 // The maximum that a row's exponents refer to only moves when it grows by
@@ -591,12 +592,12 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 // whole warps of them skip the softmax.
 //
 // Bound: keys and values up to about 64 rows of head size 128 (a context of
-// 131001 keys, 16 drafts, 8 heads of 128, 64 rows on each: 537 MB in 89.5 us,
-// 6.0 TB/s, 0.88 of a copy's rate).  Above that each tile's chain of S, its
+// 131001 keys, 16 drafts, 8 heads of 128, 64 rows on each: 537 MB in 90 us,
+// 6.0 TB/s, 0.89 of a copy's rate).  Above that each tile's chain of S, its
 // softmax and P V, which two streams only partly hide from each other (4
 // requests of 64 drafts over up to 32768 keys, 512 rows on each of 8 heads:
-// 154 us, 940 TFLOP/s, 0.51 of the matrix rate; 8 requests of 29 drafts over up
-// to 20003 keys, 232 rows on each of 2 heads of 256: 77 us, 540 TFLOP/s).  Short
+// 156 us, 930 TFLOP/s, 0.48 of the matrix rate; 8 requests of 29 drafts over up
+// to 20003 keys, 232 rows on each of 2 heads of 256: 79 us, 525 TFLOP/s).  Short
 // items are bound by filling and draining each part (16 requests of 23 drafts
 // over up to 4099 keys, 16 heads of 64: 47 us, 3.9 TB/s).
 // A tile of 128 rows and keys took a stream 3800 cycles when the first of these
@@ -614,7 +615,7 @@ template <int D, int MODE>
 struct Tile {
   static constexpr int TKT = D == 256 ? 64 : 128;        // keys of a tile
   static constexpr int RT = MODE == ROWS ? 256 : 128;
-  // an item's cost beside its tiles: 16 requests of 4099 keys, 16 heads of 64:
+  // an item's cost beside its tiles: 16 requests of up to 4099 keys, 16 heads of 64:
   // 51.2 us with 1, 47.6 with 3, 48.9 with 6
   static constexpr int PAD = D == 64 ? 3 : 2;
   static constexpr int LEAST = PAD + 1;                   // places of a CTA's piece at least
@@ -1369,12 +1370,12 @@ Ws ws_layout(int64_t grid, int64_t rt, int64_t D) {
 
 // Which kernel serves requests of up to `rows` rows on a key head, as its
 // rows an item and its CTAs an SM.  8 key heads, device time:
-//   16 rows, 16 requests of 1000 keys / 1 of 100000: rows kernel 14.8 / 44.4 us
+//   16 rows, 16 requests of up to 1000 keys / 1 of 100000: rows kernel 14.8 / 44.4 us
 //     with head size 64, 20.1 / 74.7 with 128, 31.8 / 136 with 256; tile kernel
 //     18.5 / 44.6, 21.1 / 72.7, 24.0 / 127.  Over 26 sizes from 3 to 20000 keys
 //     the tile kernel takes 1.15 of the rows kernel's time with head size 64,
 //     0.99 with 128, 0.80 with 256 (and 1.16 with 256 and 1, 4 and 8 rows).
-//   256 rows, 16 requests of 6000 keys / 4 of 30000: ROWS 58.9 / 75.2 us with
+//   256 rows, 16 requests of up to 6000 keys / 4 of up to 30000: ROWS 58.9 / 75.2 us with
 //     head size 64, 75.5 / 96.1 with 128; SHARED twice, the second reading the
 //     keys from L2 where it keeps pace, 59.7 / 81.1 and 88.9 / 133.  144 rows:
 //     56.2 / 64.8 and 70.3 / 77.6 against 45.8 / 52.4 and 67.6 / 71.7; over

@@ -19,7 +19,7 @@ namespace {
 // the cached lengths and the pages held in shared memory, so one launch is
 // enough and no CTA waits for another; a row or a page then finds its request
 // by bisection and has one number to read, its page.  Bound: the launch and
-// two dependent round trips to L2 (16 requests, 204 rows: 4.3 us on the
+// two dependent round trips to L2 (16 requests, 204 rows: 4.2 us on the
 // device), then the steps of the bisections before the 16 bytes written for
 // each row (1024 requests, 1.17 million rows: 12.7 us, 1.5 TB/s; written at
 // copy rate the rows would take 2.8).
@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(PLAN_THREADS, 2) plan_kernel(const __grid_cons
 // A copy of 16-byte chunks to slots: `tpt` threads (a power of two) share a
 // row, so that a few rows still use many threads and many rows keep a warp's
 // accesses in one row.  Bound: the rows read and written once (95601 rows of
-// 8 heads of 128: 784 MB in 122 us, 6.4 TB/s, 0.95 of a copy's rate; 16 rows of
-// 20 heads: 1.8 us, the launch).
+// 8 heads of 128: 784 MB in 122 us, 6.4 TB/s, 0.96 of a copy's rate; 16 rows of
+// 20 heads: 1.7 us, the launch).
 
 constexpr int COPY_THREADS = 256;
 
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(COPY_THREADS) write_kernel(const WriteArgs a) 
 // may run ahead of stores and no thread waits for another.  Bound: the
 // moved rows read and written once (61 requests of up to 64 drafts, 16 layers:
 // 452 MB in 73 us, 6.2 TB/s); at decode sizes the launch and three dependent
-// round trips (path, table, rows: 2 requests, 16 layers 5.1 us).
+// round trips (path, table, rows: 2 requests, 16 layers 4.9 us with the write).
 
 constexpr int MAX_PATH = 256;
 constexpr int COMMIT_LAYERS = 64;   // layers of one launch: their pointers are kernel arguments

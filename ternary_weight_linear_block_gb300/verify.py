@@ -2,8 +2,8 @@
 
 ``VerifyStack`` runs one step of speculative decoding over a stack of blocks
 (qkv linear, paged attention, output linear): the step's pages and slots are
-planned on the GPU, every block writes its new keys and values and attends
-over the cache, and once the caller knows the accepted paths, ``commit``
+planned on the GPU, every block writes its new keys and values (turned by the
+caller's rotary embedding, if it gives one) and attends over the cache, and once the caller knows the accepted paths, ``commit``
 makes them contiguous in all blocks at once.  Norms, the MLP and sampling
 belong to the model around it; here a block's output is added to its input.
 
