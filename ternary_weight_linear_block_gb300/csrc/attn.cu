@@ -378,7 +378,7 @@ __global__ void __launch_bounds__((Rows<D, NT>::THREADS), (Rows<D, NT>::CTAS))
 
     for (int t = s.t0; t < s.t1; ++t) {
       const int k0 = t * TK + warp * 16;         // this warp's first key
-      const bool edge = k0 + 16 > s.ctx;     // new tokens, or past the last
+      const bool edge = k0 > s.ctx - 16;     // new tokens, or past the last
       uint32_t vis[NT][2];
       if (edge) {
 #pragma unroll
@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (!ok) return;
         const uint64_t dv = v_desc + sv * (C::SLOT >> 4);
         // steps of 16 keys up to the request's last
-        const int steps = __shfl_sync(~0u, (s.r.len - (s.t0 + i) * TKT + 15) >> 4, 0);
+        const int steps = __shfl_sync(~0u, (min(s.r.len - (s.t0 + i) * TKT, TKT) + 15) >> 4, 0);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < TKT / 16; ++k)
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           s_phase = ((tile0 + i) / NS) & 1u;
         }
         const int k0 = (s.t0 + i) * TKT;
-        const bool edge = k0 + TKT > s.r.ctx;
+        const bool edge = k0 > s.r.ctx - TKT;
         uint64_t vis[TKT / 64];
         if (edge && active) {
 #pragma unroll

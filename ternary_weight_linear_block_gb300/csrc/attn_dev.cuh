@@ -76,7 +76,7 @@ __device__ __forceinline__ Req load_req(const Args& a, int b) {
   r.n = ok ? s1 - s0 : 0;
   r.ctx = min(max(a.ctx_len[b], 0), cap);
   r.len = static_cast<int>(min(int64_t(r.ctx) + r.n, int64_t(cap)));
-  r.tiles = r.n > 0 ? max((r.len + TK - 1) / TK, 1) : 0;
+  r.tiles = r.n > 0 ? max(r.len - 1, 0) / TK + 1 : 0;   // (a position may be the last of 31 bits)
   const uint32_t rt = a.tile_rows;
   r.rts = static_cast<int>((uint32_t(r.n) * uint32_t(a.group) + rt - 1) / rt);   // below 2^28 rows
   return r;
