@@ -138,10 +138,10 @@ def _prepare_sample(case, gen, dev):
     def uniform(lo, hi):
         return lo + (hi - lo) * torch.rand(rows, generator=gen, device=dev)
 
-    # a wide bulk and a few likely tokens a row, as a trained model's logits have
+    # a wide bulk and a few likely tokens a row, as a trained model's logits have; some rows are sure, some open
     logits = torch.randn(rows, vocab, generator=gen, device=dev) * 2
     likely = torch.randint(vocab, (rows, 40), generator=gen, device=dev)
-    logits.scatter_add_(1, likely, 12 * torch.rand(rows, 40, generator=gen, device=dev))
+    logits.scatter_add_(1, likely, uniform(8, 18)[:, None] * torch.rand(rows, 40, generator=gen, device=dev))
     s = dict(case=case, logits=logits.to(TYPES[case["dtype"]]), u=torch.rand(rows, generator=gen, device=dev),
              temperature=uniform(0.6, 1.3), top_k=None, top_p=None, min_p=None)
     if filters in ("top_k", "all", "mixed"):
