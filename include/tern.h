@@ -670,6 +670,92 @@ tern_status tern_tree_attention(const void* q, int64_t q_token_stride, int64_t q
                                 int64_t max_new, float scale, void* out, float* lse, void* ws,
                                 size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit cache, rotated rows
+ *
+ * A key or value of one token and head is D codes and one float, its unit:
+ * it stands for code * unit.  Written, the unit is the largest magnitude
+ * divided by 127 (int8) or 448 (e4m3), and a code is value * (127 or 448 /
+ * the largest magnitude) in float, rounded to the nearest (ties to even).
+ * A row whose largest magnitude is below 2^-100 is stored as zeros with unit
+ * 0, a row with an infinity or NaN as zeros with unit NaN.  An e4m3 code is
+ * never the NaN; calls that read a cache rely on that.
+ * ---------------------------------------------------------------------- */
+
+#define TERN_KV_I8 2
+#define TERN_KV_E4M3 3
+
+/* An 8-bit cache: code [page][row][head][d] of keys or values at page *
+ * page_stride + row * token_stride + head * head_stride + d (strides in
+ * bytes, multiples of 16), its unit at page * scale_page_stride + head *
+ * scale_head_stride + row (strides in floats, multiples of 4).  Sizes as of
+ * tern_kv_cache. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages, page_size, heads, dim;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t scale_page_stride, scale_head_stride;
+  int32_t dtype; /* TERN_KV_I8 or TERN_KV_E4M3 */
+} tern_kv_cache8;
+
+/* The rows of a step as the qkv linear leaves them, and what is done to them
+ * on their way into a cache. */
+typedef struct {
+  const void* q; /* [T][Hq][D], rows and heads as the strides say (elements,
+                    multiples of 8), of `dtype`; NULL with Hq = 0 */
+  const void* k; /* [T][H][D] */
+  const void* v; /* [T][H][D] */
+  void* q_out;   /* [T][Hq][D], dense; q itself where that is dense */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t T, Hq;
+  const int64_t* slots;     /* [T]; a slot outside the cache leaves it as it is */
+  const int32_t* positions; /* [axes][T], rows position_stride apart (rot > 0) */
+  int64_t axes, position_stride;
+  const uint64_t* turns; /* [rot / 2]: turns of pair j a position, in 2^-64 of a turn */
+  const int32_t* axis;   /* [rot / 2]: the axis whose position turns pair j; NULL: axis 0 */
+  int64_t rot;           /* elements of a head that are rotated, a multiple of 16 (0: none) */
+  const void* q_norm;    /* [D] or NULL: no norm */
+  const void* k_norm;
+  int32_t neighbours; /* pairs are (2j, 2j + 1), not (j, j + rot / 2) */
+  int32_t dtype;      /* of the rows: TERN_KV_BF16 or TERN_KV_F16 */
+  int32_t norm_f32;   /* q_norm and k_norm are float, not of `dtype` */
+  float eps;
+} tern_kv_rows;
+
+/* tern_kv_rotate_write -- queries and keys normalised for each head and
+ * rotated by their positions, keys and values into the cache's slots.
+ *
+ *   x' = x / sqrt(mean x^2 + eps) * norm      (with q_norm, k_norm)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)  for pair j of the first `rot`
+ *             elements, of the angle position * turns[j]
+ *
+ * Everything is in 32 bits (angles in 64-bit integers, exact for every
+ * position), rounded once: to `dtype`, or to the 8-bit cache's codes.  Exactly
+ * one of `cache` (of the rows' type) and `cache8` is given.  An entry of
+ * `axis` outside [0, axes) counts as 0.  Two rows of one call must not have
+ * the same slot.
+ * Requirements: 16-byte alignment of rows, q_out and norms; T < 2^31; Hq <= 65535;
+ * axes <= 16. */
+tern_status tern_kv_rotate_write(const tern_kv_cache* cache, const tern_kv_cache8* cache8,
+                                 const tern_kv_rows* rows, void* stream);
+
+/* tern_kv8_read -- the rows in slots[0 .. T - 1] of an 8-bit cache as 16-bit
+ * values, code * unit rounded once: k, v [T][H][D], dense, of `dtype`
+ * (TERN_KV_BF16 or TERN_KV_F16).  A slot outside the cache gives zeros. */
+tern_status tern_kv8_read(const tern_kv_cache8* cache, const int64_t* slots, int64_t T, void* k,
+                          void* v, int32_t dtype, void* stream);
+
+/* tern_kv8_commit -- tern_kv_commit for 8-bit caches: codes and units move. */
+tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const int32_t* table,
+                            int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                            const int32_t* path, int64_t path_width, const int32_t* path_len,
+                            int32_t* ctx_out, int64_t B, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,6 +38,8 @@ TERN_FWHT_F16 = 3
 TERN_FWHT_I8H = 4
 TERN_KV_BF16 = 0
 TERN_KV_F16 = 1
+TERN_KV_I8 = 2
+TERN_KV_E4M3 = 3
 TERN_TREE_ATTENTION_ZERO_BYTES = 8192
 TERN_OP_GEMV = 1
 TERN_OP_GEMM = 2
@@ -89,6 +91,9 @@ _SIGS = {
     "tern_tree_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "tern_tree_attention": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _i64, _i64, _p, _p, _p, _i64,
                                            _i64, _i64, _i64, _i64, _f32, _p, _p, _p, _sz, _p]),
+    "tern_kv_rotate_write": (ctypes.c_int, [_p, _p, _p, _p]),
+    "tern_kv8_read": (ctypes.c_int, [_p, _p, _i64, _p, _p, _i32, _p]),
+    "tern_kv8_commit": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p]),
 }
 
 
@@ -97,6 +102,25 @@ class KVCacheDesc(ctypes.Structure):
     _fields_ = [("k", _p), ("v", _p), ("pages", _i64), ("page_size", _i64), ("heads", _i64),
                 ("dim", _i64), ("page_stride", _i64), ("token_stride", _i64),
                 ("head_stride", _i64), ("dtype", _i32)]
+
+
+class KVCache8Desc(ctypes.Structure):
+    """tern_kv_cache8 of include/tern.h."""
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("pages", _i64),
+                ("page_size", _i64), ("heads", _i64), ("dim", _i64), ("page_stride", _i64),
+                ("token_stride", _i64), ("head_stride", _i64), ("scale_page_stride", _i64),
+                ("scale_head_stride", _i64), ("dtype", _i32)]
+
+
+class KVRows(ctypes.Structure):
+    """tern_kv_rows of include/tern.h."""
+    _fields_ = [("q", _p), ("k", _p), ("v", _p), ("q_out", _p), ("q_token_stride", _i64),
+                ("q_head_stride", _i64), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v_token_stride", _i64), ("v_head_stride", _i64), ("T", _i64), ("Hq", _i64),
+                ("slots", _p), ("positions", _p), ("axes", _i64), ("position_stride", _i64),
+                ("turns", _p), ("axis", _p), ("rot", _i64), ("q_norm", _p), ("k_norm", _p),
+                ("neighbours", _i32), ("dtype", _i32), ("norm_f32", _i32), ("eps", _f32)]
+
 
 _lib = None
 
@@ -330,6 +354,23 @@ def tern_tree_attention(q, q_token_stride, q_head_stride, cache, table, table_st
                  _ptr(table), table_stride, table_width, _ptr(ctx_len), _ptr(row_start),
                  _ptr(mask), mask_words, b, t, hq, max_new, scale, _ptr(out), _ptr(lse), _ptr(ws),
                  ws_bytes, _stream(stream))
+
+
+def tern_kv_rotate_write(cache, cache8, rows, stream=None):
+    """One of ``cache`` (KVCacheDesc) and ``cache8`` (KVCache8Desc) is None; ``rows`` a KVRows."""
+    return _call("tern_kv_rotate_write", _desc(cache), _desc(cache8), _desc(rows), _stream(stream))
+
+
+def tern_kv8_read(cache, slots, t, k, v, dtype, stream=None):
+    return _call("tern_kv8_read", _desc(cache), _ptr(slots), t, _ptr(k), _ptr(v), dtype,
+                 _stream(stream))
+
+
+def tern_kv8_commit(caches, layers, table, table_stride, table_width, ctx_len, path, path_width,
+                    path_len, ctx_out, b, stream=None):
+    return _call("tern_kv8_commit", _desc(caches), layers, _ptr(table), table_stride, table_width,
+                 _ptr(ctx_len), _ptr(path), path_width, _ptr(path_len), _ptr(ctx_out), b,
+                 _stream(stream))
 
 
 # ---------------------------------------------------------------- conveniences

@@ -24,6 +24,15 @@ cudaError_t launch_kv_commit(const tern_kv_cache* caches, int64_t layers, const 
                              const int32_t* path, int64_t path_width, const int32_t* path_len,
                              int32_t* ctx_out, int64_t B, cudaStream_t st);
 
+cudaError_t launch_kv_rotate_write(const tern_kv_cache* c, const tern_kv_cache8* c8,
+                                   const tern_kv_rows& r, cudaStream_t st);
+cudaError_t launch_kv8_read(const tern_kv_cache8& c, const int64_t* slots, int64_t T, void* k, void* v,
+                            int dtype, cudaStream_t st);
+cudaError_t launch_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const int32_t* table,
+                              int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                              const int32_t* path, int64_t path_width, const int32_t* path_len,
+                              int32_t* ctx_out, int64_t B, cudaStream_t st);
+
 // One tree-attention call.
 struct TreeAttnCall {
   const void* q;

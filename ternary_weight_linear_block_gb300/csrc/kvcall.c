@@ -27,10 +27,20 @@ typedef tern_status (*attn_fn)(const void*, int64_t, int64_t, const tern_kv_cach
 typedef tern_status (*commit_fn)(const tern_kv_cache*, int64_t, const int32_t*, int64_t, int64_t,
                                  const int32_t*, const int32_t*, int64_t, const int32_t*, int32_t*,
                                  int64_t, void*);
+typedef tern_status (*rotate_fn)(const tern_kv_cache*, const tern_kv_cache8*, const tern_kv_rows*,
+                                 void*);
+typedef tern_status (*read_fn)(const tern_kv_cache8*, const int64_t*, int64_t, void*, void*, int32_t,
+                               void*);
+typedef tern_status (*commit8_fn)(const tern_kv_cache8*, int64_t, const int32_t*, int64_t, int64_t,
+                                  const int32_t*, const int32_t*, int64_t, const int32_t*, int32_t*,
+                                  int64_t, void*);
 static plan_fn f_plan;
 static write_fn f_write;
 static attn_fn f_attn;
 static commit_fn f_commit;
+static rotate_fn f_rotate;
+static read_fn f_read;
+static commit8_fn f_commit8;
 
 typedef struct {
   void* p;
@@ -305,8 +315,9 @@ static PyObject* py_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) 
                        lse.p, ws, ws_bytes, stream));
 }
 
-/* commit(descriptions as bytes, layers, the caches' device, table, ctx_len, path, path_len, ctx_out, stream) */
-static PyObject* py_commit(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+/* commit(descriptions as bytes, layers, the caches' device, table, ctx_len, path, path_len, ctx_out, stream)
+ * commit8: the same of 8-bit caches */
+static PyObject* commit(PyObject* const* a, Py_ssize_t n, int eight) {
   Tensor table, ctx, path, len, out;
   int64_t stride;
   if (!counted(n, 9)) return NULL;
@@ -315,7 +326,8 @@ static PyObject* py_commit(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   void* stream = PyLong_AsVoidPtr(a[8]);
   if (PyErr_Occurred()) return NULL;
   if (!PyBytes_Check(a[0]) ||
-      PyBytes_GET_SIZE(a[0]) != layers * (Py_ssize_t)sizeof(tern_kv_cache))
+      PyBytes_GET_SIZE(a[0]) !=
+          layers * (Py_ssize_t)(eight ? sizeof(tern_kv_cache8) : sizeof(tern_kv_cache)))
     return refuse("caches: expected a description each"), NULL;
   if (!read_dense(a[4], t_int32, 1, "ctx_len", &ctx) ||
       !read_table(a[3], ctx.shape[0], &table, &stride) ||
@@ -327,9 +339,130 @@ static PyObject* py_commit(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (path.shape[0] != b || len.shape[0] != b || out.shape[0] != b)
     return refuse("path, path_len, ctx_out: expected a row each request"), NULL;
   if (!ON_CURRENT_DEVICE(device, &table, &ctx, &path, &len, &out)) return NULL;
+  if (eight)
+    RETURN_STATUS(f_commit8((const tern_kv_cache8*)PyBytes_AS_STRING(a[0]), layers, table.p, stride,
+                            table.shape[1], ctx.p, path.p, path.shape[1], len.p, out.p, b, stream));
   RETURN_STATUS(f_commit((const tern_kv_cache*)PyBytes_AS_STRING(a[0]), layers, table.p,
                          stride, table.shape[1], ctx.p, path.p, path.shape[1], len.p,
                          out.p, b, stream));
+}
+
+static PyObject* py_commit(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  return commit(a, n, 0);
+}
+static PyObject* py_commit8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  return commit(a, n, 1);
+}
+
+/* An argument that may be None: none of it, or a dense tensor. */
+static int read_if(PyObject* o, PyObject* dtype, const char* name, Tensor* t) {
+  t->p = NULL;
+  t->device = -1;
+  t->shape[0] = -1;
+  return o == Py_None || read_dense(o, dtype, 1, name, t);
+}
+
+/* rotate(16-bit cache's address or 0, 8-bit cache's or 0, rows' dtype, its number, heads, dim, the
+ *        cache's device, q or None, k, v, slots, positions or None, whether they have axes, turns or
+ *        None, axis or None, neighbours, q_norm or None, k_norm or None, the norms' dtype, eps, out
+ *        or None, stream) */
+static PyObject* py_rotate(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor q, k, v, slots, pos, turns, axis, qn, kn, out;
+  if (!counted(n, 22)) return NULL;
+  const tern_kv_cache* cache = PyLong_AsVoidPtr(a[0]);
+  const tern_kv_cache8* cache8 = PyLong_AsVoidPtr(a[1]);
+  const int64_t heads = integer(a[4]), dim = integer(a[5]);
+  const long device = PyLong_AsLong(a[6]);
+  tern_kv_rows r = {0};
+  r.dtype = (int32_t)integer(a[3]);
+  const int axes = PyObject_IsTrue(a[12]);
+  r.neighbours = PyObject_IsTrue(a[15]);
+  r.norm_f32 = a[18] == t_float32;
+  r.eps = (float)PyFloat_AsDouble(a[19]);
+  void* stream = PyLong_AsVoidPtr(a[21]);
+  if (PyErr_Occurred()) return NULL;
+  if (!read_heads(a[8], a[2], heads, dim, "k", &k, &r.k_token_stride, &r.k_head_stride) ||
+      !read_heads(a[9], a[2], heads, dim, "v", &v, &r.v_token_stride, &r.v_head_stride) ||
+      !read_dense(a[10], t_int64, 1, "slots", &slots))
+    return NULL;
+  r.T = k.shape[0];
+  if (v.shape[0] != r.T || slots.shape[0] < r.T)
+    return refuse("v, slots: expected as many rows as k"), NULL;
+  q.p = out.p = pos.p = NULL;
+  q.device = out.device = pos.device = -1;
+  if (a[7] != Py_None) {
+    if (!read_heads(a[7], a[2], -1, dim, "q", &q, &r.q_token_stride, &r.q_head_stride) ||
+        !read_dense(a[20], a[2], 3, "out", &out))
+      return NULL;
+    r.Hq = q.shape[1];
+    if (q.shape[0] != r.T) return refuse("q: expected as many rows as k"), NULL;
+    if (out.shape[0] != r.T || out.shape[1] != r.Hq || out.shape[2] != dim)
+      return refuse("out: expected [rows, query heads, dim]"), NULL;
+  }
+  if (!read_if(a[13], t_int64, "turns", &turns) || !read_if(a[14], t_int32, "axis", &axis) ||
+      !read_if(a[16], a[18], "q_norm", &qn) || !read_if(a[17], a[18], "k_norm", &kn))
+    return NULL;
+  if ((qn.p != NULL && qn.shape[0] != dim) || (kn.p != NULL && kn.shape[0] != dim))
+    return refuse("q_norm, k_norm: expected a weight each element of a head"), NULL;
+  if (turns.p != NULL) {
+    r.rot = 2 * turns.shape[0];
+    if (axis.p != NULL && axis.shape[0] != turns.shape[0])
+      return refuse("axis: expected one each pair"), NULL;
+    r.axes = 1;
+    if (axes) {
+      if (!read_tensor(a[11], t_int32, 2, "positions", &pos)) return NULL;
+      r.axes = pos.shape[0];
+      if (pos.shape[1] != r.T || (r.T > 1 && pos.stride[1] != 1))
+        return refuse("positions: expected [axes, rows], dense along the rows"), NULL;
+      r.position_stride = r.axes > 1 ? pos.stride[0] : r.T;
+    } else {
+      if (!read_dense(a[11], t_int32, 1, "positions", &pos)) return NULL;
+      if (pos.shape[0] < r.T) return refuse("positions: expected one each row"), NULL;
+    }
+  }
+  if (!ON_CURRENT_DEVICE(device, &q, &k, &v, &slots, &pos, &turns, &axis, &qn, &kn, &out)) return NULL;
+  r.q = q.p;
+  r.k = k.p;
+  r.v = v.p;
+  r.q_out = out.p;
+  r.slots = slots.p;
+  r.positions = pos.p;
+  r.turns = turns.p;
+  r.axis = axis.p;
+  r.q_norm = qn.p;
+  r.k_norm = kn.p;
+  RETURN_STATUS(f_rotate(cache, cache8, &r, stream));
+}
+
+/* read(cache address, heads, dim, its device, slots, dtype, its number, k, v, stream) */
+static PyObject* py_read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor slots, k, v;
+  if (!counted(n, 10)) return NULL;
+  const tern_kv_cache8* cache = PyLong_AsVoidPtr(a[0]);
+  const int64_t heads = integer(a[1]), dim = integer(a[2]);
+  const long device = PyLong_AsLong(a[3]);
+  const int32_t type = (int32_t)integer(a[6]);
+  void* stream = PyLong_AsVoidPtr(a[9]);
+  if (PyErr_Occurred()) return NULL;
+  if (!read_dense(a[4], t_int64, 1, "slots", &slots) || !read_dense(a[7], a[5], 3, "k", &k) ||
+      !read_dense(a[8], a[5], 3, "v", &v))
+    return NULL;
+  const int64_t t = k.shape[0];
+  if (k.shape[1] != heads || k.shape[2] != dim || v.shape[0] != t || v.shape[1] != heads ||
+      v.shape[2] != dim || slots.shape[0] < t)
+    return refuse("k, v: expected [rows, heads, dim], a slot each row"), NULL;
+  if (!ON_CURRENT_DEVICE(device, &slots, &k, &v)) return NULL;
+  RETURN_STATUS(f_read(cache, slots.p, t, k.p, v.p, type, stream));
+}
+
+/* bind8(rotate_write, read, commit8), after bind */
+static PyObject* py_bind8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (!counted(n, 3)) return NULL;
+  f_rotate = (rotate_fn)PyLong_AsVoidPtr(a[0]);
+  f_read = (read_fn)PyLong_AsVoidPtr(a[1]);
+  f_commit8 = (commit8_fn)PyLong_AsVoidPtr(a[2]);
+  if (PyErr_Occurred()) return NULL;
+  Py_RETURN_NONE;
 }
 
 static PyMethodDef methods[] = {
@@ -338,6 +471,10 @@ static PyMethodDef methods[] = {
     {"write", (PyCFunction)(void (*)(void))py_write, METH_FASTCALL, NULL},
     {"attention", (PyCFunction)(void (*)(void))py_attention, METH_FASTCALL, NULL},
     {"commit", (PyCFunction)(void (*)(void))py_commit, METH_FASTCALL, NULL},
+    {"bind8", (PyCFunction)(void (*)(void))py_bind8, METH_FASTCALL, NULL},
+    {"rotate", (PyCFunction)(void (*)(void))py_rotate, METH_FASTCALL, NULL},
+    {"read", (PyCFunction)(void (*)(void))py_read, METH_FASTCALL, NULL},
+    {"commit8", (PyCFunction)(void (*)(void))py_commit8, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvcall", NULL, -1, methods};
 

@@ -83,6 +83,28 @@ tern_status cache_ok(const tern_kv_cache* c) {
   return TERN_OK;
 }
 
+// A stride in bytes of 8-bit codes, and one in floats of their units.
+bool stride8_ok(int64_t s) { return s > 0 && s % 16 == 0 && s < (int64_t(1) << 39); }
+bool unit_stride_ok(int64_t s) { return s > 0 && s % 4 == 0 && s < (int64_t(1) << 39); }
+
+tern_status cache8_ok(const tern_kv_cache8* c) {
+  if (c == nullptr) return TERN_ERR_INVALID_ARG;
+  if (c->dtype != TERN_KV_I8 && c->dtype != TERN_KV_E4M3) return TERN_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->pages >= (int64_t(1) << 31) || c->heads < 1 || c->heads > 65535)
+    return TERN_ERR_SHAPE;
+  if (!pow2(c->page_size) || c->page_size < 8 || c->page_size > 256) return TERN_ERR_SHAPE;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return TERN_ERR_SHAPE;
+  if (c->k == nullptr || c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr)
+    return TERN_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
+      !stride8_ok(c->page_stride) || !stride8_ok(c->token_stride) || !stride8_ok(c->head_stride) ||
+      !unit_stride_ok(c->scale_page_stride) || !unit_stride_ok(c->scale_head_stride))
+    return TERN_ERR_ALIGN;
+  return TERN_OK;
+}
+
+bool kv16(int32_t dtype) { return dtype == TERN_KV_BF16 || dtype == TERN_KV_F16; }
+
 bool table_ok(int64_t stride, int64_t width, int64_t page_size) {
   return width >= 0 && stride >= width && width < (int64_t(1) << 31) / page_size;
 }
@@ -557,6 +579,75 @@ tern_status tern_tree_attention(const void* q, int64_t q_token_stride, int64_t q
                           table_width, ctx_len, row_start, mask, mask_words, B, T, Hq, max_new,
                           scale, out, lse, ws};
   return from_cuda(launch_tree_attention(call, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_kv_rotate_write(const tern_kv_cache* cache, const tern_kv_cache8* cache8,
+                                 const tern_kv_rows* rows, void* stream) {
+  if (rows == nullptr || (cache == nullptr) == (cache8 == nullptr)) return TERN_ERR_INVALID_ARG;
+  const tern_status ok = cache != nullptr ? cache_ok(cache) : cache8_ok(cache8);
+  if (ok != TERN_OK) return ok;
+  const tern_kv_rows& r = *rows;
+  const int64_t dim = cache != nullptr ? cache->dim : cache8->dim;
+  if (!kv16(r.dtype) || (cache != nullptr && cache->dtype != r.dtype) || r.T < 0 || r.Hq < 0 ||
+      r.rot < 0 || !(r.eps >= 0.0f))
+    return TERN_ERR_INVALID_ARG;
+  if (r.T >= (int64_t(1) << 31) || r.Hq > 65535 || r.rot > dim || r.rot % 16 != 0) return TERN_ERR_SHAPE;
+  if (r.rot > 0 && (r.axes < 1 || r.axes > 16 || (r.axes > 1 && r.position_stride < r.T)))
+    return TERN_ERR_SHAPE;
+  if (r.T == 0) return TERN_OK;
+  if (r.k == nullptr || r.v == nullptr || r.slots == nullptr ||
+      (r.Hq > 0 && (r.q == nullptr || r.q_out == nullptr)) ||
+      (r.rot > 0 && (r.positions == nullptr || r.turns == nullptr)))
+    return TERN_ERR_INVALID_ARG;
+  if (!aligned16(r.k) || !aligned16(r.v) || !stride_ok(r.k_token_stride) || !stride_ok(r.k_head_stride) ||
+      !stride_ok(r.v_token_stride) || !stride_ok(r.v_head_stride) || !aligned16(r.q_norm) ||
+      !aligned16(r.k_norm) ||
+      (r.Hq > 0 && (!aligned16(r.q) || !aligned16(r.q_out) || !stride_ok(r.q_token_stride) ||
+                    !stride_ok(r.q_head_stride))))
+    return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_kv_rotate_write(cache, cache8, r, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_kv8_read(const tern_kv_cache8* cache, const int64_t* slots, int64_t T, void* k,
+                          void* v, int32_t dtype, void* stream) {
+  const tern_status ok = cache8_ok(cache);
+  if (ok != TERN_OK) return ok;
+  if (T < 0 || !kv16(dtype)) return TERN_ERR_INVALID_ARG;
+  if (T >= (int64_t(1) << 31)) return TERN_ERR_SHAPE;
+  if (T == 0) return TERN_OK;
+  if (slots == nullptr || k == nullptr || v == nullptr) return TERN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_kv8_read(*cache, slots, T, k, v, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const int32_t* table,
+                            int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                            const int32_t* path, int64_t path_width, const int32_t* path_len,
+                            int32_t* ctx_out, int64_t B, void* stream) {
+  if (B < 0 || layers < 1 || path_width < 0 || caches == nullptr) return TERN_ERR_INVALID_ARG;
+  for (int64_t l = 0; l < layers; ++l) {
+    const tern_status ok = cache8_ok(caches + l);
+    if (ok != TERN_OK) return ok;
+    const tern_kv_cache8 &c = caches[l], &c0 = caches[0];
+    if (c.pages != c0.pages || c.page_size != c0.page_size || c.heads != c0.heads ||
+        c.dim != c0.dim || c.page_stride != c0.page_stride ||
+        c.token_stride != c0.token_stride || c.head_stride != c0.head_stride ||
+        c.scale_page_stride != c0.scale_page_stride || c.scale_head_stride != c0.scale_head_stride)
+      return TERN_ERR_SHAPE;
+  }
+  if (B > 65535 || layers > 65535 || path_width > 256 ||
+      !table_ok(table_stride, table_width, caches->page_size))
+    return TERN_ERR_SHAPE;
+  if (B == 0) return TERN_OK;
+  if (ctx_len == nullptr || path_len == nullptr || ctx_out == nullptr || ctx_out == ctx_len ||
+      (path_width > 0 && path == nullptr) || (table_width > 0 && table == nullptr))
+    return TERN_ERR_INVALID_ARG;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_kv8_commit(caches, layers, table, table_stride, table_width, ctx_len, path,
+                                     path_width, path_len, ctx_out, B,
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -9,17 +9,25 @@ output linear, over the C entry points of the same names:
   request's new tokens, those that its mask names;
 * ``kv_commit``: the accepted path of each tree made contiguous, all layers.
 
+The cache holds 16-bit values (``KVCache``) or 8-bit codes with a unit for
+each row (``KVCache8``, ``kv_read``).  ``rotate_write`` writes rows as
+``kv_write`` does, with the norms of queries and keys and their rotary
+positions in the same pass.
+
 Lengths, tables, masks and paths are device tensors that only the kernels
 read, so a step can be captured in a CUDA graph and replayed as they change.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import importlib.machinery
 import importlib.util
+import math
 import os
+from fractions import Fraction
 from typing import NamedTuple, Sequence
 
 import torch
@@ -27,6 +35,7 @@ import torch
 from . import binding as B
 
 _TYPES = {torch.bfloat16: B.TERN_KV_BF16, torch.float16: B.TERN_KV_F16}
+_CODES = {torch.int8: B.TERN_KV_I8, torch.float8_e4m3fn: B.TERN_KV_E4M3}
 
 
 def _check(ok: bool, what: str):
@@ -52,9 +61,12 @@ def _native():
         loader.exec_module(module)
         lib = B.lib()
         names = ("tern_kv_plan", "tern_kv_write", "tern_tree_attention", "tern_kv_commit")
-        module.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names),
-                    torch.int32, torch.int64, torch.float32,
+
+        def at(*names):
+            return [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names]
+        module.bind(*at(*names), torch.int32, torch.int64, torch.float32,
                     torch._C._cuda_getDevice if _several_devices() else None)
+        module.bind8(*at("tern_kv_rotate_write", "tern_kv8_read", "tern_kv8_commit"))
         _calls = module
     return _calls
 
@@ -109,6 +121,94 @@ class KVCache:
         return cls(k, v)
 
 
+class KVCache8:
+    """Keys and values of one layer in 8 bits: ``k`` and ``v`` [pages,
+    page_size, heads, dim] of int8 or float8_e4m3fn as for KVCache, and a
+    unit for each token and head, ``k_scale`` and ``v_scale`` float32 [pages,
+    heads, page_size] with the same strides (dense along the last axis).  A
+    value is its code times its row's unit; written, a row's unit is its
+    largest magnitude divided by 127 or 448.
+
+    int8 keeps all of a row's values to 1/254 of the largest, e4m3 each to
+    1/16 of itself: the first is more exact by a factor of about four unless a
+    few channels are much larger than the others."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        _check(k.is_cuda and k.ndim == 4 and k.dtype in _CODES,
+               "k: expected a 4-D CUDA tensor of int8 or float8_e4m3fn")
+        _check(v.is_cuda and v.device == k.device and v.dtype == k.dtype and v.shape == k.shape and
+               v.stride() == k.stride(), "v: expected the device, type, shape and strides of k")
+        _check(k.stride(3) == 1, "k, v: expected to be dense along the last axis")
+        self.pages, self.page_size, self.heads, self.dim = k.shape
+        for t in (k_scale, v_scale):
+            _check(t.is_cuda and t.device == k.device and t.dtype == torch.float32 and
+                   t.shape == (self.pages, self.heads, self.page_size) and
+                   t.stride() == k_scale.stride() and t.stride(2) == 1,
+                   "k_scale, v_scale: expected float32 [pages, heads, page_size] on k's device, "
+                   "dense along the last axis")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.dtype, self.device, self.index = k.dtype, k.device, k.get_device()
+        # an axis of length one may have any stride: give it one that passes
+        ps, ts, hs = (k.stride(i) if k.shape[i] > 1 else self.page_size * self.heads * self.dim
+                      for i in range(3))
+        sp, sh = (k_scale.stride(i) if k_scale.shape[i] > 1 else self.page_size * self.heads
+                  for i in range(2))
+        self.desc = B.KVCache8Desc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                   self.pages, self.page_size, self.heads, self.dim, ps, ts, hs, sp, sh,
+                                   _CODES[k.dtype])
+        self.desc_bytes = bytes(self.desc)
+        self.address = ctypes.addressof(self.desc)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, dim: int, dtype=torch.int8, device="cuda",
+              heads_first: bool = False) -> "KVCache8":
+        """A cache of uninitialised pages, rows of heads or (``heads_first``) heads of rows."""
+        if heads_first:
+            k, v = (torch.empty((pages, heads, page_size, dim), dtype=dtype, device=device)
+                    .transpose(1, 2) for _ in range(2))
+        else:
+            k, v = (torch.empty((pages, page_size, heads, dim), dtype=dtype, device=device)
+                    for _ in range(2))
+        units = (torch.empty((pages, heads, page_size), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, *units)
+
+
+# 1 / (2 pi), to 2^-120
+_TURNS = Fraction(10 ** 40, 62831853071795864769252867665590057683943)
+
+
+class Rotary:
+    """Rotary positions: pair j of a head's first 2 * len(freq) elements (a
+    multiple of 16; the others stay) is turned by position * freq[j] radians.
+    ``axis`` [pairs] says which of several positions of a token turns each
+    pair, e.g. time, height and width of an image's tokens.  Pairs are (j, j +
+    pairs), or with ``neighbours`` (2 j, 2 j + 1).  ``freq``, numbers or a tensor
+    of them, is read once; it holds any scaling of long contexts."""
+
+    def __init__(self, freq, axis=None, neighbours: bool = False, device="cuda"):
+        if isinstance(freq, torch.Tensor):
+            device = freq.device if freq.is_cuda else device
+            freq = freq.tolist()
+        if isinstance(axis, torch.Tensor):
+            axis = axis.tolist()
+        _check(len(freq) > 0 and len(freq) % 8 == 0 and all(math.isfinite(f) for f in freq),
+               "freq: expected a multiple of 8 finite numbers")
+        _check(axis is None or (len(axis) == len(freq) and min(axis) >= 0),
+               "axis: expected a number each of freq")
+        # turns a position as a 64-bit fraction: of an angle only what is past whole turns counts
+        turn = [int(Fraction(f) * _TURNS * 2 ** 64) % 2 ** 64 for f in freq]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turn], dtype=torch.int64,
+                                  device=device)
+        self.axes = 1 if axis is None else max(axis) + 1
+        self.axis = None if axis is None else torch.tensor(axis, dtype=torch.int32, device=device)
+        self.rot, self.neighbours = 2 * len(freq), bool(neighbours)
+
+    @classmethod
+    def geometric(cls, rot: int, base: float = 1e6, **kw) -> "Rotary":
+        """The usual frequencies of ``rot`` elements, base^(-2 j / rot)."""
+        return cls([base ** (-2 * j / rot) for j in range(rot // 2)], **kw)
+
+
 class KVPlan(NamedTuple):
     row_start: torch.Tensor   # int32 [requests + 1]: first row of each request
     slots: torch.Tensor       # int64 [capacity]: where each row's keys and values go, -1: nowhere
@@ -158,12 +258,74 @@ def kv_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor,
     return plan
 
 
-def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
-    """Rows of keys and values [T, heads, dim] into the cache's slots (-1: skipped)."""
+def kv_write(cache: KVCache | KVCache8, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None):
+    """Rows of keys and values [T, heads, dim] into the cache's slots (-1: skipped);
+    bf16 or fp16 rows are quantised on their way into an 8-bit cache."""
+    if isinstance(cache, KVCache8):
+        rotate_write(cache, None, k, v, slots, stream=stream)
+        return
     st = (_calls or _native()).write(cache.address, cache.dtype, cache.heads, cache.dim,
                                      cache.index, k, v, slots, B._stream(stream))
     if st:
         _failed("tern_kv_write", st)
+
+
+def rotate_write(cache: KVCache | KVCache8, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                 slots: torch.Tensor, rotary: Rotary | None = None, positions: torch.Tensor | None = None,
+                 q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, eps: float = 1e-6,
+                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """kv_write with what comes before it, in one pass: queries [T, query
+    heads, dim] and keys divided by their root mean square of each head and
+    multiplied by ``q_norm`` and ``k_norm`` [dim] (of the rows' type or both
+    float32; None: no norm), then turned by ``rotary`` at ``positions``, int32
+    [T], or [axes, T] where it has several axes.  Returns the queries (``out``,
+    which may be q itself where that is contiguous).  All of it is in 32 bits
+    and rounded once."""
+    dtype, eight = k.dtype, isinstance(cache, KVCache8)
+    _check(dtype in _TYPES, "k: expected bf16 or fp16")
+    _check(eight or dtype == cache.dtype, "k: expected the cache's type")
+    if q is not None and out is None:
+        with contextlib.nullcontext() if stream is None else B._on(stream):
+            out = torch.empty(q.shape, dtype=dtype, device=cache.device)
+    several, turns, axis, neighbours = False, None, None, False
+    if rotary is not None:
+        _check(positions is not None, "positions: expected with rotary")
+        several = positions.ndim == 2
+        turns, axis, neighbours = rotary.turns, rotary.axis, rotary.neighbours
+        _check(rotary.axes == 1 or (several and positions.shape[0] >= rotary.axes),
+               "positions: expected [axes, rows], as rotary has several axes")
+        _check(rotary.rot <= cache.dim, "rotary: expected no more elements than a head has")
+    norm = q_norm if q_norm is not None else k_norm
+    norm = dtype if norm is None else norm.dtype
+    _check(norm in (dtype, torch.float32), "q_norm, k_norm: expected the rows' type or float32")
+    st = (_calls or _native()).rotate(
+        0 if eight else cache.address, cache.address if eight else 0, dtype, _TYPES[dtype], cache.heads,
+        cache.dim, cache.index, q, k, v, slots, positions, several, turns, axis, neighbours, q_norm,
+        k_norm, norm, eps, out, B._stream(stream))
+    if st:
+        _failed("tern_kv_rotate_write", st)
+    return out
+
+
+def kv_read(cache: KVCache8, slots: torch.Tensor, dtype=torch.bfloat16, k: torch.Tensor | None = None,
+            v: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The rows in ``slots`` of an 8-bit cache as 16-bit values: keys and
+    values [T, heads, dim] (zeros for a slot outside the cache)."""
+    _check(isinstance(cache, KVCache8), "cache: expected an 8-bit one")
+    given = k if k is not None else v
+    if given is not None:
+        dtype = given.dtype
+    _check(dtype in _TYPES, "dtype: expected bf16 or fp16")
+    if k is None or v is None:
+        shape = (slots.shape[0] if given is None else given.shape[0], cache.heads, cache.dim)
+        with contextlib.nullcontext() if stream is None else B._on(stream):
+            k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
+            v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+    st = (_calls or _native()).read(cache.address, cache.heads, cache.dim, cache.index, slots, dtype,
+                                    _TYPES[dtype], k, v, B._stream(stream))
+    if st:
+        _failed("tern_kv8_read", st)
+    return k, v
 
 
 def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len: torch.Tensor,
@@ -204,28 +366,31 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
     return (out, lse) if return_lse else out
 
 
-def kv_commit(caches: KVCache | Sequence[KVCache], table: torch.Tensor, ctx_len: torch.Tensor,
+def kv_commit(caches: KVCache | KVCache8 | Sequence[KVCache | KVCache8], table: torch.Tensor, ctx_len: torch.Tensor,
               path: torch.Tensor, path_len: torch.Tensor, ctx_out: torch.Tensor | None = None,
               stream=None) -> torch.Tensor:
     """Keep the accepted path of every request: the token path[b][j] of its
     new ones moves to place j behind its ctx_len[b] cached tokens, for
     j < path_len[b] and in every layer's cache.  Returns the new lengths.  A
     path has to increase; it is cut where it does not."""
-    if isinstance(caches, KVCache):
+    if isinstance(caches, (KVCache, KVCache8)):
         caches = (caches,)
     _check(len(caches) > 0 and (not _several_devices() or len({c.index for c in caches}) == 1),
            "caches: expected one or more, on the same device")
+    eight = isinstance(caches[0], KVCache8)
+    _check(all(isinstance(c, KVCache8) == eight for c in caches), "caches: expected all of 16 bits or all of 8")
     if ctx_out is None:
         if stream is None:
             ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
         else:
             with B._on(stream):
                 ctx_out = torch.empty(ctx_len.shape[0], dtype=torch.int32, device=ctx_len.device)
-    st = (_calls or _native()).commit(b"".join([c.desc_bytes for c in caches]), len(caches),
-                                      caches[0].index, table, ctx_len, path, path_len, ctx_out,
-                                      B._stream(stream))
+    calls = _calls or _native()
+    st = (calls.commit8 if eight else calls.commit)(
+        b"".join([c.desc_bytes for c in caches]), len(caches), caches[0].index, table, ctx_len, path,
+        path_len, ctx_out, B._stream(stream))
     if st:
-        _failed("tern_kv_commit", st)
+        _failed("tern_kv8_commit" if eight else "tern_kv_commit", st)
     return ctx_out
 
 
