@@ -756,6 +756,61 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
                             const int32_t* path, int64_t path_width, const int32_t* path_len,
                             int32_t* ctx_out, int64_t B, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Tokens from logits, and the drafts that agree with them
+ * ---------------------------------------------------------------------- */
+
+#define TERN_LOGITS_BF16 0
+#define TERN_LOGITS_F16 1
+#define TERN_LOGITS_F32 2
+
+/* tern_sample -- one token of each row of logits.
+ *   logits       [rows][vocab], rows row_stride elements apart, of `dtype`
+ *   u            float [rows], in [0, 1): the random numbers
+ *   temperature  float [rows] or NULL (1); 0 or less: the largest logit
+ *   top_k        int32 [rows] or NULL; 0 or less: all
+ *   top_p        float [rows] or NULL; 1 or more: all
+ *   min_p        float [rows] or NULL; 0 or less: all
+ *   token        int32 [rows]
+ * Token i weighs w_i = exp((x_i - max x) / temperature).  In the order of
+ * their logits, of equal ones the lower index first, are kept: the first
+ * top_k tokens, of those the ones with w_i >= min_p, and of those every token
+ * before which the sum of weights is less than top_p of the sum of all (the
+ * first token always).  The token is the first, by index, up to which the
+ * kept weights add to more than u times their sum.
+ * Weights are within 2^-28 of exp, relatively, or 2^-44 of the largest; sums
+ * are exact (64-bit integers), so a result does not depend on the order of
+ * additions.  A min_p above 1 counts as 1, a u outside [0, 1) as the nearest
+ * number inside (NaN: 0), a NaN temperature as 0, a NaN top_p as 1.  A NaN
+ * logit counts as -infinity; where +infinity is the largest, such logits
+ * weigh 1 and others 0; a row of nothing but -infinity gives -1.
+ * Requirements: 1 <= vocab <= 2^18; 0 <= rows < 2^20; row_stride >= vocab;
+ * the logits aligned to their type. */
+tern_status tern_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab,
+                        int32_t dtype, const float* u, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* token, void* stream);
+
+/* tern_tree_accept -- the path of every tree of drafts that the sampled
+ * tokens agree with.
+ *   tokens     int32 [T]: the rows' tokens; row 0 of a request is its last
+ *              known token, the others are drafts
+ *   target     int32 [T]: the token that was sampled behind each row
+ *   parent     int32 [T]: each row's parent among its request's rows, lower
+ *              than its own index (row 0's is not looked at); a row whose
+ *              parent is not is on no path
+ *   row_start  int32 [B + 1]
+ *   path       int32 [B][path_width]: from row 0 on, the lowest row whose
+ *              parent is the one before and whose token is that one's target;
+ *              -1 behind the last
+ *   path_len   int32 [B];  next int32 [B]: the target of the path's last row,
+ *              the request's next token (a request without rows: 0 and -1)
+ * Only a request's first path_width rows are looked at.
+ * Requirements: 0 <= B <= 65536; 1 <= path_width <= 256; T < 2^31. */
+tern_status tern_tree_accept(const int32_t* tokens, const int32_t* target, const int32_t* parent,
+                             const int32_t* row_start, int64_t B, int64_t T, int64_t path_width,
+                             int32_t* path, int32_t* path_len, int32_t* next, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

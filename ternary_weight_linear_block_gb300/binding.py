@@ -40,6 +40,9 @@ TERN_KV_BF16 = 0
 TERN_KV_F16 = 1
 TERN_KV_I8 = 2
 TERN_KV_E4M3 = 3
+TERN_LOGITS_BF16 = 0
+TERN_LOGITS_F16 = 1
+TERN_LOGITS_F32 = 2
 TERN_TREE_ATTENTION_ZERO_BYTES = 8192
 TERN_OP_GEMV = 1
 TERN_OP_GEMM = 2
@@ -94,6 +97,8 @@ _SIGS = {
     "tern_kv_rotate_write": (ctypes.c_int, [_p, _p, _p, _p]),
     "tern_kv8_read": (ctypes.c_int, [_p, _p, _i64, _p, _p, _i32, _p]),
     "tern_kv8_commit": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p]),
+    "tern_sample": (ctypes.c_int, [_p, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p, _p]),
+    "tern_tree_accept": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p]),
 }
 
 
@@ -371,6 +376,19 @@ def tern_kv8_commit(caches, layers, table, table_stride, table_width, ctx_len, p
     return _call("tern_kv8_commit", _desc(caches), layers, _ptr(table), table_stride, table_width,
                  _ptr(ctx_len), _ptr(path), path_width, _ptr(path_len), _ptr(ctx_out), b,
                  _stream(stream))
+
+
+def tern_sample(logits, row_stride, rows, vocab, dtype, u, temperature, top_k, top_p, min_p, token,
+                stream=None):
+    return _call("tern_sample", _ptr(logits), row_stride, rows, vocab, dtype, _ptr(u),
+                 _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token),
+                 _stream(stream))
+
+
+def tern_tree_accept(tokens, target, parent, row_start, b, t, path_width, path, path_len, next,
+                     stream=None):
+    return _call("tern_tree_accept", _ptr(tokens), _ptr(target), _ptr(parent), _ptr(row_start), b, t,
+                 path_width, _ptr(path), _ptr(path_len), _ptr(next), _stream(stream))
 
 
 # ---------------------------------------------------------------- conveniences

@@ -33,6 +33,14 @@ cudaError_t launch_kv8_commit(const tern_kv_cache8* caches, int64_t layers, cons
                               const int32_t* path, int64_t path_width, const int32_t* path_len,
                               int32_t* ctx_out, int64_t B, cudaStream_t st);
 
+cudaError_t launch_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab,
+                          int dtype, const float* u, const float* temperature,
+                          const int32_t* top_k, const float* top_p, const float* min_p,
+                          int32_t* token, cudaStream_t st);
+cudaError_t launch_tree_accept(const int32_t* tokens, const int32_t* target, const int32_t* parent,
+                               const int32_t* row_start, int64_t B, int64_t T, int64_t path_width,
+                               int32_t* path, int32_t* path_len, int32_t* next, cudaStream_t st);
+
 // One tree-attention call.
 struct TreeAttnCall {
   const void* q;

@@ -1,4 +1,4 @@
-/* The checks and the argument marshalling of kv.py's calls, in C: at decode
+/* The checks and the argument marshalling of kv.py's and sampling.py's calls, in C: at decode
  * sizes they cost more host time in Python than the launch itself.
  *
  * A tensor is read through its own attributes (is_cuda, dtype, shape, stride,
@@ -34,6 +34,11 @@ typedef tern_status (*read_fn)(const tern_kv_cache8*, const int64_t*, int64_t, v
 typedef tern_status (*commit8_fn)(const tern_kv_cache8*, int64_t, const int32_t*, int64_t, int64_t,
                                   const int32_t*, const int32_t*, int64_t, const int32_t*, int32_t*,
                                   int64_t, void*);
+typedef tern_status (*sample_fn)(const void*, int64_t, int64_t, int64_t, int32_t, const float*,
+                                 const float*, const int32_t*, const float*, const float*, int32_t*,
+                                 void*);
+typedef tern_status (*accept_fn)(const int32_t*, const int32_t*, const int32_t*, const int32_t*,
+                                 int64_t, int64_t, int64_t, int32_t*, int32_t*, int32_t*, void*);
 static plan_fn f_plan;
 static write_fn f_write;
 static attn_fn f_attn;
@@ -41,6 +46,8 @@ static commit_fn f_commit;
 static rotate_fn f_rotate;
 static read_fn f_read;
 static commit8_fn f_commit8;
+static sample_fn f_sample;
+static accept_fn f_accept;
 
 typedef struct {
   void* p;
@@ -465,6 +472,64 @@ static PyObject* py_bind8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+/* sample(logits, dtype, its number, u, temperature or None, top_k or None, top_p or None, min_p or
+ *        None, token, stream) */
+static PyObject* py_sample(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor x, u, temperature, top_k, top_p, min_p, token;
+  if (!counted(n, 10)) return NULL;
+  const int32_t type = (int32_t)integer(a[2]);
+  void* stream = PyLong_AsVoidPtr(a[9]);
+  if (PyErr_Occurred()) return NULL;
+  if (!read_tensor(a[0], a[1], 2, "logits", &x) || !read_dense(a[3], t_float32, 1, "u", &u) ||
+      !read_if(a[4], t_float32, "temperature", &temperature) ||
+      !read_if(a[5], t_int32, "top_k", &top_k) || !read_if(a[6], t_float32, "top_p", &top_p) ||
+      !read_if(a[7], t_float32, "min_p", &min_p) || !read_dense(a[8], t_int32, 1, "token", &token))
+    return NULL;
+  const int64_t rows = x.shape[0], vocab = x.shape[1];
+  if (rows > 0 && vocab > 1 && x.stride[1] != 1)
+    return refuse("logits: expected to be dense along the last axis"), NULL;
+  if (u.shape[0] != rows || token.shape[0] != rows ||
+      (a[4] != Py_None && temperature.shape[0] != rows) || (a[5] != Py_None && top_k.shape[0] != rows) ||
+      (a[6] != Py_None && top_p.shape[0] != rows) || (a[7] != Py_None && min_p.shape[0] != rows))
+    return refuse("u, temperature, top_k, top_p, min_p, out: expected one number each row of logits"), NULL;
+  if (!ON_CURRENT_DEVICE(-1, &x, &u, &temperature, &top_k, &top_p, &min_p, &token)) return NULL;
+  RETURN_STATUS(f_sample(x.p, rows > 1 ? x.stride[0] : vocab, rows, vocab, type, u.p, temperature.p,
+                         top_k.p, top_p.p, min_p.p, token.p, stream));
+}
+
+/* accept(tokens, target, parents, row_start, path, path_len, next, stream) */
+static PyObject* py_accept(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  Tensor tokens, target, parent, start, path, len, next;
+  if (!counted(n, 8)) return NULL;
+  void* stream = PyLong_AsVoidPtr(a[7]);
+  if (PyErr_Occurred()) return NULL;
+  if (!read_dense(a[0], t_int32, 1, "tokens", &tokens) ||
+      !read_dense(a[1], t_int32, 1, "target", &target) ||
+      !read_dense(a[2], t_int32, 1, "parents", &parent) ||
+      !read_dense(a[3], t_int32, 1, "row_start", &start) ||
+      !read_dense(a[4], t_int32, 2, "path", &path) || !read_dense(a[5], t_int32, 1, "path_len", &len) ||
+      !read_dense(a[6], t_int32, 1, "next", &next))
+    return NULL;
+  const int64_t t = tokens.shape[0], b = start.shape[0] - 1;
+  if (b < 0) return refuse("row_start: expected one more entry than requests"), NULL;
+  if (target.shape[0] != t || parent.shape[0] != t)
+    return refuse("target, parents: expected one each token"), NULL;
+  if (path.shape[0] != b || len.shape[0] != b || next.shape[0] != b)
+    return refuse("path, path_len, next: expected a row each request"), NULL;
+  if (!ON_CURRENT_DEVICE(-1, &tokens, &target, &parent, &start, &path, &len, &next)) return NULL;
+  RETURN_STATUS(f_accept(tokens.p, target.p, parent.p, start.p, b, t, path.shape[1], path.p, len.p,
+                         next.p, stream));
+}
+
+/* bind_tokens(sample, accept), after bind */
+static PyObject* py_bind_tokens(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  if (!counted(n, 2)) return NULL;
+  f_sample = (sample_fn)PyLong_AsVoidPtr(a[0]);
+  f_accept = (accept_fn)PyLong_AsVoidPtr(a[1]);
+  if (PyErr_Occurred()) return NULL;
+  Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
     {"bind", (PyCFunction)(void (*)(void))py_bind, METH_FASTCALL, NULL},
     {"plan", (PyCFunction)(void (*)(void))py_plan, METH_FASTCALL, NULL},
@@ -475,6 +540,9 @@ static PyMethodDef methods[] = {
     {"rotate", (PyCFunction)(void (*)(void))py_rotate, METH_FASTCALL, NULL},
     {"read", (PyCFunction)(void (*)(void))py_read, METH_FASTCALL, NULL},
     {"commit8", (PyCFunction)(void (*)(void))py_commit8, METH_FASTCALL, NULL},
+    {"bind_tokens", (PyCFunction)(void (*)(void))py_bind_tokens, METH_FASTCALL, NULL},
+    {"sample", (PyCFunction)(void (*)(void))py_sample, METH_FASTCALL, NULL},
+    {"accept", (PyCFunction)(void (*)(void))py_accept, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvcall", NULL, -1, methods};
 

@@ -1,0 +1,885 @@
+// Tokens from logits (tern_sample), and the path of a tree of drafts that
+// agrees with them (tern_tree_accept).
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_internal.cuh"
+#include "sm100_ptx.cuh"
+#include "tern_internal.cuh"
+
+namespace tern {
+namespace {
+
+// ------------------------------------------------------------------ sample
+//
+// The filters keep a prefix of the tokens in the order of their logits (of
+// equal ones the lower index first), so all that has to be found is its last
+// logit and how many of that logit's tokens are in.  A cluster of CTAs has a
+// row, each a stretch of its indices.
+//
+//  1. The largest logit, and of every thread's elements the largest.
+//  2. Few survivors: a bound that at least `aim` of the threads' largest
+//     reach, so that about as many tokens do, is found from a histogram of
+//     these alone.  The tokens from it on are gathered in the first CTA, sorted,
+//     and their weights summed in that order: top-k and top-p fall out where
+//     the prefix ends inside the list.  The kept tokens are sorted by index
+//     and the drawn one is found in their running sum.
+//  3. Otherwise the border is searched by histograms of counts and weights
+//     (narrow), in steps of the logit and then of its bits until a single
+//     logit is left.  The draw is a pass over the row: every warp sums the kept
+//     weights of its own stretch, and the one where the sum passes u times the
+//     whole looks for the token.
+//
+// Weights are whole numbers of 2^-45 of the largest, so sums are exact and in
+// any order the same.
+
+constexpr int NT = 512;              // threads, and places of the list
+constexpr int WARPS = NT / 32;
+constexpr int BINS = 1024;
+constexpr int MAX_CL = 8;
+constexpr uint64_t ONE = uint64_t(1) << 45;
+constexpr float kReach = 46.f;       // weights below 2^-46 count as none
+
+// 2^(i / 32) in whole numbers of 2^-31.
+__constant__ uint32_t kRoots[32] = {
+    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
+    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u, 2908241642u, 2971923842u,
+    3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
+    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
+
+struct SampleArgs {
+  const uint8_t* logits;
+  const float* u;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* token;
+  int64_t row_stride;      // elements
+  int vocab;
+};
+
+// What the search for the border has found.
+struct Border {
+  uint32_t key;            // of the last kept logit
+  uint32_t ties;           // its tokens that are kept
+  uint64_t above_mass;     // of the tokens above it
+  uint32_t above;          // their number
+  bool found;              // no: everything from `key` on is kept
+};
+
+struct Shared {
+  uint32_t count[BINS];
+  uint64_t mass[BINS];
+  uint64_t list[NT];       // key << 32 | ~index, largest first
+  uint64_t sum[NT];
+  uint64_t warp_mass[WARPS];
+  uint32_t warp_ties[WARPS];
+  uint64_t scan[2][WARPS];
+  float warp_max[WARPS];
+  uint2 table[32];         // 2^(i / 32) as a whole number of 2^-31 and as a float
+  float cta_max;
+  float c, c_lo;           // log2(e) / temperature
+  double span;             // how far below the largest a logit counts
+  uint32_t n;              // entries of the list
+  int32_t done;            // the list was enough
+  // narrow: the interval of keys, what is above it and in all, the goal
+  uint32_t lo, hi, above, all, in_bin;
+  int32_t found;
+  uint64_t above_mass, all_mass, want;
+};
+
+// Order-preserving whole number of a float (not NaN).
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);     // one zero
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// floor(f n) for 0 <= f < 1; `more` says that something was cut off.
+__device__ __forceinline__ uint64_t part_of(uint64_t n, float f, bool& more) {
+  const uint32_t b = __float_as_uint(f);
+  const uint32_t e = b >> 23;
+  const uint64_t m = (b & 0x7FFFFFu) | (e > 0 ? 0x800000u : 0u);
+  const int shift = 150 - static_cast<int>(e > 0 ? e : 1);     // f = m 2^-shift, 24 <= shift <= 149
+  const uint64_t lo = n * m, hi = __umul64hi(n, m);
+  if (shift >= 128) {
+    more = (lo | hi) != 0;
+    return 0;
+  }
+  if (shift >= 64) {
+    const int s = shift - 64;
+    more = lo != 0 || (hi & ((uint64_t(1) << s) - 1)) != 0;
+    return hi >> s;
+  }
+  more = (lo & ((uint64_t(1) << shift) - 1)) != 0;
+  return (lo >> shift) | (hi << (64 - shift));
+}
+// The least whole number that is not below f n, and at least 1.
+__device__ __forceinline__ uint64_t goal_of(uint64_t n, float f) {
+  bool more;
+  const uint64_t x = part_of(n, f, more);
+  return max(x + (more ? 1 : 0), uint64_t(1));
+}
+
+// exp((x - most) / temperature) as 2^z, in whole numbers of 2^-45.
+//
+// z is a product of 32-bit numbers kept as a sum of two, 2^z a power of two
+// times 2^(i / 32) from the table times 2^r, |r| < 1/64, by four terms of its
+// series: within 2^-29 before the last bit.
+struct Weigh {
+  float most, c, c_lo;       // log2(e) / temperature in two parts
+  const uint2* table;
+  template <bool EXACT>      // x - most is exact in 32 bits, or nearly: 16-bit logits
+  __device__ __forceinline__ uint64_t at(float x) const {
+    if (x == most) return ONE;
+    const float d = x - most;
+    const float z = d * c;
+    if (!(z > -kReach)) return 0;
+    float lo = fmaf(d, c, -z) + d * c_lo;
+    if constexpr (!EXACT) {
+      const float b = d - x;              // what of -most is in d
+      lo += ((x - (d - b)) - (most + b)) * c;
+    }
+    const float m = fmaf(z, 32.f, 12582912.f);
+    const int j = __float_as_int(m) - 0x4B400000;
+    const float r = fmaf(m - 12582912.f, -0.03125f, z) + lo;
+    const float q = r * (0.693147181f + r * (0.240226507f + r * (0.0555041087f + r * 0.00961812911f)));
+    const uint2 t = table[j & 31];
+    const uint32_t w = t.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(t.y) * q));
+    return (static_cast<uint64_t>(w) << 14) >> -(j >> 5);
+  }
+};
+
+template <int DT>
+struct Elt {
+  static constexpr int BYTES = DT == TERN_LOGITS_F32 ? 4 : 2;
+  static constexpr int E = 16 / BYTES;       // elements of a 16-byte slot
+  static constexpr bool EXACT = DT != TERN_LOGITS_F32;
+};
+
+template <int DT>
+__device__ __forceinline__ float element(const uint8_t* row, int64_t i) {
+  if constexpr (DT == TERN_LOGITS_F32) {
+    return __ldg(reinterpret_cast<const float*>(row) + i);
+  } else {
+    const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(row) + i);
+    if constexpr (DT == TERN_LOGITS_BF16) return __uint_as_float(uint32_t(w) << 16);
+    else return __half2float(*reinterpret_cast<const __half*>(&w));
+  }
+}
+
+// A row in slots of 16 aligned bytes; its first element is element `off` of slot 0.
+struct Row {
+  const uint8_t* at;
+  int off, vocab;
+};
+
+// Elements of a slot; NaN, and what is not the row's, as -infinity.
+template <int DT>
+__device__ __forceinline__ void load_slot(const Row& r, int slot, float (&x)[Elt<DT>::E]) {
+  constexpr int E = Elt<DT>::E;
+  const int i0 = slot * E - r.off;
+  if (i0 >= 0 && i0 + E <= r.vocab) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(r.at + int64_t(i0) * Elt<DT>::BYTES));
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == TERN_LOGITS_F32) {
+        x[i] = __uint_as_float(u[i]);
+      } else if constexpr (DT == TERN_LOGITS_BF16) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      x[i] = i0 + i >= 0 && i0 + i < r.vocab ? element<DT>(r.at, i0 + i) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = fmaxf(x[i], -INFINITY);
+}
+
+template <int CL>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (CL == 1) {
+    __syncthreads();
+  } else {
+    __syncwarp();
+    ptx::cluster_sync();
+  }
+}
+
+// `p` of this CTA's shared memory, in CTA `rank`'s.
+template <int CL, class V>
+__device__ __forceinline__ V* in_cta(V* p, uint32_t rank) {
+  if constexpr (CL == 1) {
+    return p;
+  } else {
+    uint64_t a;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<V*>(a);
+  }
+}
+
+// Running sums over the CTA's threads of two numbers, without the own ones; in
+// all_a and all_b the whole.  Synchronises.
+__device__ __forceinline__ void scan_cta(Shared& s, uint64_t& a, uint64_t& b, uint64_t& all_a, uint64_t& all_b) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t a0 = a, b0 = b;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint64_t x = __shfl_up_sync(~0u, a, d), y = __shfl_up_sync(~0u, b, d);
+    if (lane >= d) {
+      a += x;
+      b += y;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    s.scan[0][warp] = a;
+    s.scan[1][warp] = b;
+  }
+  __syncthreads();
+  a -= a0;
+  b -= b0;
+  all_a = all_b = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const uint64_t x = s.scan[0][w], y = s.scan[1][w];
+    if (w < warp) {
+      a += x;
+      b += y;
+    }
+    all_a += x;
+    all_b += y;
+  }
+}
+
+// Sorts one value a thread, the largest first, over the first n (a power of
+// two, 32 at least) threads.
+template <class V>
+__device__ __forceinline__ V sort_cta(V* buf, V x, int n) {
+  const int tid = threadIdx.x;
+  for (int size = 2; size <= n; size <<= 1) {
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      V y;
+      if (d >= 32) {
+        __syncthreads();
+        buf[tid] = x;
+        __syncthreads();
+        y = buf[tid ^ d];
+      } else {
+        y = __shfl_xor_sync(~0u, x, d);
+      }
+      const bool larger = ((tid & d) == 0) == ((tid & size) == 0);
+      if (tid < n) x = larger == (x > y) ? x : y;
+    }
+  }
+  return x;
+}
+
+// Bin of a logit: linear in it from the largest down.  Does not grow with x.
+__device__ __forceinline__ int linear_bin(float x, float most, float step) {
+  return x == most ? 0 : static_cast<int>(fminf((most - x) * step, static_cast<float>(BINS - 1)));
+}
+
+// The lowest key from lo to hi (which has one) whose bin is `bin` or less.
+__device__ __noinline__ uint32_t lowest_key(uint32_t lo, uint32_t hi, float most, float step, int bin) {
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (linear_bin(of_key(mid), most, step) <= bin) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+template <int DT, int CL>
+struct Sampler {
+  static constexpr int E = Elt<DT>::E;
+  static constexpr bool EXACT = Elt<DT>::EXACT;
+  Shared& s;
+  const Row& row;
+  const Weigh& weigh;
+  int begin, end;          // this CTA's slots
+  uint32_t rank;
+  int tid, lane, warp;
+  uint32_t top_key;
+
+  // A warp's own stretch of the slots.
+  __device__ __forceinline__ void stretch(int& lo, int& hi) const {
+    const int each = (end - begin + WARPS * 32 - 1) / (WARPS * 32) * 32;
+    lo = min(begin + warp * each, end);
+    hi = min(lo + each, end);
+  }
+
+  // The border in the keys [lo, hi], hi the largest logit's: where from the top
+  // the tokens number `want` (by_count), or weigh `want`; want = 0: a share `p` of
+  // the weight of all.  Every thread has the result.
+  __device__ Border narrow(uint32_t lo, uint32_t hi, bool by_count, bool masses, uint64_t want, float p) {
+    Border b{lo, ~0u, 0, 0, false};
+    uint64_t above_mass = 0;
+    uint32_t above = 0;
+    const float most = weigh.most, low = of_key(lo);
+    const float step = (BINS - 1) / (most - low);
+    bool linear = most - low < INFINITY && step < INFINITY;
+    while (true) {
+      int shift = 0;
+      while (((hi - lo) >> shift) >= BINS) ++shift;
+      for (int i = tid; i < BINS; i += NT) {
+        s.count[i] = 0;
+        s.mass[i] = 0;
+      }
+      __syncthreads();
+      int w0, w1;
+      stretch(w0, w1);
+      for (int at = w0 + lane; at < w1; at += 32) {
+        float x[E];
+        load_slot<DT>(row, at, x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint32_t key = key_of(x[e]);
+          if (key >= lo && key <= hi) {
+            const int bin = linear ? linear_bin(x[e], most, step) : (hi - key) >> shift;
+            atomicAdd(&s.count[bin], 1u);
+            if (masses)
+              atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[bin]),
+                        static_cast<unsigned long long>(weigh.template at<EXACT>(x[e])));
+          }
+        }
+      }
+      sync_all<CL>();
+      if (rank == 0) {
+        constexpr int PER = BINS / NT;
+        uint64_t cnt[PER], mass[PER], c = 0, m = 0, all_c, all_m;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          cnt[i] = mass[i] = 0;
+          for (int r = 0; r < CL; ++r) {
+            cnt[i] += in_cta<CL>(s.count, r)[tid * PER + i];
+            if (masses) mass[i] += in_cta<CL>(s.mass, r)[tid * PER + i];
+          }
+          c += cnt[i];
+          m += mass[i];
+        }
+        if (tid == 0) s.found = 0;
+        scan_cta(s, c, m, all_c, all_m);
+        if (want == 0) want = goal_of(all_m, p);          // once: the weight of all is known now
+        if (tid == 0) {
+          s.want = want;
+          s.all = static_cast<uint32_t>(above + all_c);
+          s.all_mass = above_mass + all_m;
+        }
+        uint64_t acc_c = above + c, acc_m = above_mass + m;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const uint64_t before = by_count ? acc_c : acc_m, here = by_count ? cnt[i] : mass[i];
+          if (before < want && before + here >= want) {
+            const int bin = tid * PER + i;
+            s.found = 1;
+            s.above = static_cast<uint32_t>(acc_c);
+            s.above_mass = acc_m;
+            s.in_bin = static_cast<uint32_t>(cnt[i]);
+            if (linear) {
+              s.lo = lowest_key(lo, hi, most, step, bin);
+              s.hi = bin == 0 ? hi : lowest_key(lo, hi, most, step, bin - 1) - 1;
+            } else {
+              s.hi = hi - (static_cast<uint32_t>(bin) << shift);
+              const uint32_t width = (1u << shift) - 1;
+              s.lo = s.hi - lo > width ? s.hi - width : lo;
+            }
+          }
+          acc_c += cnt[i];
+          acc_m += mass[i];
+        }
+      }
+      sync_all<CL>();
+      const Shared& first = *in_cta<CL>(&s, 0);
+      const bool found = first.found != 0;
+      const uint32_t in_bin = first.in_bin, all = first.all;
+      const uint64_t all_mass = first.all_mass;
+      want = first.want;
+      if (found) {
+        lo = first.lo;
+        hi = first.hi;
+        above = first.above;
+        above_mass = first.above_mass;
+      }
+      sync_all<CL>();
+      if (!found) {            // fewer than wanted: all are kept
+        b.above = all;
+        b.above_mass = all_mass;
+        return b;
+      }
+      linear = false;
+      if (lo == hi) {
+        b.key = lo;
+        b.found = true;
+        b.above = above;
+        b.above_mass = above_mass;
+        if (by_count) {
+          b.ties = static_cast<uint32_t>(want - above);
+        } else {
+          const uint64_t each = max(weigh.template at<EXACT>(of_key(lo)), uint64_t(1));
+          b.ties = static_cast<uint32_t>(min((want - above_mass + each - 1) / each, static_cast<uint64_t>(in_bin)));
+        }
+        return b;
+      }
+    }
+  }
+
+  // The token of the tokens from logit `key` on, of that logit itself the
+  // first `ties`, at u of their weight.
+  __device__ void draw(uint32_t key, uint32_t ties, float u, int32_t* token) {
+    const float last = of_key(key);
+    const uint64_t each = weigh.template at<EXACT>(last);
+    int w0, w1;
+    stretch(w0, w1);
+    uint64_t mass = 0;
+    uint32_t mine = 0;
+    for (int at = w0 + lane; at < w1; at += 32) {
+      float x[E];
+      load_slot<DT>(row, at, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (x[e] > last) mass += weigh.template at<EXACT>(x[e]);
+        mine += x[e] == last ? 1 : 0;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      mass += __shfl_xor_sync(~0u, mass, d);
+      mine += __shfl_xor_sync(~0u, mine, d);
+    }
+    if (lane == 0) {
+      s.warp_mass[warp] = mass;
+      s.warp_ties[warp] = mine;
+    }
+    sync_all<CL>();
+    // every warp finds what stands before its own stretch, and the whole
+    uint64_t before = 0, all = 0;
+    uint32_t ties_before = 0, ties_all = 0;
+    const int self = rank * WARPS + warp;
+    for (int base = 0; base < CL * WARPS; base += 32) {
+      const int w = base + lane;
+      uint64_t m = 0;
+      uint32_t t = 0;
+      if (w < CL * WARPS) {
+        const Shared& o = *in_cta<CL>(&s, w / WARPS);
+        m = o.warp_mass[w % WARPS];
+        t = o.warp_ties[w % WARPS];
+      }
+      uint64_t mb = w < self ? m : 0;
+      uint32_t tb = w < self ? t : 0;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) {
+        m += __shfl_xor_sync(~0u, m, d);
+        t += __shfl_xor_sync(~0u, t, d);
+        mb += __shfl_xor_sync(~0u, mb, d);
+        tb += __shfl_xor_sync(~0u, tb, d);
+      }
+      all += m;
+      ties_all += t;
+      before += mb;
+      ties_before += tb;
+    }
+    all += each * min(ties, ties_all);
+    before += each * min(ties, ties_before);
+    bool more;
+    const uint64_t at_u = part_of(all, u, more);
+    const uint64_t own = mass + each * (min(ties, ties_before + mine) - min(ties, ties_before));
+    if (before <= at_u && at_u < before + own) {
+      for (int at = w0; at < w1; at += 32) {
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = -INFINITY;
+        if (at + lane < w1) load_slot<DT>(row, at + lane, x);
+        uint64_t m = 0;
+        uint32_t t = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) t += at + lane < w1 && x[e] == last ? 1 : 0;
+        uint32_t t_up = t;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(~0u, t_up, d);
+          if (lane >= d) t_up += y;
+        }
+        const uint32_t seen = ties_before + t_up - t;        // ties before this lane's
+        uint32_t k = seen;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (x[e] > last) m += weigh.template at<EXACT>(x[e]);
+          else if (x[e] == last && k++ < ties) m += each;
+        }
+        uint64_t up = m;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint64_t y = __shfl_up_sync(~0u, up, d);
+          if (lane >= d) up += y;
+        }
+        const uint32_t past = __ballot_sync(~0u, before + up > at_u);
+        if (past != 0) {
+          if (lane == __ffs(past) - 1) {
+            uint64_t sum = before + up - m;
+            k = seen;
+            int hit = -1;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              if (x[e] > last) sum += weigh.template at<EXACT>(x[e]);
+              else if (x[e] == last && k++ < ties) sum += each;
+              if (hit < 0 && sum > at_u) hit = e;
+            }
+            *token = (at + lane) * E - row.off + hit;
+          }
+          break;
+        }
+        before += __shfl_sync(~0u, up, 31);
+        ties_before += __shfl_sync(~0u, t_up, 31);
+      }
+    }
+  }
+
+  // The list: the n tokens from some logit on; `all`: no others count.  Whether
+  // the prefix ends inside it; then also the token.  For the first CTA.
+  __device__ bool from_list(int n, bool all, int k, float p, uint64_t row_mass, float u, int32_t* token) {
+    int size = 32;
+    while (size < n) size <<= 1;
+    const uint64_t x = sort_cta(s.sum, tid < n ? s.list[tid] : uint64_t(0), size);
+    const uint32_t key = static_cast<uint32_t>(x >> 32), index = ~static_cast<uint32_t>(x);
+    const uint64_t w = tid < n ? weigh.template at<EXACT>(of_key(key)) : 0;
+    uint64_t before = w, none = 0, sum, z;
+    scan_cta(s, before, none, sum, z);
+    int kept = n;
+    bool closed = all;         // what top-k and min-p leave is in the list
+    if (k > 0 && k <= n) {
+      kept = k;
+      closed = true;
+    }
+    if (!closed && k > 0) return false;
+    if (p < 1.f) {
+      uint64_t whole = row_mass;
+      if (closed) {
+        if (tid == kept - 1) s.want = before + w;
+        __syncthreads();
+        whole = s.want;
+      }
+      const uint64_t want = goal_of(whole, p);
+      if (!closed && sum < want) return false;
+      kept = max(__syncthreads_count(tid < kept && before < want), 1);
+    }
+    // by index, with the weights behind
+    __syncthreads();
+    s.list[tid] = w;
+    const uint32_t y = sort_cta(reinterpret_cast<uint32_t*>(s.sum),
+                                tid < kept ? ~(index << 9 | static_cast<uint32_t>(tid)) : 0u, size);
+    __syncthreads();
+    const uint32_t place = ~y;
+    const uint64_t own = tid < kept ? s.list[place & 511] : 0;
+    uint64_t up = own;
+    none = 0;
+    scan_cta(s, up, none, sum, z);
+    bool more;
+    const uint64_t at_u = part_of(sum, u, more);
+    if (tid < kept && up <= at_u && at_u < up + own) *token = static_cast<int32_t>(place >> 9);
+    return true;
+  }
+};
+
+template <int DT, int CL>
+__global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
+  constexpr int E = Elt<DT>::E;
+  constexpr bool EXACT = Elt<DT>::EXACT;
+  __shared__ Shared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = CL == 1 ? 0 : ptx::cluster_ctarank();
+  const int64_t r = blockIdx.x / CL;
+  if (tid < 32) s.table[tid] = make_uint2(kRoots[tid], __float_as_uint(static_cast<float>(kRoots[tid])));
+  if (tid == 0) {
+    s.n = 0;
+    s.done = 0;
+  }
+  for (int i = tid; i < BINS; i += NT) s.count[i] = 0;
+  pdl_wait();
+  pdl_launch_dependents();
+  Row row;
+  row.at = a.logits + r * a.row_stride * Elt<DT>::BYTES;
+  row.off = static_cast<int>((reinterpret_cast<uintptr_t>(row.at) & 15) / Elt<DT>::BYTES);
+  row.vocab = a.vocab;
+  const int slots = (row.off + a.vocab + E - 1) / E;
+  const int each = (slots + CL - 1) / CL;
+  const int begin = min(static_cast<int>(rank) * each, slots), end = min(begin + each, slots);
+  const float temperature = a.temperature != nullptr ? a.temperature[r] : 1.f;
+  int k = a.top_k != nullptr ? a.top_k[r] : 0;
+  float p = a.top_p != nullptr ? a.top_p[r] : 1.f;
+  const float min_p = a.min_p != nullptr ? fminf(a.min_p[r], 1.f) : 0.f;
+  float u = a.u[r];
+  u = u > 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f;
+  if (k >= a.vocab || k < 0) k = 0;
+  p = p < 1.f ? fmaxf(p, 0.f) : 1.f;                // (a NaN: 1)
+
+  // 64-bit arithmetic is slow here: one warp's, while the others wait for the row
+  if (warp == WARPS - 1) {
+    const double c = 1.4426950408889634 / static_cast<double>(temperature);
+    double span = -static_cast<double>(kReach) / c;                 // with a weight, and min-p's
+    if (min_p > 0.f) span = fmax(span, log(static_cast<double>(min_p)) * static_cast<double>(temperature));
+    const float c_hi = static_cast<float>(c), c_lo = static_cast<float>(c - static_cast<double>(c_hi));
+    s.c = c_hi;
+    s.c_lo = fabsf(c_lo) < INFINITY ? c_lo : 0.f;
+    s.span = span;
+  }
+
+  // the largest
+  float mine = -INFINITY;
+  for (int at = begin + tid; at < end; at += NT) {
+    float x[E];
+    load_slot<DT>(row, at, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
+  }
+  __syncwarp();
+  float most = mine;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+  if (lane == 0) s.warp_max[warp] = most;
+  __syncthreads();
+  most = s.warp_max[0];
+#pragma unroll
+  for (int w = 1; w < WARPS; ++w) most = fmaxf(most, s.warp_max[w]);
+  if constexpr (CL > 1) {
+    if (tid == 0) s.cta_max = most;
+    sync_all<CL>();
+    for (int i = 0; i < CL; ++i) most = fmaxf(most, *in_cta<CL>(&s.cta_max, i));
+  }
+
+  const Weigh weigh{most, s.c, s.c_lo, s.table};
+  Sampler<DT, CL> sampler{s, row, weigh, begin, end, rank, tid, lane, warp, key_of(most)};
+  if (most == -INFINITY) {
+    if (rank == 0 && tid == 0) a.token[r] = -1;
+    if constexpr (CL > 1) sync_all<CL>();      // others still read this CTA's largest
+    return;
+  }
+  if (!(temperature > 0.f) || k == 1 || p == 0.f) {
+    sampler.draw(key_of(most), 1, 0.f, a.token + r);
+    if constexpr (CL > 1) sync_all<CL>();
+    return;
+  }
+  // the lowest logit that counts
+  const double low = static_cast<double>(most) + s.span;
+  const float cut = fminf(low == low ? __double2float_ru(low) : most, most);
+  const uint32_t cut_key = key_of(cut);
+  if (k == 0 && p >= 1.f) {
+    sampler.draw(cut_key, ~0u, u, a.token + r);
+    if constexpr (CL > 1) sync_all<CL>();
+    return;
+  }
+
+  // a bound that `aim` of the threads' largest reach
+  const int aim = max(k, 160);
+  uint32_t bound = cut_key;
+  const float step = (BINS - 1) / (most - cut);
+  const bool list = aim <= 384;
+  if (list && most - cut < INFINITY && step < INFINITY) {
+    if (mine >= cut) atomicAdd(&s.count[linear_bin(mine, most, step)], 1u);
+    sync_all<CL>();
+    if (rank == 0) {
+      constexpr int PER = BINS / NT;
+      uint64_t cnt[PER], sum = 0, none = 0, all, z;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        cnt[i] = 0;
+        for (int q = 0; q < CL; ++q) cnt[i] += in_cta<CL>(s.count, q)[tid * PER + i];
+        sum += cnt[i];
+      }
+      if (tid == 0) s.lo = cut_key;
+      scan_cta(s, sum, none, all, z);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (sum < aim && sum + cnt[i] >= aim)
+          s.lo = lowest_key(cut_key, key_of(most), most, step, tid * PER + i);
+        sum += cnt[i];
+      }
+    }
+    sync_all<CL>();
+    bound = in_cta<CL>(&s, 0)->lo;
+  }
+  if (list) {
+    // gather; where a share of all of the row's weight is asked for, add that up too
+    const bool all = bound <= cut_key;
+    const bool sums = p < 1.f && k == 0 && !all;
+    const float from = of_key(bound);
+    uint64_t mass = 0;
+    Shared& first = *in_cta<CL>(&s, 0);
+    for (int at = begin + tid; at < end; at += NT) {
+      float x[E];
+      load_slot<DT>(row, at, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (sums && x[e] >= cut) mass += weigh.template at<EXACT>(x[e]);
+        const int index = at * E - row.off + e;
+        if (x[e] >= from && index >= 0 && index < a.vocab) {
+          const uint32_t i = atomicAdd(&first.n, 1u);
+          if (i < NT) first.list[i] = static_cast<uint64_t>(key_of(x[e])) << 32 | ~static_cast<uint32_t>(index);
+        }
+      }
+    }
+    __syncwarp();
+    if (sums) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mass += __shfl_xor_sync(~0u, mass, d);
+      if (lane == 0) s.warp_mass[warp] = mass;
+    }
+    sync_all<CL>();
+    if (rank == 0) {
+      const int n = static_cast<int>(min(s.n, static_cast<uint32_t>(NT + 1)));
+      uint64_t row_mass = 0;
+      if (sums)
+        for (int q = 0; q < CL; ++q)
+          for (int w = 0; w < WARPS; ++w) row_mass += in_cta<CL>(s.warp_mass, q)[w];
+      if (n <= NT) {
+        const bool ok = sampler.from_list(n, all, k, p, row_mass, u, a.token + r);
+        if (tid == 0) s.done = ok ? 1 : 0;
+      }
+    }
+    sync_all<CL>();
+    const bool done = first.done != 0;
+    if constexpr (CL > 1) sync_all<CL>();
+    if (done) return;
+  }
+
+  // the border by histograms
+  const uint32_t top = key_of(most);
+  Border b{cut_key, ~0u, 0, 0, false};
+  uint64_t want = 0;
+  uint32_t k_key = cut_key, k_ties = ~0u;
+  if (k > 0) {
+    b = sampler.narrow(cut_key, top, true, p < 1.f, static_cast<uint64_t>(k), 0.f);
+    if (b.found) {
+      k_key = b.key;
+      k_ties = b.ties;
+    }
+    if (p < 1.f)
+      want = goal_of(b.found ? b.above_mass + b.ties * weigh.template at<EXACT>(of_key(b.key)) : b.above_mass, p);
+  }
+  if (p < 1.f) {
+    const Border q = sampler.narrow(k_key, top, false, true, want, p);
+    if (q.found) {
+      b = q;
+      if (q.key == k_key) b.ties = min(q.ties, k_ties);
+    }
+  }
+  sampler.draw(b.key, b.found ? b.ties : ~0u, u, a.token + r);
+  if constexpr (CL > 1) sync_all<CL>();
+}
+
+// ------------------------------------------------------------------ accept
+//
+// A warp a request.  A path goes up, so 32 rows at a time are looked at once:
+// the first that fits the path's last row is the next, and its target is in
+// the lane that has it.  Bound: the launch and two dependent reads.
+
+constexpr int ACCEPT_THREADS = 128;
+
+struct AcceptArgs {
+  const int32_t* tokens;
+  const int32_t* target;
+  const int32_t* parent;
+  const int32_t* row_start;
+  int32_t* path;
+  int32_t* path_len;
+  int32_t* next;
+  int64_t T;
+  int B, width;
+};
+
+__global__ void __launch_bounds__(ACCEPT_THREADS) accept_kernel(const __grid_constant__ AcceptArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int b = (blockIdx.x * ACCEPT_THREADS + threadIdx.x) >> 5;
+  if (b >= a.B) return;
+  const int64_t s0 = a.row_start[b], s1 = a.row_start[b + 1];
+  const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.T;
+  const int n = ok ? static_cast<int>(min(s1 - s0, int64_t(a.width))) : 0;
+  int32_t* path = a.path + int64_t(b) * a.width;
+  int len = 0, cur = -1, want = -1;
+  for (int base = 0; base < n; base += 32) {
+    const int j = base + lane;
+    const bool in = j < n;
+    const int token = in ? a.tokens[s0 + j] : 0;
+    const int parent = in && j > 0 ? a.parent[s0 + j] : -1;
+    const int target = in ? a.target[s0 + j] : 0;
+    if (base == 0) {
+      cur = 0;
+      want = __shfl_sync(~0u, target, 0);
+      if (lane == 0) path[0] = 0;
+      len = 1;
+    }
+    while (true) {
+      const uint32_t fits = __ballot_sync(~0u, in && j > cur && parent == cur && token == want);
+      if (fits == 0) break;
+      const int l = __ffs(fits) - 1;
+      cur = base + l;
+      want = __shfl_sync(~0u, target, l);
+      if (lane == 0) path[len] = cur;
+      ++len;
+    }
+  }
+  for (int i = len + lane; i < a.width; i += 32) path[i] = -1;
+  if (lane == 0) {
+    a.path_len[b] = len;
+    a.next[b] = want;
+  }
+}
+
+template <int DT, int CL>
+cudaError_t launch_sample_cl(const SampleArgs& a, int64_t rows, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(rows * CL));
+  if constexpr (CL == 1) return launch(sample_kernel<DT, 1>, grid, dim3(NT), 0, st, a);
+  else return launch_cluster(sample_kernel<DT, CL>, grid, dim3(NT), 0, st, CL, a);
+}
+
+template <int DT>
+cudaError_t launch_sample_type(const SampleArgs& a, int64_t rows, cudaStream_t st) {
+  // CTAs a row: as many as the GPU has room for, while half of the threads have
+  // a slot of their own
+  const int64_t room = 2 * int64_t(kv_sm_count());
+  int cl = 1;
+  while (cl < MAX_CL && rows * (2 * cl) <= room && a.vocab / Elt<DT>::E / (2 * cl) >= NT / 2) cl *= 2;
+  if (cl == 8) return launch_sample_cl<DT, 8>(a, rows, st);
+  if (cl == 4) return launch_sample_cl<DT, 4>(a, rows, st);
+  if (cl == 2) return launch_sample_cl<DT, 2>(a, rows, st);
+  return launch_sample_cl<DT, 1>(a, rows, st);
+}
+
+}  // namespace
+
+cudaError_t launch_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab, int dtype,
+                          const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                          const float* min_p, int32_t* token, cudaStream_t st) {
+  const SampleArgs a{static_cast<const uint8_t*>(logits), u, temperature, top_k, top_p, min_p, token, row_stride,
+                     static_cast<int>(vocab)};
+  if (dtype == TERN_LOGITS_BF16) return launch_sample_type<TERN_LOGITS_BF16>(a, rows, st);
+  if (dtype == TERN_LOGITS_F16) return launch_sample_type<TERN_LOGITS_F16>(a, rows, st);
+  return launch_sample_type<TERN_LOGITS_F32>(a, rows, st);
+}
+
+cudaError_t launch_tree_accept(const int32_t* tokens, const int32_t* target, const int32_t* parent,
+                               const int32_t* row_start, int64_t B, int64_t T, int64_t path_width, int32_t* path,
+                               int32_t* path_len, int32_t* next, cudaStream_t st) {
+  const AcceptArgs a{tokens, target, parent, row_start, path, path_len, next, T, static_cast<int>(B),
+                     static_cast<int>(path_width)};
+  const int64_t blocks = (B + ACCEPT_THREADS / 32 - 1) / (ACCEPT_THREADS / 32);
+  return launch(accept_kernel, dim3(static_cast<unsigned>(blocks)), dim3(ACCEPT_THREADS), 0, st, a);
+}
+
+}  // namespace tern

@@ -650,4 +650,35 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
                                      static_cast<cudaStream_t>(stream)));
 }
 
+tern_status tern_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab,
+                        int32_t dtype, const float* u, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* token, void* stream) {
+  if (rows < 0 || dtype < TERN_LOGITS_BF16 || dtype > TERN_LOGITS_F32) return TERN_ERR_INVALID_ARG;
+  if (vocab < 1 || vocab > (int64_t(1) << 18) || rows >= (int64_t(1) << 20) || row_stride < vocab ||
+      row_stride >= (int64_t(1) << 39))
+    return TERN_ERR_SHAPE;
+  if (rows == 0) return TERN_OK;
+  if (logits == nullptr || u == nullptr || token == nullptr) return TERN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(logits) & (dtype == TERN_LOGITS_F32 ? 3u : 1u)) != 0)
+    return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_sample(logits, row_stride, rows, vocab, dtype, u, temperature, top_k, top_p,
+                                 min_p, token, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_tree_accept(const int32_t* tokens, const int32_t* target, const int32_t* parent,
+                             const int32_t* row_start, int64_t B, int64_t T, int64_t path_width,
+                             int32_t* path, int32_t* path_len, int32_t* next, void* stream) {
+  if (B < 0 || T < 0) return TERN_ERR_INVALID_ARG;
+  if (B > 65536 || T >= (int64_t(1) << 31) || path_width < 1 || path_width > 256) return TERN_ERR_SHAPE;
+  if (B == 0) return TERN_OK;
+  if (row_start == nullptr || path == nullptr || path_len == nullptr || next == nullptr ||
+      (T > 0 && (tokens == nullptr || target == nullptr || parent == nullptr)))
+    return TERN_ERR_INVALID_ARG;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  return from_cuda(launch_tree_accept(tokens, target, parent, row_start, B, T, path_width, path,
+                                      path_len, next, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -67,6 +67,7 @@ def _native():
         module.bind(*at(*names), torch.int32, torch.int64, torch.float32,
                     torch._C._cuda_getDevice if _several_devices() else None)
         module.bind8(*at("tern_kv_rotate_write", "tern_kv8_read", "tern_kv8_commit"))
+        module.bind_tokens(*at("tern_sample", "tern_tree_accept"))
         _calls = module
     return _calls
 
