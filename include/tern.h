@@ -756,6 +756,26 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
                             const int32_t* path, int64_t path_width, const int32_t* path_len,
                             int32_t* ctx_out, int64_t B, void* stream);
 
+/* tern_tree_attention8 -- tern_tree_attention over an 8-bit cache.
+ *   q, out   of `dtype`, TERN_KV_BF16 or TERN_KV_F16
+ *   ws       tern_tree_attention8_workspace_bytes() bytes, otherwise as for
+ *            tern_tree_attention (the two may share one)
+ * Codes enter the products as they are, units multiply scores and
+ * probabilities in 32 bits.  The queries and the probabilities times the
+ * values' units are rounded to fp16 for their products, relatively to the
+ * largest of their row (a bf16 query keeps all its bits unless it is below
+ * 2^-28 of its row's largest).  A key that a row does not see has no
+ * influence, whatever its unit is; one whose unit is NaN makes every row that
+ * sees it NaN. */
+size_t tern_tree_attention8_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D);
+tern_status tern_tree_attention8(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 int32_t dtype, const tern_kv_cache8* cache, const int32_t* table,
+                                 int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                                 const int32_t* row_start, const uint64_t* mask,
+                                 int64_t mask_words, int64_t B, int64_t T, int64_t Hq,
+                                 int64_t max_new, float scale, void* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------
  * Tokens from logits, and the drafts that agree with them
  * ---------------------------------------------------------------------- */

@@ -97,6 +97,10 @@ _SIGS = {
     "tern_kv_rotate_write": (ctypes.c_int, [_p, _p, _p, _p]),
     "tern_kv8_read": (ctypes.c_int, [_p, _p, _i64, _p, _p, _i32, _p]),
     "tern_kv8_commit": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _p, _p, _i64, _p, _p, _i64, _p]),
+    "tern_tree_attention8_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "tern_tree_attention8": (ctypes.c_int, [_p, _i64, _i64, _i32, _p, _p, _i64, _i64, _p, _p, _p,
+                                            _i64, _i64, _i64, _i64, _i64, _f32, _p, _p, _p, _sz,
+                                            _p]),
     "tern_sample": (ctypes.c_int, [_p, _i64, _i64, _i64, _i32, _p, _p, _p, _p, _p, _p, _p]),
     "tern_tree_accept": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p]),
 }
@@ -376,6 +380,19 @@ def tern_kv8_commit(caches, layers, table, table_stride, table_width, ctx_len, p
     return _call("tern_kv8_commit", _desc(caches), layers, _ptr(table), table_stride, table_width,
                  _ptr(ctx_len), _ptr(path), path_width, _ptr(path_len), _ptr(ctx_out), b,
                  _stream(stream))
+
+
+def tern_tree_attention8_workspace_bytes(max_new: int, hq: int, h: int, d: int) -> int:
+    return lib().tern_tree_attention8_workspace_bytes(max_new, hq, h, d)
+
+
+def tern_tree_attention8(q, q_token_stride, q_head_stride, dtype, cache, table, table_stride,
+                         table_width, ctx_len, row_start, mask, mask_words, b, t, hq, max_new, scale,
+                         out, lse, ws, ws_bytes, stream=None):
+    return _call("tern_tree_attention8", _ptr(q), q_token_stride, q_head_stride, dtype, _desc(cache),
+                 _ptr(table), table_stride, table_width, _ptr(ctx_len), _ptr(row_start),
+                 _ptr(mask), mask_words, b, t, hq, max_new, scale, _ptr(out), _ptr(lse), _ptr(ws),
+                 ws_bytes, _stream(stream))
 
 
 def tern_sample(logits, row_stride, rows, vocab, dtype, u, temperature, top_k, top_p, min_p, token,

@@ -36,53 +36,9 @@ namespace {
 
 using namespace attn;
 
-constexpr uint32_t WAIT_LIMIT = 1u << 18;   // polls of a bounded wait, about a second
-enum : unsigned int { ERR_PRODUCER = 1u, ERR_CONSUMER = 2u, ERR_DRAIN = 4u };
-
 __device__ __forceinline__ void fail(volatile int* abort_flag, unsigned int code) {
   *abort_flag = 1;
   atomicOr(&g_attn_error, code);
-}
-
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-}
-template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(ptx::smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
-      "r"(c3)
-      : "memory");
-}
-
-// Transposes an 8x8 matrix of 16-bit values held one row in 4 lanes.
-__device__ __forceinline__ uint32_t movm(uint32_t x) {
-  uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
 }
 
 // ------------------------------------------------------------------ rows kernel
@@ -116,41 +72,6 @@ struct Rows {
   static constexpr size_t SMEM = size_t(STAGES) * STAGE + MERGE + QBYTES + 1024;
   static_assert(STAGES >= 2, "ring");
 };
-
-// What the keys' producer tells the consumers of an item's part.
-struct Part {
-  int b, h, r0, rows, row0, ctx, n, len;
-  int t0, t1;             // key tiles; none: there is no further item
-  int whole, begins;      // all of the item's tiles; its first
-  int first, follow;      // CTAs that share it
-  int pad[2];
-};
-
-// Whether any of the N threads at named barrier `id` says so.
-__device__ __forceinline__ bool named_any(int id, int count, bool mine) {
-  uint32_t r;
-  asm volatile(
-      "{\n.reg .pred p, q;\n"
-      "setp.ne.u32 p, %3, 0;\n"
-      "barrier.cta.red.or.pred q, %1, %2, p;\n"
-      "selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"(static_cast<uint32_t>(mine))
-      : "memory");
-  return r != 0;
-}
-
-// The pages of a tile of TKEYS keys: lane i has the page of its i-th box (a
-// page's part of the tile, 1 << box_shift keys); a page out of range is turned
-// into one past the last, of which TMA copies zeros.
-template <int TKEYS>
-__device__ __forceinline__ int page_at(const Args& a, const Seg& s, int t, int box_shift, int lane) {
-  const int64_t pos = int64_t(t) * TKEYS + (int64_t(lane) << box_shift);
-  int pg = -1;
-  if (lane < (TKEYS >> box_shift) && pos < s.r.len)
-    pg = a.table[int64_t(s.b) * a.table_stride + (pos >> a.page_shift)];
-  return pg < 0 || pg >= a.pages ? a.pages : pg;
-}
 
 // Keys or values of tile t into `dst` (64-column halves of TKEYS rows of 128
 // swizzled bytes), one box and half a lane; the warp first announces the
@@ -1298,27 +1219,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) combine_kernel(const Args a, int
 
 // ------------------------------------------------------------------ host
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static std::atomic<EncodeTiledFn> fn{nullptr};
-  EncodeTiledFn f = fn.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess) {
-      f = reinterpret_cast<EncodeTiledFn>(p);
-      fn.store(f, std::memory_order_release);
-    }
-  }
-  return f;
-}
-
 // The cache as [pages][heads][rows][dim]: boxes of `rows` rows of one page
 // and head, 64 values wide (128 bytes, swizzled).
 bool make_map(CUtensorMap* map, const tern_kv_cache& c, void* base, int rows) {
@@ -1352,20 +1252,6 @@ bool make_query_map(CUtensorMap* map, const TreeAttnCall& call, int tokens, int 
   return enc(map, type, 3, const_cast<void*>(call.q), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The workspace: arrival counters, which are zero between calls, then the
-// pieces.
-struct Ws {
-  size_t o, ml, items, bytes;
-};
-Ws ws_layout(int64_t grid, int64_t rt, int64_t D) {
-  Ws w;
-  w.o = TERN_TREE_ATTENTION_ZERO_BYTES;
-  w.ml = w.o + static_cast<size_t>(2 * grid * rt * D) * sizeof(float);
-  w.items = w.ml + static_cast<size_t>(4 * grid * rt) * sizeof(float2);
-  w.bytes = w.items + static_cast<size_t>(grid) * sizeof(Item);
-  return w;
 }
 
 // Which kernel serves requests of up to `rows` rows on a key head, as its

@@ -61,4 +61,25 @@ size_t tree_attention_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, in
 cudaError_t launch_tree_attention(const TreeAttnCall& call, cudaStream_t st);
 cudaError_t attn_read_clear_error(unsigned int* err);
 
+// One tree-attention call over an 8-bit cache.
+struct TreeAttn8Call {
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  int dtype;
+  tern_kv_cache8 cache;
+  const int32_t* table;
+  int64_t table_stride, table_width;
+  const int32_t* ctx_len;
+  const int32_t* row_start;
+  const uint64_t* mask;
+  int64_t mask_words, B, T, Hq, max_new;
+  float scale;
+  void* out;
+  float* lse;
+  void* ws;
+};
+size_t tree_attention8_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D);
+cudaError_t launch_tree_attention8(const TreeAttn8Call& call, cudaStream_t st);
+cudaError_t attn8_read_clear_error(unsigned int* err);
+
 }  // namespace tern

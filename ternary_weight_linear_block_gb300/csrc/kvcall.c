@@ -31,6 +31,10 @@ typedef tern_status (*rotate_fn)(const tern_kv_cache*, const tern_kv_cache8*, co
                                  void*);
 typedef tern_status (*read_fn)(const tern_kv_cache8*, const int64_t*, int64_t, void*, void*, int32_t,
                                void*);
+typedef tern_status (*attn8_fn)(const void*, int64_t, int64_t, int32_t, const tern_kv_cache8*,
+                                const int32_t*, int64_t, int64_t, const int32_t*, const int32_t*,
+                                const uint64_t*, int64_t, int64_t, int64_t, int64_t, int64_t, float,
+                                void*, float*, void*, size_t, void*);
 typedef tern_status (*commit8_fn)(const tern_kv_cache8*, int64_t, const int32_t*, int64_t, int64_t,
                                   const int32_t*, const int32_t*, int64_t, const int32_t*, int32_t*,
                                   int64_t, void*);
@@ -46,6 +50,7 @@ static commit_fn f_commit;
 static rotate_fn f_rotate;
 static read_fn f_read;
 static commit8_fn f_commit8;
+static attn8_fn f_attn8;
 static sample_fn f_sample;
 static accept_fn f_accept;
 
@@ -276,12 +281,14 @@ static PyObject* py_write(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* attention(cache address, dtype, heads, dim, its device, q, table, ctx_len, row_start,
- *           max_new, mask or None, scale, out, lse or None, workspace address, its bytes, stream) */
-static PyObject* py_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+ *           max_new, mask or None, scale, out, lse or None, workspace address, its bytes, stream)
+ * attention8: the same over an 8-bit cache, with the number of the rows' type behind */
+static PyObject* attention(PyObject* const* a, Py_ssize_t n, int eight) {
   Tensor q, table, ctx, start, mask, out, lse;
   int64_t qr, qh, stride;
-  if (!counted(n, 17)) return NULL;
-  const tern_kv_cache* cache = PyLong_AsVoidPtr(a[0]);
+  if (!counted(n, eight ? 18 : 17)) return NULL;
+  const void* cache = PyLong_AsVoidPtr(a[0]);
+  const int32_t type = eight ? (int32_t)integer(a[17]) : 0;
   const int64_t heads = integer(a[2]), dim = integer(a[3]), max_new = integer(a[9]);
   const long device = PyLong_AsLong(a[4]);
   const double scale = PyFloat_AsDouble(a[11]);
@@ -317,9 +324,20 @@ static PyObject* py_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) 
       return refuse("lse: expected [rows, query heads]"), NULL;
   }
   if (!ON_CURRENT_DEVICE(device, &q, &table, &ctx, &start, &out, &mask, &lse)) return NULL;
+  if (eight)
+    RETURN_STATUS(f_attn8(q.p, qr, qh, type, cache, table.p, stride, table.shape[1], ctx.p, start.p,
+                          mask.p, mask.shape[1], b, t, hq, max_new, (float)scale, out.p, lse.p, ws,
+                          ws_bytes, stream));
   RETURN_STATUS(f_attn(q.p, qr, qh, cache, table.p, stride, table.shape[1], ctx.p, start.p,
                        mask.p, mask.shape[1], b, t, hq, max_new, (float)scale, out.p,
                        lse.p, ws, ws_bytes, stream));
+}
+
+static PyObject* py_attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  return attention(a, n, 0);
+}
+static PyObject* py_attention8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  return attention(a, n, 1);
 }
 
 /* commit(descriptions as bytes, layers, the caches' device, table, ctx_len, path, path_len, ctx_out, stream)
@@ -462,12 +480,13 @@ static PyObject* py_read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   RETURN_STATUS(f_read(cache, slots.p, t, k.p, v.p, type, stream));
 }
 
-/* bind8(rotate_write, read, commit8), after bind */
+/* bind8(rotate_write, read, commit8, attention8), after bind */
 static PyObject* py_bind8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-  if (!counted(n, 3)) return NULL;
+  if (!counted(n, 4)) return NULL;
   f_rotate = (rotate_fn)PyLong_AsVoidPtr(a[0]);
   f_read = (read_fn)PyLong_AsVoidPtr(a[1]);
   f_commit8 = (commit8_fn)PyLong_AsVoidPtr(a[2]);
+  f_attn8 = (attn8_fn)PyLong_AsVoidPtr(a[3]);
   if (PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
@@ -539,6 +558,7 @@ static PyMethodDef methods[] = {
     {"bind8", (PyCFunction)(void (*)(void))py_bind8, METH_FASTCALL, NULL},
     {"rotate", (PyCFunction)(void (*)(void))py_rotate, METH_FASTCALL, NULL},
     {"read", (PyCFunction)(void (*)(void))py_read, METH_FASTCALL, NULL},
+    {"attention8", (PyCFunction)(void (*)(void))py_attention8, METH_FASTCALL, NULL},
     {"commit8", (PyCFunction)(void (*)(void))py_commit8, METH_FASTCALL, NULL},
     {"bind_tokens", (PyCFunction)(void (*)(void))py_bind_tokens, METH_FASTCALL, NULL},
     {"sample", (PyCFunction)(void (*)(void))py_sample, METH_FASTCALL, NULL},

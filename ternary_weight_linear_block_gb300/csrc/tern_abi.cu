@@ -465,11 +465,12 @@ tern_status tern_selftest_wait(uint32_t polls, void* stream) {
 tern_status tern_check(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return TERN_ERR_CUDA;
-  unsigned int err_gemm = 0, err_gemv = 0, err_attn = 0;
+  unsigned int err_gemm = 0, err_gemv = 0, err_attn = 0, err_attn8 = 0;
   if (gemm_read_clear_error(&err_gemm) != cudaSuccess) return TERN_ERR_CUDA;
   if (gemv_read_clear_error(&err_gemv) != cudaSuccess) return TERN_ERR_CUDA;
   if (attn_read_clear_error(&err_attn) != cudaSuccess) return TERN_ERR_CUDA;
-  return (err_gemm | err_gemv | err_attn) ? TERN_ERR_TIMEOUT : TERN_OK;
+  if (attn8_read_clear_error(&err_attn8) != cudaSuccess) return TERN_ERR_CUDA;
+  return (err_gemm | err_gemv | err_attn | err_attn8) ? TERN_ERR_TIMEOUT : TERN_OK;
 }
 
 tern_status tern_kv_plan(const int32_t* ctx_len, const int32_t* new_len, int64_t B,
@@ -648,6 +649,46 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
   return from_cuda(launch_kv8_commit(caches, layers, table, table_stride, table_width, ctx_len, path,
                                      path_width, path_len, ctx_out, B,
                                      static_cast<cudaStream_t>(stream)));
+}
+
+size_t tern_tree_attention8_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
+  if (max_new < 1 || max_new > 256 || H < 1 || Hq < H || Hq % H != 0 ||
+      (D != 64 && D != 128 && D != 256))
+    return 0;
+  return tree_attention8_workspace_bytes(max_new, Hq, H, D);
+}
+
+tern_status tern_tree_attention8(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                 int32_t dtype, const tern_kv_cache8* cache, const int32_t* table,
+                                 int64_t table_stride, int64_t table_width, const int32_t* ctx_len,
+                                 const int32_t* row_start, const uint64_t* mask,
+                                 int64_t mask_words, int64_t B, int64_t T, int64_t Hq,
+                                 int64_t max_new, float scale, void* out, float* lse, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  if (B < 0 || T < 0 || mask_words < 0 || max_new < 0 || !kv16(dtype) || !(scale == scale) ||
+      scale - scale != 0.0f)
+    return TERN_ERR_INVALID_ARG;
+  const tern_status ok = cache8_ok(cache);
+  if (ok != TERN_OK) return ok;
+  if (Hq < 1 || Hq % cache->heads != 0 || B > 65536 || max_new > 256 || mask_words > 4 ||
+      !table_ok(table_stride, table_width, cache->page_size) ||
+      T >= (int64_t(1) << 34) / (Hq * cache->dim))
+    return TERN_ERR_SHAPE;
+  if (B == 0 || T == 0 || max_new == 0) return TERN_OK;
+  if (q == nullptr || ctx_len == nullptr || row_start == nullptr || out == nullptr ||
+      (table_width > 0 && table == nullptr) || (mask != nullptr && mask_words == 0))
+    return TERN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !stride_ok(q_token_stride) || !stride_ok(q_head_stride))
+    return TERN_ERR_ALIGN;
+  if (ws == nullptr ||
+      ws_bytes < tree_attention8_workspace_bytes(max_new, Hq, cache->heads, cache->dim))
+    return TERN_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TERN_ERR_ALIGN;
+  if (!device_supported()) return TERN_ERR_UNSUPPORTED;
+  const TreeAttn8Call call{q, q_token_stride, q_head_stride, dtype, *cache, table, table_stride,
+                           table_width, ctx_len, row_start, mask, mask_words, B, T, Hq, max_new,
+                           scale, out, lse, ws};
+  return from_cuda(launch_tree_attention8(call, static_cast<cudaStream_t>(stream)));
 }
 
 tern_status tern_sample(const void* logits, int64_t row_stride, int64_t rows, int64_t vocab,

@@ -10,7 +10,7 @@ output linear, over the C entry points of the same names:
 * ``kv_commit``: the accepted path of each tree made contiguous, all layers.
 
 The cache holds 16-bit values (``KVCache``) or 8-bit codes with a unit for
-each row (``KVCache8``, ``kv_read``).  ``rotate_write`` writes rows as
+each row (``KVCache8``, ``kv_read``); the same calls take both.  ``rotate_write`` writes rows as
 ``kv_write`` does, with the norms of queries and keys and their rotary
 positions in the same pass.
 
@@ -66,7 +66,7 @@ def _native():
             return [ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names]
         module.bind(*at(*names), torch.int32, torch.int64, torch.float32,
                     torch._C._cuda_getDevice if _several_devices() else None)
-        module.bind8(*at("tern_kv_rotate_write", "tern_kv8_read", "tern_kv8_commit"))
+        module.bind8(*at("tern_kv_rotate_write", "tern_kv8_read", "tern_kv8_commit", "tern_tree_attention8"))
         module.bind_tokens(*at("tern_sample", "tern_tree_accept"))
         _calls = module
     return _calls
@@ -84,7 +84,9 @@ def _failed(name: str, status: int):
 
 
 @functools.lru_cache(maxsize=None)
-def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int, index: int) -> int:
+def _workspace_bytes(max_new: int, hq: int, heads: int, dim: int, index: int, eight: bool) -> int:
+    if eight:
+        return B.tern_tree_attention8_workspace_bytes(max_new, hq, heads, dim)
     return B.tern_tree_attention_workspace_bytes(max_new, hq, heads, dim)
 
 
@@ -329,7 +331,7 @@ def kv_read(cache: KVCache8, slots: torch.Tensor, dtype=torch.bfloat16, k: torch
     return k, v
 
 
-def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len: torch.Tensor,
+def tree_attention(q: torch.Tensor, cache: KVCache | KVCache8, table: torch.Tensor, ctx_len: torch.Tensor,
                    row_start: torch.Tensor, max_new: int, mask: torch.Tensor | None = None,
                    scale: float | None = None, out: torch.Tensor | None = None,
                    return_lse: bool = False, lse: torch.Tensor | None = None,
@@ -342,9 +344,15 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
     also the logarithm of each row's sum of exponentials (fp32 [T, query heads]).
     A row that sees nothing is 0, its lse -infinity.  The probabilities are
     rounded to the cache's type for their product with the values; everything
-    else up to the output's own rounding is in 32 bits."""
+    else up to the output's own rounding is in 32 bits.
+
+    Over an 8-bit cache q is bf16 or fp16, and out of its type; codes enter the
+    products as they are, and probabilities times the values' units are rounded
+    to fp16."""
     t, hq, _ = q.shape
-    heads, dim, dtype = cache.heads, cache.dim, cache.dtype
+    heads, dim, eight = cache.heads, cache.dim, isinstance(cache, KVCache8)
+    dtype = q.dtype if eight else cache.dtype
+    _check(dtype in _TYPES, "q: expected bf16 or fp16")
     if stream is not None and (out is None or ws is None or (return_lse and lse is None)):
         with B._on(stream):          # what is allocated here belongs to that stream
             return tree_attention(q, cache, table, ctx_len, row_start, max_new, mask, scale, out,
@@ -353,17 +361,18 @@ def tree_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, ctx_len
         out = torch.empty((t, hq, dim), dtype=dtype, device=cache.device)
     if return_lse and lse is None:
         lse = torch.empty((t, hq), dtype=torch.float32, device=cache.device)
-    need, at, size = _workspace_bytes(max_new, hq, heads, dim, cache.index), 0, 0
+    need, at, size = _workspace_bytes(max_new, hq, heads, dim, cache.index, eight), 0, 0
     if need:      # none: there are no new tokens, or the call below refuses what it gets
         buf = (B.Workspace(cache.device) if ws is None else ws).head(
             need, B.TERN_TREE_ATTENTION_ZERO_BYTES, stream)
         _check(buf.get_device() == cache.index, "ws: expected a workspace on the cache's device")
         at, size = buf.data_ptr(), buf.numel()
-    st = (_calls or _native()).attention(
-        cache.address, dtype, heads, dim, cache.index, q, table, ctx_len, row_start, max_new, mask,
-        dim ** -0.5 if scale is None else scale, out, lse, at, size, B._stream(stream))
+    calls = _calls or _native()
+    args = (cache.address, dtype, heads, dim, cache.index, q, table, ctx_len, row_start, max_new, mask,
+            dim ** -0.5 if scale is None else scale, out, lse, at, size, B._stream(stream))
+    st = calls.attention8(*args, _TYPES[dtype]) if eight else calls.attention(*args)
     if st:
-        _failed("tern_tree_attention", st)
+        _failed("tern_tree_attention8" if eight else "tern_tree_attention", st)
     return (out, lse) if return_lse else out
 
 
