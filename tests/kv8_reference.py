@@ -14,9 +14,11 @@ def quantise(x, kind):
     nan = torch.isnan(x).any(-1, keepdim=True)
     whole = torch.isfinite(most) & ~nan
     some = whole & (most >= 2.0 ** -100)
-    y = torch.where(some, x * (LARGEST[kind] / torch.where(some, most, torch.ones(()))), torch.zeros(()))
+    # (a number divided by a tensor is a product with its reciprocal, two roundings)
+    largest = torch.full_like(most, LARGEST[kind])
+    y = torch.where(some, x * (largest / torch.where(some, most, torch.ones(()))), torch.zeros(()))
     codes = y.round().to(torch.int8) if kind == torch.int8 else y.to(kind)
-    unit = torch.where(some, most / LARGEST[kind], torch.where(whole, torch.zeros(()), torch.full((), math.nan)))
+    unit = torch.where(some, most / largest, torch.where(whole, torch.zeros(()), torch.full((), math.nan)))
     return codes, unit[..., 0]
 
 

@@ -91,14 +91,14 @@ def check(rng, ctx, new, page, heads, group, dim, dtype, kind, masks=None, scale
     B.tern_check()
     ref, rl, weight = R.attention(q.double().numpy(), k, v, table, page, ctx, new, seen, scale)
     keys = max(c + n for c, n in zip(ctx, new))
-    units = cache.v_scale[cache.v_scale == cache.v_scale]
+    units = cache.v_scale[torch.isfinite(cache.v_scale)]
     ob, lb = bounds(q.double().numpy(), k, dim, keys, scale, dtype, ref, weight, rl,
                     float(units.max()) if units.numel() else 0.0, LARGEST[kind])
     got, gl = out[:t].double().cpu().numpy(), lse[:t].double().cpu().numpy()
     assert np.array_equal(np.isinf(gl), np.isinf(rl))
     assert (np.abs(got - ref) <= ob).all(), float((np.abs(got - ref) / ob).max())
     fin = np.isfinite(rl)
-    assert (np.abs(gl - rl)[fin] <= lb[fin]).all()
+    assert (np.abs(gl[fin] - rl[fin]) <= lb[fin]).all()
     assert (got[~fin] == 0).all()
     assert (out[t:].view(torch.uint8) == 0xFF).all() and (lse[t:].view(torch.uint8) == 0xFF).all()
     return out[:t], lse[:t]

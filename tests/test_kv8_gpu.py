@@ -85,7 +85,7 @@ def test_write_and_read(rows, page, heads, dim, heads_first, dtype, kind):
         for g, codes, units in zip(got, want[:2], want[2:]):
             inside = (slots >= 0) & (slots < pages * page)
             at = np.where(inside, slots, 0)
-            ref = codes.view(kind)[at // page, at % page].float() * units[at // page, :, at % page][..., None]
+            ref = codes[at // page, at % page].view(kind).float() * units[at // page, :, at % page][..., None]
             ref[~inside] = 0
             assert torch.equal(g.cpu(), ref.to(out))
 
@@ -181,7 +181,7 @@ def test_rotate_write(rows, hq, heads, dim, rot, axes, neighbours, norm, dtype, 
         return
     # a code is off by half a step: of int8 1/2, of e4m3 2^-4 of itself and 2^-10 at least; and the unit and
     # the value as the rotation rounds them
-    codes = c.k.view(torch.int8).view(kind).cpu()[at, r].double()
+    codes = c.k.view(torch.int8).cpu()[at, r].view(kind).double()
     units = c.k_scale.cpu()[at, :, r].double()[..., None]
     most = ref[inside].abs().amax(-1, keepdim=True)
     assert ((units * R.LARGEST[kind] - most).abs() <= bound[inside].amax(-1, keepdim=True) + most * 2.0 ** -22).all()
