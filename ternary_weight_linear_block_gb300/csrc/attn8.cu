@@ -75,14 +75,14 @@ struct Rows8 {
   static constexpr int CODES = TK * D;
   static constexpr int UNITS = TK * 4;
   static constexpr int STAGE = 2 * CODES;                 // keys, values
-  static constexpr int CTAS = D == 256 && NT > 1 ? 1 : 2;
+  static constexpr int CTAS = D == 256 ? (NT > 1 ? 1 : 2) : NT == 1 ? 3 : 2;
   static constexpr int IC = D == 64 || NT > 1 ? 4 : 8;    // value tiles that are joined at a time
   static constexpr int COLS = 16 * IC;
   static constexpr int LD = COLS + 4;
   static constexpr int MERGE = 2 * RT * LD * 4;
   static constexpr int QLD = D * 2 + 16;
   static constexpr int QBYTES = RT * QLD;
-  static constexpr int ROOM = (CTAS == 2 ? 115200 : 232448) - MERGE - QBYTES - 1024 - 2048;
+  static constexpr int ROOM = (CTAS == 3 ? 76800 : CTAS == 2 ? 115200 : 232448) - MERGE - QBYTES - 1024 - 2048;
   static constexpr int FIT = ROOM / (STAGE + 2 * UNITS);
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
   static constexpr size_t SMEM = size_t(STAGES) * (STAGE + 2 * UNITS) + MERGE + QBYTES + 1024;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
     uint32_t phase = 0, q_phase = 1;
     long issued = 0, q_issued = 0;
     bool ok = true;
-    const int box_shift = min(a.page_shift, 6);      // rows of a box: a page, or the tile
+    const int box_shift = min(a.page_shift, TK == 128 ? 7 : 6);      // rows of a box: a page, or the tile
     const auto give_up = [&](bool good) {
       if (!good && lane == 0 && !*abort_flag) fail(abort_flag, ERR_PRODUCER);
       return good;
@@ -363,9 +363,12 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
       if (k0 < s.len || k0 == 0) {     // else past the last token: nothing to add
         const float* un = units + st * 2 * TK + warp * 16 + row_b;
         const float ku[2] = {un[0], un[8]}, vu[2] = {un[TK], un[TK + 8]};
-        float c[NT][4];
+        // two sums, of alternate steps: an MMA waits for the one before in its own
+        float c[NT][4], c2[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[n][e] = c2[n][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < KS; k += 2) {
           uint32_t x[4], f[2][4];
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
             widen<KIND>(x[2 * e], f[e][0], f[e][2]);
             widen<KIND>(x[2 * e + 1], f[e][1], f[e][3]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<false>(c[n], f[e], qf[k + e][n][0], qf[k + e][n][1]);
+            for (int n = 0; n < NT; ++n) mma16816<false>(e ? c2[n] : c[n], f[e], qf[k + e][n][0], qf[k + e][n][1]);
           }
         }
         // c[n]: keys lane / 4 and + 8, rows row_c and + 1
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            c[n][e] *= ku[e >> 1] * row_scale[n][e & 1];
+            c[n][e] = (c[n][e] + c2[n][e]) * (ku[e >> 1] * row_scale[n][e & 1]);
             hid[n][e] = edge && !((vis[n][e & 1] >> (row_b + (e >> 1) * 8)) & 1);
             if (hid[n][e]) c[n][e] = -INFINITY;
           }
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
     for (int i0 = 0; i0 < KS; i0 += IC) {
       if (i0 > 0) ptx::named_sync(1, NW * 32);
 #pragma unroll 1
-      for (int round = 0; round < 2; ++round) {
+      for (int round = 0; round < NW / 2; ++round) {
         if ((warp >> 1) == round) {
 #pragma unroll
           for (int i = 0; i < IC; ++i)
@@ -630,7 +633,7 @@ cudaError_t launch_kind8(const TreeAttn8Call& call, const Args8& g, cudaStream_t
 
 size_t tree_attention8_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
   const int nt = eights_of(max_new, Hq / H);
-  return ws_layout(std::min(kv_sm_count() * 2, MAX_GRID), 8 * nt, D).bytes;
+  return ws_layout(std::min(kv_sm_count() * 3, MAX_GRID), 8 * nt, D).bytes;
 }
 
 cudaError_t launch_tree_attention8(const TreeAttn8Call& call, cudaStream_t st) {

@@ -94,6 +94,23 @@ struct RotArgs {
   float eps;
 };
 
+// The largest magnitude of a lane's 8 elements, as bits of a float: of 32-bit
+// values, and of 16-bit ones as they were read (their bits compare likewise).
+__device__ __forceinline__ uint32_t top_of(const float (&x)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return top;
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t top_of(const uint4& w) {
+  const uint32_t m = 0x7FFF7FFFu;
+  const uint32_t top = __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+  const uint16_t one = static_cast<uint16_t>(max(top & 0xFFFFu, top >> 16));
+  if constexpr (BF16) return static_cast<uint32_t>(one) << 16;
+  else return __float_as_uint(__half2float(*reinterpret_cast<const __half*>(&one)));
+}
+
 template <int LPH>
 __device__ __forceinline__ float sum_over(float x) {
 #pragma unroll
@@ -101,13 +118,11 @@ __device__ __forceinline__ float sum_over(float x) {
   return x;
 }
 
-// The 8 codes of a lane and the row's unit.  The magnitudes' bits compare as
-// the magnitudes do, infinities and NaN above all others.
+// The 8 codes of a lane and the row's unit, from the lane's largest magnitude.
+// The magnitudes' bits compare as the magnitudes do, infinities and NaN above
+// all others.
 template <int KIND, int LPH>
-__device__ __forceinline__ uint2 quantise(const float (&x)[8], float& unit) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+__device__ __forceinline__ uint2 quantise(const float (&x)[8], uint32_t top, float& unit) {
 #pragma unroll
   for (int d = LPH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
   const float most = __uint_as_float(top);
@@ -136,8 +151,9 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[8], float& unit) {
   return some ? make_uint2(w[0], w[1]) : make_uint2(0, 0);
 }
 
-template <bool BF16, int D, int KIND>
-__global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_constant__ RotArgs a) {
+// TURN: queries, norms or a rotation; without them the rows are only written.
+template <bool BF16, int D, int KIND, bool TURN>
+__global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(const __grid_constant__ RotArgs a) {
   constexpr int LPH = D / 8, HPW = 32 / LPH;
   const int lane = threadIdx.x & 31;
   const int sub = lane % LPH, part = lane / LPH;
@@ -170,7 +186,7 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
 
 #pragma unroll 1
   for (int u = 0; u < n; ++u) {
-    const int kind = i < a.uq ? 0 : i < a.uq + a.uk ? 1 : 2;      // queries, keys, values
+    const int kind = TURN && i < a.uq ? 0 : i < a.uq + a.uk ? 1 : 2;      // queries, keys, values
     const int h0 = (kind == 0 ? i : kind == 1 ? i - a.uq : i - a.uq - a.uk) * (UNROLL * HPW);
     const int heads = kind == 0 ? a.Hq : a.H;
     const uint16_t* src = kind == 0 ? a.q + t * a.q_token : kind == 1 ? a.k + t * a.k_token
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
       const int64_t row = known ? slot & ((int64_t(1) << a.page_shift) - 1) : 0;
       to = page * a.page_stride + row * a.token_stride;
       to_scale = page * a.scale_page + row;
-      if (turned && kind != 2) {
+      if (TURN && turned && kind != 2) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (a.neighbours && (j & 1)) {
@@ -214,7 +230,7 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
         }
       }
     }
-    const void* norm = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+    const void* norm = !TURN || kind == 2 ? nullptr : kind == 0 ? a.q_norm : a.k_norm;
     if (norm != nullptr && wt_of != kind) {
       wt_of = kind;
       if (a.norm_f32) {
@@ -244,7 +260,7 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wt[j];
       }
-      if (a.rot > 0 && kind != 2) {
+      if (TURN && a.rot > 0 && kind != 2) {
         float y[8];
         if (a.neighbours) {
 #pragma unroll
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
               pack8<BF16>(x);
       } else {
         float unit;
-        const uint2 c = quantise<KIND, LPH>(x, unit);
+        const uint2 c = quantise<KIND, LPH>(x, TURN && kind == 1 ? top_of(x) : top_of<BF16>(in[s]), unit);
         if (known && h < heads) {
           *reinterpret_cast<uint2*>((kind == 1 ? a.ck : a.cv) + to + h * a.head_stride + e0) = c;
           if (sub == 0) (kind == 1 ? a.ks : a.vs)[to_scale + h * a.scale_head] = unit;
@@ -457,9 +473,13 @@ int log2_of(int64_t v) {
 template <bool BF16, int D>
 cudaError_t launch_rotate_dim(int kind, const RotArgs& a, unsigned blocks, cudaStream_t st) {
   const dim3 g(blocks), b(ROT_THREADS);
-  if (kind == SAME) return launch(rotate_kernel<BF16, D, SAME>, g, b, 0, st, a);
-  if (kind == I8) return launch(rotate_kernel<BF16, D, I8>, g, b, 0, st, a);
-  return launch(rotate_kernel<BF16, D, E4M3>, g, b, 0, st, a);
+  const bool turn = a.Hq > 0 || a.rot > 0 || a.k_norm != nullptr;
+  if (kind == SAME) return launch(rotate_kernel<BF16, D, SAME, true>, g, b, 0, st, a);
+  if (kind == I8)
+    return turn ? launch(rotate_kernel<BF16, D, I8, true>, g, b, 0, st, a)
+                : launch(rotate_kernel<BF16, D, I8, false>, g, b, 0, st, a);
+  return turn ? launch(rotate_kernel<BF16, D, E4M3, true>, g, b, 0, st, a)
+              : launch(rotate_kernel<BF16, D, E4M3, false>, g, b, 0, st, a);
 }
 
 template <bool BF16>

@@ -28,7 +28,8 @@ namespace {
 //     and the drawn one is found in their running sum.
 //  3. Otherwise the border is searched by histograms of counts and weights
 //     (narrow), in steps of the logit and then of its bits until a single
-//     logit is left.  The draw is a pass over the row: every warp sums the kept
+//     logit is left; of bf16 logits, which have few values, by one histogram of
+//     counts (Places).  The draw is a pass over the row: every warp sums the kept
 //     weights of its own stretch, and the one where the sum passes u times the
 //     whole looks for the token.
 //
@@ -162,51 +163,91 @@ struct Elt {
   static constexpr bool EXACT = DT != TERN_LOGITS_F32;
 };
 
-template <int DT>
-__device__ __forceinline__ float element(const uint8_t* row, int64_t i) {
-  if constexpr (DT == TERN_LOGITS_F32) {
-    return __ldg(reinterpret_cast<const float*>(row) + i);
-  } else {
-    const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(row) + i);
-    if constexpr (DT == TERN_LOGITS_BF16) return __uint_as_float(uint32_t(w) << 16);
-    else return __half2float(*reinterpret_cast<const __half*>(&w));
-  }
-}
-
 // A row in slots of 16 aligned bytes; its first element is element `off` of slot 0.
 struct Row {
   const uint8_t* at;
   int off, vocab;
 };
 
-// Elements of a slot; NaN, and what is not the row's, as -infinity.
+// A slot as it is; what is not the row's is -infinity.
 template <int DT>
-__device__ __forceinline__ void load_slot(const Row& r, int slot, float (&x)[Elt<DT>::E]) {
+__device__ __forceinline__ uint4 load_slot(const Row& r, int slot) {
   constexpr int E = Elt<DT>::E;
   const int i0 = slot * E - r.off;
-  if (i0 >= 0 && i0 + E <= r.vocab) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(r.at + int64_t(i0) * Elt<DT>::BYTES));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if (i0 >= 0 && i0 + E <= r.vocab)
+    return __ldg(reinterpret_cast<const uint4*>(r.at + int64_t(i0) * Elt<DT>::BYTES));
+  uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT == TERN_LOGITS_F32) {
-        x[i] = __uint_as_float(u[i]);
-      } else if constexpr (DT == TERN_LOGITS_BF16) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == TERN_LOGITS_F32) {
+      u[i] = i0 + i >= 0 && i0 + i < r.vocab ? __ldg(reinterpret_cast<const uint32_t*>(r.at) + i0 + i) : 0xFF800000u;
+    } else {
+      u[i] = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int at = i0 + 2 * i + h;
+        const uint32_t w = at >= 0 && at < r.vocab ? __ldg(reinterpret_cast<const uint16_t*>(r.at) + at)
+                                                   : DT == TERN_LOGITS_BF16 ? 0xFF80u : 0xFC00u;
+        u[i] |= w << (16 * h);
       }
     }
-  } else {
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// f(slot, w) for slots first, first + step, .. below end; four reads are on their
+// way together (one at a time kept a pass at 20 bytes a ns and SM, half of what
+// memory gives).
+template <int DT, class F>
+__device__ __forceinline__ void for_slots(const Row& r, int first, int end, int step, const F& f) {
+  constexpr int U = 4;
+  for (int at = first; at < end; at += U * step) {
+    uint4 w[U];
 #pragma unroll
-    for (int i = 0; i < E; ++i)
-      x[i] = i0 + i >= 0 && i0 + i < r.vocab ? element<DT>(r.at, i0 + i) : -INFINITY;
+    for (int j = 0; j < U; ++j)
+      if (at + j * step < end) w[j] = load_slot<DT>(r, at + j * step);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (at + j * step < end) f(at + j * step, w[j]);
+  }
+  __syncwarp();
+}
+
+// Its elements, NaN as -infinity.
+template <int DT>
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[Elt<DT>::E]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == TERN_LOGITS_F32) {
+      x[i] = __uint_as_float(u[i]);
+    } else if constexpr (DT == TERN_LOGITS_BF16) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = fmaxf(x[i], -INFINITY);
+  for (int i = 0; i < Elt<DT>::E; ++i) x[i] = fmaxf(x[i], -INFINITY);
+}
+
+// The largest of them (16-bit ones compared two at a time); NaN only where all are.
+template <int DT>
+__device__ __forceinline__ float largest(const uint4& w) {
+  if constexpr (DT == TERN_LOGITS_F32) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else if constexpr (DT == TERN_LOGITS_BF16) {
+    const __nv_bfloat162* v = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const float2 f = __bfloat1622float2(__hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3])));
+    return fmaxf(f.x, f.y);
+  } else {
+    const __half2* v = reinterpret_cast<const __half2*>(&w);
+    const float2 f = __half22float2(__hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3])));
+    return fmaxf(f.x, f.y);
+  }
 }
 
 template <int CL>
@@ -303,6 +344,27 @@ __device__ __noinline__ uint32_t lowest_key(uint32_t lo, uint32_t hi, float most
   return lo;
 }
 
+// bf16 logits have few values: a place for each of magnitude 2^-14 to 2^7 in
+// their order, from the largest down, and one in the middle for all that are
+// smaller.  Weights are then looked up, and a histogram of the places says all
+// that a border needs, unless it is in the middle.
+struct Places {
+  static constexpr int HALF = 2688, LOW = 0x3880;      // 2^-14 as the upper 16 bits
+  static constexpr int COUNT = 2 * HALF + 1;
+  static constexpr float MOST = 128.f;
+  uint64_t weight[COUNT + 7];
+  uint32_t count[COUNT + 7];
+  static __device__ __forceinline__ int of(float x) {
+    const uint32_t b = __float_as_uint(x);
+    const int mag = max(static_cast<int>((b >> 16) & 0x7FFFu) - (LOW - 1), 0);
+    return HALF + (static_cast<int>(b) < 0 ? mag : -mag);
+  }
+  static __device__ __forceinline__ float value(int place) {     // (not of the middle)
+    const uint32_t mag = static_cast<uint32_t>(abs(place - HALF) + (LOW - 1));
+    return __uint_as_float((mag << 16) | (place > HALF ? 0x80000000u : 0u));
+  }
+};
+
 template <int DT, int CL>
 struct Sampler {
   static constexpr int E = Elt<DT>::E;
@@ -342,9 +404,11 @@ struct Sampler {
       __syncthreads();
       int w0, w1;
       stretch(w0, w1);
-      for (int at = w0 + lane; at < w1; at += 32) {
+      const float floor = of_key(lo);
+      for_slots<DT>(row, w0 + lane, w1, 32, [&](int, const uint4& w) {
+        if (!(largest<DT>(w) >= floor)) return;
         float x[E];
-        load_slot<DT>(row, at, x);
+        unpack<DT>(w, x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const uint32_t key = key_of(x[e]);
@@ -356,7 +420,7 @@ struct Sampler {
                         static_cast<unsigned long long>(weigh.template at<EXACT>(x[e])));
           }
         }
-      }
+      });
       sync_all<CL>();
       if (rank == 0) {
         constexpr int PER = BINS / NT;
@@ -437,116 +501,146 @@ struct Sampler {
     }
   }
 
-  // The token of the tokens from logit `key` on, of that logit itself the
-  // first `ties`, at u of their weight.
-  __device__ void draw(uint32_t key, uint32_t ties, float u, int32_t* token) {
-    const float last = of_key(key);
-    const uint64_t each = weigh.template at<EXACT>(last);
-    int w0, w1;
-    stretch(w0, w1);
+  // This warp's weight above `last` and its tokens of that logit, in slots [w0, w1).
+  template <class Weight>
+  __device__ __forceinline__ void add_up(int w0, int w1, float last, const Weight& weight) {
     uint64_t mass = 0;
-    uint32_t mine = 0;
-    for (int at = w0 + lane; at < w1; at += 32) {
+    uint32_t ties = 0;
+    for_slots<DT>(row, w0 + lane, w1, 32, [&](int, const uint4& w) {
+      if (!(largest<DT>(w) >= last)) return;
       float x[E];
-      load_slot<DT>(row, at, x);
+      unpack<DT>(w, x);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (x[e] > last) mass += weigh.template at<EXACT>(x[e]);
-        mine += x[e] == last ? 1 : 0;
+        if (x[e] > last) mass += weight(x[e]);
+        ties += x[e] == last ? 1 : 0;
       }
-    }
-    __syncwarp();
+    });
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       mass += __shfl_xor_sync(~0u, mass, d);
-      mine += __shfl_xor_sync(~0u, mine, d);
+      ties += __shfl_xor_sync(~0u, ties, d);
     }
     if (lane == 0) {
       s.warp_mass[warp] = mass;
-      s.warp_ties[warp] = mine;
+      s.warp_ties[warp] = ties;
     }
-    sync_all<CL>();
-    // every warp finds what stands before its own stretch, and the whole
-    uint64_t before = 0, all = 0;
-    uint32_t ties_before = 0, ties_all = 0;
-    const int self = rank * WARPS + warp;
-    for (int base = 0; base < CL * WARPS; base += 32) {
-      const int w = base + lane;
-      uint64_t m = 0;
-      uint32_t t = 0;
-      if (w < CL * WARPS) {
-        const Shared& o = *in_cta<CL>(&s, w / WARPS);
-        m = o.warp_mass[w % WARPS];
-        t = o.warp_ties[w % WARPS];
-      }
-      uint64_t mb = w < self ? m : 0;
-      uint32_t tb = w < self ? t : 0;
+  }
+
+  // Of N warps' sums, where with what is before the kept weight passes `at`; what
+  // is before becomes what is before that warp.  For every warp alike.
+  template <int N>
+  __device__ __forceinline__ int passes(const uint64_t (&m)[(N + 31) / 32], const uint32_t (&t)[(N + 31) / 32],
+                                        uint64_t each, uint32_t ties, uint64_t at, uint64_t& mass_before,
+                                        uint32_t& ties_before) const {
+    int found = -1;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        m += __shfl_xor_sync(~0u, m, d);
-        t += __shfl_xor_sync(~0u, t, d);
-        mb += __shfl_xor_sync(~0u, mb, d);
-        tb += __shfl_xor_sync(~0u, tb, d);
-      }
-      all += m;
-      ties_all += t;
-      before += mb;
-      ties_before += tb;
-    }
-    all += each * min(ties, ties_all);
-    before += each * min(ties, ties_before);
-    bool more;
-    const uint64_t at_u = part_of(all, u, more);
-    const uint64_t own = mass + each * (min(ties, ties_before + mine) - min(ties, ties_before));
-    if (before <= at_u && at_u < before + own) {
-      for (int at = w0; at < w1; at += 32) {
-        float x[E];
+    for (int i = 0; i < (N + 31) / 32; ++i) {
+      uint64_t up = m[i];
+      uint32_t t_up = t[i];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = -INFINITY;
-        if (at + lane < w1) load_slot<DT>(row, at + lane, x);
-        uint64_t m = 0;
-        uint32_t t = 0;
-#pragma unroll
-        for (int e = 0; e < E; ++e) t += at + lane < w1 && x[e] == last ? 1 : 0;
-        uint32_t t_up = t;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t y = __shfl_up_sync(~0u, t_up, d);
-          if (lane >= d) t_up += y;
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t y = __shfl_up_sync(~0u, up, d);
+        const uint32_t z = __shfl_up_sync(~0u, t_up, d);
+        if (lane >= d) {
+          up += y;
+          t_up += z;
         }
-        const uint32_t seen = ties_before + t_up - t;        // ties before this lane's
-        uint32_t k = seen;
+      }
+      const uint32_t past =
+          __ballot_sync(~0u, mass_before + up + each * min(ties, ties_before + t_up) > at);
+      const int l = past != 0 ? __ffs(past) - 1 : 31;
+      const uint64_t here = __shfl_sync(~0u, past != 0 ? up - m[i] : up, l);
+      const uint32_t t_here = __shfl_sync(~0u, past != 0 ? t_up - t[i] : t_up, l);
+      if (found < 0) {
+        mass_before += here;
+        ties_before += t_here;
+        if (past != 0) found = i * 32 + l;
+      }
+    }
+    return found;
+  }
+
+  // The token of the tokens from logit `key` on, of that logit itself the
+  // first `ties`, at u of their weight.  The warps add up their stretches; the
+  // CTA that has the one where the sum passes divides it among its warps once
+  // more, and the warp where it passes then looks at 32 slots at a time.
+  template <class Weight>
+  __device__ void draw(uint32_t key, uint32_t ties, float u, int32_t* token, const Weight& weight) {
+    const float last = of_key(key);
+    const uint64_t each = weight(last);
+    int w0, w1;
+    stretch(w0, w1);
+    add_up(w0, w1, last, weight);
+    sync_all<CL>();
+    constexpr int N = CL * WARPS, PER = (N + 31) / 32;
+    uint64_t m[PER], all = 0;
+    uint32_t t[PER], ties_all = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int w = i * 32 + lane;
+      m[i] = t[i] = 0;
+      if (w < N) {
+        const Shared& o = *in_cta<CL>(&s, w / WARPS);
+        m[i] = o.warp_mass[w % WARPS];
+        t[i] = o.warp_ties[w % WARPS];
+      }
+      all += m[i];
+      ties_all += t[i];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      all += __shfl_xor_sync(~0u, all, d);
+      ties_all += __shfl_xor_sync(~0u, ties_all, d);
+    }
+    bool more;
+    const uint64_t at_u = part_of(all + each * min(ties, ties_all), u, more);
+    uint64_t before = 0;
+    uint32_t ties_before = 0;
+    const int owner = passes<N>(m, t, each, ties, at_u, before, ties_before);
+    sync_all<CL>();                     // every CTA has read the sums
+    if (owner < 0 || owner / WARPS != static_cast<int>(rank)) return;
+    const int per_warp = (end - begin + WARPS * 32 - 1) / (WARPS * 32) * 32;
+    w0 = min(begin + owner % WARPS * per_warp, end);
+    w1 = min(w0 + per_warp, end);
+    const int part = (w1 - w0 + WARPS - 1) / WARPS;
+    const int p0 = min(w0 + warp * part, w1), p1 = min(p0 + part, w1);
+    add_up(p0, p1, last, weight);
+    __syncthreads();
+    uint64_t mm[1] = {lane < WARPS ? s.warp_mass[lane] : 0};
+    uint32_t tt[1] = {lane < WARPS ? s.warp_ties[lane] : 0};
+    if (passes<WARPS>(mm, tt, each, ties, at_u, before, ties_before) != warp) return;
+    for (int at = p0; at < p1; at += 32) {
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = -INFINITY;
+      const bool in = at + lane < p1;
+      if (in) unpack<DT>(load_slot<DT>(row, at + lane), x);
+      uint64_t mass[1] = {0};
+      uint32_t of_last[1] = {0};
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (x[e] > last) mass[0] += weight(x[e]);
+        of_last[0] += in && x[e] == last ? 1 : 0;
+      }
+      const int l = passes<32>(mass, of_last, each, ties, at_u, before, ties_before);
+      if (l < 0) continue;
+      if (lane == l) {
+        int hit = -1;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          if (x[e] > last) m += weigh.template at<EXACT>(x[e]);
-          else if (x[e] == last && k++ < ties) m += each;
+          if (x[e] > last) before += weight(x[e]);
+          else if (in && x[e] == last) ++ties_before;
+          if (hit < 0 && before + each * min(ties, ties_before) > at_u) hit = e;
         }
-        uint64_t up = m;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint64_t y = __shfl_up_sync(~0u, up, d);
-          if (lane >= d) up += y;
-        }
-        const uint32_t past = __ballot_sync(~0u, before + up > at_u);
-        if (past != 0) {
-          if (lane == __ffs(past) - 1) {
-            uint64_t sum = before + up - m;
-            k = seen;
-            int hit = -1;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              if (x[e] > last) sum += weigh.template at<EXACT>(x[e]);
-              else if (x[e] == last && k++ < ties) sum += each;
-              if (hit < 0 && sum > at_u) hit = e;
-            }
-            *token = (at + lane) * E - row.off + hit;
-          }
-          break;
-        }
-        before += __shfl_sync(~0u, up, 31);
-        ties_before += __shfl_sync(~0u, t_up, 31);
+        *token = (at + lane) * E - row.off + hit;
       }
+      return;
     }
+  }
+
+  __device__ void draw(uint32_t key, uint32_t ties, float u, int32_t* token) {
+    draw(key, ties, u, token, [this](float x) { return weigh.template at<EXACT>(x); });
   }
 
   // The list: the n tokens from some logit on; `all`: no others count.  Whether
@@ -595,11 +689,112 @@ struct Sampler {
   }
 };
 
+// The border by places: bf16 logits below 128 of which those above `cut` count.
+// false: it is among the values of the middle place.  Every thread has the result.
+template <int CL>
+__device__ bool places_border(Shared& s, Places& t, const Row& row, const Weigh& weigh, int begin, int end,
+                              uint32_t rank, float cut, int k, float p, Border& b) {
+  constexpr int DT = TERN_LOGITS_BF16, E = Elt<DT>::E;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t middle = 0;
+  for_slots<DT>(row, begin + tid, end, NT, [&](int, const uint4& w) {
+    if (!(largest<DT>(w) >= cut)) return;
+    float x[E];
+    unpack<DT>(w, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (x[e] >= cut) {
+        const int place = Places::of(x[e]);
+        atomicAdd(&t.count[place], 1u);
+        if (place == Places::HALF) middle += weigh.at<true>(x[e]);
+      }
+    }
+  });
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) middle += __shfl_xor_sync(~0u, middle, d);
+  if (lane == 0) s.warp_mass[warp] = middle;
+  sync_all<CL>();
+  if (rank == 0) {
+    constexpr int PER = (Places::COUNT + NT - 1) / NT;
+    const int first = tid * PER;
+    uint32_t cnt[PER];
+    uint64_t c = 0, m = 0, all_c, all_m, mid = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      cnt[i] = 0;
+      if (first + i < Places::COUNT)
+        for (int r = 0; r < CL; ++r) cnt[i] += in_cta<CL>(t.count, r)[first + i];
+      if (first + i == Places::HALF)
+        for (int r = 0; r < CL; ++r)
+          for (int w = 0; w < WARPS; ++w) mid += in_cta<CL>(s.warp_mass, r)[w];
+      c += cnt[i];
+    }
+    const auto mass = [&](int i) {
+      return first + i == Places::HALF ? mid : first + i < Places::COUNT ? cnt[i] * t.weight[first + i] : uint64_t(0);
+    };
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m += mass(i);
+    if (tid == 0) s.found = 0;
+    scan_cta(s, c, m, all_c, all_m);
+    // top-k: the place where the count reaches it, and the weight of what it leaves
+    if (tid == 0) s.all_mass = all_m;
+    __syncthreads();
+    uint64_t acc = c, acc_m = m;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (k > 0 && acc < k && acc + cnt[i] >= k) {
+        const uint32_t ties = static_cast<uint32_t>(k - acc);
+        s.found = first + i == Places::HALF ? -1 : 1;
+        s.hi = first + i;
+        s.in_bin = ties;
+        if (first + i != Places::HALF) s.all_mass = acc_m + ties * t.weight[first + i];
+      }
+      acc += cnt[i];
+      acc_m += mass(i);
+    }
+    __syncthreads();
+    const int found = s.found;
+    const uint32_t k_place = s.hi, k_ties = s.in_bin;
+    __syncthreads();
+    if (p < 1.f && found >= 0) {
+      const uint64_t want = goal_of(s.all_mass, p);
+      acc_m = m;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const uint64_t here = mass(i);
+        if (acc_m < want && acc_m + here >= want) {
+          const int place = first + i;
+          s.found = place == Places::HALF ? -1 : 1;
+          const uint64_t each = max(t.weight[place], uint64_t(1));
+          uint32_t ties = static_cast<uint32_t>(min((want - acc_m + each - 1) / each, static_cast<uint64_t>(cnt[i])));
+          if (found == 1 && k_place == place) ties = min(ties, k_ties);
+          s.lo = place;
+          s.above = ties;
+        }
+        acc_m += here;
+      }
+    } else if (tid == 0) {
+      s.lo = k_place;
+      s.above = k_ties;
+    }
+  }
+  sync_all<CL>();
+  const Shared& from = *in_cta<CL>(&s, 0);
+  const int found = from.found;
+  b.found = found > 0;
+  b.key = key_of(found > 0 ? Places::value(from.lo) : cut);
+  b.ties = found > 0 ? from.above : ~0u;
+  sync_all<CL>();
+  return found >= 0;
+}
+
 template <int DT, int CL>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int E = Elt<DT>::E;
   constexpr bool EXACT = Elt<DT>::EXACT;
   __shared__ Shared s;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  Places& places = *reinterpret_cast<Places*>(dynamic);      // bf16
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = CL == 1 ? 0 : ptx::cluster_ctarank();
   const int64_t r = blockIdx.x / CL;
@@ -640,13 +835,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
 
   // the largest
   float mine = -INFINITY;
-  for (int at = begin + tid; at < end; at += NT) {
-    float x[E];
-    load_slot<DT>(row, at, x);
-#pragma unroll
-    for (int e = 0; e < E; ++e) mine = fmaxf(mine, x[e]);
-  }
-  __syncwarp();
+  for_slots<DT>(row, begin + tid, end, NT, [&](int, const uint4& w) { mine = fmaxf(mine, largest<DT>(w)); });
   float most = mine;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
@@ -677,6 +866,28 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
   const double low = static_cast<double>(most) + s.span;
   const float cut = fminf(low == low ? __double2float_ru(low) : most, most);
   const uint32_t cut_key = key_of(cut);
+  const int aim = max(k, 160);
+  const bool list = aim <= 384;
+  // a bf16 row whose survivors may be many: by places
+  if constexpr (DT == TERN_LOGITS_BF16) {
+    if (most < Places::MOST && cut > -Places::MOST && !(k > 0 && list)) {
+      for (int i = tid; i < Places::COUNT; i += NT) {
+        const float x = Places::value(i);
+        places.weight[i] = i != Places::HALF && x <= most && x >= cut ? weigh.at<true>(x) : 0;
+        places.count[i] = 0;
+      }
+      __syncthreads();
+      Border b{cut_key, ~0u, 0, 0, false};
+      if ((k == 0 && p >= 1.f) || places_border<CL>(s, places, row, weigh, begin, end, rank, cut, k, p, b)) {
+        sampler.draw(b.key, b.ties, u, a.token + r, [&](float x) {
+          const int place = Places::of(x);
+          return place == Places::HALF ? weigh.at<true>(x) : places.weight[place];
+        });
+        if constexpr (CL > 1) sync_all<CL>();
+        return;
+      }
+    }
+  }
   if (k == 0 && p >= 1.f) {
     sampler.draw(cut_key, ~0u, u, a.token + r);
     if constexpr (CL > 1) sync_all<CL>();
@@ -684,10 +895,8 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
   }
 
   // a bound that `aim` of the threads' largest reach
-  const int aim = max(k, 160);
   uint32_t bound = cut_key;
   const float step = (BINS - 1) / (most - cut);
-  const bool list = aim <= 384;
   if (list && most - cut < INFINITY && step < INFINITY) {
     if (mine >= cut) atomicAdd(&s.count[linear_bin(mine, most, step)], 1u);
     sync_all<CL>();
@@ -719,9 +928,10 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
     const float from = of_key(bound);
     uint64_t mass = 0;
     Shared& first = *in_cta<CL>(&s, 0);
-    for (int at = begin + tid; at < end; at += NT) {
+    for_slots<DT>(row, begin + tid, end, NT, [&](int at, const uint4& w) {
+      if (!(largest<DT>(w) >= (sums ? cut : from))) return;
       float x[E];
-      load_slot<DT>(row, at, x);
+      unpack<DT>(w, x);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         if (sums && x[e] >= cut) mass += weigh.template at<EXACT>(x[e]);
@@ -731,8 +941,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
           if (i < NT) first.list[i] = static_cast<uint64_t>(key_of(x[e])) << 32 | ~static_cast<uint32_t>(index);
         }
       }
-    }
-    __syncwarp();
+    });
     if (sums) {
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) mass += __shfl_xor_sync(~0u, mass, d);
@@ -843,9 +1052,16 @@ __global__ void __launch_bounds__(ACCEPT_THREADS) accept_kernel(const __grid_con
 
 template <int DT, int CL>
 cudaError_t launch_sample_cl(const SampleArgs& a, int64_t rows, cudaStream_t st) {
+  constexpr size_t smem = DT == TERN_LOGITS_BF16 ? sizeof(Places) : 0;
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(sample_kernel<DT, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(smem));
+  });
+  if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(rows * CL));
-  if constexpr (CL == 1) return launch(sample_kernel<DT, 1>, grid, dim3(NT), 0, st, a);
-  else return launch_cluster(sample_kernel<DT, CL>, grid, dim3(NT), 0, st, CL, a);
+  if constexpr (CL == 1) return launch(sample_kernel<DT, 1>, grid, dim3(NT), smem, st, a);
+  else return launch_cluster(sample_kernel<DT, CL>, grid, dim3(NT), smem, st, CL, a);
 }
 
 template <int DT>
