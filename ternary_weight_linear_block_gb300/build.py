@@ -23,7 +23,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtern.so")
 EXT = os.path.join(PKG, "_kvcall.so")
 SOURCES = ["tern_abi.cu", "fwht.cu", "pack.cu", "gemv.cu", "gemm.cu", "noalloc.cu", "kv.cu",
-           "kv8.cu", "attn.cu", "attn8.cu", "sample.cu"]
+           "kv8.cu", "attn.cu", "attn8.cu",
+           "attn8_tile.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -12,12 +12,12 @@
 // t_j + log2 vu_j (less kLift's 7), not of t_j: p_j vu_j <= 2^7 when m is set.
 // l and lse do not depend on which reference was taken.
 //
-// Work division, the ring of tiles and the join of pieces are those of
-// attn_rows_kernel; a tile of a stage has the codes as their pages hold them,
+// attn8_rows_kernel: up to 16 rows an item.  Work division, the ring of tiles and
+// the join of pieces are those of attn_rows_kernel; a tile of a stage has the codes as their pages hold them,
 // and 4 bytes a key for its unit.
 #include <algorithm>
 
-#include "attn_dev.cuh"
+#include "attn8_dev.cuh"
 
 namespace tern {
 
@@ -27,37 +27,9 @@ namespace {
 
 using namespace attn;
 
-enum Kind { I8 = 1, E4M3 = 2 };
-
-struct Args8 {
-  Args a;
-  const float* ku;
-  const float* vu;
-  int64_t unit_page, unit_head;
-};
-
 __device__ __forceinline__ void fail(volatile int* abort_flag, unsigned int code) {
   *abort_flag = 1;
   atomicOr(&g_attn8_error, code);
-}
-
-// Four codes to two pairs of fp16: (0, 1) and (2, 3).
-template <int KIND>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (KIND == I8) {
-    // 1024 + (code + 128) has the byte in its last bits
-    w ^= 0x80808080u;
-    const __half2 bias = __half2half2(__ushort_as_half(0x6480));     // 1152
-    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\n"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-  }
 }
 
 // NT eights of rows an item, NW warps that share a tile's keys, 16 each.
@@ -88,12 +60,6 @@ struct Rows8 {
   static constexpr size_t SMEM = size_t(STAGES) * (STAGE + 2 * UNITS) + MERGE + QBYTES + 1024;
   static_assert(STAGES >= 2, "ring");
 };
-
-// Where 16-byte chunk c of row r of a tile's part is (the copies' swizzle).
-template <int ROWB>
-__device__ __forceinline__ int chunk_at(int r, int c) {
-  return ROWB == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-}
 
 template <bool BF16, int KIND, int D, int NT>
 __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
@@ -567,29 +533,14 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
 
 // ------------------------------------------------------------------ host
 
-constexpr int MAX_GRID = TERN_TREE_ATTENTION_ZERO_BYTES / (3 * sizeof(int));
-
-// The cache as [pages][heads][rows][dim]: boxes of `rows` rows of one page and
-// head, up to 128 codes wide (swizzled).
-bool make_map8(CUtensorMap* map, const tern_kv_cache8& c, void* base, int rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
-                              static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride),
-                                 static_cast<cuuint64_t>(c.head_stride),
-                                 static_cast<cuuint64_t>(c.page_stride)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(std::min<int64_t>(c.dim, 128)),
-                             static_cast<cuuint32_t>(rows), 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE,
-             c.dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// Eights of rows an item of the rows kernel for requests of up to `max_new` tokens,
+// 0: the tile kernel (which takes whole tokens, so a group above 128 heads is
+// not its).
+int eights_of(int64_t max_new, int64_t group, int64_t D) {
+  const int64_t rows = max_new * group;
+  if (rows <= 8) return 1;
+  return (rows <= 16 && D < 256) || group > 128 ? 2 : 0;
 }
-
-// Eights of rows an item for requests of up to `rows` rows on a key head.
-int eights_of(int64_t max_new, int64_t group) { return max_new * group <= 8 ? 1 : 2; }
 
 template <bool BF16, int KIND, int D, int NT>
 cudaError_t launch_rows8(const TreeAttn8Call& call, Args8 g, cudaStream_t st) {
@@ -601,7 +552,7 @@ cudaError_t launch_rows8(const TreeAttn8Call& call, Args8 g, cudaStream_t st) {
                                 static_cast<int>(C::SMEM));
   });
   if (e != cudaSuccess) return e;
-  const int grid = std::min(kv_sm_count() * C::CTAS, MAX_GRID);
+  const int grid = std::min(kv_sm_count() * C::CTAS, MAX_GRID8);
   const int box = static_cast<int>(std::min<int64_t>(call.cache.page_size, C::TK));
   CUtensorMap tk, tv;
   if (!make_map8(&tk, call.cache, call.cache.k, box) || !make_map8(&tv, call.cache, call.cache.v, box))
@@ -618,8 +569,8 @@ cudaError_t launch_rows8(const TreeAttn8Call& call, Args8 g, cudaStream_t st) {
 
 template <bool BF16, int KIND, int D>
 cudaError_t launch_dim8(const TreeAttn8Call& call, const Args8& g, cudaStream_t st) {
-  return eights_of(call.max_new, g.a.group) == 1 ? launch_rows8<BF16, KIND, D, 1>(call, g, st)
-                                                 : launch_rows8<BF16, KIND, D, 2>(call, g, st);
+  return eights_of(call.max_new, g.a.group, D) == 1 ? launch_rows8<BF16, KIND, D, 1>(call, g, st)
+                                                    : launch_rows8<BF16, KIND, D, 2>(call, g, st);
 }
 
 template <bool BF16, int KIND>
@@ -632,8 +583,9 @@ cudaError_t launch_kind8(const TreeAttn8Call& call, const Args8& g, cudaStream_t
 }  // namespace
 
 size_t tree_attention8_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D) {
-  const int nt = eights_of(max_new, Hq / H);
-  return ws_layout(std::min(kv_sm_count() * 3, MAX_GRID), 8 * nt, D).bytes;
+  const int nt = eights_of(max_new, Hq / H, D);
+  if (nt == 0) return ws_layout(std::min(kv_sm_count(), MAX_GRID8), 128, D).bytes;
+  return ws_layout(std::min(kv_sm_count() * 3, MAX_GRID8), 8 * nt, D).bytes;
 }
 
 cudaError_t launch_tree_attention8(const TreeAttn8Call& call, cudaStream_t st) {
@@ -670,16 +622,23 @@ cudaError_t launch_tree_attention8(const TreeAttn8Call& call, cudaStream_t st) {
   g.vu = c.v_scale;
   g.unit_page = c.scale_page_stride;
   g.unit_head = c.scale_head_stride;
+  if (eights_of(call.max_new, a.group, c.dim) == 0) return launch_attn8_tile(call, g, st);
   if (call.dtype == TERN_KV_BF16)
     return c.dtype == TERN_KV_I8 ? launch_kind8<true, I8>(call, g, st) : launch_kind8<true, E4M3>(call, g, st);
   return c.dtype == TERN_KV_I8 ? launch_kind8<false, I8>(call, g, st) : launch_kind8<false, E4M3>(call, g, st);
 }
 
 cudaError_t attn8_read_clear_error(unsigned int* err) {
-  cudaError_t e = cudaMemcpyFromSymbol(err, g_attn8_error, sizeof(unsigned int));
-  if (e != cudaSuccess || *err == 0) return e;
-  const unsigned int zero = 0;
-  return cudaMemcpyToSymbol(g_attn8_error, &zero, sizeof(unsigned int));
+  unsigned int tile = 0;
+  cudaError_t e = attn8_tile_read_clear_error(&tile);
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(err, g_attn8_error, sizeof(unsigned int));
+  if (e != cudaSuccess) return e;
+  if (*err != 0) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_attn8_error, &zero, sizeof(unsigned int));
+  }
+  *err |= tile;
+  return e;
 }
 
 }  // namespace tern

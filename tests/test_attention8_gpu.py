@@ -205,6 +205,14 @@ def test_long_context_of_few_heads():
     check(np.random.default_rng(10), [9000], [1], 16, 1, 4, 256, BF, I8)
 
 
+@pytest.mark.parametrize("dim,page,kind,dtype", [(128, 32, I8, BF), (64, 16, E4, HF), (256, 64, I8, HF),
+                                                 (128, 256, E4, BF)])
+def test_many_tiles_of_many_rows(dim, page, kind, dtype):
+    """Every ring of the tile kernel goes round many times, over several items."""
+    check(np.random.default_rng(dim), [3001, 640, 5], [5, 12, 3], page, 2, 6, dim, dtype, kind)
+    check(np.random.default_rng(dim + 1), [9000], [30], page, 1, 1, dim, dtype, kind)
+
+
 def test_same_result_each_time_and_on_streams():
     rng = np.random.default_rng(11)
     cache, k, v, table, q, starts = make(rng, [3000, 20, 700], [3, 1, 2], 16, 2, 4, 128, BF, I8)
