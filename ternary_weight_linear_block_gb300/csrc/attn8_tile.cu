@@ -4,11 +4,19 @@
 // The SHARED kernel of the 16-bit cache (attn.cu) with a stage more: tiles of
 // codes arrive in a ring of their own, and four warps turn them into fp16 tiles,
 // exactly, as the MMAs want them.  They also turn bf16 queries into fp16 by a
-// power of two for each row.  Units stay out of the products: a score column is
-// multiplied by its key's unit, a probability column by its value's, both in
-// 32 bits as the softmax reads a row.  m is the maximum of t_j + log2 vu_j less
-// kLift's 7, so that what is rounded to fp16, p_j vu_j, has its bits whatever
-// the units are, and moves only when it grows by more than 2^8.
+// power of two for each row.  A score column is multiplied by its key's unit in 32
+// bits as the softmax reads a row.  The values' units:
+//   folded  a tile of cached tokens whose units are within 2^10 of each other:
+//           code * unit / 2^E goes to the fp16 tile (one rounding, as
+//           relatively small as that of the probabilities, which then take 2^E),
+//           E the largest unit's exponent, so the softmax has nothing to read
+//   exact   a tile with new tokens (which a row may not see), or with units far
+//           apart: probabilities are multiplied by the unit in 32 bits
+// The reference m of a row's exponents is the largest t_j + log2 vu_j of the tile
+// that set it.  A folded tile first takes a bound of its own: the largest score
+// times the largest (or, below zero, the least) unit, one pass over the scores
+// alone.  Only where fp16 could not hold what the bound allows, and in exact
+// tiles, is the maximum itself looked for.
 #include <algorithm>
 
 #include "attn8_dev.cuh"
@@ -22,8 +30,8 @@ namespace {
 
 using namespace attn;
 
-// a producer, MMA, queries (and a warp without work); two warpgroups of softmax;
-// four warps that widen codes
+// a warp each for copies, MMAs, queries and units; two warpgroups of softmax; four
+// warps that widen codes
 constexpr int THREADS = 512;
 
 template <int D>
@@ -41,7 +49,7 @@ struct Tile8 {
   static constexpr size_t SMEM = size_t(SLOTS) * SLOT + size_t(RAWS) * RAW + QB + 1024;
   static constexpr int AHEAD = 2;                         // tiles that S runs ahead
   static constexpr int NS = 3;                            // buffers of S
-  static constexpr int NU = 6;                            // tiles' units that are held
+  static constexpr int NU = 4;                            // tiles' units that are held (even)
   static constexpr uint32_t S_COL = 0, O_COL = D < 256 ? 384 : 256;
   static_assert(SMEM + 18 * 1024 <= 232448, "shared memory");
 };
@@ -51,12 +59,41 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, unsigned int code
   atomicOr(&g_attn8_tile_error, code);
 }
 
+// What a row's exponents refer to is the largest t_j + log2 vu_j less kRef, when it
+// is set; it moves when that grows by more than 2^8.  Below 2^15, which a bound
+// has to say for a tile, fp16 holds what is rounded to it.
+constexpr float kRef = 3.f, kMove = 8.f, kTop = 15.f;
+
+// The units of a tile: the largest and least of the keys, and of the values (of
+// those that are not 0).
+struct TileUnits {
+  float k_most, k_least, v_most;
+  int e;             // exponent of v_most
+  bool fold;         // the values' units are within 2^10 of each other, or 0
+};
+__device__ __forceinline__ TileUnits tile_units(const float4& q) {
+  TileUnits u;
+  u.k_most = q.x;
+  u.k_least = q.y;
+  u.v_most = q.z;
+  u.fold = q.z == 0.f || (q.z >= 0x1p-100f && q.z <= 1024.f * q.w);
+  u.e = q.z == 0.f ? 0 : (__float_as_int(q.z) >> 23) - 127;
+  return u;
+}
+
 __device__ __forceinline__ float2 mul2(float2 x, float2 y) {
   float2 d;
   asm("mul.rn.f32x2 %0, %1, %2;"
       : "=l"(reinterpret_cast<uint64_t&>(d))
       : "l"(reinterpret_cast<uint64_t&>(x)), "l"(reinterpret_cast<uint64_t&>(y)));
   return d;
+}
+
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+      "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+      : "memory");
 }
 
 template <bool BF16, int KIND, int D>
@@ -79,6 +116,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   // its phase is awaited); a tile's maximum known
   __shared__ uint64_t o_step[2], m_ready[4];
   __shared__ __align__(16) float s_ku[NU][TKT], s_vu[NU][TKT], s_lu[NU][TKT];   // units, log2 of the values'
+  __shared__ __align__(16) uint2 s_fold[NU][TKT];  // folded tiles: a value's unit over 2^E in two fp16 parts
+  __shared__ __align__(16) float4 s_range[NU];     // units: largest and least of keys, of values
   __shared__ float s_scale[4][128];      // of four items' rows: S may run three items ahead
   __shared__ float s_m[128];
   __shared__ PieceScratch<THREADS> scratch;
@@ -99,7 +138,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int s = 0; s < NU; ++s) {
       ptx::mbar_init(&u_full[s], 1);
-      ptx::mbar_init(&u_ready[s], 4);
+      ptx::mbar_init(&u_ready[s], 1);
       ptx::mbar_init(&u_empty[s], 4);
     }
     ptx::mbar_init(&q_full, 1);
@@ -315,6 +354,52 @@ __global__ void __launch_bounds__(THREADS, 1)
                          s.r.row0 + s.rt * tokens);
     }
     if (!ptx::mbar_wait_bounded(&q_full, parity, WAIT_LIMIT)) atomicOr(&g_attn8_tile_error, ERR_DRAIN);
+  } else if (warp == 3) {
+    // ---------------- units: what the softmax and the widening of values take of
+    // them
+    bool ok = true;
+    uint32_t tile0 = 0;
+    constexpr int EACH = TKT / 32;
+    while (ok && walk.next(s)) {
+      const int cnt = s.t1 - s.t0;
+      for (int i = 0; i < cnt; ++i) {
+        const uint32_t us = (tile0 + i) % NU;
+        ok = ptx::mbar_wait_warp(&u_full[us], ((tile0 + i) / NU) & 1u, abort_flag, WAIT_LIMIT);
+        if (!ok) {
+          if (lane == 0 && !*abort_flag) fail(abort_flag, ERR_CONSUMER);
+          break;
+        }
+        float4 q = make_float4(0.f, INFINITY, 0.f, INFINITY);
+        float vu[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+          const float ku = s_ku[us][e * 32 + lane];
+          vu[e] = s_vu[us][e * 32 + lane];
+          s_lu[us][e * 32 + lane] = __log2f(fmaxf(vu[e], 0x1p-100f));
+          q = make_float4(fmaxf(q.x, ku), fminf(q.y, ku), fmaxf(q.z, vu[e]), fminf(q.w, vu[e] == 0.f ? INFINITY : vu[e]));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+          q.x = fmaxf(q.x, __shfl_xor_sync(~0u, q.x, d));
+          q.y = fminf(q.y, __shfl_xor_sync(~0u, q.y, d));
+          q.z = fmaxf(q.z, __shfl_xor_sync(~0u, q.z, d));
+          q.w = fminf(q.w, __shfl_xor_sync(~0u, q.w, d));
+        }
+        if (lane == 0) s_range[us] = q;
+        const float by = __int_as_float(max(127 - tile_units(q).e, 1) << 23);
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+          const float f = vu[e] * by;
+          const __half hi = __float2half_rn(f), lo = __float2half_rn(f - __half2float(hi));
+          const __half2 h2 = __half2half2(hi), l2 = __half2half2(lo);
+          s_fold[us][e * 32 + lane] =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&l2));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&u_ready[us]);
+      }
+      tile0 += cnt;
+    }
   } else if (warp >= 12) {
     // ---------------- codes to fp16, in the ring's order: 128 threads
     const int t = tid - 384;
@@ -365,39 +450,77 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool key = ik < cnt && k_place<C::AHEAD>(ik) == static_cast<uint32_t>(n);
         const int i = key ? ik++ : iv++;
         const uint32_t nn = seq0 + n, sl = nn % SLOTS, rs = nn % RAWS;
-        if (key) {
-          const uint32_t us = (tile0 + i) % NU;
-          wait(&u_full[us], ((tile0 + i) / NU) & 1u);
-          if (!ok) break;
-          if (t < TKT) s_lu[us][t] = __log2f(fmaxf(s_vu[us][t], 0x1p-100f));
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&u_ready[us]);
-        }
+        const uint32_t us = (tile0 + i) % NU;
+        if (!key) wait(&u_ready[us], ((tile0 + i) / NU) & 1u);
         wait(&raw_full[rs], (nn / RAWS) & 1u);
         wait(&empty[sl], ((nn / SLOTS) & 1u) ^ 1u);
         if (!ok) break;
-        const uint8_t* from = codes + rs * C::RAW;
-        uint8_t* to = ring + sl * C::SLOT;
+        // a thread has the same 16-code chunk of every 128 / CH-th row, so that all
+        // its places are constants apart.  A chunk becomes two 8-value chunks of
+        // a 64-column part; where two lanes of eight would meet in a bank, one
+        // takes its halves the other way round.
+        constexpr int CH = D / 16, STEP = 128 / CH, ROWS = TKT / STEP;
+        const int c = t % CH, r0 = t / CH;
+        const bool turn = D >= 128 && (c & 4) != 0;
+        const uint8_t* from = codes + rs * C::RAW + (c >> 3) * (TKT * C::ROWB) + chunk_at<C::ROWB>(r0, c & 7);
+        uint8_t* row = ring + sl * C::SLOT + (c >> 2) * HB + r0 * 128;
+        uint8_t* to0 = row + ((((c & 3) * 2 + (turn ? 1 : 0)) ^ (r0 & 7)) << 4);
+        uint8_t* to1 = row + ((((c & 3) * 2 + (turn ? 0 : 1)) ^ (r0 & 7)) << 4);
         const int k0 = (s.t0 + i) * TKT;
-        constexpr int CH = D / 16;            // 16-code chunks of a row
-#pragma unroll 4
-        for (int p = 0; p < TKT * CH / 128; ++p) {
-          const int id = p * 128 + t, r = id / CH, c = id % CH;
-          uint4 w = *reinterpret_cast<const uint4*>(from + (c >> 3) * (TKT * C::ROWB) + chunk_at<C::ROWB>(r, c & 7));
-          // values past the last token count as zero
-          if (!key && k0 + r >= s.r.len) w = make_uint4(0, 0, 0, 0);
-          uint4 lo, hi;
-          widen<KIND>(w.x, lo.x, lo.y);
-          widen<KIND>(w.y, lo.z, lo.w);
-          widen<KIND>(w.z, hi.x, hi.y);
-          widen<KIND>(w.w, hi.z, hi.w);
-          // two 8-value chunks of a 64-column part; four lanes store the second
-          // first, so that eight lanes fill all banks
-          uint8_t* row = to + (c >> 2) * HB + r * 128;
-          const int c0 = (c & 3) * 2, x = r & 7;
-          const bool swap = D >= 128 && (c & 4) != 0;
-          *reinterpret_cast<uint4*>(row + (((c0 + (swap ? 1 : 0)) ^ x) << 4)) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(row + (((c0 + (swap ? 0 : 1)) ^ x) << 4)) = swap ? lo : hi;
+        const bool fold = !key && k0 <= s.r.ctx - TKT && tile_units(s_range[us]).fold;
+        const int keys = key ? TKT : s.r.len - k0;        // values past the last token count as zero
+        const auto turned = [&](uint4 w, uint32_t (&o)[8]) {
+          widen<KIND>(turn ? w.z : w.x, o[0], o[1]);
+          widen<KIND>(turn ? w.w : w.y, o[2], o[3]);
+          widen<KIND>(turn ? w.x : w.z, o[4], o[5]);
+          widen<KIND>(turn ? w.y : w.w, o[6], o[7]);
+        };
+        const auto store = [&](int p, const uint32_t (&o)[8]) {
+          *reinterpret_cast<uint4*>(to0 + p * STEP * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(to1 + p * STEP * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+        };
+        const auto codes_of = [&](int p) { return *reinterpret_cast<const uint4*>(from + p * STEP * C::ROWB); };
+        // (loads ahead of the stores: the compiler does not know that they are apart)
+        constexpr int AT = 4;
+        if (fold) {
+#pragma unroll 1
+          for (int p0 = 0; p0 < ROWS; p0 += AT) {
+            uint4 w[AT];
+            uint2 f[AT];
+#pragma unroll
+            for (int p = 0; p < AT; ++p) {
+              w[p] = codes_of(p0 + p);
+              f[p] = s_fold[us][r0 + (p0 + p) * STEP];
+            }
+#pragma unroll
+            for (int p = 0; p < AT; ++p) {
+              uint32_t o[8];
+              turned(w[p], o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = ptx::fma_f16x2(o[e], f[p].x, ptx::mul_f16x2(o[e], f[p].y));
+              store(p0 + p, o);
+            }
+          }
+        } else if (keys >= TKT) {
+#pragma unroll 1
+          for (int p0 = 0; p0 < ROWS; p0 += AT) {
+            uint4 w[AT];
+#pragma unroll
+            for (int p = 0; p < AT; ++p) w[p] = codes_of(p0 + p);
+#pragma unroll
+            for (int p = 0; p < AT; ++p) {
+              uint32_t o[8];
+              turned(w[p], o);
+              store(p0 + p, o);
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int p = 0; p < ROWS; ++p) {
+            uint32_t o[8];
+            turned(r0 + p * STEP < keys ? codes_of(p) : make_uint4(0, 0, 0, 0), o);
+            store(p, o);
+          }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -457,45 +580,65 @@ __global__ void __launch_bounds__(THREADS, 1)
         wait(&s_full[buf], ((tile0 + i) / NS) & 1u);
         if (!ok) break;
         if (active) {
-          constexpr int NC = TKT / 32;       // a row of S is read twice, 32 columns at a time
+          // a row of S is read twice, 16 columns at a time with the next on their
+          // way (32 at a time spilled registers)
+          constexpr int NC = TKT / 16;
           const float rs = scale * s_scale[item & 3][lrow];
           const float2 rs2 = make_float2(rs, rs);
-          uint32_t v[2][32];
+          uint32_t v[2][16];
+          const TileUnits tu = tile_units(s_range[us]);
+          const bool fold = !edge && tu.fold;
+          // the largest score: the last columns stay for the second pass
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          ptx::tmem_ld_32x32b_x32(s_addr, v[0]);
+          const auto largest = [&](const uint32_t (&x)[16]) {
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            tmem_ld_wait_for(v[c & 1]);
-            if (c + 1 < NC) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (c + 1), v[(c + 1) & 1]);
-            const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][32 * c]);
-            const float4* lu = reinterpret_cast<const float4*>(&s_lu[us][32 * c]);
-            const uint32_t bits = edge ? static_cast<uint32_t>(vis[c >> 1] >> (32 * (c & 1))) : ~0u;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 k4 = ku[e >> 2], l4 = lu[e >> 2];
-              const uint32_t* w = &v[c & 1][e];
-              float2 y = fma2(mul2(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), rs2),
-                              make_float2(k4.x, k4.y), make_float2(l4.x, l4.y));
-              float2 z = fma2(mul2(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), rs2),
-                              make_float2(k4.z, k4.w), make_float2(l4.z, l4.w));
-              if (edge) {
-                if (!((bits >> e) & 1)) y.x = -INFINITY;
-                if (!((bits >> (e + 1)) & 1)) y.y = -INFINITY;
-                if (!((bits >> (e + 2)) & 1)) z.x = -INFINITY;
-                if (!((bits >> (e + 3)) & 1)) z.y = -INFINITY;
-              }
-              mx[(e >> 2) & 1] = fmaxf(mx[(e >> 2) & 1], fmaxf(y.x, y.y));
-              mx[2 + ((e >> 2) & 1)] = fmaxf(mx[2 + ((e >> 2) & 1)], fmaxf(z.x, z.y));
-            }
+            for (int e = 0; e < 16; e += 2)
+              mx[(e >> 1) & 3] = fmaxf(mx[(e >> 1) & 3], fmaxf(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+          };
+          ptx::tmem_ld_32x32b_x16(s_addr, v[0]);
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 2) {
+            tmem_ld_wait_for(v[0]);
+            ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c + 1), v[1]);
+            largest(v[0]);
+            tmem_ld_wait_for(v[1]);
+            if (c + 2 < NC) ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c + 2), v[0]);
+            largest(v[1]);
           }
-          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kLift<false>;
+          const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * rs;
           float mp = -INFINITY;   // the other warpgroup's, of the tile before
           if (i > 0) {
             wait(&m_ready[warp & 3], (tile0 + i - 1) & 1u);
             mp = *reinterpret_cast<volatile float*>(&s_m[lrow]);
           }
+          const float top = (most > 0.f ? most * tu.k_most : most * tu.k_least) + __log2f(fmaxf(tu.v_most, 0x1p-100f));
           float mn = mp;
-          if (mt > mp + 8.f || (mp == -INFINITY && mt != mp)) mn = mt;
+          if (!fold || __any_sync(~0u, !(top <= mp + kTop))) {
+            // the maximum itself, of what the row sees
+            float mt = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < TKT / 16; ++c) {
+              uint32_t x[16];
+              ptx::tmem_ld_32x32b_x16(s_addr + 16 * c, x);
+              tmem_ld_wait_for(x);
+              const uint32_t bits = edge ? static_cast<uint32_t>(vis[TKT == 64 ? 0 : c >> 2] >> (16 * (c & 3))) : ~0u;
+              const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][16 * c]);
+              const float4* lu = reinterpret_cast<const float4*>(&s_lu[us][16 * c]);
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 k4 = ku[e >> 2], l4 = lu[e >> 2];
+                const float y[4] = {fmaf(__uint_as_float(x[e]) * rs, k4.x, l4.x),
+                                    fmaf(__uint_as_float(x[e + 1]) * rs, k4.y, l4.y),
+                                    fmaf(__uint_as_float(x[e + 2]) * rs, k4.z, l4.z),
+                                    fmaf(__uint_as_float(x[e + 3]) * rs, k4.w, l4.w)};
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                  if ((bits >> (e + h)) & 1) mt = fmaxf(mt, y[h]);
+              }
+            }
+            mt -= kRef;
+            if (mt > mp + kMove || (mp == -INFINITY && mt != mp)) mn = mt;
+          }
           *reinterpret_cast<volatile float*>(&s_m[lrow]) = mn;
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&m_ready[warp & 3]);
@@ -518,41 +661,50 @@ __global__ void __launch_bounds__(THREADS, 1)
               tmem_st_x16(o_addr + 16 * c, o);
             }
           }
-          const float ms = m == -INFINITY ? 0.f : m;
+          // folded: what the values were divided by comes with the probabilities
+          const float ms = (m == -INFINITY ? 0.f : m) - (fold ? static_cast<float>(tu.e) : 0.f);
           const float2 ms2 = make_float2(-ms, -ms);
           float2 sum[2] = {};
           // from the last columns, which are there, down: P goes over the upper
           // half of S, behind what is still to be read
+          const auto step = [&](const uint32_t (&x)[16], int c) {
+            const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][16 * c]);
+            const float4* vu = reinterpret_cast<const float4*>(&s_vu[us][16 * c]);
+            uint32_t w[8];
+            const uint32_t bits = edge ? static_cast<uint32_t>(vis[TKT == 64 ? 0 : c >> 2] >> (16 * (c & 3))) : ~0u;
 #pragma unroll
-          for (int c = NC - 1; c >= 0; --c) {
-            if (c < NC - 1) tmem_ld_wait_for(v[c & 1]);
-            if (c > 0) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (c - 1), v[(c - 1) & 1]);
-            const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][32 * c]);
-            const float4* vu = reinterpret_cast<const float4*>(&s_vu[us][32 * c]);
-            const uint32_t bits = edge ? static_cast<uint32_t>(vis[c >> 1] >> (32 * (c & 1))) : ~0u;
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 k4 = ku[e >> 2], v4 = vu[e >> 2];
-              const uint32_t* sc = &v[c & 1][e];
+            for (int e = 0; e < 16; e += 4) {
+              const float4 k4 = ku[e >> 2];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const float2 y = fma2(mul2(make_float2(__uint_as_float(sc[2 * h]), __uint_as_float(sc[2 * h + 1])), rs2),
+                const int j = e + 2 * h;
+                const float2 y = fma2(mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), rs2),
                                       h ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y), ms2);
                 float2 p = make_float2(ex2(y.x), ex2(y.y));
-                float2 pv = mul2(p, h ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y));
-                if (edge) {
-                  if (!((bits >> (e + 2 * h)) & 1)) p.x = pv.x = 0.f;
-                  if (!((bits >> (e + 2 * h + 1)) & 1)) p.y = pv.y = 0.f;
+                float2 pv = p;
+                if (!fold) {
+                  const float2 u = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(vu) + j);
+                  pv = mul2(p, u);
+                  if (!((bits >> j) & 1)) p.x = pv.x = 0.f;
+                  if (!((bits >> (j + 1)) & 1)) p.y = pv.y = 0.f;
                 }
                 sum[h] = add2(sum[h], p);
-                w[(e >> 1) + h] = pack2<false>(pv.x, pv.y);
+                w[j >> 1] = pack2<false>(pv.x, pv.y);
               }
             }
-            tmem_st_x16(s_addr + TKT / 2 + 16 * c, w);
+            tmem_st_x8(s_addr + TKT / 2 + 8 * c, w);
+          };
+#pragma unroll 1
+          for (int c = NC - 1; c > 0; c -= 2) {
+            tmem_ld_wait_for(v[1]);
+            ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c - 1), v[0]);
+            step(v[1], c);
+            tmem_ld_wait_for(v[0]);
+            if (c > 1) ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c - 2), v[1]);
+            step(v[0], c - 1);
           }
           const float2 all = add2(sum[0], sum[1]);
-          l = l * f + (all.x + all.y);
+          l = l * f + (all.x + all.y) * (fold ? ex2(-static_cast<float>(tu.e)) : 1.f);
           ptx::tmem_st_wait();
         } else if (lane == 0) {
           ptx::mbar_arrive(&m_ready[warp & 3]);    // its phases count tiles, whoever is active
@@ -578,11 +730,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float mm = fmaxf(m, y.x);
         l = l * (mm == -INFINITY ? 0.f : ex2(m - mm)) + y.y * (mm == -INFINITY ? 0.f : ex2(y.x - mm));
         m = mm;
-        // pieces and bf16's lse refer to the maximum itself
-        constexpr float kDown = BF16 ? 1.f / 128.f : 1.f;
-        l *= kDown;
-        if (BF16) m += kLift<false>;
-        const float inv = l == 0.f ? 0.f : kDown / l;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = (int64_t(s.r.row0) + tok) * a.Hq + s.h * a.group + (r0 + lrow - tok * a.group);
         // this warpgroup's half of the columns, which refer to the larger maximum already
         constexpr int HALF = D / 2;
@@ -594,7 +742,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tmem_ld_wait_for(u);
           if (!has) continue;
           float o[16];
-          const float fo = whole ? inv : kDown;
+          const float fo = whole ? inv : 1.f;
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(u[e]) * fo;
           const int d = col0 + 16 * c;
