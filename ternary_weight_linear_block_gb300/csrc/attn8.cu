@@ -535,11 +535,21 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
 
 // Eights of rows an item of the rows kernel for requests of up to `max_new` tokens,
 // 0: the tile kernel (which takes whole tokens, so a group above 128 heads is
-// not its).
+// not its).  Items of 16 rows read the keys again for every 16, from L2 for the
+// most part, and are still ahead up to the counts below (rows kernel / tile
+// kernel, us, int8, 8 requests of up to 20003 keys and 32 of up to 1500; 16, 8 and 4
+// key heads of 64, 128 and 256):
+//    64   32 rows 167 / 226 and 69 / 110, 48 rows 259 / 248 and 93 / 116,
+//         64 rows 305 / 228 and 112 / 112
+//   128   24 rows 89 / 111 and 46 / 61, 32 rows 126 / 130 and 59 / 67,
+//         48 rows 188 / 142 and 78 / 70
+//   256   16 rows 77 / 100 and 42 / 53, 24 rows 100 / 97 and 54 / 52
+// Items of 32 rows of head size 64 took 187 and 83 for 32 rows: a loop that no
+// longer fits the instruction cache.
 int eights_of(int64_t max_new, int64_t group, int64_t D) {
   const int64_t rows = max_new * group;
   if (rows <= 8) return 1;
-  return (rows <= 16 && D < 256) || group > 128 ? 2 : 0;
+  return group > 128 || rows <= (D == 64 ? 48 : D == 128 ? 32 : 16) ? 2 : 0;
 }
 
 template <bool BF16, int KIND, int D, int NT>
@@ -569,8 +579,8 @@ cudaError_t launch_rows8(const TreeAttn8Call& call, Args8 g, cudaStream_t st) {
 
 template <bool BF16, int KIND, int D>
 cudaError_t launch_dim8(const TreeAttn8Call& call, const Args8& g, cudaStream_t st) {
-  return eights_of(call.max_new, g.a.group, D) == 1 ? launch_rows8<BF16, KIND, D, 1>(call, g, st)
-                                                    : launch_rows8<BF16, KIND, D, 2>(call, g, st);
+  const int nt = eights_of(call.max_new, g.a.group, D);
+  return nt == 1 ? launch_rows8<BF16, KIND, D, 1>(call, g, st) : launch_rows8<BF16, KIND, D, 2>(call, g, st);
 }
 
 template <bool BF16, int KIND>

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int s = 0; s < NU; ++s) {
       ptx::mbar_init(&u_full[s], 1);
       ptx::mbar_init(&u_ready[s], 1);
-      ptx::mbar_init(&u_empty[s], 4);
+      ptx::mbar_init(&u_empty[s], 8);      // softmax and widening of values
     }
     ptx::mbar_init(&q_full, 1);
     ptx::mbar_init(&q_ready, 4);
@@ -480,46 +480,28 @@ __global__ void __launch_bounds__(THREADS, 1)
           *reinterpret_cast<uint4*>(to1 + p * STEP * 128) = make_uint4(o[4], o[5], o[6], o[7]);
         };
         const auto codes_of = [&](int p) { return *reinterpret_cast<const uint4*>(from + p * STEP * C::ROWB); };
-        // (loads ahead of the stores: the compiler does not know that they are apart)
+        // loads ahead of the stores, as the compiler does not know that they are
+        // apart; one loop for all tiles, so that the kernel's loops fit the
+        // instruction cache
         constexpr int AT = 4;
-        if (fold) {
+        const uint2 one = make_uint2(0x3C003C00u, 0u);
 #pragma unroll 1
-          for (int p0 = 0; p0 < ROWS; p0 += AT) {
-            uint4 w[AT];
-            uint2 f[AT];
+        for (int p0 = 0; p0 < ROWS; p0 += AT) {
+          uint4 w[AT];
+          uint2 f[AT];
 #pragma unroll
-            for (int p = 0; p < AT; ++p) {
-              w[p] = codes_of(p0 + p);
-              f[p] = s_fold[us][r0 + (p0 + p) * STEP];
-            }
-#pragma unroll
-            for (int p = 0; p < AT; ++p) {
-              uint32_t o[8];
-              turned(w[p], o);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = ptx::fma_f16x2(o[e], f[p].x, ptx::mul_f16x2(o[e], f[p].y));
-              store(p0 + p, o);
-            }
+          for (int p = 0; p < AT; ++p) {
+            w[p] = codes_of(p0 + p);
+            f[p] = fold ? s_fold[us][r0 + (p0 + p) * STEP] : one;
+            if (r0 + (p0 + p) * STEP >= keys) w[p] = make_uint4(0, 0, 0, 0);
           }
-        } else if (keys >= TKT) {
-#pragma unroll 1
-          for (int p0 = 0; p0 < ROWS; p0 += AT) {
-            uint4 w[AT];
 #pragma unroll
-            for (int p = 0; p < AT; ++p) w[p] = codes_of(p0 + p);
-#pragma unroll
-            for (int p = 0; p < AT; ++p) {
-              uint32_t o[8];
-              turned(w[p], o);
-              store(p0 + p, o);
-            }
-          }
-        } else {
-#pragma unroll 1
-          for (int p = 0; p < ROWS; ++p) {
+          for (int p = 0; p < AT; ++p) {
             uint32_t o[8];
-            turned(r0 + p * STEP < keys ? codes_of(p) : make_uint4(0, 0, 0, 0), o);
-            store(p, o);
+            turned(w[p], o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = ptx::fma_f16x2(o[e], f[p].x, ptx::mul_f16x2(o[e], f[p].y));
+            store(p0 + p, o);
           }
         }
         ptx::fence_proxy_async_smem();
@@ -527,6 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) {
           ptx::mbar_arrive(&full[sl]);
           ptx::mbar_arrive(&raw_empty[rs]);
+          if (!key) ptx::mbar_arrive(&u_empty[us]);
         }
       }
       seq0 += 2u * cnt;
@@ -667,41 +650,56 @@ __global__ void __launch_bounds__(THREADS, 1)
           float2 sum[2] = {};
           // from the last columns, which are there, down: P goes over the upper
           // half of S, behind what is still to be read
-          const auto step = [&](const uint32_t (&x)[16], int c) {
-            const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][16 * c]);
-            const float4* vu = reinterpret_cast<const float4*>(&s_vu[us][16 * c]);
-            uint32_t w[8];
-            const uint32_t bits = edge ? static_cast<uint32_t>(vis[TKT == 64 ? 0 : c >> 2] >> (16 * (c & 3))) : ~0u;
+          if (fold) {
+            const auto step = [&](const uint32_t (&x)[16], int c) {
+              const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][16 * c]);
+              uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 k4 = ku[e >> 2];
+              for (int e = 0; e < 16; e += 4) {
+                const float4 k4 = ku[e >> 2];
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int j = e + 2 * h;
-                const float2 y = fma2(mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), rs2),
-                                      h ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y), ms2);
-                float2 p = make_float2(ex2(y.x), ex2(y.y));
-                float2 pv = p;
-                if (!fold) {
-                  const float2 u = *reinterpret_cast<const float2*>(reinterpret_cast<const float*>(vu) + j);
-                  pv = mul2(p, u);
-                  if (!((bits >> j) & 1)) p.x = pv.x = 0.f;
-                  if (!((bits >> (j + 1)) & 1)) p.y = pv.y = 0.f;
+                for (int h = 0; h < 2; ++h) {
+                  const int j = e + 2 * h;
+                  const float2 y = fma2(mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), rs2),
+                                        h ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y), ms2);
+                  const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                  sum[h] = add2(sum[h], p);
+                  w[j >> 1] = pack2<false>(p.x, p.y);
                 }
-                sum[h] = add2(sum[h], p);
+              }
+              tmem_st_x8(s_addr + TKT / 2 + 8 * c, w);
+            };
+#pragma unroll 1
+            for (int c = NC - 1; c > 0; c -= 2) {
+              tmem_ld_wait_for(v[1]);
+              ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c - 1), v[0]);
+              step(v[1], c);
+              tmem_ld_wait_for(v[0]);
+              if (c > 1) ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c - 2), v[1]);
+              step(v[0], c - 1);
+            }
+          } else {
+            // (few tiles, so short code rather than reads ahead)
+#pragma unroll 1
+            for (int c = NC - 1; c >= 0; --c) {
+              ptx::tmem_ld_32x32b_x16(s_addr + 16 * c, v[0]);
+              tmem_ld_wait_for(v[0]);
+              const uint32_t bits = edge ? static_cast<uint32_t>(vis[TKT == 64 ? 0 : c >> 2] >> (16 * (c & 3))) : ~0u;
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float2 ku = *reinterpret_cast<const float2*>(&s_ku[us][16 * c + j]);
+                const float2 vu = *reinterpret_cast<const float2*>(&s_vu[us][16 * c + j]);
+                const float2 y = fma2(mul2(make_float2(__uint_as_float(v[0][j]), __uint_as_float(v[0][j + 1])), rs2), ku, ms2);
+                float2 p = make_float2(ex2(y.x), ex2(y.y));
+                float2 pv = mul2(p, vu);
+                if (!((bits >> j) & 1)) p.x = pv.x = 0.f;
+                if (!((bits >> (j + 1)) & 1)) p.y = pv.y = 0.f;
+                sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], p);
                 w[j >> 1] = pack2<false>(pv.x, pv.y);
               }
+              tmem_st_x8(s_addr + TKT / 2 + 8 * c, w);
             }
-            tmem_st_x8(s_addr + TKT / 2 + 8 * c, w);
-          };
-#pragma unroll 1
-          for (int c = NC - 1; c > 0; c -= 2) {
-            tmem_ld_wait_for(v[1]);
-            ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c - 1), v[0]);
-            step(v[1], c);
-            tmem_ld_wait_for(v[0]);
-            if (c > 1) ptx::tmem_ld_32x32b_x16(s_addr + 16 * (c - 2), v[1]);
-            step(v[0], c - 1);
           }
           const float2 all = add2(sum[0], sum[1]);
           l = l * f + (all.x + all.y) * (fold ? ex2(-static_cast<float>(tu.e)) : 1.f);

@@ -210,7 +210,15 @@ def test_long_context_of_few_heads():
 def test_many_tiles_of_many_rows(dim, page, kind, dtype):
     """Every ring of the tile kernel goes round many times, over several items."""
     check(np.random.default_rng(dim), [3001, 640, 5], [5, 12, 3], page, 2, 6, dim, dtype, kind)
-    check(np.random.default_rng(dim + 1), [9000], [30], page, 1, 1, dim, dtype, kind)
+    check(np.random.default_rng(dim + 1), [9000], [70], page, 1, 1, dim, dtype, kind)
+
+
+@pytest.mark.parametrize("dim,group,new", [(64, 4, 15), (64, 1, 60), (128, 4, 9), (256, 2, 10), (64, 8, 8), (64, 2, 9)])
+def test_many_items_of_few_tiles(dim, group, new):
+    """Items of one to four tiles one after another in a CTA: what is held of a tile is held until all have it."""
+    rng = np.random.default_rng(dim + new)
+    ctx = [int(c) for c in rng.integers(0, 400, 24)]
+    check(rng, ctx, [int(n) for n in rng.integers(1, new + 1, 24)], 16, 8, group, dim, BF, I8)
 
 
 def test_same_result_each_time_and_on_streams():
