@@ -6,17 +6,18 @@
 // exactly, as the MMAs want them.  They also turn bf16 queries into fp16 by a
 // power of two for each row.  A score column is multiplied by its key's unit in 32
 // bits as the softmax reads a row.  The values' units:
-//   folded  a tile of cached tokens whose units are within 2^10 of each other:
-//           code * unit / 2^E goes to the fp16 tile (one rounding, as
-//           relatively small as that of the probabilities, which then take 2^E),
-//           E the largest unit's exponent, so the softmax has nothing to read
-//   exact   a tile with new tokens (which a row may not see), or with units far
-//           apart: probabilities are multiplied by the unit in 32 bits
+//   folded  bf16 rows, a tile of cached tokens whose units are within 2^10 of each
+//           other: code * unit / 2^E goes to the fp16 tile (one rounding, as
+//           relatively small as that of the probabilities, which then take 2^E;
+//           beside an fp16 output's it would show), E the largest unit's
+//           exponent, so the softmax has nothing to read
+//   exact   others, and a tile with new tokens (which a row may not see):
+//           probabilities are multiplied by the unit in 32 bits
 // The reference m of a row's exponents is the largest t_j + log2 vu_j of the tile
-// that set it.  A folded tile first takes a bound of its own: the largest score
-// times the largest (or, below zero, the least) unit, one pass over the scores
-// alone.  Only where fp16 could not hold what the bound allows, and in exact
-// tiles, is the maximum itself looked for.
+// that set it.  A tile of cached tokens first takes a bound of its own: the largest
+// score times the largest (or, below zero, the least) key's unit, one pass over
+// the scores alone.  Only where fp16 could not hold what the bound allows, and
+// in tiles with new tokens, is the maximum itself looked for.
 #include <algorithm>
 
 #include "attn8_dev.cuh"
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint8_t* to0 = row + ((((c & 3) * 2 + (turn ? 1 : 0)) ^ (r0 & 7)) << 4);
         uint8_t* to1 = row + ((((c & 3) * 2 + (turn ? 0 : 1)) ^ (r0 & 7)) << 4);
         const int k0 = (s.t0 + i) * TKT;
-        const bool fold = !key && k0 <= s.r.ctx - TKT && tile_units(s_range[us]).fold;
+        const bool fold = BF16 && !key && k0 <= s.r.ctx - TKT && tile_units(s_range[us]).fold;
         const int keys = key ? TKT : s.r.len - k0;        // values past the last token count as zero
         const auto turned = [&](uint4 w, uint32_t (&o)[8]) {
           widen<KIND>(turn ? w.z : w.x, o[0], o[1]);
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float2 rs2 = make_float2(rs, rs);
           uint32_t v[2][16];
           const TileUnits tu = tile_units(s_range[us]);
-          const bool fold = !edge && tu.fold;
+          const bool fold = BF16 && !edge && tu.fold;
           // the largest score: the last columns stay for the second pass
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           const auto largest = [&](const uint32_t (&x)[16]) {
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const float top = (most > 0.f ? most * tu.k_most : most * tu.k_least) + __log2f(fmaxf(tu.v_most, 0x1p-100f));
           float mn = mp;
-          if (!fold || __any_sync(~0u, !(top <= mp + kTop))) {
+          if (edge || __any_sync(~0u, !(top <= mp + kTop))) {
             // the maximum itself, of what the row sees
             float mt = -INFINITY;
 #pragma unroll 1
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           float2 sum[2] = {};
           // from the last columns, which are there, down: P goes over the upper
           // half of S, behind what is still to be read
-          if (fold) {
+          if (BF16 ? fold : !edge) {
             const auto step = [&](const uint32_t (&x)[16], int c) {
               const float4* ku = reinterpret_cast<const float4*>(&s_ku[us][16 * c]);
               uint32_t w[8];
@@ -662,8 +663,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const int j = e + 2 * h;
                   const float2 y = fma2(mul2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), rs2),
                                         h ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y), ms2);
-                  const float2 p = make_float2(ex2(y.x), ex2(y.y));
+                  float2 p = make_float2(ex2(y.x), ex2(y.y));
                   sum[h] = add2(sum[h], p);
+                  if constexpr (!BF16) p = mul2(p, *reinterpret_cast<const float2*>(&s_vu[us][16 * c + j]));
                   w[j >> 1] = pack2<false>(p.x, p.y);
                 }
               }
