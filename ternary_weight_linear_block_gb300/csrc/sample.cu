@@ -1066,11 +1066,25 @@ cudaError_t launch_sample_cl(const SampleArgs& a, int64_t rows, cudaStream_t st)
 
 template <int DT>
 cudaError_t launch_sample_type(const SampleArgs& a, int64_t rows, cudaStream_t st) {
-  // CTAs a row: as many as the GPU has room for, while half of the threads have
-  // a slot of their own
-  const int64_t room = 2 * int64_t(kv_sm_count());
+  // CTAs a row: as many as the GPU holds at once (two an SM), while half of the
+  // threads have a slot of their own. Beyond that, up to `most` an SM in turn,
+  // while each keeps `least` elements: long rows then end together, although
+  // some need more passes than others, but each CTA of a bf16 row also clears and
+  // adds up places. us with the CTAs that the GPU holds, then with this rule
+  // (mixed filters, top_k alone):
+  //   304 x 250007 bf16     222, 93 -> 158, 99      304 x 250007 fp32   668 -> 310
+  //   200 x 128256 bf16     121, 60 ->  85, 67      200 x 128256 fp32   349 -> 196
+  //   152 x 250007 bf16     106, 53 (4 a row: 107, 82)
+  //   152 x  32011 bf16      35, 25 (2 a row: 65, 49)
+  constexpr bool PLACES = DT == TERN_LOGITS_BF16;
+  constexpr int64_t most = PLACES ? 6 : 12, least = PLACES ? 64000 : 16000;
+  const int64_t sms = kv_sm_count();
   int cl = 1;
-  while (cl < MAX_CL && rows * (2 * cl) <= room && a.vocab / Elt<DT>::E / (2 * cl) >= NT / 2) cl *= 2;
+  while (cl < MAX_CL) {
+    const int64_t ctas = rows * (2 * cl), part = a.vocab / (2 * cl);
+    if (!(ctas <= 2 * sms && part / Elt<DT>::E >= NT / 2) && !(ctas <= most * sms && part >= least)) break;
+    cl *= 2;
+  }
   if (cl == 8) return launch_sample_cl<DT, 8>(a, rows, st);
   if (cl == 4) return launch_sample_cl<DT, 4>(a, rows, st);
   if (cl == 2) return launch_sample_cl<DT, 2>(a, rows, st);
