@@ -764,7 +764,9 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
  * probabilities in 32 bits.  The queries and the probabilities times the
  * values' units are rounded to fp16 for their products, relatively to the
  * largest of their row (a bf16 query keeps all its bits unless it is below
- * 2^-28 of its row's largest).  A key that a row does not see has no
+ * 2^-28 of its row's largest).  With many bf16 rows the values times their
+ * units are rounded to fp16 too, where a tile's units are within 2^10 of each
+ * other.  A key that a row does not see has no
  * influence, whatever its unit is; one whose unit is NaN makes every row that
  * sees it NaN. */
 size_t tern_tree_attention8_workspace_bytes(int64_t max_new, int64_t Hq, int64_t H, int64_t D);

@@ -58,6 +58,15 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // keys or values), whose loads are on their way together; a warp takes
 // a.per units in a row.
 //
+// One read and one write of everything, so memory bounds it; with a rotation and a
+// norm nearly as much the shuffles of the sum of squares and of the partners.
+// Measured: 206 us for the rows of 16-bit keys and values that would take 172 at
+// the copy rate (0.84; their reading alone is 94, writing alone 115, a code's row
+// being half as long), 321 for rotated and normalised queries and keys that would
+// take 191 (0.60).  Turning: 3 CTAs an SM and 4 steps a unit; 2 CTAs 353, 4 CTAs
+// with 2 steps 329, 2 with 2 414.  Writing alone: 2 steps 219.  A call of few
+// rows is a launch and two dependent reads, 4 to 5 us.
+//
 // The angle of pair j is position * turns[j] in 64-bit integers, turns of 2^-64:
 // the product wraps where the angle does, so that its top 32 bits are the angle
 // at any position, to 2^-32 of a turn.
@@ -336,6 +345,8 @@ __device__ __forceinline__ void widen4(uint32_t w, float (&x)[4]) {
   }
 }
 
+// code * unit, rounded once.  Memory bounds it: half of the bytes that it writes
+// are read, 16 of codes a thread, for which one unit is enough.
 template <bool BF16, int KIND>
 __global__ void __launch_bounds__(READ_THREADS) read_kernel(const __grid_constant__ ReadArgs a) {
   pdl_wait();
@@ -415,6 +426,10 @@ __device__ __forceinline__ void move_column(V* x, const int64_t* from, const int
   }
 }
 
+// The path moves towards the start of its tokens, so a thread that has a column of
+// bytes of every row may move them in the path's order, four reads ahead of
+// their writes; no thread needs another's.  Three dependent reads (path, table,
+// row) are its time for one step.
 __global__ void __launch_bounds__(MOVE_THREADS) move_kernel(const __grid_constant__ MoveArgs a) {
   // byte offsets of the path's rows: of codes, and of units
   __shared__ int64_t s_from[2][MAX_PATH], s_to[2][MAX_PATH];

@@ -35,6 +35,15 @@ namespace {
 //
 // Weights are whole numbers of 2^-45 of the largest, so sums are exact and in
 // any order the same.
+//
+// A row is read two (few survivors) to five times, from L2 after the first, and every
+// step that a cluster takes together costs it a few us; the vocabulary is too
+// short for either memory (18 us for 250 rows of 250007 in bf16) or arithmetic to
+// bound it.  Those take 142 us with all kinds of filters (689 with the search by
+// histograms for all rows, 259 with the list, 207 with places), 93 with top_k
+// alone; 255 and 245 with filters of all kinds in fp32 and fp16, which have no
+// places: their search takes three to five passes.  4 rows of 131072: 15 us, of
+// which the launch of the clusters and 12 joint steps are most.
 
 constexpr int NT = 512;              // threads, and places of the list
 constexpr int WARPS = NT / 32;
@@ -1010,6 +1019,9 @@ struct AcceptArgs {
   int B, width;
 };
 
+// A warp has a request: its lanes look among 32 drafts at a time for the child with
+// the wanted token.  A chain of dependent reads, 2.2 us for one step's requests,
+// launch included (2.8 for 1000).
 __global__ void __launch_bounds__(ACCEPT_THREADS) accept_kernel(const __grid_constant__ AcceptArgs a) {
   pdl_wait();
   pdl_launch_dependents();

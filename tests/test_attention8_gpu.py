@@ -27,12 +27,16 @@ def ints(x, dtype=torch.int32):
 def bounds(q, k, dim, keys, scale, dtype, ref, weight, lse, unit_most, largest):
     """As for the 16-bit cache, with the roundings that differ: probabilities times units to fp16 (2^-11
     relatively, 2^-32 of the row's largest where they have no exponent left, times codes up to `largest`), the
-    score's units and powers of two (8 in all), the queries as they are."""
+    score's units and powers of two (8 in all), the queries as they are.  For bf16 rows the many-row kernel may
+    also round value * unit / 2^E to fp16, unit / 2^E in [2^-10, 2): relatively 2^-11, so that both roundings give
+    (1 + 2^-11)^2 - 1 < 2^-10 (1 + 2^-11), and where it has no exponent left by 2^-25 2^E <= 2^-25 of the largest
+    unit for a row whose probabilities sum to 1."""
     unit, eps = R.UNIT[dtype], 2.0 ** -24
     most = abs(scale) * np.sqrt((q ** 2).sum(-1)).max() * np.sqrt((k ** 2).sum(-1)).max()
     rel = (dim + 10) * eps * most + 2.0 ** -21 + (keys + 8) * eps
-    out = weight * (2.0 ** -11 + 2 * rel) * (1 + 2.0 ** -11) + unit * np.abs(ref) + 2.0 ** -24
-    out = out + keys * 2.0 ** -32 * unit_most * largest
+    folds = dtype is BF
+    out = weight * (2.0 ** (-10 if folds else -11) + 2 * rel) * (1 + 2.0 ** -11) + unit * np.abs(ref) + 2.0 ** -24
+    out = out + (keys * 2.0 ** -32 * largest + folds * 2.0 ** -25) * unit_most
     return out, rel + 4 * eps * np.abs(np.where(np.isfinite(lse), lse, 0)) + 2.0 ** -19
 
 
