@@ -51,21 +51,23 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 
 // ------------------------------------------------------------------ rotate and write
 //
-// A lane has 8 elements of a head (16 bytes), D / 8 lanes a head, so a warp
-// takes 32 / (D / 8) heads at a time; its lanes' places in the head, and with
-// them the cosines and sines of a token, stay the same for all of a token's
-// heads.  A unit is UNROLL such steps of one token and of one kind (queries,
-// keys or values), whose loads are on their way together; a warp takes
-// a.per units in a row.
+// A lane has two chunks of 8 elements of a head (16 bytes each), D / 16 lanes a
+// head, so a warp takes 32 / (D / 16) heads at a time.  The chunks are those whose
+// elements turn together, so a rotation needs no other lane; where rows are only
+// quantised they are neighbours, so their codes are stored as one.  A lane's
+// places in the head, and with them the cosines and sines of a token, stay the
+// same for all of a token's heads.  A unit is UNROLL such steps of one token and
+// of one kind (queries, keys or values), whose loads are on their way together; a
+// warp takes a.per units in a row.
 //
 // One read and one write of everything, so memory bounds it; with a rotation and a
-// norm nearly as much the shuffles of the sum of squares and of the partners.
-// Measured: 206 us for the rows of 16-bit keys and values that would take 172 at
-// the copy rate (0.84; their reading alone is 94, writing alone 115, a code's row
-// being half as long), 321 for rotated and normalised queries and keys that would
-// take 191 (0.60).  Turning: 3 CTAs an SM and 4 steps a unit; 2 CTAs 353, 4 CTAs
-// with 2 steps 329, 2 with 2 414.  Writing alone: 2 steps 219.  A call of few
-// rows is a launch and two dependent reads, 4 to 5 us.
+// norm the instructions of both beside it.  Measured: 185 us for the rows of 16-bit
+// keys and values that would take 172 at the copy rate (0.93), 273 for rotated and
+// normalised queries and keys that would take 191 (0.70); 206 and 321 with one
+// chunk a lane, twice the lanes in a sum and partners from other lanes.  CTAs an
+// SM (turning, writing) and steps: 3, 5 and 2; 4, 6 and 1: 300, 191; 2, 4 and 2: 299,
+// 192; 2, 4 and 3: 286, 194; 2, 3 and 4: 281, 209.  A call of few rows is a launch
+// and two dependent reads, 4 to 5 us.
 //
 // The angle of pair j is position * turns[j] in 64-bit integers, turns of 2^-64:
 // the product wraps where the angle does, so that its top 32 bits are the angle
@@ -74,7 +76,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 // Bound: rows read once and written once.
 
 constexpr int ROT_THREADS = 256;
-constexpr int UNROLL = 4;
+constexpr int UNROLL = 2;
 constexpr float kSmallest = 0x1p-100f;   // rows below are stored as zeros
 
 struct RotArgs {
@@ -127,18 +129,22 @@ __device__ __forceinline__ float sum_over(float x) {
   return x;
 }
 
-// The 8 codes of a lane and the row's unit, from the lane's largest magnitude.
-// The magnitudes' bits compare as the magnitudes do, infinities and NaN above
-// all others.
+// A row's unit and what its elements are multiplied by, from a lane's largest
+// magnitude.  The magnitudes' bits compare as the magnitudes do, infinities and
+// NaN above all others.  0: the row is stored as zeros.
 template <int KIND, int LPH>
-__device__ __forceinline__ uint2 quantise(const float (&x)[8], uint32_t top, float& unit) {
+__device__ __forceinline__ float unit_of(uint32_t top, float& unit) {
 #pragma unroll
   for (int d = LPH / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
   const float most = __uint_as_float(top);
   constexpr float kLargest = KIND == I8 ? 127.f : 448.f;
   const bool whole = top < 0x7F800000u, some = whole && most >= kSmallest;
   unit = some ? __fdiv_rn(most, kLargest) : whole ? 0.f : __uint_as_float(0x7FC00000u);
-  const float f = some ? __fdiv_rn(kLargest, most) : 0.f;
+  return some ? __fdiv_rn(kLargest, most) : 0.f;
+}
+// The codes of 8 elements.
+template <int KIND>
+__device__ __forceinline__ uint2 codes_of(const float (&x)[8], float f) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -157,16 +163,38 @@ __device__ __forceinline__ uint2 quantise(const float (&x)[8], uint32_t top, flo
       w[h] = lo | hi << 16;
     }
   }
-  return some ? make_uint2(w[0], w[1]) : make_uint2(0, 0);
+  return f > 0.f ? make_uint2(w[0], w[1]) : make_uint2(0, 0);
+}
+
+__device__ __forceinline__ void turn_neighbours(float (&x)[8], const float* cs, const float* sn) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float b = x[2 * j];
+    x[2 * j] = b * cs[j] - x[2 * j + 1] * sn[j];
+    x[2 * j + 1] = x[2 * j + 1] * cs[j] + b * sn[j];
+  }
 }
 
 // TURN: queries, norms or a rotation; without them the rows are only written.
 template <bool BF16, int D, int KIND, bool TURN>
 __global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(const __grid_constant__ RotArgs a) {
-  constexpr int LPH = D / 8, HPW = 32 / LPH;
+  constexpr int LPH = D / 16, HPW = 32 / LPH;
   const int lane = threadIdx.x & 31;
   const int sub = lane % LPH, part = lane / LPH;
-  const int e0 = sub * 8;
+  // a lane's two chunks of 8 elements
+  const int pairs = TURN && !a.neighbours ? a.rot / 16 : 0;     // lanes whose chunks turn together
+  const bool together = sub < pairs;
+  int c0 = sub, c1 = sub + LPH;
+  if (!TURN && KIND != SAME) {
+    c0 = 2 * sub;
+    c1 = c0 + 1;
+  } else if (together) {
+    c1 = sub + pairs;
+  } else {
+    c0 = sub + pairs;
+    c1 = c0 + LPH - pairs;
+  }
+  const int e0 = c0 * 8, e1 = c1 * 8;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t w = (int64_t(blockIdx.x) * ROT_THREADS + threadIdx.x) >> 5;
@@ -176,21 +204,11 @@ __global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(con
   const int upt = a.uq + 2 * a.uk;
   int64_t t = first / upt;
   int i = static_cast<int>(first - t * upt);
-  // which lane has the other half of this lane's pairs
-  const int half = a.rot / 2;
-  const bool turned = e0 < a.rot;
-  const bool second = e0 >= half;
-  const int partner = a.neighbours || !turned ? lane : second ? lane - half / 8 : lane + half / 8;
-  float cs[8], sn[8];         // (the sine with the sign of the other half's share)
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    cs[j] = 1.f;
-    sn[j] = 0.f;
-  }
+  float cs[8], sn[8];         // of `together`: of both chunks; of neighbours: four pairs of each
   int64_t at = -1;            // the token that cs, sn and to are of
   int64_t to = 0, to_scale = 0;
   bool known = false;
-  float wt[8];
+  float wt[16];
   int wt_of = -1;             // whose norm wt has
 
 #pragma unroll 1
@@ -201,12 +219,16 @@ __global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(con
     const uint16_t* src = kind == 0 ? a.q + t * a.q_token : kind == 1 ? a.k + t * a.k_token
                                                                      : a.v + t * a.v_token;
     const int64_t head = kind == 0 ? a.q_head : kind == 1 ? a.k_head : a.v_head;
-    uint4 in[UNROLL];
+    uint4 in[UNROLL][2];
 #pragma unroll
     for (int s = 0; s < UNROLL; ++s) {
       const int h = h0 + s * HPW + part;
-      if (h < heads) in[s] = *reinterpret_cast<const uint4*>(src + h * head + e0);
-      else in[s] = make_uint4(0, 0, 0, 0);
+      if (h < heads) {
+        in[s][0] = *reinterpret_cast<const uint4*>(src + h * head + e0);
+        in[s][1] = *reinterpret_cast<const uint4*>(src + h * head + e1);
+      } else {
+        in[s][0] = in[s][1] = make_uint4(0, 0, 0, 0);
+      }
     }
     if (t != at) {
       at = t;
@@ -216,15 +238,11 @@ __global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(con
       const int64_t row = known ? slot & ((int64_t(1) << a.page_shift) - 1) : 0;
       to = page * a.page_stride + row * a.token_stride;
       to_scale = page * a.scale_page + row;
-      if (TURN && turned && kind != 2) {
+      if (TURN && kind != 2 && (together || a.neighbours)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (a.neighbours && (j & 1)) {
-            cs[j] = cs[j - 1];
-            sn[j] = sn[j - 1];
-            continue;
-          }
-          const int f = a.neighbours ? (e0 + j) / 2 : second ? e0 + j - half : e0 + j;
+          const int f = a.neighbours ? (j < 4 ? e0 / 2 + j : e1 / 2 + j - 4) : e0 + j;
+          if (2 * f >= a.rot) continue;
           int ax = a.axis != nullptr ? __ldg(a.axis + f) : 0;
           if (ax < 0 || ax >= a.axes) ax = 0;
           const int32_t p = __ldg(a.positions + ax * a.position_stride + t);
@@ -233,20 +251,21 @@ __global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(con
           const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
           sincospif(x, &sn[j], &cs[j]);
         }
-        if (!a.neighbours && !second) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sn[j] = -sn[j];
-        }
       }
     }
     const void* norm = !TURN || kind == 2 ? nullptr : kind == 0 ? a.q_norm : a.k_norm;
     if (norm != nullptr && wt_of != kind) {
       wt_of = kind;
-      if (a.norm_f32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) wt[j] = __ldg(static_cast<const float*>(norm) + e0 + j);
-      } else {
-        unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(norm) + e0)), wt);
+      for (int c = 0; c < 2; ++c) {
+        const int e = c == 0 ? e0 : e1;
+        float (&y)[8] = *reinterpret_cast<float (*)[8]>(wt + 8 * c);
+        if (a.norm_f32) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = __ldg(static_cast<const float*>(norm) + e + j);
+        } else {
+          unpack8<BF16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(norm) + e)), y);
+        }
       }
     }
 #pragma unroll
@@ -254,50 +273,67 @@ __global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(con
       const int h = h0 + s * HPW + part;
       if (h0 + s * HPW >= heads) break;                     // the same for the whole warp
       if (KIND == SAME && kind == 2) {
-        if (known && h < heads)
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.cv) + to + h * a.head_stride + e0) = in[s];
+        if (known && h < heads) {
+          uint16_t* row = reinterpret_cast<uint16_t*>(a.cv) + to + h * a.head_stride;
+          *reinterpret_cast<uint4*>(row + e0) = in[s][0];
+          *reinterpret_cast<uint4*>(row + e1) = in[s][1];
+        }
         continue;
       }
-      float x[8];
-      unpack8<BF16>(in[s], x);
+      float x[8], y[8];
+      unpack8<BF16>(in[s][0], x);
+      unpack8<BF16>(in[s][1], y);
       if (norm != nullptr) {
         float sq = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sq = fmaf(x[j], x[j], sq);
+        for (int j = 0; j < 8; ++j) sq = fmaf(y[j], y[j], fmaf(x[j], x[j], sq));
         sq = sum_over<LPH>(sq);
         const float r = rsqrtf(sq * (1.f / D) + a.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = x[j] * r * wt[j];
-      }
-      if (TURN && a.rot > 0 && kind != 2) {
-        float y[8];
-        if (a.neighbours) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            y[j] = x[j] * cs[j] - x[j + 1] * sn[j];
-            y[j + 1] = x[j + 1] * cs[j] + x[j] * sn[j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = x[j] * cs[j] + __shfl_sync(~0u, x[j], partner) * sn[j];
+        for (int j = 0; j < 8; ++j) {
+          x[j] = x[j] * r * wt[j];
+          y[j] = y[j] * r * wt[8 + j];
         }
-        if (turned) {
+      }
+      if (TURN && kind != 2) {
+        if (together) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = y[j];
+          for (int j = 0; j < 8; ++j) {
+            const float b = x[j];
+            x[j] = b * cs[j] - y[j] * sn[j];
+            y[j] = y[j] * cs[j] + b * sn[j];
+          }
+        } else if (a.neighbours) {
+          if (e0 < a.rot) turn_neighbours(x, cs, sn);
+          if (e1 < a.rot) turn_neighbours(y, cs + 4, sn + 4);
         }
       }
       if (kind == 0) {
-        if (h < heads)
-          *reinterpret_cast<uint4*>(a.q_out + (t * a.Hq + h) * D + e0) = pack8<BF16>(x);
+        if (h < heads) {
+          uint16_t* row = a.q_out + (t * a.Hq + h) * D;
+          *reinterpret_cast<uint4*>(row + e0) = pack8<BF16>(x);
+          *reinterpret_cast<uint4*>(row + e1) = pack8<BF16>(y);
+        }
       } else if constexpr (KIND == SAME) {
-        if (known && h < heads)
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.ck) + to + h * a.head_stride + e0) =
-              pack8<BF16>(x);
+        if (known && h < heads) {
+          uint16_t* row = reinterpret_cast<uint16_t*>(a.ck) + to + h * a.head_stride;
+          *reinterpret_cast<uint4*>(row + e0) = pack8<BF16>(x);
+          *reinterpret_cast<uint4*>(row + e1) = pack8<BF16>(y);
+        }
       } else {
         float unit;
-        const uint2 c = quantise<KIND, LPH>(x, TURN && kind == 1 ? top_of(x) : top_of<BF16>(in[s]), unit);
+        const uint32_t top = TURN && kind == 1 ? max(top_of(x), top_of(y))
+                                               : max(top_of<BF16>(in[s][0]), top_of<BF16>(in[s][1]));
+        const float f = unit_of<KIND, LPH>(top, unit);
+        const uint2 lo = codes_of<KIND>(x, f), hi = codes_of<KIND>(y, f);
         if (known && h < heads) {
-          *reinterpret_cast<uint2*>((kind == 1 ? a.ck : a.cv) + to + h * a.head_stride + e0) = c;
+          uint8_t* row = (kind == 1 ? a.ck : a.cv) + to + h * a.head_stride;
+          if constexpr (!TURN) {
+            *reinterpret_cast<uint4*>(row + e0) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          } else {
+            *reinterpret_cast<uint2*>(row + e0) = lo;
+            *reinterpret_cast<uint2*>(row + e1) = hi;
+          }
           if (sub == 0) (kind == 1 ? a.ks : a.vs)[to_scale + h * a.scale_head] = unit;
         }
       }
@@ -559,7 +595,7 @@ cudaError_t launch_kv_rotate_write(const tern_kv_cache* c, const tern_kv_cache8*
   }
   a.page_shift = log2_of(page_size);
   a.n_slots = pages * page_size;
-  const int step = static_cast<int>(UNROLL * 256 / dim);        // heads of a unit
+  const int step = static_cast<int>(UNROLL * 512 / dim);        // heads of a unit
   a.uq = (a.Hq + step - 1) / step;
   a.uk = (a.H + step - 1) / step;
   const int upt = a.uq + 2 * a.uk;
