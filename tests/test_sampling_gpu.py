@@ -70,6 +70,14 @@ def test_sample(rows, vocab, dtype, names):
     check(logits(rng, rows, vocab, dtype), rng.random(rows), **filters(rng, rows, names))
 
 
+@pytest.mark.parametrize("rows,vocab,dtype,names", [
+    (310, 33001, F32, "tp"), (120, 70001, HF, "tkp"), (307, 128257, BF, "tp")])
+def test_more_rows_than_fit(rows, vocab, dtype, names):
+    """Long rows that several CTAs share although not all of them run at once."""
+    rng = np.random.default_rng(rows + vocab)
+    check(logits(rng, rows, vocab, dtype), rng.random(rows), **filters(rng, rows, names))
+
+
 @pytest.mark.parametrize("rows,vocab", [(3, 150001), (30, 40000), (200, 5000)])
 def test_filters_that_keep_many(rows, vocab):
     """Borders beyond the short list: searched by histograms."""
