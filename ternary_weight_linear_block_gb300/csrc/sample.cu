@@ -41,9 +41,10 @@ namespace {
 // short for either memory (18 us for 250 rows of 250007 in bf16) or arithmetic to
 // bound it.  Those take 142 us with all kinds of filters (689 with the search by
 // histograms for all rows, 259 with the list, 207 with places), 93 with top_k
-// alone; 255 and 245 with filters of all kinds in fp32 and fp16, which have no
-// places: their search takes three to five passes.  4 rows of 131072: 15 us, of
-// which the launch of the clusters and 12 joint steps are most.
+// alone.  fp32 has no places, so its search takes three to five passes, and a weight
+// about 40 instructions: 265 with filters of all kinds, 526 with top_p alone.  4
+// rows of 131072: 15 us, of which the launch of the clusters and 12 joint steps are
+// most.
 
 constexpr int NT = 512;              // threads, and places of the list
 constexpr int WARPS = NT / 32;
@@ -374,6 +375,17 @@ struct Places {
   }
 };
 
+// *sum += w in shared memory, as two 32-bit additions, the upper one only where there
+// is something to add: of the bulk of a row's weights seldom (250 rows of 250007 in
+// fp32 by top_p 526 us, with 64-bit additions 592).
+__device__ __forceinline__ void add_shared(uint64_t* sum, uint64_t w) {
+  uint32_t* half = reinterpret_cast<uint32_t*>(sum);      // (little-endian)
+  const uint32_t lo = static_cast<uint32_t>(w);
+  const uint32_t old = atomicAdd(half, lo);
+  const uint32_t up = static_cast<uint32_t>(w >> 32) + (old + lo < lo ? 1u : 0u);
+  if (up != 0) atomicAdd(half + 1, up);
+}
+
 template <int DT, int CL>
 struct Sampler {
   static constexpr int E = Elt<DT>::E;
@@ -424,9 +436,7 @@ struct Sampler {
           if (key >= lo && key <= hi) {
             const int bin = linear ? linear_bin(x[e], most, step) : (hi - key) >> shift;
             atomicAdd(&s.count[bin], 1u);
-            if (masses)
-              atomicAdd(reinterpret_cast<unsigned long long*>(&s.mass[bin]),
-                        static_cast<unsigned long long>(weigh.template at<EXACT>(x[e])));
+            if (masses) add_shared(&s.mass[bin], weigh.template at<EXACT>(x[e]));
           }
         }
       });
