@@ -62,12 +62,13 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 //
 // One read and one write of everything, so memory bounds it; with a rotation and a
 // norm the instructions of both beside it.  Measured: 185 us for the rows of 16-bit
-// keys and values that would take 172 at the copy rate (0.93), 273 for rotated and
-// normalised queries and keys that would take 191 (0.70); 206 and 321 with one
-// chunk a lane, twice the lanes in a sum and partners from other lanes.  CTAs an
-// SM (turning, writing) and steps: 3, 5 and 2; 4, 6 and 1: 300, 191; 2, 4 and 2: 299,
+// keys and values that would take 172 at the copy rate (0.93), 263 for rotated and
+// normalised queries and keys that would take 191 (0.73); 206 and 321 with one
+// chunk a lane, twice the lanes in a sum and partners from other lanes.  CTAs of 128
+// threads an SM (turning, writing): 5, 9; 6, 11: 265, 184; 7, 12: 268, 184; CTAs of
+// 256 and steps: 3, 5 and 2: 271 (spills), 184; 4, 6 and 1: 300, 191; 2, 4 and 2: 299,
 // 192; 2, 4 and 3: 286, 194; 2, 3 and 4: 281, 209.  A call of few rows is a launch
-// and two dependent reads, 4 to 5 us.
+// and two dependent reads, 4 us.
 //
 // The angle of pair j is position * turns[j] in 64-bit integers, turns of 2^-64:
 // the product wraps where the angle does, so that its top 32 bits are the angle
@@ -75,7 +76,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 //
 // Bound: rows read once and written once.
 
-constexpr int ROT_THREADS = 256;
+constexpr int ROT_THREADS = 128;
 constexpr int UNROLL = 2;
 constexpr float kSmallest = 0x1p-100f;   // rows below are stored as zeros
 
@@ -177,7 +178,7 @@ __device__ __forceinline__ void turn_neighbours(float (&x)[8], const float* cs, 
 
 // TURN: queries, norms or a rotation; without them the rows are only written.
 template <bool BF16, int D, int KIND, bool TURN>
-__global__ void __launch_bounds__(ROT_THREADS, (TURN ? 3 : 5)) rotate_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(ROT_THREADS, (TURN ? 5 : 9)) rotate_kernel(const __grid_constant__ RotArgs a) {
   constexpr int LPH = D / 16, HPW = 32 / LPH;
   const int lane = threadIdx.x & 31;
   const int sub = lane % LPH, part = lane / LPH;
