@@ -79,19 +79,21 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, unsigned int code
 // has to say for a tile, fp16 holds what is rounded to it.
 constexpr float kRef = 3.f, kMove = 8.f, kTop = 15.f;
 
-// The units of a tile: the largest and least of the keys, and of the values (of
-// those that are not 0).
+// The units of a tile: the largest and least of the keys, and of the values.  A
+// value unit of 0 (a row of zeros, or a page out of range) bounds no probability,
+// so a tile that has one is exact: there it is multiplied by the probability in
+// 32 bits, before that is rounded.
 struct TileUnits {
   float k_most, k_least, v_most;
   int e;             // exponent of v_most
-  bool fold;         // the values' units are within 2^10 of each other, or 0
+  bool fold;         // the values' units are within 2^10 of each other
 };
 __device__ __forceinline__ TileUnits tile_units(const float4& q) {
   TileUnits u;
   u.k_most = q.x;
   u.k_least = q.y;
   u.v_most = q.z;
-  u.fold = q.z == 0.f || (q.z >= 0x1p-100f && q.z <= 1024.f * q.w);
+  u.fold = q.z >= 0x1p-100f && q.z <= 1024.f * q.w;
   u.e = q.z == 0.f ? 0 : (__float_as_int(q.z) >> 23) - 127;
   return u;
 }
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float ku = s_ku[us][e * 32 + lane];
           vu[e] = s_vu[us][e * 32 + lane];
           s_lu[us][e * 32 + lane] = __log2f(fmaxf(vu[e], 0x1p-100f));
-          q = make_float4(fmaxf(q.x, ku), fminf(q.y, ku), fmaxf(q.z, vu[e]), fminf(q.w, vu[e] == 0.f ? INFINITY : vu[e]));
+          q = make_float4(fmaxf(q.x, ku), fminf(q.y, ku), fmaxf(q.z, vu[e]), fminf(q.w, vu[e]));
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {

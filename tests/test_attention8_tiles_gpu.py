@@ -1,0 +1,156 @@
+"""Many rows over the 8-bit cache where values' units are unlike: rows of zeros, high scores on small values,
+probabilities far below the largest.  The tile kernel against the statement in 64 bits."""
+
+import types
+
+import numpy as np
+import pytest
+import torch
+
+from ternary_weight_linear_block_gb300 import binding as B
+from ternary_weight_linear_block_gb300 import kv
+from tests import kv_reference as R
+from tests.gpu_helpers import ensure_lib
+
+pytestmark = pytest.mark.gpu
+I8, E4 = torch.int8, torch.float8_e4m3fn
+BF, HF = torch.bfloat16, torch.float16
+LARGEST = {I8: 127.0, E4: 448.0}
+SCALE, Q0 = 0.25, 32.0       # a key whose first element is x has 8 x more than its score otherwise
+GROUP, NEW = 2, 30           # 60 rows a key head: the tile kernel's for every head size
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_lib()
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def given(rng, ctx, heads, dim, dtype, kind, new=NEW, spread=0.2, group=GROUP, other=0.5):
+    """Tokens [ctx + new] of one request: codes (as numbers), units, queries; scores apart from the first element
+    are `other` times as wide as usual."""
+    n = ctx + new
+    g = types.SimpleNamespace(ctx=ctx, new=new, heads=heads, dim=dim, dtype=dtype, kind=kind)
+    for name in ("k", "v"):
+        x = torch.from_numpy(rng.standard_normal((n, heads, dim)).astype(np.float32)).mul_(LARGEST[kind] / 7)
+        x.clamp_(-LARGEST[kind], LARGEST[kind])
+        if name == "k":
+            x[..., 0] = 0
+        setattr(g, name, x.round() if kind == I8 else x.to(E4).float())
+        unit = np.exp(spread * rng.standard_normal((n, heads))) * 7 / LARGEST[kind]
+        setattr(g, name + "u", torch.from_numpy(unit.astype(np.float32)))
+    q = other * rng.standard_normal((new, heads * group, dim))
+    q[..., 0] = Q0
+    g.q = torch.from_numpy(q.astype(np.float32)).to(dtype)
+    return g
+
+
+def raise_score(g, at, by, head=slice(None)):
+    """Key `at` scores `by` more than without its first element (nats)."""
+    x = by / (SCALE * Q0) / g.ku[at, head]
+    assert float(x.abs().max()) <= LARGEST[g.kind]
+    g.k[at, head, 0] = x.round() if g.kind == I8 else x.to(E4).float()
+
+
+def bounds(g, k, ref, weight, lse):
+    """Scores and sums as for the 16-bit cache (kv_reference.attention_bounds), with 8 roundings more for units and
+    powers of two.  Probability times unit is rounded to fp16: 2^-11 relatively, and by 2^-25 where it has no exponent
+    left, the row's largest being 2^7 at least, so by 2^-32 of the largest unit, times a code.  bf16 rows: value times
+    unit is rounded to fp16 too, its unit first in two parts of which the second is off by 2^-25 of a 2^-8 or more:
+    (1 + 2^-11)(1 + 2^-11 + 2^-17 + 2^-22) - 1 < 2^-10 + 2^-16, and twice by 2^-25 of the largest unit where values
+    have no exponent left."""
+    keys, eps, unit = g.ctx + g.new, 2.0 ** -24, R.UNIT[g.dtype]
+    q = g.q.double().numpy()
+    most = SCALE * np.sqrt((q ** 2).sum(-1)).max() * np.sqrt((k ** 2).sum(-1)).max()
+    rel = (g.dim + 10) * eps * most + 2.0 ** -21 + (keys + 8) * eps
+    folds, vu = g.dtype is BF, float(g.vu.max())
+    out = weight * ((2.0 ** -10 + 2.0 ** -16 if folds else 2.0 ** -11) + 2 * rel) * (1 + 2.0 ** -11)
+    out = out + unit * np.abs(ref) + (keys * 2.0 ** -32 * LARGEST[g.kind] + folds * 2.0 ** -24) * vu
+    out = out + (2.0 ** -25 if g.dtype is HF else 0.0)
+    return out, rel + 4 * eps * np.abs(np.where(np.isfinite(lse), lse, 0)) + 2.0 ** -19
+
+
+def run(g, page=16, copies=1, lost=(), seed=0):
+    """(out, lse) of `copies` requests that share the tokens' pages; pages `lost` of the table are none."""
+    n = g.ctx + g.new
+    need = -(-n // page)
+    order = np.random.default_rng(seed).permutation(need + 3)[:need]
+    cache = kv.KVCache8.empty(need + 3, page, g.heads, g.dim, g.kind)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        t.view(torch.uint8).fill_(0xFF)
+    pos = np.arange(n)
+    pg, r = (torch.from_numpy(x).cuda() for x in (order[pos // page], pos % page))
+    for codes, units, x, u in ((cache.k, cache.k_scale, g.k, g.ku), (cache.v, cache.v_scale, g.v, g.vu)):
+        codes.view(I8)[pg, r] = x.to(g.kind).view(I8).cuda()
+        units[pg, :, r] = u.cuda()
+    table = order.copy()
+    for i, p in enumerate(lost):
+        table[p] = -1 if i % 2 == 0 else 1 << 20
+    out, lse = kv.tree_attention(g.q.cuda().repeat(copies, 1, 1), cache, ints(np.tile(table, (copies, 1))),
+                                 ints([g.ctx] * copies), ints([g.new * i for i in range(copies + 1)]), g.new,
+                                 scale=SCALE, return_lse=True)
+    B.tern_check()
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+def compare(g, copies=1, **kw):
+    k, v = ((x * u[..., None]).double().numpy()[None] for x, u in ((g.k, g.ku), (g.v, g.vu)))
+    ref, rl, weight = R.attention(g.q.double().numpy(), k, v, [[0]], g.ctx + g.new, [g.ctx], [g.new],
+                                  lambda b, i, j: j <= i, SCALE)
+    ob, lb = bounds(g, k, ref, weight, rl)
+    out, lse = run(g, copies=copies, **kw)
+    for i in range(copies):
+        o, l = out[i * g.new:(i + 1) * g.new], lse[i * g.new:(i + 1) * g.new]
+        assert (np.abs(o - ref) <= ob).all(), float(np.nan_to_num(np.abs(o - ref) / ob, nan=np.inf).max())
+        assert (np.abs(l - rl) <= lb).all(), float(np.nan_to_num(np.abs(l - rl) / lb, nan=np.inf).max())
+
+
+KINDS = pytest.mark.parametrize("dtype,kind,dim", [(BF, I8, 64), (BF, I8, 128), (BF, E4, 128), (BF, E4, 256),
+                                                   (HF, I8, 128), (HF, E4, 256)])
+
+
+# ---------------------------------------------------------------- rows of zeros
+
+@KINDS
+def test_zero_filled_cache(dtype, kind, dim):
+    """Nothing but zeros, as in a first step over a cleared cache."""
+    g = given(np.random.default_rng(1), 1000, 2, dim, dtype, kind)
+    for x in (g.k, g.v, g.ku, g.vu):
+        x.zero_()
+    out, lse = run(g)
+    assert (out == 0).all()
+    want = np.log(1001 + np.arange(NEW))[:, None]
+    assert (np.abs(lse - want) <= 2.0 ** -18).all()
+
+
+@KINDS
+@pytest.mark.parametrize("first,last", [(0, 128), (256, 512), (872, 1000), (0, 1000)])
+def test_tiles_of_zero_values(dtype, kind, dim, first, last):
+    g = given(np.random.default_rng(first + dim), 1000, 2, dim, dtype, kind)
+    g.v[first:last, 1], g.vu[first:last, 1] = 0, 0
+    compare(g)
+
+
+@KINDS
+@pytest.mark.parametrize("at", [3, 700])
+@pytest.mark.parametrize("by", [0.0, 9.7, 25.0])
+def test_one_zero_valued_key(dtype, kind, dim, at, by):
+    """One among others, scored as they are and far above them."""
+    g = given(np.random.default_rng(at + dim), 1000, 2, dim, dtype, kind)
+    g.v[at, 0], g.vu[at, 0] = 0, 0
+    raise_score(g, at, by)
+    compare(g)
+
+
+@KINDS
+def test_lost_pages(dtype, kind, dim):
+    """Pages out of range count as zeros: some, and all of several tiles."""
+    g = given(np.random.default_rng(dim), 1000, 2, dim, dtype, kind)
+    lost = [0, 5] + list(range(16, 33)) + [50]
+    for p in lost:
+        for x in (g.k, g.v):
+            x[p * 16:p * 16 + 16] = 0
+    compare(g, lost=lost)
