@@ -765,7 +765,7 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
  * values' units are rounded to fp16 for their products, relatively to the
  * largest of their row (a bf16 query keeps all its bits unless it is below
  * 2^-28 of its row's largest).  With many bf16 rows the values times their
- * units are rounded to fp16 too, where a tile's units are within 2^10 of each
+ * units are rounded to fp16 too, where a tile's units are within 2^8 of each
  * other.  A key that a row does not see has no
  * influence, whatever its unit is; one whose unit is NaN makes every row that
  * sees it NaN. */

@@ -6,7 +6,7 @@
 // exactly, as the MMAs want them.  They also turn bf16 queries into fp16 by a
 // power of two for each row.  A score column is multiplied by its key's unit in 32
 // bits as the softmax reads a row.  The values' units:
-//   folded  bf16 rows, a tile of cached tokens whose units are within 2^10 of each
+//   folded  bf16 rows, a tile of cached tokens whose units are within 2^8 of each
 //           other: code * unit / 2^E goes to the fp16 tile (one rounding, as
 //           relatively small as that of the probabilities, which then take 2^E;
 //           beside an fp16 output's it would show), E the largest unit's
@@ -17,7 +17,10 @@
 // that set it.  A tile of cached tokens first takes a bound of its own: the largest
 // score times the largest (or, below zero, the least) key's unit, one pass over
 // the scores alone.  Only where fp16 could not hold what the bound allows, and
-// in tiles with new tokens, is the maximum itself looked for.
+// in tiles with new tokens, is the maximum itself looked for.  What a folded tile
+// rounds to fp16 is 2^(t_j - m + E), of a key whose unit is less than 2^E more than
+// m knows of, so there m is also at least the largest t_j + E - 15: 2^15 fits, and
+// as t_j + log2 vu_j is 2^8 below at most, its product keeps 2^7.
 //
 // Neither memory nor the tensor cores bound it but what the warps issue: widening,
 // and two passes over the scores.  4 requests of 29 drafts of 4 heads (116 rows) of
@@ -75,7 +78,7 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, unsigned int code
 }
 
 // What a row's exponents refer to is the largest t_j + log2 vu_j less kRef, when it
-// is set; it moves when that grows by more than 2^8.  Below 2^15, which a bound
+// is set; it moves when that grows by more than 2^8.  Up to 2^15, which a bound
 // has to say for a tile, fp16 holds what is rounded to it.
 constexpr float kRef = 3.f, kMove = 8.f, kTop = 15.f;
 
@@ -86,14 +89,14 @@ constexpr float kRef = 3.f, kMove = 8.f, kTop = 15.f;
 struct TileUnits {
   float k_most, k_least, v_most;
   int e;             // exponent of v_most
-  bool fold;         // the values' units are within 2^10 of each other
+  bool fold;         // the values' units are within 2^8 of each other
 };
 __device__ __forceinline__ TileUnits tile_units(const float4& q) {
   TileUnits u;
   u.k_most = q.x;
   u.k_least = q.y;
   u.v_most = q.z;
-  u.fold = q.z >= 0x1p-100f && q.z <= 1024.f * q.w;
+  u.fold = q.z >= 0x1p-100f && q.z <= 256.f * q.w;
   u.e = q.z == 0.f ? 0 : (__float_as_int(q.z) >> 23) - 127;
   return u;
 }
@@ -614,8 +617,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float top = (most > 0.f ? most * tu.k_most : most * tu.k_least) + __log2f(fmaxf(tu.v_most, 0x1p-100f));
           float mn = mp;
           if (edge || __any_sync(~0u, !(top <= mp + kTop))) {
-            // the maximum itself, of what the row sees
-            float mt = -INFINITY;
+            // the maximum itself, of what the row sees; tt of scores alone
+            float mt = -INFINITY, tt = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < TKT / 16; ++c) {
               uint32_t x[16];
@@ -627,17 +630,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
                 const float4 k4 = ku[e >> 2], l4 = lu[e >> 2];
-                const float y[4] = {fmaf(__uint_as_float(x[e]) * rs, k4.x, l4.x),
-                                    fmaf(__uint_as_float(x[e + 1]) * rs, k4.y, l4.y),
-                                    fmaf(__uint_as_float(x[e + 2]) * rs, k4.z, l4.z),
-                                    fmaf(__uint_as_float(x[e + 3]) * rs, k4.w, l4.w)};
+                const float y[4] = {__uint_as_float(x[e]) * rs * k4.x, __uint_as_float(x[e + 1]) * rs * k4.y,
+                                    __uint_as_float(x[e + 2]) * rs * k4.z, __uint_as_float(x[e + 3]) * rs * k4.w};
+                const float lg[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                  if ((bits >> (e + h)) & 1) mt = fmaxf(mt, y[h]);
+                  if ((bits >> (e + h)) & 1) {
+                    tt = fmaxf(tt, y[h]);
+                    mt = fmaxf(mt, y[h] + lg[h]);
+                  }
               }
             }
             mt -= kRef;
             if (mt > mp + kMove || (mp == -INFINITY && mt != mp)) mn = mt;
+            if (fold) mn = fmaxf(mn, tt + static_cast<float>(tu.e) - kTop);
           }
           *reinterpret_cast<volatile float*>(&s_m[lrow]) = mn;
           __syncwarp();

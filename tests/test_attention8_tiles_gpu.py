@@ -154,3 +154,37 @@ def test_lost_pages(dtype, kind, dim):
         for x in (g.k, g.v):
             x[p * 16:p * 16 + 16] = 0
     compare(g, lost=lost)
+
+
+# ---------------------------------------------------------------- high scores on small values
+
+@KINDS
+@pytest.mark.parametrize("at", [3, 300, 700])
+@pytest.mark.parametrize("by,smaller", [(7.0, 5), (9.4, 6), (9.4, 8), (12.0, 7), (12.0, 10), (16.0, 9), (16.0, 12)])
+def test_high_score_on_a_small_value(dtype, kind, dim, at, by, smaller):
+    """A key as the first tokens of a text often are: by `by` above the others (nats), its value's unit 2^-smaller of
+    theirs; in an item's first tile and in later ones.  Items enough that most have one CTA."""
+    g = given(np.random.default_rng(at + dim + smaller), 1000, 2, dim, dtype, kind)
+    raise_score(g, at, by)
+    g.vu[at] *= 2.0 ** -smaller
+    compare(g, copies=48)
+
+
+@KINDS
+@pytest.mark.parametrize("most", [7, 9, 11, 30])
+def test_scores_and_units_against_each_other(dtype, kind, dim, most):
+    """Every key's value unit is down to 2^-most of the largest, and its score the higher for it, by as much or more."""
+    rng = np.random.default_rng(most + dim)
+    g = given(rng, 1000, 2, dim, dtype, kind, spread=0.0, other=0.1)
+    down = rng.uniform(0, most, g.vu.shape)
+    g.vu *= torch.from_numpy(2.0 ** -down).float()
+    x = torch.from_numpy(down * np.log(2) * 1.5).float() / (SCALE * Q0) / g.ku
+    g.k[..., 0] = x.round() if kind == I8 else x.to(E4).float()
+    compare(g, copies=24)
+
+
+@KINDS
+@pytest.mark.parametrize("spread", [0.6, 0.9, 1.2, 2.0])
+def test_units_apart(dtype, kind, dim, spread):
+    """Tiles on both sides of where units are folded into the values, one after another."""
+    compare(given(np.random.default_rng(dim), 2000, 2, dim, dtype, kind, spread=spread, other=0.2), copies=8)
