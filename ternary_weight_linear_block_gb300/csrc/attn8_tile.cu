@@ -19,15 +19,16 @@
 // the scores alone.  Only where fp16 could not hold what the bound allows, and
 // in tiles with new tokens, is the maximum itself looked for.  What a folded tile
 // rounds to fp16 is 2^(t_j - m + E), of a key whose unit is less than 2^E more than
-// m knows of, so there m is also at least the largest t_j + E - 15: 2^15 fits, and
-// as t_j + log2 vu_j is 2^8 below at most, its product keeps 2^7.
+// m knows of, so there m is also at least the largest t_j + E - kTop; as its t_j +
+// log2 vu_j is 2^8 below at most, the product keeps 2^7.
 //
 // Neither memory nor the tensor cores bound it but what the warps issue: widening,
 // and two passes over the scores.  4 requests of 29 drafts of 4 heads (116 rows) of
-// 128 over up to 20003 keys: 90 us, 162 MB of codes at 1.8 TB/s; 24 rows of 256 over
+// 128 over up to 20003 keys: 94 us, 162 MB of codes at 1.7 TB/s; 24 rows of 256 over
 // 131001 keys: 116 us, 2.4 TB/s.  Steps of the first: 254 as items of 16 rows; 123
-// as tiles; 106 with the units folded and the loops rolled; 102 and 90 with a tile's
-// bound in place of its maximum and short code for exact tiles.  The code matters
+// as tiles; 106 with the units folded and the loops rolled; 102 and 89 with a tile's
+// bound in place of its maximum and short code for exact tiles, 94 with more bits
+// for small probabilities (kRef).  The code matters
 // twice: a profile of the first version waited 1.9 cycles an instruction for the
 // instruction itself, since eight kinds of warps run as many loops, so loops stay
 // rolled and short (widening unrolled eight times 159, against 124).  Not better:
@@ -78,9 +79,14 @@ __device__ __forceinline__ void fail(volatile int* abort_flag, unsigned int code
 }
 
 // What a row's exponents refer to is the largest t_j + log2 vu_j less kRef, when it
-// is set; it moves when that grows by more than 2^8.  Up to 2^15, which a bound
-// has to say for a tile, fp16 holds what is rounded to it.
-constexpr float kRef = 3.f, kMove = 8.f, kTop = 15.f;
+// is set; it moves when that grows by more than 2^kMove.  Up to 2^kTop, which a
+// bound has to say for a tile, fp16 holds what is rounded to it (its largest is just
+// below 2^16).  So what is rounded has 2^-25 where it has no exponent left and
+// 2^kRef at the row's largest: 2^-33 of that, 2^-32 in folded tiles, whose values
+// are multiplied by the unit's fraction of up to 2 behind it.  A reference 2^3 below
+// lost small probabilities that 32-bit sums count, but looked for the maximum less
+// often: 4 x 29 drafts over up to 20003 keys 89 us, now 94.
+constexpr float kRef = 8.f, kMove = 7.9f, kTop = 15.9f;
 
 // The units of a tile: the largest and least of the keys, and of the values.  A
 // value unit of 0 (a row of zeros, or a page out of range) bounds no probability,

@@ -188,3 +188,17 @@ def test_scores_and_units_against_each_other(dtype, kind, dim, most):
 def test_units_apart(dtype, kind, dim, spread):
     """Tiles on both sides of where units are folded into the values, one after another."""
     compare(given(np.random.default_rng(dim), 2000, 2, dim, dtype, kind, spread=spread, other=0.2), copies=8)
+
+
+# ---------------------------------------------------------------- probabilities far below the largest
+
+@KINDS
+@pytest.mark.parametrize("below", [27, 29, 31])
+def test_many_keys_far_below_one(dtype, kind, dim, below):
+    """One key with a value of zero in some columns, and in an item's other tiles thousands whose probability is
+    2^-below of its: these columns are all theirs, and 2^-32 of the largest is what a probability may lose."""
+    g = given(np.random.default_rng(below), 4000, 1, dim, dtype, kind, new=60, spread=0.0, group=1, other=0.0)
+    g.k[:], g.v[:, :, :8] = 0, 0.8 * LARGEST[kind] // 16 * 16
+    raise_score(g, 5, below * np.log(2))
+    g.v[5, :, :8] = 0
+    compare(g, copies=200)
