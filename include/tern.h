@@ -764,7 +764,8 @@ tern_status tern_kv8_commit(const tern_kv_cache8* caches, int64_t layers, const 
  * probabilities in 32 bits.  The queries and the probabilities times the
  * values' units are rounded to fp16 for their products, relatively to the
  * largest of their row (a bf16 query keeps all its bits unless it is below
- * 2^-28 of its row's largest).  With many bf16 rows the values times their
+ * 2^-28 of its row's largest; where all of a row's units are below 2^-90,
+ * products keep 2^-16 of the largest, else 2^-32).  With many bf16 rows the values times their
  * units are rounded to fp16 too, where a tile's units are within 2^8 of each
  * other.  A key that a row does not see has no
  * influence, whatever its unit is; one whose unit is NaN makes every row that

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__((Rows8<D, NT>::THREADS), (Rows8<D, NT>::CTAS))
           }
         }
         // c[n]: keys lane / 4 and + 8, rows row_c and + 1
-        const float lu[2] = {__log2f(fmaxf(vu[0], 0x1p-100f)), __log2f(fmaxf(vu[1], 0x1p-100f))};
+        const float lu[2] = {__log2f(fmaxf(vu[0], kLeastUnit)), __log2f(fmaxf(vu[1], kLeastUnit))};
         bool hid[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)

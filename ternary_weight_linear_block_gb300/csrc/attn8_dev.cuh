@@ -12,6 +12,13 @@ constexpr int MAX_GRID8 = TERN_TREE_ATTENTION_ZERO_BYTES / (3 * sizeof(int));
 
 enum Kind { I8 = 1, E4M3 = 2 };
 
+// Values' units below this count as this in the reference of a row's exponents, as
+// a unit of 0 would leave none.  So a key's 2^(t_j - m) is below 2^106 whatever its
+// unit is, and sums over millions of such keys stay below 2^128 (2^-100 let some
+// thousands pass it).  What is rounded to fp16 then has 2^-25 of 2^-9 left at the
+// smallest unit that is written, 2^-107, and all its bits from 2^-90 on.
+constexpr float kLeastUnit = 0x1p-90f;
+
 struct Args8 {
   Args a;
   const float* ku;

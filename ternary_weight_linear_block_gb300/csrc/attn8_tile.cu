@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int e = 0; e < EACH; ++e) {
           const float ku = s_ku[us][e * 32 + lane];
           vu[e] = s_vu[us][e * 32 + lane];
-          s_lu[us][e * 32 + lane] = __log2f(fmaxf(vu[e], 0x1p-100f));
+          s_lu[us][e * 32 + lane] = __log2f(fmaxf(vu[e], kLeastUnit));
           q = make_float4(fmaxf(q.x, ku), fminf(q.y, ku), fmaxf(q.z, vu[e]), fminf(q.w, vu[e]));
         }
 #pragma unroll
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             wait(&m_ready[warp & 3], (tile0 + i - 1) & 1u);
             mp = *reinterpret_cast<volatile float*>(&s_m[lrow]);
           }
-          const float top = (most > 0.f ? most * tu.k_most : most * tu.k_least) + __log2f(fmaxf(tu.v_most, 0x1p-100f));
+          const float top = (most > 0.f ? most * tu.k_most : most * tu.k_least) + __log2f(fmaxf(tu.v_most, kLeastUnit));
           float mn = mp;
           if (edge || __any_sync(~0u, !(top <= mp + kTop))) {
             // the maximum itself, of what the row sees; tt of scores alone

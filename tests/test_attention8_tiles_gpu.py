@@ -202,3 +202,20 @@ def test_many_keys_far_below_one(dtype, kind, dim, below):
     raise_score(g, 5, below * np.log(2))
     g.v[5, :, :8] = 0
     compare(g, copies=200)
+
+
+# ---------------------------------------------------------------- sums of probabilities
+
+@KINDS
+@pytest.mark.parametrize("last", [0, 200])
+def test_sums_over_many_zero_valued_keys(dtype, kind, dim, last):
+    """A head whose values are zeros (but for the last cached tokens), its first tile's scores below the others': the
+    reference follows scores less the log2 of a least unit, and thousands of probabilities far above it are added up."""
+    g = given(np.random.default_rng(dim), 20000, 1, dim, dtype, kind, new=60, spread=0.0, group=1, other=0.0)
+    g.k[:] = 0
+    raise_score(g, slice(128, None), 7.5 * np.log(2))
+    zero = slice(0, g.ctx - last)
+    g.v[zero], g.vu[zero] = 0, 0
+    if last == 0:
+        g.v[:], g.vu[:] = 0, 0
+    compare(g, copies=160)
