@@ -55,7 +55,7 @@ def raise_score(g, at, by, head=slice(None)):
     g.k[at, head, 0] = x.round() if g.kind == I8 else x.to(E4).float()
 
 
-def bounds(g, k, ref, weight, lse):
+def bounds(g, k, ref, weight, lse, scale):
     """Scores and sums as for the 16-bit cache (kv_reference.attention_bounds), with 8 roundings more for units and
     powers of two.  Probability times unit is rounded to fp16: 2^-11 relatively, and by 2^-25 where it has no exponent
     left, the row's largest being 2^7 at least, so by 2^-32 of the largest unit, times a code.  bf16 rows: value times
@@ -64,7 +64,7 @@ def bounds(g, k, ref, weight, lse):
     have no exponent left."""
     keys, eps, unit = g.ctx + g.new, 2.0 ** -24, R.UNIT[g.dtype]
     q = g.q.double().numpy()
-    most = SCALE * np.sqrt((q ** 2).sum(-1)).max() * np.sqrt((k ** 2).sum(-1)).max()
+    most = scale * np.sqrt((q ** 2).sum(-1)).max() * np.sqrt((k ** 2).sum(-1)).max()
     rel = (g.dim + 10) * eps * most + 2.0 ** -21 + (keys + 8) * eps
     folds, vu = g.dtype is BF, float(g.vu.max())
     out = weight * ((2.0 ** -10 + 2.0 ** -16 if folds else 2.0 ** -11) + 2 * rel) * (1 + 2.0 ** -11)
@@ -73,11 +73,11 @@ def bounds(g, k, ref, weight, lse):
     return out, rel + 4 * eps * np.abs(np.where(np.isfinite(lse), lse, 0)) + 2.0 ** -19
 
 
-def run(g, page=16, copies=1, lost=(), seed=0):
+def run(g, page=16, copies=1, lost=(), scale=SCALE, mask=None):
     """(out, lse) of `copies` requests that share the tokens' pages; pages `lost` of the table are none."""
     n = g.ctx + g.new
     need = -(-n // page)
-    order = np.random.default_rng(seed).permutation(need + 3)[:need]
+    order = np.random.default_rng(0).permutation(need + 3)[:need]
     cache = kv.KVCache8.empty(need + 3, page, g.heads, g.dim, g.kind)
     for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
         t.view(torch.uint8).fill_(0xFF)
@@ -91,17 +91,17 @@ def run(g, page=16, copies=1, lost=(), seed=0):
         table[p] = -1 if i % 2 == 0 else 1 << 20
     out, lse = kv.tree_attention(g.q.cuda().repeat(copies, 1, 1), cache, ints(np.tile(table, (copies, 1))),
                                  ints([g.ctx] * copies), ints([g.new * i for i in range(copies + 1)]), g.new,
-                                 scale=SCALE, return_lse=True)
+                                 mask=mask, scale=scale, return_lse=True)
     B.tern_check()
     return out.double().cpu().numpy(), lse.double().cpu().numpy()
 
 
-def compare(g, copies=1, **kw):
+def compare(g, copies=1, scale=SCALE, **kw):
     k, v = ((x * u[..., None]).double().numpy()[None] for x, u in ((g.k, g.ku), (g.v, g.vu)))
     ref, rl, weight = R.attention(g.q.double().numpy(), k, v, [[0]], g.ctx + g.new, [g.ctx], [g.new],
-                                  lambda b, i, j: j <= i, SCALE)
-    ob, lb = bounds(g, k, ref, weight, rl)
-    out, lse = run(g, copies=copies, **kw)
+                                  lambda b, i, j: j <= i, scale)
+    ob, lb = bounds(g, k, ref, weight, rl, scale)
+    out, lse = run(g, copies=copies, scale=scale, **kw)
     for i in range(copies):
         o, l = out[i * g.new:(i + 1) * g.new], lse[i * g.new:(i + 1) * g.new]
         assert (np.abs(o - ref) <= ob).all(), float(np.nan_to_num(np.abs(o - ref) / ob, nan=np.inf).max())
@@ -219,3 +219,63 @@ def test_sums_over_many_zero_valued_keys(dtype, kind, dim, last):
     if last == 0:
         g.v[:], g.vu[:] = 0, 0
     compare(g, copies=160)
+
+
+# ---------------------------------------------------------------- what the kernel of few rows is tested with
+
+@KINDS
+@pytest.mark.parametrize("spread", [4.0, 8.0])
+def test_units_far_apart(dtype, kind, dim, spread):
+    """Units of keys and values over many orders of magnitude."""
+    g = given(np.random.default_rng(dim), 900, 2, dim, dtype, kind, spread=spread, other=0.5 * np.exp(-2.5 * spread))
+    g.q[..., 0] = 0
+    g.vu /= float(g.vu.max())
+    compare(g, copies=4)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("kind,dim", [(I8, 64), (E4, 128), (I8, 256)])
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -9, 2.0 ** 8, 2.0 ** 14])
+def test_queries_of_any_size(dtype, kind, dim, size):
+    """Queries and the scale in inverse proportion: the same scores."""
+    if dtype is HF and not 2.0 ** -10 < size < 2.0 ** 9:
+        size = 2.0 ** (8 if size > 1 else -10)
+    g = given(np.random.default_rng(3), 500, 2, dim, dtype, kind)
+    g.q[..., 0] = 0
+    want, wl = run(g)
+    g.q = (g.q.double() * size).to(dtype)
+    got, gl = run(g, scale=SCALE / size)
+    if dtype is BF:              # a power of two, which the kernel takes out
+        assert np.array_equal(got, want) and np.array_equal(gl, wl)
+    else:
+        compare(g, scale=SCALE / size)
+
+
+@KINDS
+@pytest.mark.parametrize("new", [3, 30])
+def test_drafts_that_a_row_does_not_see_may_be_anything(dtype, kind, dim, new):
+    """A draft's units NaN: its siblings' rows are the same as without, the rows that see it NaN; in both kernels."""
+    g = given(np.random.default_rng(dim), 37, 2, dim, dtype, kind, new=new)
+    parents = [-1, 0, 0] + [2 if i % 3 == 0 else 1 for i in range(3, new)]
+    mask = kv.ancestor_masks(parents)
+    want, wl = run(g, mask=mask)
+    sees = [2] + [i for i in range(3, new) if i % 3 == 0]
+    keep = [i for i in range(new) if i not in sees]
+    g.ku[39], g.vu[39] = float("nan"), float("nan")
+    got, gl = run(g, mask=mask)
+    assert np.array_equal(got[keep], want[keep]) and np.array_equal(gl[keep], wl[keep])
+    assert np.isnan(got[sees]).all() and np.isnan(gl[sees]).all()
+
+
+@KINDS
+@pytest.mark.parametrize("at", [0, 200, 999])
+@pytest.mark.parametrize("unit", ["ku", "vu"])
+def test_cached_token_that_is_nan(dtype, kind, dim, at, unit):
+    """One head's unit of a cached token: all of that head's rows are NaN, the other head's as without."""
+    g = given(np.random.default_rng(at), 1000, 2, dim, dtype, kind)
+    want, wl = run(g)
+    getattr(g, unit)[at, 1] = float("nan")
+    got, gl = run(g)
+    assert np.array_equal(got[:, :GROUP], want[:, :GROUP]) and np.array_equal(gl[:, :GROUP], wl[:, :GROUP])
+    assert np.isnan(got[:, GROUP:]).all()
+    assert np.isnan(gl[:, GROUP:]).all() == (unit == "ku")
