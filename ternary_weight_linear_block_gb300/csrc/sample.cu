@@ -39,11 +39,11 @@ namespace {
 // A row is read two (few survivors) to five times, from L2 after the first, and every
 // step that a cluster takes together costs it a few us; the vocabulary is too
 // short for either memory (18 us for 250 rows of 250007 in bf16) or arithmetic to
-// bound it.  Those take 142 us with all kinds of filters (689 with the search by
-// histograms for all rows, 259 with the list, 207 with places), 93 with top_k
-// alone.  fp32 has no places, so its search takes three to five passes, and a weight
-// about 40 instructions: 265 with filters of all kinds, 526 with top_p alone.  4
-// rows of 131072: 15 us, of which the launch of the clusters and 12 joint steps are
+// bound it.  Those take 128 us with all kinds of filters (689 with the search by
+// histograms for all rows, 259 with the list, 207 with places), 97 with top_k
+// alone.  fp16 and fp32 have no places, so their search takes three to five passes, and a
+// weight about 45 instructions: 257 and 265 with filters of all kinds, 525 and 530 with
+// top_p alone.  4 rows of 131072: 15 us, of which the launch of the clusters and 12 joint steps are
 // most.
 
 constexpr int NT = 512;              // threads, and places of the list
@@ -145,17 +145,15 @@ __device__ __forceinline__ uint64_t goal_of(uint64_t n, float f) {
 struct Weigh {
   float most, c, c_lo;       // log2(e) / temperature in two parts
   const uint2* table;
-  template <bool EXACT>      // x - most is exact in 32 bits, or nearly: 16-bit logits
   __device__ __forceinline__ uint64_t at(float x) const {
     if (x == most) return ONE;
     const float d = x - most;
     const float z = d * c;
     if (!(z > -kReach)) return 0;
-    float lo = fmaf(d, c, -z) + d * c_lo;
-    if constexpr (!EXACT) {
-      const float b = d - x;              // what of -most is in d
-      lo += ((x - (d - b)) - (most + b)) * c;
-    }
+    // with what is lost in d: 2^-25 of the largest, of logits of any type that are far
+    // smaller, which the temperature turns into 2^-21 of a weight
+    const float b = d - x;                // what of -most is in d
+    const float lo = fmaf(d, c, -z) + d * c_lo + ((x - (d - b)) - (most + b)) * c;
     const float m = fmaf(z, 32.f, 12582912.f);
     const int j = __float_as_int(m) - 0x4B400000;
     const float r = fmaf(m - 12582912.f, -0.03125f, z) + lo;
@@ -166,11 +164,15 @@ struct Weigh {
   }
 };
 
+// The same for bf16's middle place, which few logits have: out of line, as the loops
+// that may need it are unrolled over a slot's elements (250 x 250007 with all kinds of
+// filters 128 us, in line 150).
+static __device__ __noinline__ uint64_t weigh_rare(const Weigh& w, float x) { return w.at(x); }
+
 template <int DT>
 struct Elt {
   static constexpr int BYTES = DT == TERN_LOGITS_F32 ? 4 : 2;
   static constexpr int E = 16 / BYTES;       // elements of a 16-byte slot
-  static constexpr bool EXACT = DT != TERN_LOGITS_F32;
 };
 
 // A row in slots of 16 aligned bytes; its first element is element `off` of slot 0.
@@ -389,7 +391,6 @@ __device__ __forceinline__ void add_shared(uint64_t* sum, uint64_t w) {
 template <int DT, int CL>
 struct Sampler {
   static constexpr int E = Elt<DT>::E;
-  static constexpr bool EXACT = Elt<DT>::EXACT;
   Shared& s;
   const Row& row;
   const Weigh& weigh;
@@ -436,7 +437,7 @@ struct Sampler {
           if (key >= lo && key <= hi) {
             const int bin = linear ? linear_bin(x[e], most, step) : (hi - key) >> shift;
             atomicAdd(&s.count[bin], 1u);
-            if (masses) add_shared(&s.mass[bin], weigh.template at<EXACT>(x[e]));
+            if (masses) add_shared(&s.mass[bin], weigh.at(x[e]));
           }
         }
       });
@@ -512,7 +513,7 @@ struct Sampler {
         if (by_count) {
           b.ties = static_cast<uint32_t>(want - above);
         } else {
-          const uint64_t each = max(weigh.template at<EXACT>(of_key(lo)), uint64_t(1));
+          const uint64_t each = max(weigh.at(of_key(lo)), uint64_t(1));
           b.ties = static_cast<uint32_t>(min((want - above_mass + each - 1) / each, static_cast<uint64_t>(in_bin)));
         }
         return b;
@@ -659,7 +660,7 @@ struct Sampler {
   }
 
   __device__ void draw(uint32_t key, uint32_t ties, float u, int32_t* token) {
-    draw(key, ties, u, token, [this](float x) { return weigh.template at<EXACT>(x); });
+    draw(key, ties, u, token, [this](float x) { return weigh.at(x); });
   }
 
   // The list: the n tokens from some logit on; `all`: no others count.  Whether
@@ -669,7 +670,7 @@ struct Sampler {
     while (size < n) size <<= 1;
     const uint64_t x = sort_cta(s.sum, tid < n ? s.list[tid] : uint64_t(0), size);
     const uint32_t key = static_cast<uint32_t>(x >> 32), index = ~static_cast<uint32_t>(x);
-    const uint64_t w = tid < n ? weigh.template at<EXACT>(of_key(key)) : 0;
+    const uint64_t w = tid < n ? weigh.at(of_key(key)) : 0;
     uint64_t before = w, none = 0, sum, z;
     scan_cta(s, before, none, sum, z);
     int kept = n;
@@ -725,7 +726,7 @@ __device__ bool places_border(Shared& s, Places& t, const Row& row, const Weigh&
       if (x[e] >= cut) {
         const int place = Places::of(x[e]);
         atomicAdd(&t.count[place], 1u);
-        if (place == Places::HALF) middle += weigh.at<true>(x[e]);
+        if (place == Places::HALF) middle += weigh_rare(weigh, x[e]);
       }
     }
   });
@@ -810,7 +811,6 @@ __device__ bool places_border(Shared& s, Places& t, const Row& row, const Weigh&
 template <int DT, int CL>
 __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
   constexpr int E = Elt<DT>::E;
-  constexpr bool EXACT = Elt<DT>::EXACT;
   __shared__ Shared s;
   extern __shared__ __align__(16) uint8_t dynamic[];
   Places& places = *reinterpret_cast<Places*>(dynamic);      // bf16
@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
     if (most < Places::MOST && cut > -Places::MOST && !(k > 0 && list)) {
       for (int i = tid; i < Places::COUNT; i += NT) {
         const float x = Places::value(i);
-        places.weight[i] = i != Places::HALF && x <= most && x >= cut ? weigh.at<true>(x) : 0;
+        places.weight[i] = i != Places::HALF && x <= most && x >= cut ? weigh.at(x) : 0;
         places.count[i] = 0;
       }
       __syncthreads();
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
       if ((k == 0 && p >= 1.f) || places_border<CL>(s, places, row, weigh, begin, end, rank, cut, k, p, b)) {
         sampler.draw(b.key, b.ties, u, a.token + r, [&](float x) {
           const int place = Places::of(x);
-          return place == Places::HALF ? weigh.at<true>(x) : places.weight[place];
+          return place == Places::HALF ? weigh_rare(weigh, x) : places.weight[place];
         });
         if constexpr (CL > 1) sync_all<CL>();
         return;
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
       unpack<DT>(w, x);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (sums && x[e] >= cut) mass += weigh.template at<EXACT>(x[e]);
+        if (sums && x[e] >= cut) mass += weigh.at(x[e]);
         const int index = at * E - row.off + e;
         if (x[e] >= from && index >= 0 && index < a.vocab) {
           const uint32_t i = atomicAdd(&first.n, 1u);
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(NT, 2) sample_kernel(const __grid_constant__ S
       k_ties = b.ties;
     }
     if (p < 1.f)
-      want = goal_of(b.found ? b.above_mass + b.ties * weigh.template at<EXACT>(of_key(b.key)) : b.above_mass, p);
+      want = goal_of(b.found ? b.above_mass + b.ties * weigh.at(of_key(b.key)) : b.above_mass, p);
   }
   if (p < 1.f) {
     const Border q = sampler.narrow(k_key, top, false, true, want, p);
