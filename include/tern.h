@@ -734,8 +734,9 @@ typedef struct {
  *   (a, b) -> (a cos - b sin, b cos + a sin)  for pair j of the first `rot`
  *             elements, of the angle position * turns[j]
  *
- * Everything is in 32 bits (angles in 64-bit integers, exact for every
- * position), rounded once: to `dtype`, or to the 8-bit cache's codes.  Exactly
+ * Everything is in 32 bits (an angle is a 64-bit integer of 2^-64 of a turn,
+ * of which cosine and sine take 24 bits, 2^-26 of a turn at any position),
+ * rounded once: to `dtype`, or to the 8-bit cache's codes.  Exactly
  * one of `cache` (of the rows' type) and `cache8` is given.  An entry of
  * `axis` outside [0, axes) counts as 0.  Two rows of one call must not have
  * the same slot.

@@ -72,7 +72,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 //
 // The angle of pair j is position * turns[j] in 64-bit integers, turns of 2^-64:
 // the product wraps where the angle does, so that its top 32 bits are the angle
-// at any position, to 2^-32 of a turn.
+// at any position, to 2^-32 of a turn; as a float, which has 24 bits, to 2^-26.
 //
 // Bound: rows read once and written once.
 

@@ -186,7 +186,10 @@ class Rotary:
     ``axis`` [pairs] says which of several positions of a token turns each
     pair, e.g. time, height and width of an image's tokens.  Pairs are (j, j +
     pairs), or with ``neighbours`` (2 j, 2 j + 1).  ``freq``, numbers or a tensor
-    of them, is read once; it holds any scaling of long contexts."""
+    of them, is read once; a scaling of long contexts that changes angles goes
+    into it.  One that also multiplies cosines and sines by a factor is said
+    elsewhere: its square in the attention's ``scale`` where all of a head is
+    rotated, or the factor in the rotated elements of ``q_norm`` and ``k_norm``."""
 
     def __init__(self, freq, axis=None, neighbours: bool = False, device="cuda"):
         if isinstance(freq, torch.Tensor):
