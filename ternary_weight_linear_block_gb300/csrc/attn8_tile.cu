@@ -709,7 +709,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               step(v[0], c - 1);
             }
           } else {
-            // (few tiles, so short code rather than reads ahead)
+            // short code rather than reads ahead: longer code slows the other loops, and
+            // the wide trees above take 97 us, not 94, when all of their tiles come here
+            // (a zero-valued token in each page)
 #pragma unroll 1
             for (int c = NC - 1; c >= 0; --c) {
               ptx::tmem_ld_32x32b_x16(s_addr + 16 * c, v[0]);
